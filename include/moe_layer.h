@@ -401,6 +401,82 @@ moe_status moe_backward(const moe_desc* d, const void* x, const void* router_w, 
                         float* dx, float* dw_gate_up, float* dw_down, float* dw_router, float* dbias,
                         void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
+/* moe_backward with an additional gradient of the router logits, dlogits
+ * [T][E] fp32 (NULL = moe_backward), such as moe_balance_loss gives:
+ *   dl[t][e] = the layer's (above, at the selected experts) + dlogits[t][e]
+ * goes into dW_router, dbias and dx.  Everything else as moe_backward (the
+ * same workspace). */
+moe_status moe_backward_aux(const moe_desc* d, const void* x, const void* router_w, const void* w_gate_up,
+                            const void* w_down, const int32_t* topk_ids, const float* topk_weights, const void* dy,
+                            const float* dlogits, float* dx, float* dw_gate_up, float* dw_down, float* dw_router,
+                            float* dbias, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* Layer norm over the H channels of each token, the step in front of the
+ * router (and of its quantisation) in a block that trains or serves the layer:
+ *   z[t] = (x[t] - mean[t]) * rstd[t],  mean[t] = sum_h x[t,h] / H,
+ *   rstd[t] = 1 / sqrt(sum_h (x[t,h] - mean[t])^2 / H + eps),
+ *   y[t] = z[t] * gamma + beta           (fp32 throughout, rounded once)
+ * x [T][H] (in_dtype BF16 or F32), gamma [H] and beta [H] fp32 (beta NULL =
+ * zero).  y [T][H] in out_dtype: BF16 or F32 (y_scales must be NULL), or
+ * FP8_E4M3: the fp32 values quantised as moe_quantize_input does (scale_mode
+ * as there), codes in y and fp32 scales in y_scales [T][H/128], the layout
+ * moe_forward takes.  mean and rstd [T] fp32: optional outputs, both or
+ * neither, for moe_layer_norm_backward.  1 <= T, H a multiple of 128 up to
+ * 16384, eps >= 0; pointers 16-byte aligned; y must not overlap x.  Enqueued
+ * on `stream`; errors as moe_forward. */
+moe_status moe_layer_norm(int32_t T, int32_t H, int32_t in_dtype, int32_t out_dtype, int32_t scale_mode,
+                          const void* x, const float* gamma, const float* beta, float eps, void* y, float* y_scales,
+                          float* mean, float* rstd, moe_stream_t stream);
+
+/* Backward pass of moe_layer_norm: with g = dy * gamma and z as above,
+ *   dx[t]  = rstd[t] * (g[t] - sum_h g[t,h] / H - z[t] * sum_h g[t,h] z[t,h] / H)
+ *   dgamma = sum_t dy[t] * z[t],  dbeta = sum_t dy[t]
+ * x [T][H] (x_dtype BF16 or F32) and gamma, mean, rstd as in the forward
+ * call; dy [T][H] (dy_dtype BF16 or F32), e.g. the dx of moe_backward.
+ * Outputs (fp32, overwritten): dx [T][H] (dx may be dy where dy is fp32; no
+ * other overlap), dgamma [H] and dbeta [H] (each optional, NULL = not
+ * computed).  Limits as moe_layer_norm.  workspace: of
+ * moe_layer_norm_backward_workspace_size(T, H) bytes (0 for a shape that is
+ * refused), not needed when neither dgamma nor dbeta is asked for.
+ * Enqueued on `stream`. */
+size_t moe_layer_norm_backward_workspace_size(int32_t T, int32_t H);
+moe_status moe_layer_norm_backward(int32_t T, int32_t H, int32_t x_dtype, int32_t dy_dtype, const void* x,
+                                   const float* gamma, const float* mean, const float* rstd, const void* dy,
+                                   float* dx, float* dgamma, float* dbeta, void* workspace, size_t workspace_bytes,
+                                   moe_stream_t stream);
+
+/* Load-balance loss of a routing, the experts' counts, and the loss's
+ * gradient in the logits.  The T tokens are n_seq sequences, sequence s
+ * being tokens seq_offsets[s] .. seq_offsets[s+1] - 1 (device memory,
+ * [n_seq+1], ascending within 0 .. T; NULL: one sequence of all tokens);
+ * a token counts if token_mask[t] is nonzero ([T] bytes; NULL: every token
+ * counts) and it lies in a sequence.  With p[t] = softmax(logits[t]) over all
+ * E experts, N_s the tokens of sequence s that count, and c_s[e] the entries
+ * of their topk_ids equal to e:
+ *   counts[s][e] = c_s[e]
+ *   probs[s][e]  = sum_t p[t][e] / N_s
+ *   loss         = alpha / S' * sum_s sum_e E c_s[e] / (top_k N_s) * probs[s][e]
+ *   dlogits[t]   = the gradient of loss in logits[t], the counts held fixed
+ * S' being the number of sequences with N_s > 0 (loss 0 if there is none; a
+ * sequence with N_s = 0 has zero counts and probs).  Tokens that do not count
+ * are not read, and their rows of dlogits are zero.  A token whose logits are
+ * all -infinity counts but has no probability and no gradient.  dlogits is
+ * meant for moe_backward_aux.
+ * logits [T][E] fp32 (moe_route's output, or the logits region of
+ * moe_forward's workspace); topk_ids [T][top_k] int32 (ids out of range are
+ * clamped, as in moe_permute).  Outputs, overwritten: counts [n_seq][E] int32,
+ * probs [n_seq][E] fp32, loss [1] fp32, and dlogits [T][E] fp32 (optional,
+ * NULL = not computed; not the logits themselves).  Sums are fp32 (the loss
+ * fp64) in a fixed order: identical inputs give identical bits.  1 <= T,
+ * 1 <= top_k <= min(E, 16), E <= 1024, T * top_k <= 2^30, 1 <= n_seq <= 2^20.
+ * workspace: moe_balance_loss_workspace_size bytes (0 for arguments that are
+ * refused).  Enqueued on `stream`; errors as moe_forward. */
+size_t moe_balance_loss_workspace_size(int32_t T, int32_t E, int32_t top_k, int32_t n_seq);
+moe_status moe_balance_loss(int32_t T, int32_t E, int32_t top_k, int32_t n_seq, const float* logits,
+                            const int32_t* topk_ids, const int32_t* seq_offsets, const uint8_t* token_mask,
+                            float alpha, int32_t* counts, float* probs, float* loss, float* dlogits, void* workspace,
+                            size_t workspace_bytes, moe_stream_t stream);
+
 const char* moe_status_string(moe_status s);
 const char* moe_last_error(void);
 

@@ -3,46 +3,61 @@
     python -m moe_layer_router_amd.build
 
 produces moe_layer_router_amd/libmoe_layer.so from csrc/kernels.hip (the
-layer) and csrc/peaks.hip (peak-rate microbenchmarks).
+layer), csrc/training.hip (the operators around it: layer norm, the balance
+loss, Newton-Schulz orthogonalisation) and csrc/peaks.hip (peak-rate
+microbenchmarks).
 """
 
 import os
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB_DIR = PKG
 LIB = os.path.join(LIB_DIR, "libmoe_layer.so")
-SOURCES = [os.path.join(PKG, "csrc", "kernels.hip"), os.path.join(PKG, "csrc", "peaks.hip")]
+SOURCES = [os.path.join(PKG, "csrc", f) for f in ("kernels.hip", "training.hip", "peaks.hip")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # Packed fp32 VALU instructions are disabled for all device code.  MFMA
 # results go to ordinary VGPRs (the GEMM promotes every MFMA result with
 # VALU FMAs; results in AGPRs would need a copy each).
-FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-mllvm", "-amdgpu-mfma-vgpr-form",
          "-I", os.path.join(ROOT, "include"), "-Wall", "-Wno-unused-function"]
+LINK_FLAGS = ["--offload-arch=gfx950", "-fPIC", "-shared"]
 
 
 def build(verbose: bool = False) -> str:
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp = LIB + ".tmp"
-    cmd = [HIPCC, *FLAGS, *SOURCES, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    # hipcc's host pass does not know the packed-fp32 feature: drop that note
-    noise = "'-packed-fp32-ops' is not a recognized feature for this target (ignoring feature)"
-    err = "\n".join(l for l in r.stderr.splitlines() if noise not in l)
-    if r.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({r.returncode}):\n{err}")
-    if verbose and err.strip():
-        print(err, file=sys.stderr)
+    with tempfile.TemporaryDirectory() as objs:
+        # one object per source, compiled side by side
+        outs = [os.path.join(objs, os.path.basename(s) + ".o") for s in SOURCES]
+        cmds = [[HIPCC, *FLAGS, "-c", s, "-o", o] for s, o in zip(SOURCES, outs)]
+        procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True) for c in cmds]
+        for c, p in zip(cmds, procs):
+            _finish(c, *p.communicate(), p.returncode, verbose)
+        link = [HIPCC, *LINK_FLAGS, *outs, "-o", tmp]
+        r = subprocess.run(link, capture_output=True, text=True)
+        _finish(link, r.stdout, r.stderr, r.returncode, verbose)
     os.replace(tmp, LIB)
     return LIB
+
+
+def _finish(cmd, out, err, rc, verbose):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    # hipcc's host pass does not know the packed-fp32 feature: drop that note
+    noise = "'-packed-fp32-ops' is not a recognized feature for this target (ignoring feature)"
+    err = "\n".join(l for l in err.splitlines() if noise not in l)
+    if rc != 0:
+        raise RuntimeError(f"hipcc failed ({rc}):\n{err}")
+    if verbose and err.strip():
+        print(err, file=sys.stderr)
 
 
 if __name__ == "__main__":

@@ -17,7 +17,8 @@
 //   dXr  [P][H]  = [dG|dU] W_gu[e]                       (linear-1 input gradient per row)
 //   dW_gu[e]     = sum_p [dG|dU]_p^T x[tok(p)]           (K = the expert's rows)
 //   dW_d[e]      = sum_p dy[tok(p)]^T Aw_p                (formed transposed: Aw is the fp32 operand)
-//   router:       dl[t][e_j] = w_j (dw_j - sum_i w_i dw_i), db[e] = sum_t dl[t][e]
+//   router:       dl[t][e_j] = w_j (dw_j - sum_i w_i dw_i) (+ an additional dense gradient
+//                 of the logits, the balance loss's), db[e] = sum_t dl[t][e]
 //   dW_r = dl^T x,  dxr = dl W_r
 //   dx[t] = sum_j dXr[row(t, j)] + dxr[t]               (fp32, ascending j)
 //
@@ -489,10 +490,12 @@ __global__ void __launch_bounds__(256) k_bwd_rows(const float* GU, const float* 
 }
 
 // Router part, one thread per token: dl_j = w_j (dw_j - sum_i w_i dw_i) into
-// the dense [T][E] gradient of the logits (hi / lo BF16 parts); the other
-// entries are left as cleared.
+// the dense [T][E] gradient of the logits (hi / lo BF16 parts), on top of the
+// additional gradient `aux` ([T][E], or NULL); the other entries are left as
+// they were filled (with aux's parts, or zero).
 __global__ void __launch_bounds__(256) k_bwd_router(const int32_t* ids, const float* topk_w, const float* dws,
-                                                    int T, int E, int k, uint16_t* dl_hi, uint16_t* dl_lo) {
+                                                    const float* aux, int T, int E, int k, uint16_t* dl_hi,
+                                                    uint16_t* dl_lo) {
   const int t = blockIdx.x * blockDim.x + threadIdx.x;
   if (t >= T) return;
   float s = 0.f;
@@ -500,7 +503,9 @@ __global__ void __launch_bounds__(256) k_bwd_router(const int32_t* ids, const fl
   for (int j = 0; j < k; ++j) {
     const size_t f = (size_t)t * k + j;
     const int e = min(max(ids[f], 0), E - 1);
-    bwd_split_store(dl_hi, dl_lo, (size_t)t * E + e, topk_w[f] * (dws[f] - s));
+    const size_t i = (size_t)t * E + e;
+    const float own = topk_w[f] * (dws[f] - s);
+    bwd_split_store(dl_hi, dl_lo, i, aux ? own + aux[i] : own);
   }
 }
 
@@ -549,6 +554,12 @@ __global__ void __launch_bounds__(256) k_bwd_gather(const uint16_t* in, const in
     *reinterpret_cast<v4i*>(out + p * H + 8 * c) =
         *reinterpret_cast<const v4i*>(in + (long)(perm[p] / k) * H + 8 * c);
   }
+}
+
+// hi / lo BF16 parts of n fp32 values.
+__global__ void __launch_bounds__(256) k_bwd_split(const float* v, size_t n, uint16_t* hi, uint16_t* lo) {
+  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x)
+    bwd_split_store(hi, lo, i, v[i]);
 }
 
 // Fill n 32-bit words with zero.

@@ -109,6 +109,26 @@ DEV float max_row_groups(float x) {
   return fmaxf(__uint_as_float(r32[0]), __uint_as_float(r32[1]));
 }
 
+// Sum over the 16 lanes of a DPP row, returned to every lane of the row.
+DEV float row_sum16(float v) {
+  v += dpp_mov<0xB1>(v);
+  v += dpp_mov<0x4E>(v);
+  v += dpp_mov<0x141>(v);
+  v += dpp_mov<0x140>(v);
+  return v;
+}
+
+// Sum over the 64 lanes, returned to every lane.
+DEV float wave_sum(float v) {
+  v = row_sum16(v);
+  const uint32_t u = __float_as_uint(v);
+  const auto r16 = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  v = __uint_as_float(r16[0]) + __uint_as_float(r16[1]);
+  const uint32_t h = __float_as_uint(v);
+  const auto r32 = __builtin_amdgcn_permlane32_swap(h, h, false, false);
+  return __uint_as_float(r32[0]) + __uint_as_float(r32[1]);
+}
+
 // Inclusive prefix sum over a workgroup of `nthreads` (multiple of 64) ints.
 // `scratch` needs nthreads/64 ints of LDS.  Returns the inclusive sum of the
 // thread's value; *total receives the workgroup total.

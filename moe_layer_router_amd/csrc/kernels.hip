@@ -516,15 +516,13 @@ k_mega(Plan p) {
 #include <mutex>
 #include <string>
 
-#include "moe_layer.h"
-
-using namespace moe;
+#include "host.h"
 
 namespace {
-
 thread_local std::string g_last_error;
+}
 
-moe_status fail(moe_status s, const char* fmt, ...) {
+moe_status moe::fail(moe_status s, const char* fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
@@ -534,7 +532,9 @@ moe_status fail(moe_status s, const char* fmt, ...) {
   return s;
 }
 
-size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+using namespace moe;
+
+namespace {
 
 struct Layout {
   size_t err, zero_begin, ctr, rdone, rtile, tkdone, done1, done2, zero_end;
@@ -642,31 +642,20 @@ moe_status check_desc(const moe_desc* d) {
   return MOE_OK;
 }
 
-moe_status check_ptr(const void* p, const char* name, bool required = true) {
+}  // namespace
+
+moe_status moe::check_ptr(const void* p, const char* name, bool required) {
   if (!p) return required ? fail(MOE_ERR_INVALID_ARGUMENT, "%s is NULL", name) : MOE_OK;
   if (!aligned16(p)) return fail(MOE_ERR_INVALID_ARGUMENT, "%s is not 16-byte aligned", name);
   return MOE_OK;
 }
 
-#define TRY(expr)                       \
-  do {                                  \
-    moe_status _s = (expr);             \
-    if (_s != MOE_OK) return _s;        \
-  } while (0)
-
-#define HIP_TRY(expr)                                                                    \
-  do {                                                                                   \
-    hipError_t _e = (expr);                                                              \
-    if (_e != hipSuccess) return fail(MOE_ERR_HIP, "%s: %s", #expr, hipGetErrorString(_e)); \
-  } while (0)
-
-struct DevInfo {
-  int checked = 0, ok = 0, cus = 0;
-};
+namespace {
 std::mutex g_dev_mu;
 DevInfo g_dev[64];
+}  // namespace
 
-moe_status device_info(DevInfo* out) {
+moe_status moe::device_info(DevInfo* out) {
   int dev = 0;
   HIP_TRY(hipGetDevice(&dev));
   if (dev < 0 || dev >= 64) return fail(MOE_ERR_UNSUPPORTED, "device index %d out of range", dev);
@@ -683,6 +672,8 @@ moe_status device_info(DevInfo* out) {
   *out = di;
   return MOE_OK;
 }
+
+namespace {
 
 // The workspace of moe_forward_static: a file-scope device array, one copy
 // per GPU.  In host code `scratch` names a host-side stand-in, not device
@@ -764,12 +755,6 @@ moe_status check_workspace(const moe_desc* d, const void* ws, size_t bytes, int 
   const size_t need = workspace_need(d, what);
   if (bytes < need)
     return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, needs %zu", bytes, need);
-  return MOE_OK;
-}
-
-template <typename K>
-moe_status set_lds_limit(K kernel, int bytes) {
-  if (bytes > 64 * 1024) HIP_TRY(hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes));
   return MOE_OK;
 }
 
@@ -1238,6 +1223,14 @@ moe_status moe_backward(const moe_desc* d, const void* x, const void* router_w, 
                         const void* w_down, const int32_t* topk_ids, const float* topk_weights, const void* dy,
                         float* dx, float* dw_gate_up, float* dw_down, float* dw_router, float* dbias,
                         void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  return moe_backward_aux(d, x, router_w, w_gate_up, w_down, topk_ids, topk_weights, dy, nullptr, dx, dw_gate_up,
+                          dw_down, dw_router, dbias, workspace, workspace_bytes, stream);
+}
+
+moe_status moe_backward_aux(const moe_desc* d, const void* x, const void* router_w, const void* w_gate_up,
+                            const void* w_down, const int32_t* topk_ids, const float* topk_weights, const void* dy,
+                            const float* dlogits, float* dx, float* dw_gate_up, float* dw_down, float* dw_router,
+                            float* dbias, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
   TRY(check_bwd_desc(d));
   TRY(check_ptr(x, "x"));
   TRY(check_ptr(router_w, "router_w"));
@@ -1246,6 +1239,7 @@ moe_status moe_backward(const moe_desc* d, const void* x, const void* router_w, 
   TRY(check_ptr(topk_ids, "topk_ids"));
   TRY(check_ptr(topk_weights, "topk_weights"));
   TRY(check_ptr(dy, "dy"));
+  TRY(check_ptr(dlogits, "dlogits", false));
   TRY(check_ptr(dx, "dx"));
   TRY(check_ptr(dw_gate_up, "dw_gate_up"));
   TRY(check_ptr(dw_down, "dw_down"));
@@ -1276,11 +1270,15 @@ moe_status moe_backward(const moe_desc* d, const void* x, const void* router_w, 
   uint16_t* dl_lo = reinterpret_cast<uint16_t*>(ws + B.dl_lo);
   float* dxr = reinterpret_cast<float*>(ws + B.dxr);
 
-  // counters, then the dense logit gradients (only the selected entries are written)
+  // counters, then the dense logit gradients (the additional ones or zero;
+  // the layer's own are written at the selected entries)
   hipLaunchKernelGGL(k_zero, dim3(16), dim3(256), 0, st, p.err, (p.zero_bytes + 256) / 4);
   HIP_TRY(hipGetLastError());
-  hipLaunchKernelGGL(k_bwd_zero, dim3(di.cus * 4), dim3(256), 0, st, reinterpret_cast<uint32_t*>(dl_hi),
-                     (B.dxr - B.dl) / 4);        // both parts
+  if (dlogits)
+    hipLaunchKernelGGL(k_bwd_split, dim3(di.cus * 4), dim3(256), 0, st, dlogits, (size_t)T * E, dl_hi, dl_lo);
+  else
+    hipLaunchKernelGGL(k_bwd_zero, dim3(di.cus * 4), dim3(256), 0, st, reinterpret_cast<uint32_t*>(dl_hi),
+                       (B.dxr - B.dl) / 4);      // both parts
   HIP_TRY(hipGetLastError());
   p.tile_rows = kBwdBM;
   TRY(launch_permute(p, p.row_of, st));          // perm, offsets, row_of, row tiles of at most kBwdBM
@@ -1339,8 +1337,8 @@ moe_status moe_backward(const moe_desc* d, const void* x, const void* router_w, 
   TRY(launch_bwd_gemm(g, up(I, kBwdBM), up(H, kBwdBN), E, st));
   g.c_trans = 0;
   // router: logit gradients, bias, W_r and the router's share of dx
-  hipLaunchKernelGGL(k_bwd_router, dim3(up(T, 256)), dim3(256), 0, st, topk_ids, topk_weights, dws, T, E, k, dl_hi,
-                     dl_lo);
+  hipLaunchKernelGGL(k_bwd_router, dim3(up(T, 256)), dim3(256), 0, st, topk_ids, topk_weights, dws, dlogits, T, E, k,
+                     dl_hi, dl_lo);
   HIP_TRY(hipGetLastError());
   if (dbias) {
     hipLaunchKernelGGL(k_bwd_dbias, dim3(E), dim3(256), 0, st, dl_hi, dl_lo, T, E, dbias);

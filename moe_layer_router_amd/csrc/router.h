@@ -284,13 +284,6 @@ DEV uint64_t row_max16_u64(uint64_t v) {
   o = dpp_mov64<0x140>(v); v = o > v ? o : v;
   return v;
 }
-DEV float row_sum16(float v) {
-  v += dpp_mov<0xB1>(v);
-  v += dpp_mov<0x4E>(v);
-  v += dpp_mov<0x141>(v);
-  v += dpp_mov<0x140>(v);
-  return v;
-}
 
 // Max of a 64-bit key over the whole wave: row maxima by DPP, then the
 // gfx950 lane swaps across row pairs and wave halves.

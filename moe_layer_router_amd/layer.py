@@ -1,5 +1,9 @@
 """Convenience wrapper: allocate outputs and workspace with PyTorch and call
-moe_forward / moe_route / moe_permute.  No arithmetic happens here."""
+moe_forward / moe_route / moe_permute, and the operators of a training step
+around the layer (layer_norm, balance_loss, backward).  No
+arithmetic happens here."""
+
+import contextlib
 
 import torch
 
@@ -144,11 +148,13 @@ def dequantize_e5m6(xq: torch.Tensor, xs: torch.Tensor, stream=None) -> torch.Te
 
 
 def backward(inputs: dict, topk_ids: torch.Tensor, topk_weights: torch.Tensor, dy: torch.Tensor,
-             workspace: Workspace = None, stream=None, want_dbias: bool = True, out: dict = None) -> dict:
+             workspace: Workspace = None, stream=None, want_dbias: bool = True, out: dict = None,
+             dlogits: torch.Tensor = None) -> dict:
     """Gradients of a BF16 layer (moe_backward) for the routing a forward
     call returned, from row-major weights (inputs as generated, not packed).
-    Returns dict(dx, dw_gate_up, dw_down, dw_router, dbias), fp32 (`out`, a
-    previous result, is reused)."""
+    dlogits: an additional gradient of the router logits [T, E] float32
+    (balance_loss's; moe_backward_aux).  Returns dict(dx, dw_gate_up, dw_down,
+    dw_router, dbias), fp32 (`out`, a previous result, is reused)."""
     if inputs.get("weights_packed"):
         raise ValueError("backward() reads the row-major weights: pass the inputs before pack_weights()")
     x = inputs["x"]
@@ -163,9 +169,176 @@ def backward(inputs: dict, topk_ids: torch.Tensor, topk_weights: torch.Tensor, d
                    dw_down=torch.empty(E, H, I, **f32), dw_router=torch.empty(E, H, **f32),
                    dbias=torch.empty(E, **f32) if want_dbias else None)
     ws = (workspace or Workspace(dev)).get(lib.moe_backward_workspace_size(desc))
-    lib.moe_backward(desc, x, inputs["router_w"], inputs["w_gate_up"].contiguous(), inputs["w_down"].contiguous(),
-                     topk_ids.contiguous(), topk_weights.contiguous(), dy.contiguous(), out["dx"], out["dw_gate_up"],
-                     out["dw_down"], out["dw_router"], out["dbias"], ws, stream)
+    if dlogits is not None:
+        _need(dlogits.shape == (T, E) and dlogits.dtype == torch.float32 and dlogits.device == dev,
+              f"dlogits must be float32 [{T}, {E}] on {dev}")
+        dlogits = dlogits.contiguous()
+    lib.moe_backward_aux(desc, x, inputs["router_w"], inputs["w_gate_up"].contiguous(), inputs["w_down"].contiguous(),
+                         topk_ids.contiguous(), topk_weights.contiguous(), dy.contiguous(), dlogits, out["dx"],
+                         out["dw_gate_up"], out["dw_down"], out["dw_router"], out["dbias"], ws, stream)
+    return out
+
+
+def logits(out: dict) -> torch.Tensor:
+    """View of the router logits [T, E] (float32, bias included) of a finished
+    forward() call that did the routing itself."""
+    desc, ws = out["desc"], out["workspace"]
+    _need(not desc.flags & lib.MOE_FLAG_ROUTING_GIVEN, "the call was given its routing: it has no logits")
+    at = lib.moe_get_workspace_regions(desc)["logits"]
+    return ws[at: at + desc.T * desc.E * 4].view(torch.float32).view(desc.T, desc.E)
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device, stream):
+    """Context in which `device` is the current device and `stream` (None: the
+    device's current stream) its current stream, so that copies, outputs and
+    workspaces of a call belong to the stream that the call runs on."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream, device)
+        return torch.cuda.stream(stream)
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _dense(t):
+    """t, or a copy of it that is contiguous and starts on a 16-byte boundary."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _is(t, name, shape, dtypes, device, out=False):
+    """Check an argument; outputs must be laid out as the library writes them."""
+    _need(isinstance(t, torch.Tensor) and tuple(t.shape) == tuple(shape), f"{name} must be a tensor {list(shape)}")
+    _need(t.dtype in dtypes, f"{name} must be {' or '.join(str(d) for d in dtypes)} (got {t.dtype})")
+    _need(t.is_cuda and t.device == device, f"{name} must be on {device} (got {t.device})")
+    _need(not out or t.is_contiguous(), f"{name} must be contiguous")
+
+
+_FLOATS = (torch.bfloat16, torch.float32)
+_F32 = (torch.float32,)
+_OUT_DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32, "fp8": torch.uint8}
+
+
+def layer_norm(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor = None, eps: float = 1e-5,
+               out_dtype: str = "bf16", scale_mode: str = "f32", want_stats: bool = False, stream=None,
+               out: dict = None) -> dict:
+    """Layer norm of [T, H] bfloat16 / float32 activations (moe_layer_norm),
+    gamma and beta [H] float32.  out_dtype "bf16", "f32", or "fp8": the layer's
+    quantised input (E4M3 codes as uint8, with scales).  Returns dict(y,
+    y_scales, mean, rstd): y [T, H], y_scales [T, H/128] float32 ("fp8", else
+    None), mean and rstd [T] float32 (want_stats, for layer_norm_backward, else
+    None); `out`, a previous result, is reused."""
+    _need(x.dim() == 2 and x.is_cuda, "x must be a [T, H] tensor on a GPU")
+    T, H = x.shape
+    dev = x.device
+    _need(x.dtype in _FLOATS, f"x must be bfloat16 or float32 (got {x.dtype})")
+    _need(out_dtype in _OUT_DTYPES, f"unknown out_dtype {out_dtype!r}")
+    _need(scale_mode in lib.INTER_SCALES, f"unknown scale_mode {scale_mode!r}")
+    _is(gamma, "gamma", (H,), _F32, dev)
+    if beta is not None:
+        _is(beta, "beta", (H,), _F32, dev)
+    dt = _OUT_DTYPES[out_dtype]
+    fp8 = out_dtype == "fp8"
+    with _on(dev, stream):
+        if out is None:
+            out = dict(y=torch.empty(T, H, dtype=dt, device=dev),
+                       y_scales=torch.empty(T, H // 128, dtype=torch.float32, device=dev) if fp8 else None,
+                       mean=torch.empty(T, dtype=torch.float32, device=dev) if want_stats else None,
+                       rstd=torch.empty(T, dtype=torch.float32, device=dev) if want_stats else None)
+        else:
+            _is(out["y"], "out['y']", (T, H), (dt,), dev, True)
+            for name, shape, wanted in (("y_scales", (T, H // 128), fp8), ("mean", (T,), want_stats),
+                                        ("rstd", (T,), want_stats)):
+                _need((out[name] is not None) == wanted, f"out[{name!r}] does not fit the call")
+                if wanted:
+                    _is(out[name], f"out[{name!r}]", shape, _F32, dev, True)
+        lib.moe_layer_norm(_dense(x), _dense(gamma), None if beta is None else _dense(beta), eps, out["y"],
+                           out["y_scales"], out["mean"], out["rstd"], scale_mode)
+    return out
+
+
+def layer_norm_backward(x: torch.Tensor, gamma: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                        dy: torch.Tensor, want_weights: bool = True, workspace: Workspace = None, stream=None,
+                        out: dict = None) -> dict:
+    """Backward pass of layer_norm (moe_layer_norm_backward) for dy [T, H]
+    bfloat16 / float32 and the statistics of the forward call.  Returns
+    dict(dx [T, H], dgamma [H], dbeta [H]), float32; without want_weights
+    dgamma and dbeta are None.  `out`, a previous result, is reused (out["dx"]
+    may be dy)."""
+    _need(x.dim() == 2 and x.is_cuda, "x must be a [T, H] tensor on a GPU")
+    T, H = x.shape
+    dev = x.device
+    _need(x.dtype in _FLOATS, f"x must be bfloat16 or float32 (got {x.dtype})")
+    _is(gamma, "gamma", (H,), _F32, dev)
+    _is(mean, "mean", (T,), _F32, dev)
+    _is(rstd, "rstd", (T,), _F32, dev)
+    _is(dy, "dy", (T, H), _FLOATS, dev)
+    with _on(dev, stream):
+        f32 = dict(dtype=torch.float32, device=dev)
+        if out is None:
+            out = dict(dx=torch.empty(T, H, **f32), dgamma=torch.empty(H, **f32) if want_weights else None,
+                       dbeta=torch.empty(H, **f32) if want_weights else None)
+        else:
+            _is(out["dx"], "out['dx']", (T, H), _F32, dev, True)
+            for name in ("dgamma", "dbeta"):
+                _need((out[name] is not None) == want_weights, f"out[{name!r}] does not fit the call")
+                if want_weights:
+                    _is(out[name], f"out[{name!r}]", (H,), _F32, dev, True)
+        ws = None
+        if want_weights:
+            nbytes = lib.moe_layer_norm_backward_workspace_size(T, H)
+            ws = (workspace or Workspace(dev)).get(nbytes)
+        lib.moe_layer_norm_backward(_dense(x), _dense(gamma), _dense(mean), _dense(rstd), _dense(dy), out["dx"],
+                                    out["dgamma"], out["dbeta"], ws)
+    return out
+
+
+def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, alpha: float = 1.0, seq_offsets: torch.Tensor = None,
+                 token_mask: torch.Tensor = None, want_grad: bool = True, workspace: Workspace = None, stream=None,
+                 out: dict = None) -> dict:
+    """Load-balance loss of a routing (moe_balance_loss): logits [T, E] float32
+    and topk_ids [T, k] as route() returns them, seq_offsets [S + 1] integers
+    (None: one sequence), token_mask [T] bool or uint8 (None: every token
+    counts).  Returns dict(loss [1] float32, counts [S, E] int32, probs [S, E]
+    float32, dlogits [T, E] float32 or, without want_grad, None); `out`, a
+    previous result, is reused."""
+    _need(logits.dim() == 2 and logits.is_cuda and logits.dtype == torch.float32,
+          "logits must be a float32 [T, E] tensor on a GPU")
+    T, E = logits.shape
+    dev = logits.device
+    _need(topk_ids.dim() == 2, "topk_ids must be [T, k]")
+    _is(topk_ids, "topk_ids", (T, topk_ids.shape[1]), (torch.int32, torch.int64), dev)
+    S = 1
+    if seq_offsets is not None:
+        _need(seq_offsets.dim() == 1 and seq_offsets.shape[0] >= 2, "seq_offsets must be [n_seq + 1]")
+        S = seq_offsets.shape[0] - 1
+        _is(seq_offsets, "seq_offsets", (S + 1,), (torch.int32, torch.int64), dev)
+    if token_mask is not None:
+        _is(token_mask, "token_mask", (T,), (torch.bool, torch.uint8), dev)
+    with _on(dev, stream):
+        f32 = dict(dtype=torch.float32, device=dev)
+        if out is None:
+            out = dict(loss=torch.empty(1, **f32), counts=torch.empty(S, E, dtype=torch.int32, device=dev),
+                       probs=torch.empty(S, E, **f32), dlogits=torch.empty(T, E, **f32) if want_grad else None)
+        else:
+            _need((out["dlogits"] is not None) == want_grad, "out['dlogits'] does not fit the call")
+            for name, shape, dt in (("loss", (1,), torch.float32), ("counts", (S, E), torch.int32),
+                                    ("probs", (S, E), torch.float32), ("dlogits", (T, E), torch.float32)):
+                if out[name] is not None:
+                    _is(out[name], f"out[{name!r}]", shape, (dt,), dev, True)
+        nbytes = lib.moe_balance_loss_workspace_size(T, E, topk_ids.shape[1], S)
+        ws = (workspace or Workspace(dev)).get(nbytes)
+        lib.moe_balance_loss(_dense(logits), _dense(topk_ids.to(torch.int32)),
+                             None if seq_offsets is None else _dense(seq_offsets.to(torch.int32)),
+                             None if token_mask is None else _dense(token_mask), alpha, out["counts"], out["probs"],
+                             out["loss"], out["dlogits"], ws)
     return out
 
 

@@ -108,6 +108,18 @@ _lib.moe_backward_workspace_size.restype = ctypes.c_size_t
 _lib.moe_backward_workspace_size.argtypes = [ctypes.POINTER(MoeDesc)]
 _lib.moe_backward.restype = ctypes.c_int
 _lib.moe_backward.argtypes = [ctypes.POINTER(MoeDesc)] + [_P] * 13 + [ctypes.c_size_t, _P]
+_lib.moe_backward_aux.restype = ctypes.c_int
+_lib.moe_backward_aux.argtypes = [ctypes.POINTER(MoeDesc)] + [_P] * 14 + [ctypes.c_size_t, _P]
+_lib.moe_layer_norm.restype = ctypes.c_int
+_lib.moe_layer_norm.argtypes = [ctypes.c_int32] * 5 + [_P] * 3 + [ctypes.c_float] + [_P] * 5
+_lib.moe_layer_norm_backward_workspace_size.restype = ctypes.c_size_t
+_lib.moe_layer_norm_backward_workspace_size.argtypes = [ctypes.c_int32] * 2
+_lib.moe_layer_norm_backward.restype = ctypes.c_int
+_lib.moe_layer_norm_backward.argtypes = [ctypes.c_int32] * 4 + [_P] * 9 + [ctypes.c_size_t, _P]
+_lib.moe_balance_loss_workspace_size.restype = ctypes.c_size_t
+_lib.moe_balance_loss_workspace_size.argtypes = [ctypes.c_int32] * 4
+_lib.moe_balance_loss.restype = ctypes.c_int
+_lib.moe_balance_loss.argtypes = [ctypes.c_int32] * 4 + [_P] * 4 + [ctypes.c_float] + [_P] * 5 + [ctypes.c_size_t, _P]
 _lib.moe_forward_static.restype = ctypes.c_int
 _lib.moe_forward_static.argtypes = [ctypes.POINTER(MoeDesc)] + [_P] * 13 + [_P]
 _lib.moe_route.restype = ctypes.c_int
@@ -232,6 +244,15 @@ def moe_backward_workspace_size(desc) -> int:
     return _lib.moe_backward_workspace_size(ctypes.byref(desc))
 
 
+def moe_backward_aux(desc, x, router_w, w_gate_up, w_down, topk_ids, topk_weights, dy, dlogits, dx, dw_gate_up,
+                     dw_down, dw_router, dbias, workspace, stream=None):
+    nbytes = _nbytes(workspace) if workspace is not None else 0
+    _check(_lib.moe_backward_aux(ctypes.byref(desc), _ptr(x), _ptr(router_w), _ptr(w_gate_up), _ptr(w_down),
+                                 _ptr(topk_ids), _ptr(topk_weights), _ptr(dy), _ptr(dlogits), _ptr(dx),
+                                 _ptr(dw_gate_up), _ptr(dw_down), _ptr(dw_router), _ptr(dbias), _ptr(workspace),
+                                 nbytes, _stream(stream)), "moe_backward_aux")
+
+
 def moe_backward(desc, x, router_w, w_gate_up, w_down, topk_ids, topk_weights, dy, dx, dw_gate_up, dw_down,
                  dw_router, dbias, workspace, stream=None):
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
@@ -264,6 +285,48 @@ def moe_dequantize_e5m6(xq, x_scales, out, stream=None):
     T, H = out.shape
     _check(_lib.moe_dequantize_e5m6(T, H, _ptr(xq), _ptr(x_scales), _ptr(out), _stream(stream)),
            "moe_dequantize_e5m6")
+
+
+def _float_dtype(t):
+    return MOE_DTYPE_BF16 if t.dtype == torch.bfloat16 else MOE_DTYPE_F32
+
+
+def moe_layer_norm(x, gamma, beta, eps, y, y_scales, mean, rstd, scale_mode="f32", stream=None):
+    """x: [T, H] bfloat16 or float32; gamma, beta (or None) [H] float32; y [T, H] bfloat16, float32 or uint8
+    (E4M3 codes, with y_scales [T, H/128] float32); mean, rstd [T] float32 or None."""
+    T, H = x.shape
+    out = MOE_DTYPE_FP8_E4M3 if y.dtype == torch.uint8 else _float_dtype(y)
+    _check(_lib.moe_layer_norm(T, H, _float_dtype(x), out, INTER_SCALES.get(scale_mode, scale_mode), _ptr(x),
+                               _ptr(gamma), _ptr(beta), eps, _ptr(y), _ptr(y_scales), _ptr(mean), _ptr(rstd),
+                               _stream(stream)), "moe_layer_norm")
+
+
+def moe_layer_norm_backward_workspace_size(T: int, H: int) -> int:
+    return _lib.moe_layer_norm_backward_workspace_size(T, H)
+
+
+def moe_layer_norm_backward(x, gamma, mean, rstd, dy, dx, dgamma, dbeta, workspace, stream=None):
+    """x, dy: [T, H] bfloat16 or float32; dx [T, H], dgamma, dbeta [H] (or None) float32."""
+    T, H = x.shape
+    nbytes = _nbytes(workspace) if workspace is not None else 0
+    _check(_lib.moe_layer_norm_backward(T, H, _float_dtype(x), _float_dtype(dy), _ptr(x), _ptr(gamma), _ptr(mean),
+                                        _ptr(rstd), _ptr(dy), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace),
+                                        nbytes, _stream(stream)), "moe_layer_norm_backward")
+
+
+def moe_balance_loss_workspace_size(T: int, E: int, top_k: int, n_seq: int) -> int:
+    return _lib.moe_balance_loss_workspace_size(T, E, top_k, n_seq)
+
+
+def moe_balance_loss(logits, topk_ids, seq_offsets, token_mask, alpha, counts, probs, loss, dlogits, workspace,
+                     stream=None):
+    """logits [T, E] float32, topk_ids [T, k] int32, seq_offsets [S + 1] int32 or None, token_mask [T] bytes or None;
+    counts [S, E] int32, probs [S, E], loss [1], dlogits [T, E] (or None) float32."""
+    T, E = logits.shape
+    _check(_lib.moe_balance_loss(T, E, topk_ids.shape[1], counts.shape[0], _ptr(logits), _ptr(topk_ids),
+                                 _ptr(seq_offsets), _ptr(token_mask), alpha, _ptr(counts), _ptr(probs), _ptr(loss),
+                                 _ptr(dlogits), _ptr(workspace), _nbytes(workspace), _stream(stream)),
+           "moe_balance_loss")
 
 
 def moe_route(desc, x, x_scales, router_w, router_bias, logits, topk_ids, topk_weights, workspace,
@@ -305,4 +368,6 @@ def exported_symbols():
             "moe_permute_workspace_size", "moe_get_workspace_regions", "moe_validate", "moe_forward", "moe_route",
             "moe_permute", "moe_pack_weights", "moe_status_string", "moe_last_error",
             "moe_peak_mfma_flops", "moe_peak_mfma", "moe_peak_hbm_read", "moe_backward_workspace_size",
-            "moe_backward", "moe_quantize_e5m6", "moe_dequantize_e5m6"]
+            "moe_backward", "moe_quantize_e5m6", "moe_dequantize_e5m6", "moe_backward_aux", "moe_layer_norm",
+            "moe_layer_norm_backward_workspace_size", "moe_layer_norm_backward", "moe_balance_loss_workspace_size",
+            "moe_balance_loss"]
