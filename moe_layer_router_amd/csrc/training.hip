@@ -5,8 +5,10 @@
 #include "host.h"
 #include "balance.h"
 #include "norm.h"
+#include "orthogonalize.h"
 
 #include <algorithm>
+#include <cmath>
 
 using namespace moe;
 
@@ -125,6 +127,118 @@ moe_status launch_bal_tokens(const BalArgs& a, int grid, hipStream_t st) {
   hipLaunchKernelGGL((k_bal_tokens<L, NJ>), dim3(grid), dim3(256), 5 * L * NJ * 4 * 4, st, a);
   HIP_TRY(hipGetLastError());
   return MOE_OK;
+}
+
+// -------------------------------------------------------- orthogonalisation
+constexpr float kOrthCoeffs[3] = {3.4445f, -4.7750f, 2.0315f};
+constexpr int kOrthMaxSteps = 32;
+constexpr size_t kOrthChunkBytes = (size_t)8 << 30;
+
+struct OrthLayout {
+  int m, n, mp, np, chunk;           // short and long side, padded; matrices worked on together
+  size_t part, hi, lo, ht0, ht1, a, b, total;
+  int sq, slabs;                     // narrow matrices: padded side, partial Gram matrices
+  size_t q;
+};
+
+OrthLayout orth_layout(int batch, int M, int N) {
+  OrthLayout L{};
+  L.m = std::min(M, N);
+  L.n = std::max(M, N);
+  L.mp = (L.m + kOrthPad - 1) / kOrthPad * kOrthPad;
+  L.np = (L.n + kOrthPad - 1) / kOrthPad * kOrthPad;
+  if (L.m <= kOrthNarrow) {
+    L.sq = L.m <= 16 ? 16 : L.m <= 32 ? 32 : 64;
+    L.slabs = std::min(kOrthSlabs, (L.n + 63) / 64);
+    L.chunk = batch;
+    const size_t e = (size_t)L.sq * L.sq * batch;
+    L.q = align256(L.slabs * e * 8);
+    L.total = L.q + align256(e * 4);
+    return L;
+  }
+  const size_t x = (size_t)L.mp * L.np * 2, q = (size_t)L.mp * L.mp * 2;
+  // a large batch goes through in parts of at most 8 GiB, each of which
+  // fills the GPU
+  L.chunk = (int)std::min((size_t)batch, std::max((size_t)1, kOrthChunkBytes / (4 * x + 2 * q)));
+  const size_t c = L.chunk;
+  size_t o = 0;
+  L.part = o; o = align256(o + c * kOrthNormParts * 8);
+  L.hi = o; o = align256(o + c * x);
+  L.lo = o; o = align256(o + c * x);
+  L.ht0 = o; o = align256(o + c * x);
+  L.ht1 = o; o = align256(o + c * x);
+  L.a = o; o = align256(o + c * q);
+  L.b = o; o = align256(o + c * q);
+  L.total = o;
+  return L;
+}
+
+moe_status check_orth(int32_t batch, int32_t M, int32_t N) {
+  if (batch < 1) return fail(MOE_ERR_INVALID_ARGUMENT, "batch must be >= 1 (got %d)", batch);
+  if (M < 1 || N < 1) return fail(MOE_ERR_INVALID_ARGUMENT, "M and N must be >= 1 (got %d, %d)", M, N);
+  // 32-bit offsets within a matrix's FP16 buffers
+  if (M > 32768 || N > 32768 || std::min(M, N) > 16384)
+    return fail(MOE_ERR_UNSUPPORTED, "matrices up to 16384 x 32768 are supported (got %d x %d)", M, N);
+  if (batch > 65535) return fail(MOE_ERR_UNSUPPORTED, "batch > 65535 is not supported (got %d)", batch);
+  return MOE_OK;
+}
+
+// Whether X, A and B stay within FP16's range times 2^-12 over the steps: the
+// singular values start in [0, 1], and a step takes [0, s] to its image under
+// the polynomial.
+bool orth_in_range(int steps, const float* co) {
+  double top = 1;
+  for (int k = 0; k < steps; ++k) {
+    const double a = co[3 * k], b = co[3 * k + 1], c = co[3 * k + 2];
+    double next = 0;
+    for (int i = 0; i <= 1024; ++i) {
+      const double s = top * i / 1024, s2 = s * s, bv = b * s2 + c * s2 * s2, to = std::fabs(s * (a + bv));
+      if (!(std::fabs(bv) < 15) || !(s2 < 15) || !(to < 14)) return false;      // (NaN: false too)
+      next = std::max(next, to);
+    }
+    top = 1.01 * next;                    // (rounding, and the grid's gaps)
+  }
+  return true;
+}
+
+template <int WM, int WN, int MI, int NJ, int MODE>
+moe_status launch_orth_gemm(OrthGemm g, int batch, hipStream_t st) {
+  using TL = OrthTile<WM, WN, MI, NJ>;
+  g.ti = (g.rows + TL::kRows - 1) / TL::kRows;
+  g.tj = (g.cols + TL::kCols - 1) / TL::kCols;
+  g.tiles = MODE == ORTH_GRAM || MODE == ORTH_POLY ? g.ti * (g.ti + 1) / 2 : g.ti * g.tj;
+  g.total = g.tiles * batch;
+  TRY(set_lds_limit(k_orth_gemm<WM, WN, MI, NJ, MODE>, TL::kLds));
+  hipLaunchKernelGGL((k_orth_gemm<WM, WN, MI, NJ, MODE>), dim3((unsigned)((g.total + 7) / 8 * 8)), dim3(TL::kThreads),
+                     TL::kLds, st, g);
+  HIP_TRY(hipGetLastError());
+  return MOE_OK;
+}
+template <int MODE>
+moe_status launch_orth_gemm(const OrthGemm& g, int batch, int cus, hipStream_t st) {
+  const long big = (long)((g.rows + 255) / 256) * ((g.cols + 255) / 256) * batch;
+  if (big >= 2L * cus) return launch_orth_gemm<2, 4, 8, 4, MODE>(g, batch, st);
+  return launch_orth_gemm<2, 2, 4, 4, MODE>(g, batch, st);
+}
+
+template <int BF, int MP>
+moe_status launch_orth_narrow(const OrthNarrow& a, int batch, hipStream_t st) {
+  hipLaunchKernelGGL((k_orth_gram64<BF, MP>), dim3(a.slabs, batch), dim3(256), 0, st, a);
+  HIP_TRY(hipGetLastError());
+  TRY(set_lds_limit(k_orth_iter64<MP>, OrthSq<MP>::kLds));
+  hipLaunchKernelGGL(k_orth_iter64<MP>, dim3(batch), dim3(256), OrthSq<MP>::kLds, st, a);
+  HIP_TRY(hipGetLastError());
+  const dim3 grid((a.n + kOrthApply - 1) / kOrthApply, batch);
+  if (a.tall) hipLaunchKernelGGL((k_orth_apply<BF, MP, 1>), grid, dim3(kOrthApply), 0, st, a);
+  else hipLaunchKernelGGL((k_orth_apply<BF, MP, 0>), grid, dim3(kOrthApply), 0, st, a);
+  HIP_TRY(hipGetLastError());
+  return MOE_OK;
+}
+template <int BF>
+moe_status launch_orth_narrow(const OrthNarrow& a, int sq, int batch, hipStream_t st) {
+  if (sq == 16) return launch_orth_narrow<BF, 16>(a, batch, st);
+  if (sq == 32) return launch_orth_narrow<BF, 32>(a, batch, st);
+  return launch_orth_narrow<BF, 64>(a, batch, st);
 }
 
 }  // namespace
@@ -254,6 +368,112 @@ moe_status moe_balance_loss(int32_t T, int32_t E, int32_t top_k, int32_t n_seq, 
   else TRY((launch_bal_tokens<64, 4>(a, L.nt, st)));
   hipLaunchKernelGGL(k_bal_final, dim3(L.gx, L.gy), dim3(256), 0, st, a);
   HIP_TRY(hipGetLastError());
+  return MOE_OK;
+}
+
+size_t moe_orthogonalize_workspace_size(int32_t batch, int32_t M, int32_t N) {
+  if (check_orth(batch, M, N) != MOE_OK) return 0;
+  return orth_layout(batch, M, N).total;
+}
+
+moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dtype, const void* u, int32_t steps,
+                             const float* coeffs, float eps, void* y, void* workspace, size_t workspace_bytes,
+                             moe_stream_t stream) {
+  TRY(check_orth(batch, M, N));
+  if (in_dtype != MOE_DTYPE_BF16 && in_dtype != MOE_DTYPE_F32)
+    return fail(MOE_ERR_UNSUPPORTED, "in_dtype must be MOE_DTYPE_BF16 or MOE_DTYPE_F32 (got %d)", in_dtype);
+  if (steps < 1) return fail(MOE_ERR_INVALID_ARGUMENT, "steps must be >= 1 (got %d)", steps);
+  if (steps > kOrthMaxSteps) return fail(MOE_ERR_UNSUPPORTED, "steps > %d is not supported (got %d)", kOrthMaxSteps, steps);
+  if (!(eps > 0.f)) return fail(MOE_ERR_INVALID_ARGUMENT, "eps must be positive (got %g)", (double)eps);
+  if (coeffs && !orth_in_range(steps, coeffs))
+    return fail(MOE_ERR_UNSUPPORTED, "coeffs let the iteration leave the range of its FP16 products");
+  TRY(check_ptr(u, "u"));
+  TRY(check_ptr(y, "y"));
+  TRY(check_ptr(workspace, "workspace"));
+  const size_t elems = (size_t)M * N, isz = in_dtype == MOE_DTYPE_BF16 ? 2 : 4;
+  const uintptr_t u0 = (uintptr_t)u, y0 = (uintptr_t)y;
+  if (u0 < y0 + batch * elems * 2 && y0 < u0 + batch * elems * isz)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "y overlaps u");
+  const OrthLayout L = orth_layout(batch, M, N);
+  if (workspace_bytes < L.total)
+    return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, needs %zu", workspace_bytes, L.total);
+  DevInfo di;
+  TRY(device_info(&di));
+  char* ws = static_cast<char*>(workspace);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const bool bf = in_dtype == MOE_DTYPE_BF16;
+  if (L.sq) {
+    OrthNarrow a{};
+    a.u = u; a.m = L.m; a.n = L.n; a.tall = M > N; a.slabs = L.slabs; a.steps = steps; a.eps = eps;
+    for (int k = 0; k < steps; ++k)
+      for (int i = 0; i < 3; ++i) a.co[k][i] = coeffs ? coeffs[3 * k + i] : kOrthCoeffs[i];
+    a.part = reinterpret_cast<double*>(ws);
+    a.q = reinterpret_cast<float*>(ws + L.q);
+    a.y = static_cast<uint16_t*>(y);
+    return bf ? launch_orth_narrow<1>(a, L.sq, batch, st) : launch_orth_narrow<0>(a, L.sq, batch, st);
+  }
+  for (int b0 = 0; b0 < batch; b0 += L.chunk) {
+    const int nb = std::min(L.chunk, batch - b0);
+    OrthArgs a{};
+    a.u = static_cast<const char*>(u) + (size_t)b0 * elems * isz;
+    a.M = M; a.N = N; a.m = L.m; a.n = L.n; a.mp = L.mp; a.np = L.np;
+    a.tall = M > N;
+    a.eps = eps;
+    a.part = reinterpret_cast<double*>(ws + L.part);
+    a.hi = reinterpret_cast<uint16_t*>(ws + L.hi);
+    a.lo = reinterpret_cast<uint16_t*>(ws + L.lo);
+    uint16_t* ht[2] = {reinterpret_cast<uint16_t*>(ws + L.ht0), reinterpret_cast<uint16_t*>(ws + L.ht1)};
+    a.ht = ht[0];
+    const dim3 norm_grid(kOrthNormParts, nb);
+    const dim3 load_grid((a.tall ? L.mp : L.np) / 64, (a.tall ? L.np : L.mp) / 64, nb);
+    if (bf) hipLaunchKernelGGL(k_orth_norm<1>, norm_grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL(k_orth_norm<0>, norm_grid, dim3(256), 0, st, a);
+    HIP_TRY(hipGetLastError());
+    if (bf) hipLaunchKernelGGL(k_orth_load<1>, load_grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL(k_orth_load<0>, load_grid, dim3(256), 0, st, a);
+    HIP_TRY(hipGetLastError());
+    uint16_t* A = reinterpret_cast<uint16_t*>(ws + L.a);
+    uint16_t* B = reinterpret_cast<uint16_t*>(ws + L.b);
+    const size_t xs = (size_t)L.mp * L.np, qs = (size_t)L.mp * L.mp;
+    for (int k = 0; k < steps; ++k) {
+      const float* co = coeffs ? coeffs + 3 * k : kOrthCoeffs;
+      OrthGemm g{};
+      g.hi = a.hi; g.lo = a.lo; g.m = L.m; g.n = L.n; g.tall = a.tall;
+      // A = X X^T: 2^24 times it in the accumulators, 2^12 in A
+      g.p = g.q = a.hi;
+      g.p_stride = g.q_stride = xs;
+      g.p_bytes = g.q_bytes = (uint32_t)(xs * 2);
+      g.ldp = g.ldq = L.np;
+      g.rows = g.cols = L.mp;
+      g.K = L.np;
+      g.s = 1.0f / kOrthScale;
+      g.c = A;
+      TRY((launch_orth_gemm<ORTH_GRAM>(g, nb, di.cus, st)));
+      // B = b A + c A A
+      g.p = g.q = A;
+      g.p_stride = g.q_stride = qs;
+      g.p_bytes = g.q_bytes = (uint32_t)(qs * 2);
+      g.ldp = g.ldq = L.mp;
+      g.K = L.mp;
+      g.a = A;
+      g.c = B;
+      g.c1 = co[1];
+      g.s = co[2] / kOrthScale;
+      TRY((launch_orth_gemm<ORTH_POLY>(g, nb, di.cus, st)));
+      // X' = a X + B X
+      g.p = B;
+      g.q = ht[k & 1];
+      g.q_stride = xs;
+      g.q_bytes = (uint32_t)(xs * 2);
+      g.cols = L.np;
+      g.c1 = co[0];
+      g.s = 1.0f / kOrthScale;
+      g.ht = ht[(k + 1) & 1];
+      g.y = static_cast<uint16_t*>(y) + (size_t)b0 * elems;
+      if (k + 1 < steps) TRY((launch_orth_gemm<ORTH_STEP>(g, nb, di.cus, st)));
+      else TRY((launch_orth_gemm<ORTH_LAST>(g, nb, di.cus, st)));
+    }
+  }
   return MOE_OK;
 }
 

@@ -1,6 +1,6 @@
 """Convenience wrapper: allocate outputs and workspace with PyTorch and call
 moe_forward / moe_route / moe_permute, and the operators of a training step
-around the layer (layer_norm, balance_loss, backward).  No
+around the layer (layer_norm, balance_loss, backward, orthogonalize).  No
 arithmetic happens here."""
 
 import contextlib
@@ -391,4 +391,28 @@ def permute(topk_ids: torch.Tensor, E: int, H: int = 128, I: int = 128, workspac
     ws = (workspace or Workspace(dev)).get(lib.moe_permute_workspace_size(desc))
     lib.moe_permute(desc, topk_ids.to(torch.int32).contiguous(), out["expert_offsets"], out["perm"],
                     out["row_of"], ws, stream)
+    return out
+
+
+def orthogonalize(u: torch.Tensor, steps: int = 5, coeffs=None, eps: float = 1e-7, workspace: Workspace = None,
+                  stream=None, out: torch.Tensor = None) -> torch.Tensor:
+    """Newton-Schulz orthogonalisation (moe_orthogonalize) of a matrix [M, N] or
+    a batch [batch, M, N], bfloat16 or float32: bfloat16 of u's shape.  coeffs:
+    `steps` triples (a, b, c), or None.  backward()'s gradients: dw_down and
+    dw_router as they are; dw_gate_up [E, 2I, H] as .view(2 * E, I, H), gate
+    and up being matrices of their own."""
+    _need(u.dim() in (2, 3) and u.is_cuda, "u must be [M, N] or [batch, M, N] on a GPU")
+    _need(u.dtype in _FLOATS, f"u must be bfloat16 or float32 (got {u.dtype})")
+    _need(coeffs is None or (len(coeffs) == steps and all(len(c) == 3 for c in coeffs)),
+          f"coeffs must be {steps} triples")
+    dev = u.device
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(u.shape, dtype=torch.bfloat16, device=dev)
+        else:
+            _is(out, "out", u.shape, (torch.bfloat16,), dev, True)
+        v = _dense(u)
+        v, y = (v, out) if u.dim() == 3 else (v[None], out[None])
+        ws = (workspace or Workspace(dev)).get(lib.moe_orthogonalize_workspace_size(*v.shape))
+        lib.moe_orthogonalize(v, steps, coeffs, eps, y, ws)
     return out

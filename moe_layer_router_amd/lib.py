@@ -120,6 +120,11 @@ _lib.moe_balance_loss_workspace_size.restype = ctypes.c_size_t
 _lib.moe_balance_loss_workspace_size.argtypes = [ctypes.c_int32] * 4
 _lib.moe_balance_loss.restype = ctypes.c_int
 _lib.moe_balance_loss.argtypes = [ctypes.c_int32] * 4 + [_P] * 4 + [ctypes.c_float] + [_P] * 5 + [ctypes.c_size_t, _P]
+_lib.moe_orthogonalize_workspace_size.restype = ctypes.c_size_t
+_lib.moe_orthogonalize_workspace_size.argtypes = [ctypes.c_int32] * 3
+_lib.moe_orthogonalize.restype = ctypes.c_int
+_lib.moe_orthogonalize.argtypes = [ctypes.c_int32] * 4 + [_P, ctypes.c_int32, _P, ctypes.c_float, _P, _P,
+                                                          ctypes.c_size_t, _P]
 _lib.moe_forward_static.restype = ctypes.c_int
 _lib.moe_forward_static.argtypes = [ctypes.POINTER(MoeDesc)] + [_P] * 13 + [_P]
 _lib.moe_route.restype = ctypes.c_int
@@ -329,6 +334,18 @@ def moe_balance_loss(logits, topk_ids, seq_offsets, token_mask, alpha, counts, p
            "moe_balance_loss")
 
 
+def moe_orthogonalize_workspace_size(batch: int, M: int, N: int) -> int:
+    return _lib.moe_orthogonalize_workspace_size(batch, M, N)
+
+
+def moe_orthogonalize(u, steps, coeffs, eps, y, workspace, stream=None):
+    """u: [batch, M, N] bfloat16 or float32; coeffs: None or `steps` triples of numbers; y [batch, M, N] bfloat16."""
+    batch, M, N = u.shape
+    co = None if coeffs is None else (ctypes.c_float * (3 * steps))(*[v for row in coeffs for v in row])
+    _check(_lib.moe_orthogonalize(batch, M, N, _float_dtype(u), _ptr(u), steps, co, eps, _ptr(y), _ptr(workspace),
+                                  _nbytes(workspace), _stream(stream)), "moe_orthogonalize")
+
+
 def moe_route(desc, x, x_scales, router_w, router_bias, logits, topk_ids, topk_weights, workspace,
               stream=None):
     st = _lib.moe_route(ctypes.byref(desc), _ptr(x), _ptr(x_scales), _ptr(router_w), _ptr(router_bias),
@@ -370,4 +387,4 @@ def exported_symbols():
             "moe_peak_mfma_flops", "moe_peak_mfma", "moe_peak_hbm_read", "moe_backward_workspace_size",
             "moe_backward", "moe_quantize_e5m6", "moe_dequantize_e5m6", "moe_backward_aux", "moe_layer_norm",
             "moe_layer_norm_backward_workspace_size", "moe_layer_norm_backward", "moe_balance_loss_workspace_size",
-            "moe_balance_loss"]
+            "moe_balance_loss", "moe_orthogonalize_workspace_size", "moe_orthogonalize"]

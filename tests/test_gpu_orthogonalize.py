@@ -1,0 +1,181 @@
+"""Newton-Schulz orthogonalisation on the GPU against the fp64 iteration.
+
+Tolerances, as the relative error of the Frobenius norm of each matrix.  The
+output's rounding to BF16 is at most half a step, 2^-8 of each element; over
+many elements (here from 4096 on) it is spread evenly over the step, and its
+root mean square is at most 2^-8 / sqrt(3).  Inside:
+- short side up to 64: fp64 iteration, Q rounded to fp32 and a product of up to
+  64 terms in fp32, |Q| |x| against |Q x|: 70 u |Q|_2 |X_0| with |Q|_2 up to
+  3.4445^5 = 485 (on the small singular values that it lifts) and |X_0| = 1:
+  70 * 2^-24 * 485 = 2e-3, while |y| is at least 0.6 (the largest singular value
+  is at least 1 / sqrt(m) = 0.125, which the polynomial takes there): 3.4e-3;
+- above: FP16 products, whose roundings, simulated in fp64 with the kernel's
+  rounding points, stay below 2.3e-3 for a side of 64 and spectra from flat to
+  1 / r^2 (and fall with the size); 3e-3."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import training as R
+
+pytestmark = pytest.mark.gpu
+
+
+def _mat(B, M, N, seed, kind="normal", dtype=torch.float32):
+    rng = np.random.default_rng(seed)
+    u = rng.normal(size=(B, M, N))
+    if kind == "decay":                       # singular values 1 / r
+        for b in range(B):
+            p, s, q = np.linalg.svd(u[b], full_matrices=False)
+            u[b] = (p / np.arange(1, len(s) + 1)) @ q
+    elif kind == "low_rank":
+        r = max(1, min(M, N) // 8)
+        u = rng.normal(size=(B, M, r)) @ rng.normal(size=(B, r, N)) + 0.01 * u
+    elif kind == "tiny":
+        u *= 1e-4
+    return torch.from_numpy(u.astype(np.float32)).to(dtype).cuda()
+
+
+def _check(y, u, steps=5, coeffs=None, eps=1e-7, what=""):
+    ref = R.orthogonalize(u.float().cpu().numpy(), steps, coeffs, eps)
+    got = y.float().cpu().numpy().astype(np.float64)
+    assert np.all(np.isfinite(got)), what
+    inner = 3.4e-3 if min(u.shape[1:]) <= 64 else 3e-3
+    half = 2.0 ** -8 * (1 if u.shape[1] * u.shape[2] < 4096 else 3 ** -0.5)
+    for b in range(len(ref)):
+        n = np.linalg.norm(ref[b])
+        err = np.linalg.norm(got[b] - ref[b])
+        assert err <= (inner + half) * n + 1e-30, f"{what} matrix {b}: {err / n:.2e}"
+
+
+# sides around the narrow limit, the padding, the tiles of both sizes; wide, tall, square, one row, one column
+SHAPES = [(1, 1, 1), (2, 1, 300), (3, 70, 1), (5, 7, 16), (2, 17, 33), (4, 40, 40), (2, 64, 200), (3, 500, 64),
+          (2, 33, 1025), (2, 65, 65), (3, 100, 130), (2, 200, 333), (1, 333, 200), (2, 128, 128), (2, 129, 257),
+          (1, 256, 1000), (8, 256, 256), (1, 700, 300)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,M,N", SHAPES)
+def test_against_definition(gpu_lib, B, M, N, dtype):
+    from moe_layer_router_amd import layer as L
+    u = _mat(B, M, N, M + N, dtype=dtype)
+    y = L.orthogonalize(u)
+    torch.cuda.synchronize()
+    assert y.shape == u.shape and y.dtype == torch.bfloat16
+    _check(y, u, what=(B, M, N))
+
+
+@pytest.mark.parametrize("kind", ["decay", "low_rank", "tiny"])
+@pytest.mark.parametrize("B,M,N", [(2, 48, 100), (2, 300, 48), (2, 96, 160), (1, 512, 300), (1, 300, 640)])
+def test_spectra(gpu_lib, B, M, N, kind):
+    from moe_layer_router_amd import layer as L
+    u = _mat(B, M, N, 5, kind)
+    y = L.orthogonalize(u)
+    torch.cuda.synchronize()
+    _check(y, u, what=kind)
+
+
+def test_large_tiles(gpu_lib):
+    """A batch large enough for the 256 x 256 tiles, with padding and partial
+    tiles on both sides, wide and tall."""
+    from moe_layer_router_amd import layer as L
+    for M, N in ((520, 1100), (1100, 520)):
+        u = _mat(40, M, N, 9)
+        y = L.orthogonalize(u)
+        torch.cuda.synchronize()
+        _check(y[[0, 17, 39]], u[[0, 17, 39]], what=(M, N))
+
+
+@pytest.mark.parametrize("M,N", [(12, 30), (90, 200)])
+def test_steps_and_coefficients(gpu_lib, M, N):
+    from moe_layer_router_amd import layer as L
+    u = _mat(2, M, N, 3)
+    y = L.orthogonalize(u, steps=1)
+    _check(y, u, steps=1)
+    co = [(3.0, -3.2, 1.2), (2.5, -2.0, 0.6), (1.5, -0.5, 0.0)]
+    y = L.orthogonalize(u, steps=3, coeffs=co, eps=1e-3)
+    torch.cuda.synchronize()
+    _check(y, u, steps=3, coeffs=co, eps=1e-3)
+
+
+@pytest.mark.parametrize("M,N", [(20, 50), (130, 90)])
+def test_zero_huge_and_non_finite_matrices(gpu_lib, M, N):
+    """An expert without tokens has a zero gradient: its update is exactly
+    zero.  A NaN or infinity stays within its matrix."""
+    from moe_layer_router_amd import layer as L
+    u = _mat(6, M, N, 1)
+    u[1] = 0
+    u[2] *= 1e25                               # its squares overflow fp32
+    u[3, 4, 5] = float("nan")
+    u[4, 0, 0] = float("inf")
+    u[5] *= 1e-20                              # its squares underflow fp32; far below eps
+    y = L.orthogonalize(u)
+    torch.cuda.synchronize()
+    assert torch.all(y[1] == 0)
+    _check(y[[0, 2]], u[[0, 2]])
+    assert torch.isnan(y[3]).any() and torch.isnan(y[4]).any()
+    ref = R.orthogonalize(u[5].cpu().numpy())
+    got = y[5].double().cpu().numpy()
+    # far below eps the update is linear in u and tiny; FP16's smallest step (2^-24 of 2^-12 in each of five
+    # steps that grow 3.44-fold) bounds what is lost
+    assert np.abs(got - ref).max() <= 2.0 ** -36 * 485 + 2.0 ** -7 * np.abs(ref).max()
+
+
+@pytest.mark.parametrize("M,N", [(24, 60), (150, 110)])
+def test_single_matrix_strided_reused_and_deterministic(gpu_lib, M, N):
+    from moe_layer_router_amd import layer as L
+    big = _mat(3, N, 2 * M, 2)
+    u = big[:, :, ::2].transpose(1, 2)         # [3, M, N], not contiguous
+    a = L.orthogonalize(u)
+    b = L.orthogonalize(u.contiguous())
+    c = L.orthogonalize(u[1])
+    flat = torch.empty(M * N + 1, device="cuda")
+    flat[1:] = u[1].reshape(-1)
+    off = flat[1:].view(M, N)
+    assert off.data_ptr() % 16 != 0
+    d = L.orthogonalize(off)
+    out = torch.full((3, M, N), 7, dtype=torch.bfloat16, device="cuda")
+    e = L.orthogonalize(u, out=out, workspace=L.Workspace("cuda"))
+    torch.cuda.synchronize()
+    assert e is out and torch.equal(a, b) and torch.equal(a[1], c) and torch.equal(c, d) and torch.equal(a, out)
+
+
+def test_streams_and_captured_graphs_with_one_workspace(gpu_lib):
+    from moe_layer_router_amd import layer as L
+    us = [_mat(2, 30, 100, 1), _mat(2, 140, 90, 2)]
+    ref = [L.orthogonalize(u) for u in us]
+    torch.cuda.synchronize()
+    ss = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [L.orthogonalize(u, stream=s) for u, s in zip(us, ss)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, r) for g, r in zip(got, ref))
+    ws = L.Workspace("cuda")
+    ws.get(1 << 24)
+    graphs, outs = [], []
+    co = [[3.4445, -4.7750, 2.0315]] * 5
+    for u in us:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(L.orthogonalize(u, coeffs=co, workspace=ws))     # (coefficients are read during the call)
+        graphs.append(g)
+    co[0][0] = 0.0
+    for i in range(6):
+        ws.buf.fill_(255)
+        outs[i % 2].fill_(-1)
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i % 2], ref[i % 2]), i
+
+
+def test_wrapper_refusals(gpu_lib):
+    from moe_layer_router_amd import layer as L, lib
+    u = torch.zeros(2, 8, 8, device="cuda")
+    for b in (dict(u=u.half()), dict(u=u.cpu()), dict(u=u[0, 0]), dict(coeffs=[(1, 2, 3)]), dict(out=u),
+              dict(out=torch.zeros(2, 8, 9, dtype=torch.bfloat16, device="cuda"))):
+        with pytest.raises(ValueError):
+            L.orthogonalize(**{**dict(u=u), **b})
+    for b in (dict(steps=0), dict(steps=33), dict(eps=0.0), dict(eps=-1.0), dict(steps=1, coeffs=[(0.0, 99.0, 0.0)]),
+              dict(u=u[:0])):
+        with pytest.raises(lib.MoeError):
+            L.orthogonalize(**{**dict(u=u), **b})

@@ -2,6 +2,8 @@
 check of the C entry points, and those of the Python wrappers, before any
 device call."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -69,6 +71,39 @@ def test_balance_loss_refusals(over, status):
     assert lib.moe_last_error() != ""
 
 
+def _orth(**over):
+    a = dict(batch=2, M=8, N=300, i=F32, u=A, steps=5, coeffs=None, eps=1e-7, y=8 * A, ws=A, nbytes=1 << 40)
+    a.update(over)
+    if a["coeffs"] is not None:
+        flat = [v for row in a["coeffs"] for v in row]
+        a["coeffs"] = (ctypes.c_float * len(flat))(*flat)
+    return lib._lib.moe_orthogonalize(*a.values(), None)
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(batch=0), INVALID), (dict(batch=65536), UNSUPPORTED), (dict(M=0), INVALID), (dict(N=-3), INVALID),
+    (dict(N=32769), UNSUPPORTED), (dict(M=16385, N=16385), UNSUPPORTED), (dict(i=FP8), UNSUPPORTED),
+    (dict(steps=0), INVALID), (dict(steps=33), UNSUPPORTED), (dict(eps=0.0), INVALID), (dict(eps=-1.0), INVALID),
+    (dict(eps=float("nan")), INVALID), (dict(u=None), INVALID), (dict(y=None), INVALID), (dict(ws=None), INVALID),
+    (dict(u=A + 4), INVALID), (dict(y=A), INVALID), (dict(y=A + 16), INVALID), (dict(nbytes=16), SMALL),
+    (dict(steps=1, coeffs=[(1, 20, 0)]), UNSUPPORTED),                  # b A past the range
+    (dict(steps=2, coeffs=[(9, 0, 0), (9, 0, 0)]), UNSUPPORTED),        # X grows past it
+    (dict(steps=1, coeffs=[(float("nan"), 0, 0)]), UNSUPPORTED),
+    (dict(steps=1, coeffs=[(1, float("inf"), 0)]), UNSUPPORTED),
+])
+def test_orthogonalize_refusals(over, status):
+    assert _orth(**over) == status
+    assert lib.moe_last_error() != ""
+
+
+def test_orthogonalize_workspace_is_bounded():
+    one = lib.moe_orthogonalize_workspace_size(1, 2048, 7168)
+    assert one >= 8 * 2048 * 7168 + 4 * 2048 * 2048
+    assert lib.moe_orthogonalize_workspace_size(512, 2048, 7168) <= (8 << 30) + (1 << 20)
+    assert lib.moe_orthogonalize_workspace_size(0, 4, 4) == 0 and lib.moe_orthogonalize_workspace_size(1, 4, 40000) == 0
+    assert lib.moe_orthogonalize_workspace_size(1, 1, 1) > 0
+
+
 def test_workspace_sizes_of_refused_shapes_are_zero():
     assert lib.moe_layer_norm_backward_workspace_size(0, 256) == 0
     assert lib.moe_layer_norm_backward_workspace_size(4, 100) == 0
@@ -94,3 +129,5 @@ def test_wrappers_refuse_host_tensors():
         L.layer_norm_backward(x, g, torch.zeros(4), torch.ones(4), x)
     with pytest.raises(ValueError):
         L.balance_loss(torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        L.orthogonalize(torch.zeros(2, 8, 8))
