@@ -485,18 +485,19 @@ moe_status moe_balance_loss(int32_t T, int32_t E, int32_t top_k, int32_t n_seq, 
  * and y = X in U's orientation: U's singular vectors, with singular values
  * near 1.  (a, b, c) of step i are coeffs[3i .. 3i+2] (host memory, read
  * during the call), or 3.4445, -4.7750, 2.0315 in each step if coeffs is NULL;
- * coefficients that let X, A or b A + c A A grow past 15 are refused
+ * coefficients that let X, A or a I + b A + c A A grow past 15 are refused
  * (MOE_ERR_UNSUPPORTED).  A zero matrix gives zero.
  * u [batch][M][N] row-major (in_dtype BF16 or F32): dw_gate_up [E][2I][H] is
  * batch = 2E gate and up matrices of I x H, dw_down [E][H][I] E matrices, and
  * dw_router one.  y [batch][M][N] BF16 (output, must not overlap u).  The
  * products are FP16 matrix-core products with fp32 accumulation on scaled
- * values, X is held in 22 bits and the norm in fp64: y is within 4e-3 of the
+ * values, X is held in 15 bits and the norm in fp64 (all of it in fp64 where the
+ * smaller of M and N is at most 64): y is within 4e-3 of the
  * exact iteration in the Frobenius norm, 1.7e-3 of it y's own rounding (default
  * coefficients, 5 steps).  1 <= M, N <= 32768, the smaller <= 16384, 1 <= batch <=
  * 65535, 1 <= steps <= 32, eps > 0; pointers (not coeffs) 16-byte aligned.
  * workspace: moe_orthogonalize_workspace_size bytes (about 10 bytes per
- * element of u, at most about 8 GiB or one matrix's; 0 for sizes that are
+ * element of u, at most 8 GiB or one matrix's; 0 for sizes that are
  * refused).  Enqueued on `stream`; errors as moe_forward. */
 size_t moe_orthogonalize_workspace_size(int32_t batch, int32_t M, int32_t N);
 moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dtype, const void* u, int32_t steps,

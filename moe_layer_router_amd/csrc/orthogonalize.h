@@ -8,22 +8,23 @@
 // the singular vectors stay.  A and B are symmetric: their products are
 // formed on and above the diagonal and mirrored.
 //
-// Precision.  X is held as two FP16 parts (hi + lo, 22 bits) of 2^12 X, A and
-// B as FP16 of 2^12 times their values (|X|, |A|, |B| stay below 3, and FP16
-// reaches 2^16; a normal FP16 number goes down to 2^-26 of the scale), the
-// products use the hi parts with fp32 accumulation, and a X is added from
-// both parts in fp32.  One FP16 product has 2^-11 relative rounding per
-// operand, eight times less than BF16: over spectra from flat to 1/r^2 the
-// result is within 1e-3 of fp64 beside the output's own BF16 rounding
-// (1.7e-3), where BF16 products are 1e-2 and, with X held in BF16 alone, up to
-// 1.6e-1 off (small singular values are lost in the rounding of the large
-// ones, which is why the lo part is kept).
+// Precision.  The products are FP16 matrix-core products with fp32
+// accumulation on 2^12 times the values of X, A and a I + B (they stay below 8,
+// and FP16 reaches 2^16; a normal FP16 number goes down to 2^-26 of the scale).
+// X is held as an FP16 part hi and the E4M3 code lo of 2^6 times what is left,
+// 15 bits: the step is X' = (a I + B) hi + a lo, the first term one product, the
+// second added in fp32.  One FP16 product has 2^-11 relative rounding per
+// operand, eight times less than BF16.  Simulated in fp64 with these roundings,
+// over spectra from flat to 1/r^2, the result is within 1.9e-3 of the exact
+// iteration for sides from 65 on, beside the output's own BF16 rounding (1.7e-3).
+// Without lo it is up to 2e-2 off (small singular values are lost in the rounding
+// of the large ones), with BF16 products 1e-2 to 1.6e-1.
 //
 // Layout.  Rows and columns are padded with zeros to multiples of 64: hi, lo
-// [mp][np], A, B [mp][mp], and the transposed hi part ht [np][mp] (two, read
-// and written in turn), so that each of the three products has both operands
-// with contiguous K: X X^T from hi and hi, A A from A and A, B X from B and
-// ht.
+// [mp][np], A, B' = a I + B [mp][mp], and the transposed hi part ht [np][mp] (two,
+// read and written in turn), so that each of the three products has both
+// operands with contiguous K: X X^T from hi and hi, A A from A and A, B' X from
+// B' and ht.
 //
 // Narrow matrices (m <= 64) go another way.  With G = X X^T and P = a + b G + c
 // G^2 a step is X' = P X, G' = P G P: the whole iteration runs on m x m
@@ -35,11 +36,11 @@
 // <= 8, below 2.3e-3 from m = 64 on).
 #pragma once
 #include "device_common.h"
+#include "norm.h"
 
 namespace moe {
 
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
-typedef _Float16 v4h __attribute__((ext_vector_type(4)));
 
 constexpr float kOrthScale = 4096.0f;
 constexpr int kOrthPad = 64;
@@ -52,9 +53,13 @@ struct OrthArgs {
   float eps;
   double* part;              // [batch][kOrthNormParts]
   uint16_t* hi;              // [batch][mp][np]
-  uint16_t* lo;
+  uint8_t* lo;
   uint16_t* ht;              // [batch][np][mp]
 };
+
+DEV uint32_t h_bits(float v) { return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v); }
+DEV float h_val(uint32_t b) { return (float)__builtin_bit_cast(_Float16, (uint16_t)b); }
+constexpr float kOrthLoScale = 64.0f;    // (|lo| <= 4 for |X| < 4, half a unit in hi's last place: within E4M3's 448)
 
 template <int BF>
 DEV float orth_ld(const void* u, size_t i) {
@@ -62,16 +67,27 @@ DEV float orth_ld(const void* u, size_t i) {
 }
 
 // Sum of squares in fp64 (fp32 squares of small gradients would underflow):
-// workgroup (p, b) sums part p of matrix b.
+// workgroup (p, b) sums part p of matrix b, 8 elements per thread and load
+// where rows of 8 line up.
 template <int BF>
 __global__ void __launch_bounds__(256) k_orth_norm(OrthArgs a) {
   __shared__ double red[256];
-  const size_t total = (size_t)a.M * a.N, per = (total + kOrthNormParts - 1) / kOrthNormParts;
-  const size_t i0 = blockIdx.x * per, i1 = i0 + per < total ? i0 + per : total;
+  const size_t total = (size_t)a.M * a.N, per = ((total + kOrthNormParts - 1) / kOrthNormParts + 7) / 8 * 8;
+  const size_t i0 = min(blockIdx.x * per, total), i1 = min(i0 + per, total);
   const size_t base = (size_t)blockIdx.y * total;
   double s = 0;
+  size_t tail = i0;
+  if (total % 8 == 0) {                    // (each matrix, and so each part, starts on 16 bytes)
+    tail = i1;
 #pragma unroll 4
-  for (size_t i = i0 + threadIdx.x; i < i1; i += 256) {
+    for (size_t i = i0 + 8 * threadIdx.x; i < i1; i += 8 * 256) {
+      float v[8];
+      ln_unpack<BF ? LN_BF16 : LN_F32>(ln_load<BF ? LN_BF16 : LN_F32>(a.u, base + i), v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s = __builtin_fma((double)v[e], (double)v[e], s);
+    }
+  }
+  for (size_t i = tail + threadIdx.x; i < i1; i += 256) {
     const double v = orth_ld<BF>(a.u, base + i);
     s += v * v;
   }
@@ -88,54 +104,63 @@ __global__ void __launch_bounds__(256) k_orth_norm(OrthArgs a) {
 // 64 x 64 tile (y, x) of U's padded matrix b.
 template <int BF>
 __global__ void __launch_bounds__(256) k_orth_load(OrthArgs a) {
+  static_assert(kOrthNormParts == 64, "one part per lane");
   __shared__ float tile[64][65];
-  __shared__ float s_scale;
-  if (threadIdx.x == 0) {
-    double s = 0;
-    for (int i = 0; i < kOrthNormParts; ++i) s += a.part[(size_t)blockIdx.z * kOrthNormParts + i];
-    // (a zero matrix stays zero: the scale is finite)
-    const double sc = (double)kOrthScale / (sqrt(s) + (double)a.eps);
-    s_scale = sc < 3e38 ? (float)sc : sc == sc ? 3e38f : (float)sc;
-  }
-  __syncthreads();
-  const float sc = s_scale;
-  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64, tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+  double ss = a.part[(size_t)blockIdx.z * kOrthNormParts + tx];
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) ss += __shfl_xor(ss, d);
+  // (a zero matrix stays zero: the scale is finite)
+  const double scd = (double)kOrthScale / (sqrt(ss) + (double)a.eps);
+  const float sc = scd > 3e38 ? 3e38f : (float)scd;
+  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
   const size_t ub = (size_t)blockIdx.z * a.M * a.N;
   const int ldd = a.tall ? a.mp : a.np;      // U's padded row length
   const size_t xb = (size_t)blockIdx.z * a.mp * a.np;
   uint16_t* direct = a.tall ? a.ht : a.hi;   // in U's own orientation
-#pragma unroll 4
-  for (int i = ty; i < 64; i += 4) {
-    const int r = r0 + i, c = c0 + tx;
-    const float v = r < a.M && c < a.N ? orth_ld<BF>(a.u, ub + (size_t)r * a.N + c) * sc : 0.f;
-    tile[i][tx] = v;
-    const _Float16 h = (_Float16)v;
-    const size_t o = xb + (size_t)r * ldd + c;
-    direct[o] = __builtin_bit_cast(uint16_t, h);
-    if (!a.tall) a.lo[o] = __builtin_bit_cast(uint16_t, (_Float16)(v - (float)h));
+  auto lo_of = [](float v, float h) { return (uint8_t)f32_to_e4m3((v - h) * kOrthLoScale); };
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    float v[8];                              // eight rows' loads together
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = r0 + ty + 4 * (8 * q + i), c = c0 + tx;
+      v[i] = r < a.M && c < a.N ? orth_ld<BF>(a.u, ub + (size_t)r * a.N + c) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = ty + 4 * (8 * q + i), r = r0 + k, c = c0 + tx;
+      const float x = v[i] * sc;
+      tile[k][tx] = x;
+      const uint32_t h = h_bits(x);
+      const size_t o = xb + (size_t)r * ldd + c;
+      direct[o] = (uint16_t)h;
+      if (!a.tall) a.lo[o] = lo_of(x, h_val(h));
+    }
   }
   __syncthreads();
   const int ldt = a.tall ? a.np : a.mp;
 #pragma unroll 4
   for (int i = ty; i < 64; i += 4) {
     const int r = r0 + tx, c = c0 + i;       // element (r, c) of U at row c of the transpose
-    const float v = tile[tx][i];
-    const _Float16 h = (_Float16)v;
+    const float x = tile[tx][i];
+    const uint32_t h = h_bits(x);
     const size_t o = xb + (size_t)c * ldt + r;
-    (a.tall ? a.hi : a.ht)[o] = __builtin_bit_cast(uint16_t, h);
-    if (a.tall) a.lo[o] = __builtin_bit_cast(uint16_t, (_Float16)(v - (float)h));
+    (a.tall ? a.hi : a.ht)[o] = (uint16_t)h;
+    if (a.tall) a.lo[o] = lo_of(x, h_val(h));
   }
 }
 
 // ------------------------------------------------------------------ products
 enum { ORTH_GRAM = 0, ORTH_POLY = 1, ORTH_STEP = 2, ORTH_LAST = 3 };
+constexpr bool orth_sym(int mode) { return mode == ORTH_GRAM || mode == ORTH_POLY; }
 
 // C[i][j] = sum_k P[i][k] Q[j][k] for each matrix of a batch, P [rows][ld], Q
 // [cols][ld] FP16, K a multiple of 64, and what follows it:
-//   GRAM   A = s C                             (symmetric)
-//   POLY   B = c1 A + s C                      (symmetric)
-//   STEP   X' = c1 X + s C as hi, lo, ht_out
-//   LAST   the result: (c1 X + s C) / 2^12 as BF16 in U's orientation
+//   GRAM   A = s C                                  (symmetric)
+//   POLY   B' = c0 2^12 I + c1 A + s C              (symmetric)
+//   STEP   X' = s C + c0 lo as hi, lo, ht
+//   LAST   the result: (s C + c0 lo) / 2^12 as BF16 in U's orientation
 struct OrthGemm {
   const uint16_t* p;
   const uint16_t* q;
@@ -143,13 +168,15 @@ struct OrthGemm {
   uint32_t p_bytes, q_bytes;           // of one matrix
   int ldp, ldq;
   int rows, cols, K;                   // padded sizes
-  int ti, tj, tiles;                   // tiles of rows and columns, tiles per matrix
-  int total;                           // tiles of all matrices
-  float c1, s;
-  uint16_t* c;                         // GRAM: A; POLY: B
+  int ti, tiles;                       // tiles of rows, tiles per matrix
+  int full;                            // tiles (of the batch) worked on whole
+  int split, rest;                     // the other `rest` tiles: parts along K of each
+  float* part;                         // [rest][split][tile] sums of the parts
+  float c0, c1, s;
+  uint16_t* c;                         // GRAM: A; POLY: B'
   const uint16_t* a;                   // POLY: A
   uint16_t* hi;
-  uint16_t* lo;
+  uint8_t* lo;
   uint16_t* ht;
   uint16_t* y;                         // LAST: [batch][M][N]
   int m, n, tall;
@@ -158,11 +185,19 @@ struct OrthGemm {
 DEV v4f mfma_f16(const v8h& a, const v8h& b, const v4f& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
-DEV uint32_t h_bits(float v) { return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v); }
-DEV float h_val(uint32_t b) { return (float)__builtin_bit_cast(_Float16, (uint16_t)b); }
 
-// Tile t of the n x n tiles on and above the diagonal: (i, j), i <= j, ordered
-// by j.
+// WM x WN waves, each 4 x NJ subtiles of 16 x 16: a tile of 64 WM rows and as
+// many columns, in steps of 64 K, ST steps in LDS.
+template <int WM_, int WN_, int NJ_, int ST_>
+struct OrthTile {
+  static constexpr int WM = WM_, WN = WN_, NJ = NJ_, ST = ST_, NW = WM * WN, kThreads = 64 * NW, kSide = 64 * WM;
+  static constexpr int kStage = 2 * kSide * 128;                        // bytes of a step's operands
+  static constexpr int kLds = ST * kStage;
+  static constexpr size_t kPart = (size_t)kSide * kSide;                // fp32 sums of one part
+  static_assert(16 * NJ * WN == kSide && NJ % 2 == 0, "square tiles");
+};
+
+// Tile t of the tiles on and above the diagonal: (i, j), i <= j, by j.
 DEV void orth_tri(int t, int* i, int* j) {
   int c = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
   while (c * (c + 1) / 2 > t) --c;
@@ -171,152 +206,269 @@ DEV void orth_tri(int t, int* i, int* j) {
   *i = t - c * (c + 1) / 2;
 }
 
-// WM x WN waves, each MI x NJ subtiles of 16 x 16: a tile of 16 MI WM rows and
-// 16 NJ WN columns, in steps of 64 K.
-template <int WM, int WN, int MI, int NJ>
-struct OrthTile {
-  static constexpr int kRows = 16 * MI * WM, kCols = 16 * NJ * WN, kThreads = 64 * WM * WN;
-  static constexpr int kStage = (kRows + kCols) * 128;        // bytes of a 64-K step
-  static constexpr int kLds = 2 * kStage;
-};
-
-// Both operands' tiles of a step go straight to LDS (16-byte buffer loads,
-// rows past the end read as zero), two stages: the next step's loads are in
-// flight during a step's products, one barrier per step.  LDS rows are 128
-// bytes, chunk c (16 bytes, K 8c .. 8c+7) of row r at chunk c ^ ((r ^ r/8) % 8),
-// so that the 16 rows of an operand read fall in distinct banks.
-template <int WM, int WN, int MI, int NJ, int MODE>
-__global__ void __launch_bounds__(64 * WM * WN) k_orth_gemm(OrthGemm g) {
-  using TL = OrthTile<WM, WN, MI, NJ>;
-  constexpr int NW = WM * WN, PP = TL::kRows / 8 / NW, QP = TL::kCols / 8 / NW;   // 1 KB pieces per wave
-  static_assert(TL::kRows % (8 * NW) == 0 && TL::kCols % (8 * NW) == 0, "whole pieces per wave");
-  extern __shared__ __attribute__((aligned(16))) char lds[];
-  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int c16 = lane & 15, gq = lane >> 4, wm = w / WN, wn = w % WN;
-
-  // XCD x (workgroup ids go round-robin) takes a contiguous range of tiles
-  const int per = (g.total + 7) / 8;
-  const int t = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
-  if (t >= g.total || (int)(blockIdx.x / 8) >= per) return;
-  const int mat = t / g.tiles;
-  int i0, j0;
-  if (MODE == ORTH_GRAM || MODE == ORTH_POLY) {
-    orth_tri(t % g.tiles, &i0, &j0);
+// Tile t of the batch: its matrix and its first row and column; whether its
+// mirror image is stored too.
+template <class TL, int MODE>
+DEV bool orth_tile(const OrthGemm& g, int t, int* mat, int* i0, int* j0) {
+  *mat = t / g.tiles;
+  const int l = t % g.tiles;
+  int i, j;
+  if (orth_sym(MODE)) {
+    orth_tri(l, &i, &j);
   } else {
-    i0 = t % g.tiles % g.ti;
-    j0 = t % g.tiles / g.ti;
+    i = l % g.ti;
+    j = l / g.ti;
   }
-  const bool mirror = (MODE == ORTH_GRAM || MODE == ORTH_POLY) && i0 != j0;
-  i0 *= TL::kRows;
-  j0 *= TL::kCols;
-  const rsrc_t pr = make_rsrc(g.p + mat * g.p_stride, g.p_bytes), qr = make_rsrc(g.q + mat * g.q_stride, g.q_bytes);
+  *i0 = i * TL::kSide;
+  *j0 = j * TL::kSide;
+  return orth_sym(MODE) && i < j;
+}
 
-  uint32_t poff[PP], qoff[QP];
+// A wave's sums acc[i][j][v] are row 64 wm + 4 c16 + i and column 16 NJ wn + 32
+// (j / 2) + 8 gq + 4 (j % 2) + v of its tile (the operands are brought to LDS in
+// that order).  A lane then holds 8 consecutive columns of a row and 4
+// consecutive rows of a column, and both orientations are stored straight
+// from registers: rows in 16-byte pieces, 64 bytes at a time, the transpose
+// in 8-byte pieces, 128 bytes at a time.  This stores the columns of j = 2 p
+// and 2 p + 1.
+template <class TL, int MODE>
+DEV void orth_store(const OrthGemm& g, int mat, int i0, int j0, bool mirror, int w, int lane, int p,
+                    const v4f (&acc)[4][2]) {
+  const int c16 = lane & 15, gq = lane >> 4;
+  const int rb = i0 + 64 * (w / TL::WN) + 4 * c16, c = j0 + 16 * TL::NJ * (w % TL::WN) + 32 * p + 8 * gq;
+  const size_t sq = (size_t)mat * g.rows * g.cols, yb = (size_t)mat * g.m * g.n;
+  if (rb >= g.rows || c >= g.cols) return;         // (rows and cols are multiples of 64)
+  uint32_t h[4][8];                                // this lane's 4 rows x 8 columns
+  v2u lq[4];
+  if (!orth_sym(MODE)) {
 #pragma unroll
-  for (int q = 0; q < PP; ++q) {
-    const int r = 8 * (q * NW + w) + (lane >> 3), c = (lane & 7) ^ ((r ^ (r >> 3)) & 7);
-    poff[q] = (uint32_t)(i0 + r) * (uint32_t)g.ldp * 2 + 16 * c;
+    for (int i = 0; i < 4; ++i) lq[i] = *reinterpret_cast<const v2u*>(g.lo + sq + (size_t)(rb + i) * g.cols + c);
   }
 #pragma unroll
-  for (int q = 0; q < QP; ++q) {
-    const int r = 8 * (q * NW + w) + (lane >> 3), c = (lane & 7) ^ ((r ^ (r >> 3)) & 7);
-    qoff[q] = (uint32_t)(j0 + r) * (uint32_t)g.ldq * 2 + 16 * c;
-  }
-  const int steps = g.K / 64;
-  auto load = [&](int s) {
-    char* st = lds + (s & 1) * TL::kStage;
+  for (int i = 0; i < 4; ++i) {
+    const size_t o = sq + (size_t)(rb + i) * g.cols + c;
+    float v[8];
 #pragma unroll
-    for (int q = 0; q < PP; ++q) buf_ld16_lds(pr, st + (q * NW + w) * 1024, poff[q], (uint32_t)s * 128);
+    for (int e = 0; e < 8; ++e) v[e] = g.s * acc[i][e >> 2][e & 3];
+    if (MODE == ORTH_POLY) {
+      const v4i q = ld16(g.a + o);
 #pragma unroll
-    for (int q = 0; q < QP; ++q)
-      buf_ld16_lds(qr, st + TL::kRows * 128 + (q * NW + w) * 1024, qoff[q], (uint32_t)s * 128);
-  };
-  // operand reads: row r's chunk 4 kh + gq
-  auto off = [&](int r, int kh) { return r * 128 + (((4 * kh + gq) ^ ((r ^ (r >> 3)) & 7)) << 4); };
-
-  v4f acc[MI][NJ];
+      for (int e = 0; e < 8; ++e) {
+        v[e] = __builtin_fmaf(g.c1, h_val((uint32_t)q[e >> 1] >> (16 * (e & 1))), v[e]);
+        if (c + e == rb + i) v[e] += g.c0 * kOrthScale;
+      }
+    }
+    if (!orth_sym(MODE)) {
+      const float c0 = g.c0 * (1.0f / kOrthLoScale);
+      typedef float v2f __attribute__((ext_vector_type(2)));
 #pragma unroll
-  for (int i = 0; i < MI; ++i)
+      for (int d = 0; d < 2; ++d) {
+        const v2f l0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)lq[i][d], false);
+        const v2f l1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)lq[i][d], true);
+        v[4 * d] = __builtin_fmaf(c0, l0[0], v[4 * d]);
+        v[4 * d + 1] = __builtin_fmaf(c0, l0[1], v[4 * d + 1]);
+        v[4 * d + 2] = __builtin_fmaf(c0, l1[0], v[4 * d + 2]);
+        v[4 * d + 3] = __builtin_fmaf(c0, l1[1], v[4 * d + 3]);
+      }
+    }
+    if (MODE == ORTH_LAST) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  load(0);
-  for (int s = 0; s < steps; ++s) {
-    barrier_vmcnt<0>();                            // step s has landed, and every wave is past step s - 1
-    if (s + 1 < steps) load(s + 1);
-    const char* pt = lds + (s & 1) * TL::kStage;
-    const char* qt = pt + TL::kRows * 128;
+      for (int e = 0; e < 8; ++e) h[i][e] = f32_to_bf16_rne(v[e] * (1.0f / kOrthScale));
+    } else {
 #pragma unroll
-    for (int kh = 0; kh < 2; ++kh) {
-      v8h qf[NJ];
+      for (int e = 0; e < 8; ++e) h[i][e] = h_bits(v[e]);
+    }
+    const v4i hw = v4i{(int)(h[i][0] | (h[i][1] << 16)), (int)(h[i][2] | (h[i][3] << 16)),
+                       (int)(h[i][4] | (h[i][5] << 16)), (int)(h[i][6] | (h[i][7] << 16))};
+    if (orth_sym(MODE)) st16(g.c + o, hw);
+    if (MODE == ORTH_STEP) {
+      float l[8];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        qf[j] = __builtin_bit_cast(v8h, ld16(qt + off(16 * NJ * wn + 16 * j + c16, kh)));
+      for (int e = 0; e < 8; ++e) l[e] = (v[e] - h_val(h[i][e])) * kOrthLoScale;
+      st16(g.hi + o, hw);
+      *reinterpret_cast<v2u*>(g.lo + o) =
+          v2u{f32x4_to_e4m3x4(l[0], l[1], l[2], l[3]), f32x4_to_e4m3x4(l[4], l[5], l[6], l[7])};
+    }
+    if (MODE == ORTH_LAST && !g.tall && rb + i < g.m) {
+      uint16_t* y = g.y + yb + (size_t)(rb + i) * g.n + c;
+      if (c + 8 <= g.n && g.n % 8 == 0) {          // (rows of y start on 16 bytes)
+        st16(y, hw);
+      } else {
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const v8h pf = __builtin_bit_cast(v8h, ld16(pt + off(16 * MI * wm + 16 * i + c16, kh)));
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_f16(qf[j], pf, acc[i][j]);
+        for (int e = 0; e < 8; ++e)
+          if (c + e < g.n) y[e] = (uint16_t)h[i][e];
       }
     }
   }
-
-  // lane: row i0 + 16 MI wm + 16 i + c16, columns j0 + 16 NJ wn + 16 j + 4 gq + v
+  if (MODE == ORTH_STEP || mirror || (MODE == ORTH_LAST && g.tall)) {
 #pragma unroll
-  for (int i = 0; i < MI; ++i)
+    for (int e = 0; e < 8; ++e) {
+      const v2u t = v2u{h[0][e] | (h[1][e] << 16), h[2][e] | (h[3][e] << 16)};
+      if (MODE == ORTH_LAST) {
+        if (c + e >= g.n) continue;
+        uint16_t* y = g.y + yb + (size_t)(c + e) * g.m + rb;
+        if (rb + 4 <= g.m && g.m % 4 == 0) {
+          *reinterpret_cast<v2u*>(y) = t;
+        } else {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int r = i0 + 16 * MI * wm + 16 * i + c16, c = j0 + 16 * NJ * wn + 16 * j + 4 * gq;
-      if (r >= g.rows || c >= g.cols) continue;    // (c is a multiple of 4, cols of 64)
-      if (MODE == ORTH_GRAM || MODE == ORTH_POLY) {
-        const size_t o = mat * (size_t)g.rows * g.rows + (size_t)r * g.rows + c;
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = g.s * acc[i][j][e];
-        if (MODE == ORTH_POLY) {
-          const v2u q = *reinterpret_cast<const v2u*>(g.a + o);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(g.c1, h_val(q[e >> 1] >> (16 * (e & 1))), v[e]);
-        }
-        uint32_t h[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = h_bits(v[e]);
-        *reinterpret_cast<v2u*>(g.c + o) = v2u{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
-        if (mirror) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            g.c[mat * (size_t)g.rows * g.rows + (size_t)(c + e) * g.rows + r] = (uint16_t)h[e];
+          for (int i = 0; i < 4; ++i)
+            if (rb + i < g.m) y[i] = (uint16_t)h[i][e];
         }
       } else {
-        const size_t o = mat * (size_t)g.rows * g.cols + (size_t)r * g.cols + c;
-        const v2u xh = *reinterpret_cast<const v2u*>(g.hi + o), xl = *reinterpret_cast<const v2u*>(g.lo + o);
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int sh = 16 * (e & 1);
-          v[e] = __builtin_fmaf(g.c1, h_val(xh[e >> 1] >> sh) + h_val(xl[e >> 1] >> sh), g.s * acc[i][j][e]);
-        }
-        if (MODE == ORTH_STEP) {
-          uint32_t h[4], l[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            h[e] = h_bits(v[e]);
-            l[e] = h_bits(v[e] - h_val(h[e]));
-          }
-          *reinterpret_cast<v2u*>(g.hi + o) = v2u{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
-          *reinterpret_cast<v2u*>(g.lo + o) = v2u{l[0] | (l[1] << 16), l[2] | (l[3] << 16)};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            g.ht[mat * (size_t)g.rows * g.cols + (size_t)(c + e) * g.rows + r] = (uint16_t)h[e];
-        } else if (r < g.m) {
-          const size_t yb = mat * (size_t)g.m * g.n;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (c + e < g.n)
-              g.y[yb + (g.tall ? (size_t)(c + e) * g.m + r : (size_t)r * g.n + c + e)] =
-                  (uint16_t)f32_to_bf16_rne(v[e] * (1.0f / kOrthScale));
-        }
+        *reinterpret_cast<v2u*>((orth_sym(MODE) ? g.c : g.ht) + sq + (size_t)(c + e) * g.rows + rb) = t;
       }
     }
+  }
+}
+
+// The operands' tiles of a step go straight to LDS (16-byte buffer loads, rows
+// past the end read as zero), ST stages, one barrier per step.  An LDS row is
+// 128 bytes (64 K), its 16-byte chunk c at c ^ ((row ^ row / 8) % 8), so that the
+// 16 rows of an operand read fall in distinct banks.
+DEV int orth_swz(int r) { return (r ^ (r >> 3)) & 7; }
+
+template <class TL, int MODE>
+__global__ void __launch_bounds__(TL::kThreads, 2) k_orth_gemm(OrthGemm g) {
+  constexpr int NJ = TL::NJ, NW = TL::NW, PP = TL::kSide / 8 / NW;      // 1 KB pieces per wave and operand
+  static_assert(TL::kSide % (8 * NW) == 0, "whole pieces per wave");
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c16 = lane & 15, gq = lane >> 4, wm = w / TL::WN, wn = w % TL::WN;
+
+  // XCD x (workgroup ids go round-robin) takes a contiguous range of the whole
+  // tiles; the parts of the others follow
+  const int per = (g.full + 7) / 8;
+  int t, part = -1;
+  if ((int)blockIdx.x < 8 * per) {
+    t = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
+    if (t >= g.full) return;
+  } else {
+    part = (int)blockIdx.x - 8 * per;
+    t = g.full + part / g.split;
+  }
+  int mat, i0, j0;
+  const bool mirror = orth_tile<TL, MODE>(g, t, &mat, &i0, &j0);
+  int s0 = 0, s1 = g.K / 64;
+  if (part >= 0) {
+    const int ks = part % g.split, n = s1;
+    s0 = (int)((long)ks * n / g.split);
+    s1 = (int)((long)(ks + 1) * n / g.split);
+  }
+  const rsrc_t pr = make_rsrc(g.p + mat * g.p_stride, g.p_bytes), qr = make_rsrc(g.q + mat * g.q_stride, g.q_bytes);
+
+  // LDS row r of the P tile is row 64 (r / 64) + 4 (r % 16) + r / 16 % 4, of the
+  // Q tile column NC (r / NC) + 32 (j / 2) + 8 (x / 4) + 4 (j % 2) + x % 4 with NC
+  // = 16 NJ, j = r % NC / 16, x = r % 16 (see orth_store)
+  uint32_t poff[PP], qoff[PP];
+#pragma unroll
+  for (int q = 0; q < PP; ++q) {
+    const int r = 8 * (q * NW + w) + (lane >> 3), c = (lane & 7) ^ orth_swz(r);
+    poff[q] = (uint32_t)(i0 + (r & ~63) + 4 * (r & 15) + ((r >> 4) & 3)) * (uint32_t)g.ldp * 2 + 16 * c;
+    const int x = r & 15, j = r % (16 * NJ) / 16;
+    const int col = r / (16 * NJ) * (16 * NJ) + 32 * (j >> 1) + 8 * (x >> 2) + 4 * (j & 1) + (x & 3);
+    qoff[q] = (uint32_t)(j0 + col) * (uint32_t)g.ldq * 2 + 16 * c;
+  }
+  auto load = [&](int s, int stage) {
+    char* st = lds + stage * TL::kStage;
+    const uint32_t k = (uint32_t)min(s, s1 - 1) * 128;         // (past the end: the last step again, never read)
+#pragma unroll
+    for (int q = 0; q < PP; ++q) {
+      buf_ld16_lds(pr, st + (q * NW + w) * 1024, poff[q], k);
+      buf_ld16_lds(qr, st + TL::kSide * 128 + (q * NW + w) * 1024, qoff[q], k);
+    }
+  };
+
+  v4f acc[4][NJ];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  // operand reads: chunk 4 kh + gq of row r0 + 16 i + c16 (r0: the wave's first)
+  const int pr0 = 64 * wm, qr0 = 16 * NJ * wn;
+  auto frag = [&](const char* op, int r0, int i, int kh) {
+    return lds_ld<v8h>(op, (uint32_t)(r0 + 16 * i + c16) * 128 + (((4 * kh + gq) ^ orth_swz(r0 + 16 * i + c16)) << 4));
+  };
+#pragma unroll
+  for (int s = 0; s < TL::ST - 1; ++s) load(s0 + s, s);
+  int stage = 0;
+  for (int s = s0; s < s1; ++s) {
+    // this wave's loads of step s have landed (later steps' may be in flight),
+    // and every wave is past step s - 1, whose stage is loaded next
+    barrier_vmcnt<(TL::ST - 2) * 2 * PP>();
+    load(s + TL::ST - 1, stage == 0 ? TL::ST - 1 : stage - 1);
+    const char* st = lds + stage * TL::kStage;
+    stage = stage == TL::ST - 1 ? 0 : stage + 1;
+#pragma unroll
+    for (int kh = 0; kh < 2; ++kh) {
+      v8h pf[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pf[i] = frag(st, pr0, i, kh);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const v8h qf = frag(st + TL::kSide * 128, qr0, j, kh);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i][j] = mfma_f16(qf, pf[i], acc[i][j]);
+      }
+    }
+  }
+  wait_vmcnt<0>();                                 // no load into LDS outlives the workgroup
+  if (part >= 0) {
+    v4f* dst = reinterpret_cast<v4f*>(g.part + (size_t)part * TL::kPart) + (size_t)w * 4 * NJ * 64 + lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) dst[(i * NJ + j) * 64] = acc[i][j];
+    return;
+  }
+#pragma unroll
+  for (int p = 0; p < NJ / 2; ++p) {
+    const v4f a[4][2] = {{acc[0][2 * p], acc[0][2 * p + 1]},
+                         {acc[1][2 * p], acc[1][2 * p + 1]},
+                         {acc[2][2 * p], acc[2][2 * p + 1]},
+                         {acc[3][2 * p], acc[3][2 * p + 1]}};
+    orth_store<TL, MODE>(g, mat, i0, j0, mirror, w, lane, p, a);
+  }
+}
+
+// The tiles worked on in parts: a workgroup adds up the parts of 32 columns of
+// what one wave of the tile holds (each of its four waves every fourth part,
+// then the four sums in order) and finishes them.
+template <class TL, int MODE>
+__global__ void __launch_bounds__(256) k_orth_join(OrthGemm g) {
+  constexpr int NJ = TL::NJ, NP = NJ / 2;
+  __shared__ v4f sum[4][8][64];
+  const int p = blockIdx.x % NP, w = blockIdx.x / NP % TL::NW, r = blockIdx.x / NP / TL::NW;
+  const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
+  int mat, i0, j0;
+  const bool mirror = orth_tile<TL, MODE>(g, g.full + r, &mat, &i0, &j0);
+  v4f acc[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+  for (int k = q; k < g.split; k += 4) {
+    const v4f* src =
+        reinterpret_cast<const v4f*>(g.part + ((size_t)r * g.split + k) * TL::kPart) + (size_t)w * 4 * NJ * 64 + lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      acc[i][0] += src[(i * NJ + 2 * p) * 64];
+      acc[i][1] += src[(i * NJ + 2 * p + 1) * 64];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    sum[q][2 * i][lane] = acc[i][0];
+    sum[q][2 * i + 1][lane] = acc[i][1];
+  }
+  __syncthreads();
+  if (q) return;
+#pragma unroll
+  for (int k = 1; k < 4; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      acc[i][0] += sum[k][2 * i][lane];
+      acc[i][1] += sum[k][2 * i + 1][lane];
+    }
+  orth_store<TL, MODE>(g, mat, i0, j0, mirror, w, lane, p, acc);
 }
 
 // ------------------------------------------------------------------- narrow

@@ -133,10 +133,25 @@ moe_status launch_bal_tokens(const BalArgs& a, int grid, hipStream_t st) {
 constexpr float kOrthCoeffs[3] = {3.4445f, -4.7750f, 2.0315f};
 constexpr int kOrthMaxSteps = 32;
 constexpr size_t kOrthChunkBytes = (size_t)8 << 30;
+// Tile shapes: 256 x 256 (eight waves of 64 x 128, one workgroup per CU), and
+// smaller ones where there are too few of those to fill the GPU.
+using OrthBig = OrthTile<4, 2, 8, 2>;
+using OrthMid = OrthTile<2, 2, 4, 2>;
+using OrthSmall = OrthTile<1, 2, 2, 3>;
+constexpr int kOrthParts = 512;      // parts of tiles in one launch (at most 128 MiB of sums)
+
+// Bytes for the sums of tiles worked on in parts, whichever tile shape is
+// taken (that depends on the device): GRAM has the larger K.
+template <class TL>
+size_t orth_part_bytes(int batch, int mp, int np) {
+  const size_t tj = (mp + TL::kSide - 1) / TL::kSide, tiles = tj * (tj + 1) / 2 * batch;
+  const size_t split = np / 256;
+  return split < 2 ? 0 : std::min((size_t)kOrthParts, tiles * split) * TL::kPart * 4;
+}
 
 struct OrthLayout {
   int m, n, mp, np, chunk;           // short and long side, padded; matrices worked on together
-  size_t part, hi, lo, ht0, ht1, a, b, total;
+  size_t part, hi, lo, ht0, ht1, a, b, sums, total;
   int sq, slabs;                     // narrow matrices: padded side, partial Gram matrices
   size_t q;
 };
@@ -159,16 +174,19 @@ OrthLayout orth_layout(int batch, int M, int N) {
   const size_t x = (size_t)L.mp * L.np * 2, q = (size_t)L.mp * L.mp * 2;
   // a large batch goes through in parts of at most 8 GiB, each of which
   // fills the GPU
-  L.chunk = (int)std::min((size_t)batch, std::max((size_t)1, kOrthChunkBytes / (4 * x + 2 * q)));
+  const size_t sums = std::max({orth_part_bytes<OrthBig>(batch, L.mp, L.np), orth_part_bytes<OrthMid>(batch, L.mp, L.np),
+                                orth_part_bytes<OrthSmall>(batch, L.mp, L.np)});
+  L.chunk = (int)std::min((size_t)batch, std::max((size_t)1, (kOrthChunkBytes - sums) / (3 * x + x / 2 + 2 * q)));
   const size_t c = L.chunk;
   size_t o = 0;
   L.part = o; o = align256(o + c * kOrthNormParts * 8);
   L.hi = o; o = align256(o + c * x);
-  L.lo = o; o = align256(o + c * x);
+  L.lo = o; o = align256(o + c * x / 2);
   L.ht0 = o; o = align256(o + c * x);
   L.ht1 = o; o = align256(o + c * x);
   L.a = o; o = align256(o + c * q);
   L.b = o; o = align256(o + c * q);
+  L.sums = o; o = align256(o + sums);
   L.total = o;
   return L;
 }
@@ -183,7 +201,7 @@ moe_status check_orth(int32_t batch, int32_t M, int32_t N) {
   return MOE_OK;
 }
 
-// Whether X, A and B stay within FP16's range times 2^-12 over the steps: the
+// Whether X, A and a I + B stay within FP16's range times 2^-12 over the steps: the
 // singular values start in [0, 1], and a step takes [0, s] to its image under
 // the polynomial.
 bool orth_in_range(int steps, const float* co) {
@@ -193,7 +211,7 @@ bool orth_in_range(int steps, const float* co) {
     double next = 0;
     for (int i = 0; i <= 1024; ++i) {
       const double s = top * i / 1024, s2 = s * s, bv = b * s2 + c * s2 * s2, to = std::fabs(s * (a + bv));
-      if (!(std::fabs(bv) < 15) || !(s2 < 15) || !(to < 14)) return false;      // (NaN: false too)
+      if (!(std::fabs(a) + std::fabs(bv) < 15) || !(s2 < 15) || !(to < 14)) return false;      // (NaN: false too)
       next = std::max(next, to);
     }
     top = 1.01 * next;                    // (rounding, and the grid's gaps)
@@ -201,24 +219,43 @@ bool orth_in_range(int steps, const float* co) {
   return true;
 }
 
-template <int WM, int WN, int MI, int NJ, int MODE>
-moe_status launch_orth_gemm(OrthGemm g, int batch, hipStream_t st) {
-  using TL = OrthTile<WM, WN, MI, NJ>;
-  g.ti = (g.rows + TL::kRows - 1) / TL::kRows;
-  g.tj = (g.cols + TL::kCols - 1) / TL::kCols;
-  g.tiles = MODE == ORTH_GRAM || MODE == ORTH_POLY ? g.ti * (g.ti + 1) / 2 : g.ti * g.tj;
-  g.total = g.tiles * batch;
-  TRY(set_lds_limit(k_orth_gemm<WM, WN, MI, NJ, MODE>, TL::kLds));
-  hipLaunchKernelGGL((k_orth_gemm<WM, WN, MI, NJ, MODE>), dim3((unsigned)((g.total + 7) / 8 * 8)), dim3(TL::kThreads),
-                     TL::kLds, st, g);
+// Tiles of a product, and how many of them are worked on in parts.
+template <class TL, int MODE>
+moe_status launch_orth_gemm(OrthGemm g, int batch, int cus, hipStream_t st) {
+  g.ti = (g.rows + TL::kSide - 1) / TL::kSide;
+  const int tj = (g.cols + TL::kSide - 1) / TL::kSide;
+  g.tiles = orth_sym(MODE) ? tj * (tj + 1) / 2 : g.ti * tj;
+  const int total = g.tiles * batch, slots = cus * (160 * 1024 / TL::kLds);
+  g.full = total;
+  g.split = 1;
+  if (orth_sym(MODE)) {
+    // what does not fill a whole round of the GPU is split along K, as far as
+    // the slots and 256-K parts go
+    const int rest = total % slots;
+    const int split = rest ? std::min({slots / rest, g.K / 256, kOrthParts / rest}) : 1;
+    if (split >= 2) {
+      g.full = total - rest;
+      g.split = split;
+      g.rest = rest;
+    }
+  }
+  TRY(set_lds_limit(k_orth_gemm<TL, MODE>, TL::kLds));
+  const unsigned grid = (unsigned)((g.full + 7) / 8 * 8 + g.rest * g.split);
+  hipLaunchKernelGGL((k_orth_gemm<TL, MODE>), dim3(grid), dim3(TL::kThreads), TL::kLds, st, g);
   HIP_TRY(hipGetLastError());
+  if (g.rest) {
+    hipLaunchKernelGGL((k_orth_join<TL, MODE>), dim3(g.rest * TL::NW * (TL::NJ / 2)), dim3(256), 0, st, g);
+    HIP_TRY(hipGetLastError());
+  }
   return MOE_OK;
 }
 template <int MODE>
 moe_status launch_orth_gemm(const OrthGemm& g, int batch, int cus, hipStream_t st) {
   const long big = (long)((g.rows + 255) / 256) * ((g.cols + 255) / 256) * batch;
-  if (big >= 2L * cus) return launch_orth_gemm<2, 4, 8, 4, MODE>(g, batch, st);
-  return launch_orth_gemm<2, 2, 4, 4, MODE>(g, batch, st);
+  if (big >= cus) return launch_orth_gemm<OrthBig, MODE>(g, batch, cus, st);
+  const long mid = (long)((g.rows + 127) / 128) * ((g.cols + 127) / 128) * batch;
+  if (mid >= cus) return launch_orth_gemm<OrthMid, MODE>(g, batch, cus, st);
+  return launch_orth_gemm<OrthSmall, MODE>(g, batch, cus, st);
 }
 
 template <int BF, int MP>
@@ -421,7 +458,7 @@ moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dty
     a.eps = eps;
     a.part = reinterpret_cast<double*>(ws + L.part);
     a.hi = reinterpret_cast<uint16_t*>(ws + L.hi);
-    a.lo = reinterpret_cast<uint16_t*>(ws + L.lo);
+    a.lo = reinterpret_cast<uint8_t*>(ws + L.lo);
     uint16_t* ht[2] = {reinterpret_cast<uint16_t*>(ws + L.ht0), reinterpret_cast<uint16_t*>(ws + L.ht1)};
     a.ht = ht[0];
     const dim3 norm_grid(kOrthNormParts, nb);
@@ -438,6 +475,7 @@ moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dty
     for (int k = 0; k < steps; ++k) {
       const float* co = coeffs ? coeffs + 3 * k : kOrthCoeffs;
       OrthGemm g{};
+      g.part = reinterpret_cast<float*>(ws + L.sums);
       g.hi = a.hi; g.lo = a.lo; g.m = L.m; g.n = L.n; g.tall = a.tall;
       // A = X X^T: 2^24 times it in the accumulators, 2^12 in A
       g.p = g.q = a.hi;
@@ -449,7 +487,7 @@ moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dty
       g.s = 1.0f / kOrthScale;
       g.c = A;
       TRY((launch_orth_gemm<ORTH_GRAM>(g, nb, di.cus, st)));
-      // B = b A + c A A
+      // B' = a I + b A + c A A
       g.p = g.q = A;
       g.p_stride = g.q_stride = qs;
       g.p_bytes = g.q_bytes = (uint32_t)(qs * 2);
@@ -457,16 +495,16 @@ moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dty
       g.K = L.mp;
       g.a = A;
       g.c = B;
+      g.c0 = co[0];
       g.c1 = co[1];
       g.s = co[2] / kOrthScale;
       TRY((launch_orth_gemm<ORTH_POLY>(g, nb, di.cus, st)));
-      // X' = a X + B X
+      // X' = B' hi + a lo
       g.p = B;
       g.q = ht[k & 1];
       g.q_stride = xs;
       g.q_bytes = (uint32_t)(xs * 2);
       g.cols = L.np;
-      g.c1 = co[0];
       g.s = 1.0f / kOrthScale;
       g.ht = ht[(k + 1) & 1];
       g.y = static_cast<uint16_t*>(y) + (size_t)b0 * elems;
