@@ -224,6 +224,20 @@ DEV bool orth_tile(const OrthGemm& g, int t, int* mat, int* i0, int* j0) {
   return orth_sym(MODE) && i < j;
 }
 
+// The lo parts of the elements that orth_store finishes, read ahead of it.
+template <class TL, int MODE>
+DEV void orth_lo(const OrthGemm& g, int mat, int i0, int j0, int w, int lane, int p, v2u (&lq)[4]) {
+  if (orth_sym(MODE)) return;
+  const int rb = i0 + 64 * (w / TL::WN) + 4 * (lane & 15);
+  const int c = j0 + 16 * TL::NJ * (w % TL::WN) + 32 * p + 8 * (lane >> 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    lq[i] = v2u{0u, 0u};
+    if (rb < g.rows && c < g.cols)
+      lq[i] = *reinterpret_cast<const v2u*>(g.lo + (size_t)mat * g.rows * g.cols + (size_t)(rb + i) * g.cols + c);
+  }
+}
+
 // A wave's sums acc[i][j][v] are row 64 wm + 4 c16 + i and column 16 NJ wn + 32
 // (j / 2) + 8 gq + 4 (j % 2) + v of its tile (the operands are brought to LDS in
 // that order).  A lane then holds 8 consecutive columns of a row and 4
@@ -233,17 +247,12 @@ DEV bool orth_tile(const OrthGemm& g, int t, int* mat, int* i0, int* j0) {
 // and 2 p + 1.
 template <class TL, int MODE>
 DEV void orth_store(const OrthGemm& g, int mat, int i0, int j0, bool mirror, int w, int lane, int p,
-                    const v4f (&acc)[4][2]) {
+                    const v4f (&acc)[4][2], const v2u (&lq)[4]) {
   const int c16 = lane & 15, gq = lane >> 4;
   const int rb = i0 + 64 * (w / TL::WN) + 4 * c16, c = j0 + 16 * TL::NJ * (w % TL::WN) + 32 * p + 8 * gq;
   const size_t sq = (size_t)mat * g.rows * g.cols, yb = (size_t)mat * g.m * g.n;
   if (rb >= g.rows || c >= g.cols) return;         // (rows and cols are multiples of 64)
   uint32_t h[4][8];                                // this lane's 4 rows x 8 columns
-  v2u lq[4];
-  if (!orth_sym(MODE)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) lq[i] = *reinterpret_cast<const v2u*>(g.lo + sq + (size_t)(rb + i) * g.cols + c);
-  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const size_t o = sq + (size_t)(rb + i) * g.cols + c;
@@ -388,28 +397,60 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_orth_gemm(OrthGemm g) {
   auto frag = [&](const char* op, int r0, int i, int kh) {
     return lds_ld<v8h>(op, (uint32_t)(r0 + 16 * i + c16) * 128 + (((4 * kh + gq) ^ orth_swz(r0 + 16 * i + c16)) << 4));
   };
+  // Every step's first operands are read during the last products of the step
+  // before (the last two of its NJ columns' subtiles), behind the barrier: their
+  // LDS latency is covered by products.
+  constexpr int NL = NJ >= 4 ? 2 : 1;              // column subtiles left behind the barrier, and read ahead
+  v8h pf[4], qf[NJ];
+  auto read_first = [&](const char* st) {
 #pragma unroll
-  for (int s = 0; s < TL::ST - 1; ++s) load(s0 + s, s);
+    for (int i = 0; i < 4; ++i) pf[i] = frag(st, pr0, i, 0);
+#pragma unroll
+    for (int j = 0; j < NL; ++j) qf[j] = frag(st + TL::kSide * 128, qr0, j, 0);
+  };
+  auto mul = [&](int j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i][j] = mfma_f16(qf[j], pf[i], acc[i][j]);
+  };
+#pragma unroll
+  for (int s = 0; s < TL::ST; ++s) load(s0 + s, s);
+  barrier_vmcnt<(TL::ST - 1) * 2 * PP>();          // the first step has landed
+  read_first(lds);
   int stage = 0;
   for (int s = s0; s < s1; ++s) {
-    // this wave's loads of step s have landed (later steps' may be in flight),
-    // and every wave is past step s - 1, whose stage is loaded next
-    barrier_vmcnt<(TL::ST - 2) * 2 * PP>();
-    load(s + TL::ST - 1, stage == 0 ? TL::ST - 1 : stage - 1);
     const char* st = lds + stage * TL::kStage;
+    const int cur = stage;
     stage = stage == TL::ST - 1 ? 0 : stage + 1;
 #pragma unroll
-    for (int kh = 0; kh < 2; ++kh) {
-      v8h pf[4];
+    for (int j = NL; j < NJ; ++j) qf[j] = frag(st + TL::kSide * 128, qr0, j, 0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pf[i] = frag(st, pr0, i, kh);
+    for (int j = 0; j < NJ; ++j) mul(j);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const v8h qf = frag(st + TL::kSide * 128, qr0, j, kh);
+    for (int i = 0; i < 4; ++i) pf[i] = frag(st, pr0, i, 1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i][j] = mfma_f16(qf, pf[i], acc[i][j]);
-      }
-    }
+    for (int j = 0; j < NJ; ++j) qf[j] = frag(st + TL::kSide * 128, qr0, j, 1);
+#pragma unroll
+    for (int j = 0; j < NJ - NL; ++j) mul(j);
+    // this wave's loads of the next step have landed and its reads of this one
+    // are done, and so are every wave's: this stage is free
+    barrier_vmcnt<(TL::ST - 2) * 2 * PP>();
+    load(s + TL::ST, cur);
+    v8h pl[4], ql[NL];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pl[i] = pf[i];
+#pragma unroll
+    for (int j = 0; j < NL; ++j) ql[j] = qf[NJ - NL + j];
+    read_first(lds + stage * TL::kStage);
+    __builtin_amdgcn_sched_barrier(0);             // (these reads are issued before the products below)
+#pragma unroll
+    for (int j = 0; j < NL; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i][NJ - NL + j] = mfma_f16(ql[j], pl[i], acc[i][NJ - NL + j]);
+    // (and stay in this step: the compiler would move them to the next one's start)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(pf[i]));
+#pragma unroll
+    for (int j = 0; j < NL; ++j) asm volatile("" : "+v"(qf[j]));
   }
   wait_vmcnt<0>();                                 // no load into LDS outlives the workgroup
   if (part >= 0) {
@@ -420,13 +461,16 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_orth_gemm(OrthGemm g) {
       for (int j = 0; j < NJ; ++j) dst[(i * NJ + j) * 64] = acc[i][j];
     return;
   }
+  v2u lq[NJ / 2][4];
+#pragma unroll
+  for (int p = 0; p < NJ / 2; ++p) orth_lo<TL, MODE>(g, mat, i0, j0, w, lane, p, lq[p]);
 #pragma unroll
   for (int p = 0; p < NJ / 2; ++p) {
     const v4f a[4][2] = {{acc[0][2 * p], acc[0][2 * p + 1]},
                          {acc[1][2 * p], acc[1][2 * p + 1]},
                          {acc[2][2 * p], acc[2][2 * p + 1]},
                          {acc[3][2 * p], acc[3][2 * p + 1]}};
-    orth_store<TL, MODE>(g, mat, i0, j0, mirror, w, lane, p, a);
+    orth_store<TL, MODE>(g, mat, i0, j0, mirror, w, lane, p, a, lq[p]);
   }
 }
 
@@ -468,7 +512,9 @@ __global__ void __launch_bounds__(256) k_orth_join(OrthGemm g) {
       acc[i][0] += sum[k][2 * i][lane];
       acc[i][1] += sum[k][2 * i + 1][lane];
     }
-  orth_store<TL, MODE>(g, mat, i0, j0, mirror, w, lane, p, acc);
+  v2u lq[4];
+  orth_lo<TL, MODE>(g, mat, i0, j0, w, lane, p, lq);
+  orth_store<TL, MODE>(g, mat, i0, j0, mirror, w, lane, p, acc, lq);
 }
 
 // ------------------------------------------------------------------- narrow
