@@ -214,11 +214,21 @@ def _dense(t):
 
 
 def _is(t, name, shape, dtypes, device, out=False):
-    """Check an argument; outputs must be laid out as the library writes them."""
-    _need(isinstance(t, torch.Tensor) and tuple(t.shape) == tuple(shape), f"{name} must be a tensor {list(shape)}")
+    """Check an argument; outputs must be laid out as the library writes them.
+    (One test on the way that every call takes, the message only when it fails.)"""
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype in dtypes and t.device == device and \
+            (not out or t.is_contiguous()):
+        return
+    _need(isinstance(t, torch.Tensor) and t.shape == shape, f"{name} must be a tensor {list(shape)}")
     _need(t.dtype in dtypes, f"{name} must be {' or '.join(str(d) for d in dtypes)} (got {t.dtype})")
-    _need(t.is_cuda and t.device == device, f"{name} must be on {device} (got {t.device})")
-    _need(not out or t.is_contiguous(), f"{name} must be contiguous")
+    _need(t.device == device, f"{name} must be on {device} (got {t.device})")
+    _need(t.is_contiguous(), f"{name} must be contiguous")
+
+
+def _matrix(t, name, dtypes):
+    """Check a 2-d input on a GPU, which the other arguments are checked against."""
+    if not (isinstance(t, torch.Tensor) and t.dim() == 2 and t.is_cuda and t.dtype in dtypes):
+        raise ValueError(f"{name} must be a 2-d tensor on a GPU, {' or '.join(str(d) for d in dtypes)}")
 
 
 _FLOATS = (torch.bfloat16, torch.float32)
@@ -235,12 +245,11 @@ def layer_norm(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor = None, 
     y_scales, mean, rstd): y [T, H], y_scales [T, H/128] float32 ("fp8", else
     None), mean and rstd [T] float32 (want_stats, for layer_norm_backward, else
     None); `out`, a previous result, is reused."""
-    _need(x.dim() == 2 and x.is_cuda, "x must be a [T, H] tensor on a GPU")
+    _matrix(x, "x", _FLOATS)
     T, H = x.shape
     dev = x.device
-    _need(x.dtype in _FLOATS, f"x must be bfloat16 or float32 (got {x.dtype})")
-    _need(out_dtype in _OUT_DTYPES, f"unknown out_dtype {out_dtype!r}")
-    _need(scale_mode in lib.INTER_SCALES, f"unknown scale_mode {scale_mode!r}")
+    if out_dtype not in _OUT_DTYPES or scale_mode not in lib.INTER_SCALES:
+        raise ValueError(f"unknown out_dtype {out_dtype!r} or scale_mode {scale_mode!r}")
     _is(gamma, "gamma", (H,), _F32, dev)
     if beta is not None:
         _is(beta, "beta", (H,), _F32, dev)
@@ -256,9 +265,9 @@ def layer_norm(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor = None, 
             _is(out["y"], "out['y']", (T, H), (dt,), dev, True)
             for name, shape, wanted in (("y_scales", (T, H // 128), fp8), ("mean", (T,), want_stats),
                                         ("rstd", (T,), want_stats)):
-                _need((out[name] is not None) == wanted, f"out[{name!r}] does not fit the call")
+                _need((out[name] is not None) == wanted, "out does not fit the call")
                 if wanted:
-                    _is(out[name], f"out[{name!r}]", shape, _F32, dev, True)
+                    _is(out[name], name, shape, _F32, dev, True)
         lib.moe_layer_norm(_dense(x), _dense(gamma), None if beta is None else _dense(beta), eps, out["y"],
                            out["y_scales"], out["mean"], out["rstd"], scale_mode)
     return out
@@ -272,10 +281,9 @@ def layer_norm_backward(x: torch.Tensor, gamma: torch.Tensor, mean: torch.Tensor
     dict(dx [T, H], dgamma [H], dbeta [H]), float32; without want_weights
     dgamma and dbeta are None.  `out`, a previous result, is reused (out["dx"]
     may be dy)."""
-    _need(x.dim() == 2 and x.is_cuda, "x must be a [T, H] tensor on a GPU")
+    _matrix(x, "x", _FLOATS)
     T, H = x.shape
     dev = x.device
-    _need(x.dtype in _FLOATS, f"x must be bfloat16 or float32 (got {x.dtype})")
     _is(gamma, "gamma", (H,), _F32, dev)
     _is(mean, "mean", (T,), _F32, dev)
     _is(rstd, "rstd", (T,), _F32, dev)
@@ -288,9 +296,9 @@ def layer_norm_backward(x: torch.Tensor, gamma: torch.Tensor, mean: torch.Tensor
         else:
             _is(out["dx"], "out['dx']", (T, H), _F32, dev, True)
             for name in ("dgamma", "dbeta"):
-                _need((out[name] is not None) == want_weights, f"out[{name!r}] does not fit the call")
+                _need((out[name] is not None) == want_weights, "out does not fit the call")
                 if want_weights:
-                    _is(out[name], f"out[{name!r}]", (H,), _F32, dev, True)
+                    _is(out[name], name, (H,), _F32, dev, True)
         ws = None
         if want_weights:
             nbytes = lib.moe_layer_norm_backward_workspace_size(T, H)
@@ -309,8 +317,7 @@ def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, alpha: float = 1.
     counts).  Returns dict(loss [1] float32, counts [S, E] int32, probs [S, E]
     float32, dlogits [T, E] float32 or, without want_grad, None); `out`, a
     previous result, is reused."""
-    _need(logits.dim() == 2 and logits.is_cuda and logits.dtype == torch.float32,
-          "logits must be a float32 [T, E] tensor on a GPU")
+    _matrix(logits, "logits", _F32)
     T, E = logits.shape
     dev = logits.device
     _need(topk_ids.dim() == 2, "topk_ids must be [T, k]")
@@ -332,10 +339,10 @@ def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, alpha: float = 1.
             for name, shape, dt in (("loss", (1,), torch.float32), ("counts", (S, E), torch.int32),
                                     ("probs", (S, E), torch.float32), ("dlogits", (T, E), torch.float32)):
                 if out[name] is not None:
-                    _is(out[name], f"out[{name!r}]", shape, (dt,), dev, True)
+                    _is(out[name], name, shape, (dt,), dev, True)
         nbytes = lib.moe_balance_loss_workspace_size(T, E, topk_ids.shape[1], S)
         ws = (workspace or Workspace(dev)).get(nbytes)
-        lib.moe_balance_loss(_dense(logits), _dense(topk_ids.to(torch.int32)),
+        lib.moe_balance_loss(_dense(logits), _dense(topk_ids if topk_ids.dtype == torch.int32 else topk_ids.to(torch.int32)),
                              None if seq_offsets is None else _dense(seq_offsets.to(torch.int32)),
                              None if token_mask is None else _dense(token_mask), alpha, out["counts"], out["probs"],
                              out["loss"], out["dlogits"], ws)
@@ -402,9 +409,9 @@ def orthogonalize(u: torch.Tensor, steps: int = 5, coeffs=None, eps: float = 1e-
     dw_router as they are; dw_gate_up [E, 2I, H] as .view(2 * E, I, H), gate
     and up being matrices of their own."""
     _need(u.dim() in (2, 3) and u.is_cuda, "u must be [M, N] or [batch, M, N] on a GPU")
-    _need(u.dtype in _FLOATS, f"u must be bfloat16 or float32 (got {u.dtype})")
+    _need(u.dtype in _FLOATS, "u must be bfloat16 or float32")
     _need(coeffs is None or (len(coeffs) == steps and all(len(c) == 3 for c in coeffs)),
-          f"coeffs must be {steps} triples")
+          "coeffs must be one triple per step")
     dev = u.device
     with _on(dev, stream):
         if out is None:

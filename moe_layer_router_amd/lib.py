@@ -171,9 +171,8 @@ def _nbytes(t):
 
 
 def _stream(stream):
-    if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:      # (the handle alone: a torch.cuda.Stream object per call would cost as much as a launch)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
