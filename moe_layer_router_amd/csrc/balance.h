@@ -36,6 +36,8 @@
 
 namespace moe {
 
+typedef float v4fu __attribute__((ext_vector_type(4), aligned(4)));   // rows of E floats: 4-byte aligned
+
 struct BalArgs {
   const float* logits;       // [T][E]
   const int32_t* ids;        // [T][k]
@@ -52,71 +54,126 @@ struct BalArgs {
   int32_t* rown;             // [count blocks + S] tokens that count
   float* rowp;               // [token blocks + S][E] sums of p
   double* lpart;             // [workgroups of k_bal_final]
+  int32_t* used;             // S', at least 1
   int32_t* done;             // workgroups of k_bal_final that have finished
 };
 
-DEV int bal_off(const BalArgs& a, int s) { return a.off ? min(max(a.off[s], 0), a.T) : (s ? a.T : 0); }
+// The sequence offsets, clamped: in LDS where they fit (a search through global
+// memory is a chain of round trips), else where they are.
+constexpr int kBalOff = 256;
+struct BalOff {
+  const int* lds;                                             // NULL: global memory
+  const BalArgs* a;
+  DEV int operator()(int s) const {
+    if (lds) return lds[s];
+    return a->off ? min(max(a->off[s], 0), a->T) : (s ? a->T : 0);
+  }
+};
+// By the whole workgroup, with a barrier; buf: kBalOff ints.
+DEV BalOff bal_offsets(const BalArgs& a, int* buf) {
+  const BalOff global{nullptr, &a};
+  if (a.S >= kBalOff) return global;
+  for (int s = threadIdx.x; s <= a.S; s += blockDim.x) buf[s] = global(s);
+  __syncthreads();
+  return BalOff{buf, &a};
+}
 
 // The first sequence that ends behind token t (S if none does).
-DEV int bal_seq_of(const BalArgs& a, int t) {
-  if (!a.off) return 0;
+DEV int bal_seq_of(const BalArgs& a, const BalOff& off, int t) {
   int lo = 0, hi = a.S;
   while (lo < hi) {
     const int m = (lo + hi) / 2;
-    if (bal_off(a, m + 1) > t) hi = m; else lo = m + 1;
+    if (off(m + 1) > t) hi = m; else lo = m + 1;
   }
   return lo;
 }
 
 // Rows [*r0, *r1) of sequence s over blocks of `bt` tokens (none if empty).
-DEV void bal_rows(const BalArgs& a, int s, int bt, int* r0, int* r1) {
-  const int t0 = bal_off(a, s), t1 = bal_off(a, s + 1);
+DEV void bal_rows(const BalOff& off, int s, int bt, int* r0, int* r1) {
+  const int t0 = off(s), t1 = off(s + 1);
   *r0 = t0 / bt + s;
   *r1 = t1 > t0 ? (t1 - 1) / bt + s + 1 : *r0;
 }
 
-constexpr int kBalCountThreads = 1024;
+// Up to kBalSegs sequences of a block are counted together, a histogram each
+// (short sequences would otherwise cost a round of memory and barriers each).
+constexpr int kBalCountThreads = 1024, kBalSegs = 4;
 __global__ void __launch_bounds__(kBalCountThreads) k_bal_count(BalArgs a) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  int* hist = reinterpret_cast<int*>(lds);
-  __shared__ int s_n;
+  int* hist = reinterpret_cast<int*>(lds);                    // [kBalSegs][E]
+  __shared__ int s_n[kBalSegs];
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
+  __shared__ int s_off[kBalOff];
+  const BalOff off = bal_offsets(a, s_off);
   const int t0 = blockIdx.x * a.cb, t1 = min(a.T, t0 + a.cb);
-  for (int s = bal_seq_of(a, t0); s < a.S && bal_off(a, s) < t1; ++s) {
-    const int lo = max(t0, bal_off(a, s)), hi = min(t1, bal_off(a, s + 1));
+  for (int s = bal_seq_of(a, off, t0); s < a.S && off(s) < t1; s += kBalSegs) {
+    int end[kBalSegs];                                        // where the sequences end
+#pragma unroll
+    for (int q = 0; q < kBalSegs; ++q) end[q] = off(min(s + q + 1, a.S));
+    const int lo = max(t0, off(s)), hi = min(t1, end[kBalSegs - 1]);
     if (lo >= hi) continue;                                   // (uniform)
-    for (int e = threadIdx.x; e < a.E; e += kBalCountThreads) hist[e] = 0;
-    if (threadIdx.x == 0) s_n = 0;
-    __syncthreads();
-    if (!a.mask) {
-      count_experts(a.ids, (size_t)lo * a.k, (hi - lo) * a.k, a.E, hist);
-    } else {
-      for (int t = lo + threadIdx.x; t < hi; t += kBalCountThreads)
-        if (a.mask[t]) {
-          atomicAdd(&s_n, 1);
-          for (int j = 0; j < a.k; ++j) atomicAdd(&hist[min(max(a.ids[(size_t)t * a.k + j], 0), a.E - 1)], 1);
+    const int nq = 1 + (hi > end[0]) + (hi > end[1]) + (hi > end[2]);   // histograms in use
+    // all loads of a pass before any of its counts (and the first pass's before
+    // the histograms are cleared); -1: an entry that does not count
+    constexpr int kU = 8;
+    const int n = (hi - lo) * a.k;
+    int mine[kBalSegs] = {0, 0, 0, 0};
+    for (int p0 = 0; p0 < n; p0 += kU * kBalCountThreads) {
+      int ev[kU], sv[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int i = p0 + u * kBalCountThreads + (int)threadIdx.x, j = min(i, n - 1), t = lo + j / a.k;
+        const int e = min(max(a.ids[(size_t)lo * a.k + j], 0), a.E - 1);
+        const bool in = i < n && (!a.mask || a.mask[t]);
+        sv[u] = (t >= end[0]) + (t >= end[1]) + (t >= end[2]);
+        ev[u] = in ? sv[u] * a.E + e : -1;
+      }
+      if (p0 == 0) {
+        for (int e = threadIdx.x; e < nq * a.E; e += kBalCountThreads) hist[e] = 0;
+        if (threadIdx.x < kBalSegs) s_n[threadIdx.x] = 0;
+        __syncthreads();
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (ev[u] >= 0) {
+          atomicAdd(&hist[ev[u]], 1);
+#pragma unroll
+          for (int q = 0; q < kBalSegs; ++q) mine[q] += sv[u] == q;
         }
     }
+#pragma unroll
+    for (int q = 0; q < kBalSegs; ++q) {
+      if (q >= nq) break;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) mine[q] += __shfl_xor(mine[q], d);
+      if ((threadIdx.x & 63) == 0 && mine[q]) atomicAdd(&s_n[q], mine[q]);
+    }
     __syncthreads();
-    int32_t* row = a.rowcnt + (size_t)(blockIdx.x + s) * a.E;
-    for (int e = threadIdx.x; e < a.E; e += kBalCountThreads) row[e] = hist[e];
-    if (threadIdx.x == 0) a.rown[blockIdx.x + s] = a.mask ? s_n : hi - lo;
+#pragma unroll
+    for (int q = 0; q < kBalSegs; ++q) {
+      // (a sequence that does not meet the block has no row: the others' are taken)
+      if (q >= nq || s + q >= a.S || max(t0, off(s + q)) >= min(t1, end[q])) continue;
+      int32_t* row = a.rowcnt + (size_t)(blockIdx.x + s + q) * a.E;
+      for (int e = threadIdx.x; e < a.E; e += kBalCountThreads) row[e] = hist[q * a.E + e];
+      if (threadIdx.x == 0) a.rown[blockIdx.x + s + q] = s_n[q] / a.k;    // (k entries for each token that counts)
+    }
     __syncthreads();
   }
 }
 
 // Tokens of sequence s that count, by one thread.
-DEV int bal_tokens_of(const BalArgs& a, int s) {
+DEV int bal_tokens_of(const BalArgs& a, const BalOff& off, int s) {
   int r0, r1, n = 0;
-  bal_rows(a, s, a.cb, &r0, &r1);
+  bal_rows(off, s, a.cb, &r0, &r1);
+#pragma unroll 8
   for (int r = r0; r < r1; ++r) n += a.rown[r];
   return n;
 }
 
 // S' (at least 1) for the whole workgroup; `red`: one int per wave.
-DEV int bal_used(const BalArgs& a, int* red) {
+DEV int bal_used(const BalArgs& a, const BalOff& off, int* red) {
   int u = 0;
-  for (int s = threadIdx.x; s < a.S; s += blockDim.x) u += bal_tokens_of(a, s) > 0;
+  for (int s = threadIdx.x; s < a.S; s += blockDim.x) u += bal_tokens_of(a, off, s) > 0;
   int tot;
   block_inclusive_scan(u, red, &tot);
   return max(tot, 1);
@@ -140,49 +197,72 @@ DEV int bal_max(int v) {
   return v;
 }
 
+// exp(x) for x <= 0 (NaN: NaN): 2^t of the rounded t = x log2 e times the 1 + e ln 2
+// of what the rounding left, log2 e in two parts: within 2 units in the last
+// place, without the range steps of a general exponential (a result below
+// the normal range, -infinity's among them, is zero).
+DEV float bal_exp(float x) {
+  x = x < -200.f ? -200.f : x;
+  constexpr float kHi = 1.44269504f, kLo = (float)(1.4426950408889634 - (double)1.44269504f);
+  const float t = x * kHi;
+  const float e = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -t));
+  const float p = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(p, e * 0.693147181f, p);
+}
+
 // One token per L lanes (16 for E <= 256, else 64), NJ chunks of 4
-// consecutive experts per lane; four waves.  The next token's logits are
-// loaded while the current one is worked on.
-typedef float v4fu __attribute__((ext_vector_type(4), aligned(4)));   // rows of E floats: 4-byte aligned
-template <int L, int NJ>
-__global__ void __launch_bounds__(256) k_bal_tokens(BalArgs a) {
+// consecutive experts per lane; four waves. The next token's logits are
+// loaded while the current one is worked on. Loads and stores are buffer
+// accesses without branches: what lies outside the row, or belongs to a token
+// that does not count, gets an offset past the buffer's end, which reads zero and
+// drops a store (a condition on each would be a branch with a wait: 41 us
+// instead of 30 at T = 16384, E = 1024). VEC: E is a multiple of 4, 16-byte
+// accesses; otherwise a chunk may reach into the next row, and each element is
+// its own access.
+constexpr uint32_t kBalSkip = 0xFFFFFFF0u;
+template <int L, int NJ, int VEC, int GRAD>
+__global__ void __launch_bounds__(256, 4) k_bal_tokens(BalArgs a) {
   constexpr int G = 256 / L;                                  // tokens in flight per workgroup
   extern __shared__ __attribute__((aligned(16))) char lds[];
   float* psum = reinterpret_cast<float*>(lds);                // [4][L * NJ * 4]
   int* cnt = reinterpret_cast<int*>(psum + 4 * L * NJ * 4);   // [L * NJ * 4] counts of the sequence
-  __shared__ int red[4];
+  __shared__ int red[4], s_off[kBalOff];
+  const BalOff off = bal_offsets(a, s_off);
   const int li = threadIdx.x % L, gi = threadIdx.x / L, w = threadIdx.x >> 6, E = a.E;
   const int t0 = blockIdx.x * a.tb, t1 = min(a.T, t0 + a.tb);
   const float ninf = -__builtin_inff();
-  const bool grad = a.dlogits != nullptr;
   auto row_max = [&](float v) { v = row_max16(v); return L == 64 ? max_row_groups(v) : v; };
   auto row_sum = [&](float v) { return L == 64 ? wave_sum(v) : row_sum16(v); };
-  auto load = [&](int t, float (&v)[NJ][4]) {
-    const float* p = a.logits + (size_t)t * E;
+  // this block's rows
+  const uint32_t bytes = (uint32_t)(t1 - t0) * (uint32_t)E * 4u;
+  const rsrc_t lr = make_rsrc(a.logits + (size_t)t0 * E, bytes);
+  const rsrc_t dr = make_rsrc(GRAD ? a.dlogits + (size_t)t0 * E : nullptr, GRAD ? bytes : 0u);
+  auto place = [&](int t, int j, int i, bool on) {            // of expert 4 (li + L j) + i of token t
+    const int e = 4 * (li + L * j) + i;
+    return on && e < E ? ((uint32_t)(t - t0) * (uint32_t)E + (uint32_t)e) * 4u : kBalSkip;
+  };
+  auto load = [&](int t, bool on, float (&v)[NJ][4]) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const int e = 4 * (li + L * j);
-      if (e + 4 <= E) {
-        const v4fu q = *reinterpret_cast<const v4fu*>(p + e);
+      if (VEC) {
+        const v4i q = buf_ld16(lr, place(t, j, 0, on), 0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[j][i] = q[i];
+        for (int i = 0; i < 4; ++i) v[j][i] = __int_as_float(q[i]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[j][i] = e + i < E ? p[e + i] : ninf;
+        for (int i = 0; i < 4; ++i) v[j][i] = buf_ldf(lr, place(t, j, i, on), 0);
       }
     }
   };
-  auto store = [&](int t, const float (&d)[NJ][4]) {
-    float* p = a.dlogits + (size_t)t * E;
+  auto store = [&](int t, bool on, const float (&d)[NJ][4]) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const int e = 4 * (li + L * j);
-      if (e + 4 <= E) {
-        *reinterpret_cast<v4fu*>(p + e) = v4fu{d[j][0], d[j][1], d[j][2], d[j][3]};
+      if (VEC) {
+        buf_st16(dr, place(t, j, 0, on), v4i{__float_as_int(d[j][0]), __float_as_int(d[j][1]),
+                                             __float_as_int(d[j][2]), __float_as_int(d[j][3])});
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (e + i < E) p[e + i] = d[j][i];
+        for (int i = 0; i < 4; ++i) buf_stf(dr, place(t, j, i, on), d[j][i]);
       }
     }
   };
@@ -191,19 +271,27 @@ __global__ void __launch_bounds__(256) k_bal_tokens(BalArgs a) {
   for (int j = 0; j < NJ; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) zero[j][i] = 0.f;
-  const int used = grad ? bal_used(a, red) : 1;
-
+  int used = 0;                                               // S', once it is needed
+  if (blockIdx.x == 0) {
+    used = bal_used(a, off, red);
+    if (threadIdx.x == 0) *a.used = used;                     // (for k_bal_final)
+  }
   int next = t0;                                              // tokens before it are done
-  for (int s = bal_seq_of(a, t0); s < a.S && bal_off(a, s) < t1; ++s) {
-    const int lo = max(t0, bal_off(a, s)), hi = min(t1, bal_off(a, s + 1));
+  for (int s = bal_seq_of(a, off, t0); s < a.S && off(s) < t1; ++s) {
+    const int lo = max(t0, off(s)), hi = min(t1, off(s + 1));
     if (lo >= hi) continue;
-    if (grad)
-      for (int t = next + gi; t < lo; t += G) store(t, zero); // tokens of no sequence
+    if (GRAD)
+      for (int t = next + gi; t < lo; t += G) store(t, true, zero);     // tokens of no sequence
     next = hi;
+    auto counts_of = [&](int t) { return t < hi && (!a.mask || a.mask[t]); };
+    float nx[NJ][4];
+    bool nv = counts_of(lo + gi);                             // the loaded token counts
+    load(lo + gi, nv, nx);
     float kappa = 0.f;
-    if (grad) {
+    if (GRAD) {                                               // (while the first logits are on their way)
+      if (!used) used = bal_used(a, off, red);
       int r0, r1;
-      bal_rows(a, s, a.cb, &r0, &r1);
+      bal_rows(off, s, a.cb, &r0, &r1);
       for (int e = threadIdx.x; e < L * NJ * 4; e += 256) {
         int c = 0;
         if (e < E) {
@@ -212,7 +300,7 @@ __global__ void __launch_bounds__(256) k_bal_tokens(BalArgs a) {
         }
         cnt[e] = c;
       }
-      const double n = (double)max(bal_tokens_of(a, s), 1);
+      const double n = (double)max(bal_tokens_of(a, off, s), 1);
       kappa = (float)((double)a.alpha * E / ((double)used * a.k * n * n));
       __syncthreads();
     }
@@ -221,77 +309,73 @@ __global__ void __launch_bounds__(256) k_bal_tokens(BalArgs a) {
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) ps[j][i] = 0.f;
-    float nx[NJ][4];
-    bool nv = false;                                          // the loaded token counts
-    if (lo + gi < hi) {
-      nv = !a.mask || a.mask[lo + gi];
-      if (nv) load(lo + gi, nx);
-    }
-    for (int t = lo + gi; t < hi; t += G) {
+    for (int tw = lo; tw < hi; tw += G) {                     // (the same passes for every lane)
+      const int t = tw + gi;
       float v[NJ][4];
       const bool valid = nv;
-      if (valid) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[j][i] = nx[j][i];
-      }
-      if (t + G < hi) {
-        nv = !a.mask || a.mask[t + G];
-        if (nv) load(t + G, nx);
-      }
-      if (!valid) {
-        if (grad) store(t, zero);
-        continue;                                             // (lanes of one token stay together)
-      }
+        for (int i = 0; i < 4; ++i) v[j][i] = 4 * (li + L * j) + i < E ? nx[j][i] : ninf;
+      nv = counts_of(t + G);
+      load(t + G, nv, nx);
       float m = ninf;
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) m = fmaxf(m, v[j][i]);
-      m = row_max(m);
-      // the count of the likeliest expert (of equal ones the most frequent)
-      int top = 0;
-      if (grad) {
+      m = fmaxf(row_max(m), -__FLT_MAX__);                    // (finite also where every logit is -inf)
+      // h: counts relative to the likeliest expert's (of equal ones the most frequent)
+      float h[NJ][4];
+      if (GRAD) {
+        int top = 0, c[NJ][4];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const v4i q = *reinterpret_cast<const v4i*>(cnt + 4 * (li + L * j));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            c[j][i] = q[i];
+            top = v[j][i] == m ? max(top, c[j][i]) : top;
+          }
+        }
+        top = bal_max<L>(top);
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (v[j][i] == m) top = max(top, cnt[4 * (li + L * j) + i]);
-        top = bal_max<L>(top);
+          for (int i = 0; i < 4; ++i) h[j][i] = (float)(c[j][i] - top);
       }
-      float sum = 0.f;
+      float sum = 0.f, dot = 0.f;
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          v[j][i] = v[j][i] == ninf ? 0.f : expf(v[j][i] - m);
+          v[j][i] = bal_exp(v[j][i] - m);
           sum += v[j][i];
+          if (GRAD) dot = __builtin_fmaf(v[j][i], h[j][i], dot);
         }
       sum = row_sum(sum);
-      const float inv = sum == 0.f ? 0.f : 1.0f / sum;        // every logit -inf: no probability anywhere
-      float dot = 0.f;
+      // every logit -inf: no probability anywhere; a token that does not count: none
+      const float inv = !valid || sum == 0.f ? 0.f : 1.0f / sum;
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           v[j][i] *= inv;
           ps[j][i] += v[j][i];
-          if (grad) dot = __builtin_fmaf(v[j][i], (float)(cnt[4 * (li + L * j) + i] - top), dot);
         }
-      if (grad) {
-        dot = row_sum(dot);
+      if (GRAD) {
+        dot = row_sum(dot) * inv;
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[j][i] = kappa * v[j][i] * ((float)(cnt[4 * (li + L * j) + i] - top) - dot);
-        store(t, v);
+          for (int i = 0; i < 4; ++i) v[j][i] = kappa * v[j][i] * (h[j][i] - dot);
+        store(t, t < hi, v);
       }
     }
     // the row of sums: the groups of a wave, then the waves
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+    for (int j = 0; j < NJ; ++j) {
+      v4f x4;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float x = ps[j][i];
@@ -299,54 +383,56 @@ __global__ void __launch_bounds__(256) k_bal_tokens(BalArgs a) {
           const uint32_t u = __float_as_uint(x);
           const auto r16 = __builtin_amdgcn_permlane16_swap(u, u, false, false);
           x = __uint_as_float(r16[0]) + __uint_as_float(r16[1]);
-          const uint32_t h = __float_as_uint(x);
-          const auto r32 = __builtin_amdgcn_permlane32_swap(h, h, false, false);
+          const uint32_t q = __float_as_uint(x);
+          const auto r32 = __builtin_amdgcn_permlane32_swap(q, q, false, false);
           x = __uint_as_float(r32[0]) + __uint_as_float(r32[1]);
         }
-        if ((threadIdx.x & 63) < L) psum[w * L * NJ * 4 + 4 * (li + L * j) + i] = x;
+        x4[i] = x;
       }
+      if ((threadIdx.x & 63) < L) *reinterpret_cast<v4f*>(psum + w * L * NJ * 4 + 4 * (li + L * j)) = x4;
+    }
     __syncthreads();
     float* row = a.rowp + (size_t)(blockIdx.x + s) * E;
     for (int e = threadIdx.x; e < E; e += 256)
       row[e] = ((psum[e] + psum[L * NJ * 4 + e]) + psum[2 * L * NJ * 4 + e]) + psum[3 * L * NJ * 4 + e];
     __syncthreads();
   }
-  if (grad)
-    for (int t = next + gi; t < t1; t += G) store(t, zero);   // tokens behind the last sequence
+  if (GRAD)
+    for (int t = next + gi; t < t1; t += G) store(t, true, zero);       // tokens behind the last sequence
 }
 
 // Workgroup (x, s): experts [64x, 64x + 64) of sequence s (s, s + gridDim.y,
-// ...): 16 groups of 16 lanes, each summing every 16th row, 4 experts per
-// lane.  The last workgroup to finish adds the loss.
-__global__ void __launch_bounds__(256) k_bal_final(BalArgs a) {
-  __shared__ float redp[16][64];
-  __shared__ int redc[16][64];
-  __shared__ int red[4], s_last;
-  __shared__ double s_part[64];
-  const int cl = threadIdx.x & 15, grp = threadIdx.x >> 4, E = a.E;
-  const int used = bal_used(a, red);
+// ...): 64 groups of 16 lanes, each summing every 64th row, 4 experts per
+// lane. The last workgroup to finish adds the loss.
+constexpr int kBalFinalThreads = 1024;
+__global__ void __launch_bounds__(kBalFinalThreads) k_bal_final(BalArgs a) {
+  constexpr int NG = kBalFinalThreads / 16;
+  __shared__ float redp[NG][64];
+  __shared__ int redc[NG][64];
+  __shared__ float redp2[16][64];
+  __shared__ int redc2[16][64];
+  __shared__ int s_last;
+  __shared__ int s_off[kBalOff];
+  const BalOff off = bal_offsets(a, s_off);
+  const int tid = threadIdx.x, cl = tid & 15, grp = tid >> 4, E = a.E;
   double part = 0;
   for (int s = blockIdx.y; s < a.S; s += gridDim.y) {
     int c0, c1, p0, p1;
-    bal_rows(a, s, a.cb, &c0, &c1);
-    bal_rows(a, s, a.tb, &p0, &p1);
-    float ps[4] = {0.f, 0.f, 0.f, 0.f};
+    bal_rows(off, s, a.cb, &c0, &c1);
+    bal_rows(off, s, a.tb, &p0, &p1);
+    v4f ps = v4f{0.f, 0.f, 0.f, 0.f};
     int cs[4] = {0, 0, 0, 0};
     const int e0 = blockIdx.x * 64 + 4 * cl;
     if (e0 + 4 <= E) {
 #pragma unroll 8
-      for (int r = p0 + grp; r < p1; r += 16) {
-        const v4fu q = *reinterpret_cast<const v4fu*>(a.rowp + (size_t)r * E + e0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ps[i] += q[i];
-      }
+      for (int r = p0 + grp; r < p1; r += NG) ps += *reinterpret_cast<const v4fu*>(a.rowp + (size_t)r * E + e0);
     } else {
-      for (int r = p0 + grp; r < p1; r += 16)
+      for (int r = p0 + grp; r < p1; r += NG)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (e0 + i < E) ps[i] += a.rowp[(size_t)r * E + e0 + i];
     }
-    for (int r = c0 + grp; r < c1; r += 16)
+    for (int r = c0 + grp; r < c1; r += NG)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (e0 + i < E) cs[i] += a.rowcnt[(size_t)r * E + e0 + i];
@@ -355,46 +441,55 @@ __global__ void __launch_bounds__(256) k_bal_final(BalArgs a) {
       redp[grp][4 * cl + i] = ps[i];
       redc[grp][4 * cl + i] = cs[i];
     }
-    const int n = bal_tokens_of(a, s);
+    const int n = bal_tokens_of(a, off, s);
     __syncthreads();
-    const int e = blockIdx.x * 64 + (int)threadIdx.x;
-    if (threadIdx.x < 64 && e < E) {
-      float p = redp[0][threadIdx.x];
-      int c = redc[0][threadIdx.x];
+    {                                                         // 64 groups to 16 sums of 4, then those
+      const int col = tid & 63, q = tid >> 6;
+      float p = redp[4 * q][col];
+      int c = redc[4 * q][col];
+#pragma unroll
+      for (int i = 1; i < 4; ++i) {
+        p += redp[4 * q + i][col];
+        c += redc[4 * q + i][col];
+      }
+      redp2[q][col] = p;
+      redc2[q][col] = c;
+    }
+    __syncthreads();
+    const int e = blockIdx.x * 64 + tid;
+    if (tid < 64 && e < E) {
+      float p = redp2[0][tid];
+      int c = redc2[0][tid];
 #pragma unroll
       for (int i = 1; i < 16; ++i) {
-        p += redp[i][threadIdx.x];
-        c += redc[i][threadIdx.x];
+        p += redp2[i][tid];
+        c += redc2[i][tid];
       }
       const float pm = n > 0 ? p / (float)n : 0.f;
       a.counts[(size_t)s * E + e] = c;
       a.probs[(size_t)s * E + e] = pm;
       if (n > 0) part += (double)c * E / ((double)a.k * n) * pm;
     }
-    __syncthreads();
   }
-  if (threadIdx.x < 64) s_part[threadIdx.x] = part;
-  __syncthreads();
+  // the workgroup's loss: the first wave holds it
   const int wg = blockIdx.y * gridDim.x + blockIdx.x, nwg = gridDim.x * gridDim.y;
-  if (threadIdx.x == 0) {
-    double v = 0;
-    for (int i = 0; i < 64; ++i) v += s_part[i];
-    st_coh(a.lpart + wg, v);
-    wait_stores();                                            // the partial is in memory before it is counted
-    s_last = __hip_atomic_fetch_add(a.done, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == nwg - 1;
+  if (tid < 64) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) part += __shfl_xor(part, d);
+    if (tid == 0) {
+      st_coh(a.lpart + wg, part);
+      wait_stores();                                          // the partial is in memory before it is counted
+      s_last = __hip_atomic_fetch_add(a.done, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == nwg - 1;
+    }
   }
   __syncthreads();
-  if (!s_last) return;
+  if (!s_last || tid >= 64) return;
   double v = 0;
-  for (int i = threadIdx.x; i < nwg; i += 256) v += ld_coh(a.lpart + i);
-  __shared__ double s_sum[256];
-  s_sum[threadIdx.x] = v;
-  __syncthreads();
-  for (int h = 128; h > 0; h >>= 1) {
-    if ((int)threadIdx.x < h) s_sum[threadIdx.x] += s_sum[threadIdx.x + h];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) *a.loss = (float)((double)a.alpha / used * s_sum[0]);
+#pragma unroll 4
+  for (int i = tid; i < nwg; i += 64) v += ld_coh(a.lpart + i);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+  if (tid == 0) *a.loss = (float)((double)a.alpha / *a.used * v);
 }
 
 }  // namespace moe

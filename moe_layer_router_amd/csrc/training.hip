@@ -8,6 +8,7 @@
 #include "orthogonalize.h"
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 using namespace moe;
@@ -23,14 +24,15 @@ moe_status check_norm_shape(int32_t T, int32_t H) {
 }
 
 // Threads of a row and chunks of 8 channels per thread: a wave per row while
-// the row fits its registers (no barrier in the sums), a workgroup above.
+// the row fits its registers (no barrier in the sums), more waves above.
 template <int IN, int OUT, int TPR, int R>
 moe_status launch_norm(const LnArgs& a, int cus, hipStream_t st) {
   constexpr int RPW = ln_threads(TPR) / TPR;
-  // several rows per workgroup once every CU has 8 of them, so that gamma and
-  // beta are read once for many rows
+  // 16 waves per CU, each going through rows with gamma and beta read once
+  // (T H = 59 M, BF16, H = 512 / 4096 / 7168: 44 / 46 / 48 us; with a quarter
+  // of them 84 / 87 / -, with twice as many 48 / 49 / 50)
   const long rows = (a.T + RPW - 1) / RPW;
-  const unsigned grid = (unsigned)std::min(rows, (long)cus * (ln_threads(TPR) > 256 ? 4 : 8));
+  const unsigned grid = (unsigned)std::min(rows, (long)cus * (1024 / ln_threads(TPR)));
   hipLaunchKernelGGL((k_layer_norm<IN, OUT, TPR, R>), dim3(grid), dim3(ln_threads(TPR)), 0, st, a);
   HIP_TRY(hipGetLastError());
   return MOE_OK;
@@ -41,8 +43,8 @@ moe_status launch_norm(const LnArgs& a, int cus, hipStream_t st) {
   if (a.H <= 1024) return launch_norm<IN, OUT, 64, 2>(a, cus, st);
   if (a.H <= 2048) return launch_norm<IN, OUT, 64, 4>(a, cus, st);
   if (a.H <= 4096) return launch_norm<IN, OUT, 256, 2>(a, cus, st);
-  if (a.H <= 8192) return launch_norm<IN, OUT, 256, 4>(a, cus, st);
-  return launch_norm<IN, OUT, 512, 4>(a, cus, st);
+  if (a.H <= 8192) return launch_norm<IN, OUT, 512, 2>(a, cus, st);
+  return launch_norm<IN, OUT, 1024, 2>(a, cus, st);
 }
 template <int IN>
 moe_status launch_norm(const LnArgs& a, int out_dtype, int cus, hipStream_t st) {
@@ -51,19 +53,14 @@ moe_status launch_norm(const LnArgs& a, int out_dtype, int cus, hipStream_t st) 
   return launch_norm<IN, LN_FP8>(a, cus, st);
 }
 
-// The backward kernel's row layout for H: threads of a row (two chunks per
-// thread above one wave's registers).
-int norm_bwd_tpr(int H) { return H <= 1024 ? 64 : H <= 4096 ? 256 : H <= 8192 ? 512 : 1024; }
-
-// Workgroups of the backward kernel on `cus` CUs: each writes one partial
-// row of dgamma and dbeta.  One per CU, or two once each has 8 rows.
+// Workgroups of the backward kernel: each writes one partial row of dgamma
+// and dbeta, so not more than one per CU (T H = 59 M, H = 4096 / 7168: 106 / 114
+// us, with two per CU 113 / 123).
 int norm_bwd_groups(long T, int H, int cus) {
-  const int tpr = norm_bwd_tpr(H), rpw = ln_threads(tpr) / tpr;
-  const long rows = (T + rpw - 1) / rpw;
-  if (rows <= cus) return (int)rows;
-  return rows >= 16L * cus && tpr < 1024 ? 2 * cus : cus;
+  const int rows_per_wg = H <= 1024 ? 4 : 1;        // (rows of one wave: launch_norm_bwd)
+  return (int)std::min((T + rows_per_wg - 1) / rows_per_wg, (long)cus);
 }
-constexpr int kNormBwdMaxGroups = 2 * 512;          // (workspace: on any device)
+constexpr int kNormBwdMaxGroups = 1024;             // (workspace: on any device)
 
 template <int XD, int DYD, int TPR, int R>
 moe_status launch_norm_bwd(const LnBwdArgs& a, int groups, hipStream_t st) {
@@ -78,7 +75,7 @@ moe_status launch_norm_bwd(const LnBwdArgs& a, int groups, hipStream_t st) {
   if (a.H <= 2048) return launch_norm_bwd<XD, DYD, 256, 1>(a, groups, st);
   if (a.H <= 4096) return launch_norm_bwd<XD, DYD, 256, 2>(a, groups, st);
   if (a.H <= 8192) return launch_norm_bwd<XD, DYD, 512, 2>(a, groups, st);
-  return launch_norm_bwd<XD, DYD, 1024, 2>(a, groups, st);
+  return launch_norm_bwd<XD, DYD, 512, 4>(a, groups, st);
 }
 
 // --------------------------------------------------------------- balance loss
@@ -101,7 +98,7 @@ BalLayout bal_layout(int T, int E, int k, int S) {
   L.gx = (E + 63) / 64;
   L.gy = std::min(S, 512);
   size_t o = 0;
-  L.done = o; o = align256(o + 4);
+  L.done = o; o = align256(o + 8);          // and S'
   L.rown = o; o = align256(o + ((size_t)L.nc + S) * 4);
   L.lpart = o; o = align256(o + (size_t)L.gx * L.gy * 8);
   L.rowcnt = o; o = align256(o + ((size_t)L.nc + S) * E * 4);
@@ -122,14 +119,34 @@ moe_status check_balance(int32_t T, int32_t E, int32_t k, int32_t S) {
   return MOE_OK;
 }
 
-template <int L, int NJ>
+template <int L, int NJ, int VEC>
 moe_status launch_bal_tokens(const BalArgs& a, int grid, hipStream_t st) {
-  hipLaunchKernelGGL((k_bal_tokens<L, NJ>), dim3(grid), dim3(256), 5 * L * NJ * 4 * 4, st, a);
+  constexpr int lds = 5 * L * NJ * 4 * 4;
+  if (a.dlogits) hipLaunchKernelGGL((k_bal_tokens<L, NJ, VEC, 1>), dim3(grid), dim3(256), lds, st, a);
+  else hipLaunchKernelGGL((k_bal_tokens<L, NJ, VEC, 0>), dim3(grid), dim3(256), lds, st, a);
   HIP_TRY(hipGetLastError());
   return MOE_OK;
 }
+template <int L, int NJ>
+moe_status launch_bal_tokens(const BalArgs& a, int grid, hipStream_t st) {
+  return a.E % 4 == 0 ? launch_bal_tokens<L, NJ, 1>(a, grid, st) : launch_bal_tokens<L, NJ, 0>(a, grid, st);
+}
 
 // -------------------------------------------------------- orthogonalisation
+// set_lds_limit, once per kernel and device (a call launches up to two dozen
+// kernels, and the attribute costs as much as half a launch).
+template <auto K>
+moe_status set_lds_limit_once(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  HIP_TRY(hipGetDevice(&dev));
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (done.load(std::memory_order_relaxed) & bit)) return MOE_OK;
+  TRY(set_lds_limit(K, bytes));
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return MOE_OK;
+}
+
 constexpr float kOrthCoeffs[3] = {3.4445f, -4.7750f, 2.0315f};
 constexpr int kOrthMaxSteps = 32;
 constexpr size_t kOrthChunkBytes = (size_t)8 << 30;
@@ -239,7 +256,7 @@ moe_status launch_orth_gemm(OrthGemm g, int batch, int cus, hipStream_t st) {
       g.rest = rest;
     }
   }
-  TRY(set_lds_limit(k_orth_gemm<TL, MODE>, TL::kLds));
+  TRY((set_lds_limit_once<k_orth_gemm<TL, MODE>>(TL::kLds)));
   const unsigned grid = (unsigned)((g.full + 7) / 8 * 8 + g.rest * g.split);
   hipLaunchKernelGGL((k_orth_gemm<TL, MODE>), dim3(grid), dim3(TL::kThreads), TL::kLds, st, g);
   HIP_TRY(hipGetLastError());
@@ -262,7 +279,7 @@ template <int BF, int MP>
 moe_status launch_orth_narrow(const OrthNarrow& a, int batch, hipStream_t st) {
   hipLaunchKernelGGL((k_orth_gram64<BF, MP>), dim3(a.slabs, batch), dim3(256), 0, st, a);
   HIP_TRY(hipGetLastError());
-  TRY(set_lds_limit(k_orth_iter64<MP>, OrthSq<MP>::kLds));
+  TRY((set_lds_limit_once<k_orth_iter64<MP>>(OrthSq<MP>::kLds)));
   hipLaunchKernelGGL(k_orth_iter64<MP>, dim3(batch), dim3(256), OrthSq<MP>::kLds, st, a);
   HIP_TRY(hipGetLastError());
   const dim3 grid((a.n + kOrthApply - 1) / kOrthApply, batch);
@@ -395,15 +412,16 @@ moe_status moe_balance_loss(int32_t T, int32_t E, int32_t top_k, int32_t n_seq, 
   a.rowp = reinterpret_cast<float*>(ws + L.rowp);
   a.lpart = reinterpret_cast<double*>(ws + L.lpart);
   a.done = reinterpret_cast<int32_t*>(ws + L.done);
+  a.used = a.done + 1;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  hipLaunchKernelGGL(k_bal_count, dim3(L.nc), dim3(kBalCountThreads), E * 4, st, a);
+  hipLaunchKernelGGL(k_bal_count, dim3(L.nc), dim3(kBalCountThreads), kBalSegs * E * 4, st, a);
   HIP_TRY(hipGetLastError());
   if (E <= 64) TRY((launch_bal_tokens<16, 1>(a, L.nt, st)));
   else if (E <= 128) TRY((launch_bal_tokens<16, 2>(a, L.nt, st)));
   else if (E <= 256) TRY((launch_bal_tokens<16, 4>(a, L.nt, st)));
   else if (E <= 512) TRY((launch_bal_tokens<64, 2>(a, L.nt, st)));
   else TRY((launch_bal_tokens<64, 4>(a, L.nt, st)));
-  hipLaunchKernelGGL(k_bal_final, dim3(L.gx, L.gy), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(k_bal_final, dim3(L.gx, L.gy), dim3(kBalFinalThreads), 0, st, a);
   HIP_TRY(hipGetLastError());
   return MOE_OK;
 }

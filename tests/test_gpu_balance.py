@@ -79,7 +79,7 @@ def _check(out, l, ids, alpha, off, mask, what=""):
     (1, 1, 1, 0, False), (1, 8, 2, 0, False), (1, 256, 8, 0, True), (3, 2, 1, 2, False), (64, 8, 2, 0, False),
     (65, 63, 4, 3, True), (130, 64, 6, 0, True), (257, 65, 16, 5, False), (300, 128, 8, 4, True), (77, 129, 3, 0, False),
     (1000, 256, 8, 7, True), (90, 257, 8, 2, True), (513, 512, 2, 0, False), (210, 515, 16, 3, True),
-    (1500, 1024, 16, 4, True), (40, 1023, 5, 40, False), (5000, 16, 4, 64, True), (3, 4, 4, 0, False),
+    (1500, 1024, 16, 4, True), (40, 1023, 5, 40, False), (900, 70, 3, 300, True), (5000, 16, 4, 64, True), (3, 4, 4, 0, False),
 ])
 @pytest.mark.parametrize("grad", [True, False])
 def test_against_definition(gpu_lib, T, E, k, S, masked, grad):
