@@ -238,6 +238,15 @@ DEV void orth_lo(const OrthGemm& g, int mat, int i0, int j0, int w, int lane, in
   }
 }
 
+// Stores of X': past the caches where there is more of it than they hold (the
+// large tiles), so that they leave the operands of the running products in the
+// L2 (8 x 2048 x 7168: 4795 -> 4680 us).
+template <class TL, typename T>
+DEV void orth_put(void* p, const T& v) {
+  if (TL::kSide >= 256) __builtin_nontemporal_store(v, static_cast<T*>(p));
+  else *static_cast<T*>(p) = v;
+}
+
 // A wave's sums acc[i][j][v] are row 64 wm + 4 c16 + i and column 16 NJ wn + 32
 // (j / 2) + 8 gq + 4 (j % 2) + v of its tile (the operands are brought to LDS in
 // that order).  A lane then holds 8 consecutive columns of a row and 4
@@ -294,9 +303,8 @@ DEV void orth_store(const OrthGemm& g, int mat, int i0, int j0, bool mirror, int
       float l[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) l[e] = (v[e] - h_val(h[i][e])) * kOrthLoScale;
-      st16(g.hi + o, hw);
-      *reinterpret_cast<v2u*>(g.lo + o) =
-          v2u{f32x4_to_e4m3x4(l[0], l[1], l[2], l[3]), f32x4_to_e4m3x4(l[4], l[5], l[6], l[7])};
+      orth_put<TL>(g.hi + o, hw);
+      orth_put<TL>(g.lo + o, v2u{f32x4_to_e4m3x4(l[0], l[1], l[2], l[3]), f32x4_to_e4m3x4(l[4], l[5], l[6], l[7])});
     }
     if (MODE == ORTH_LAST && !g.tall && rb + i < g.m) {
       uint16_t* y = g.y + yb + (size_t)(rb + i) * g.n + c;
@@ -323,8 +331,10 @@ DEV void orth_store(const OrthGemm& g, int mat, int i0, int j0, bool mirror, int
           for (int i = 0; i < 4; ++i)
             if (rb + i < g.m) y[i] = (uint16_t)h[i][e];
         }
+      } else if (orth_sym(MODE)) {
+        *reinterpret_cast<v2u*>(g.c + sq + (size_t)(c + e) * g.rows + rb) = t;
       } else {
-        *reinterpret_cast<v2u*>((orth_sym(MODE) ? g.c : g.ht) + sq + (size_t)(c + e) * g.rows + rb) = t;
+        orth_put<TL>(g.ht + sq + (size_t)(c + e) * g.rows + rb, t);
       }
     }
   }

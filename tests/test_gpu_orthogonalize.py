@@ -10,7 +10,7 @@ root mean square is at most 2^-8 / sqrt(3).  Inside:
   70 * 2^-24 * 485 = 2e-3, while |y| is at least 0.6 (the largest singular value
   is at least 1 / sqrt(m) = 0.125, which the polynomial takes there): 3.4e-3;
 - above: FP16 products, whose roundings, simulated in fp64 with the kernel's
-  rounding points, stay below 2.3e-3 for a side of 64 and spectra from flat to
+  rounding points, stay below 2.3e-3 for sides from 65 on and spectra from flat to
   1 / r^2 (and fall with the size); 3e-3."""
 
 import numpy as np
@@ -76,15 +76,37 @@ def test_spectra(gpu_lib, B, M, N, kind):
     _check(y, u, what=kind)
 
 
-def test_large_tiles(gpu_lib):
-    """A batch large enough for the 256 x 256 tiles, with padding and partial
-    tiles on both sides, wide and tall."""
+@pytest.mark.parametrize("B", [40, 12, 3])
+def test_tile_shapes(gpu_lib, B):
+    """Batches for the 256 x 256, the 128 x 128 and the 64 x 64 tiles, with padding
+    and partial tiles on both sides and a partial round split along K, wide
+    and tall."""
     from moe_layer_router_amd import layer as L
     for M, N in ((520, 1100), (1100, 520)):
-        u = _mat(40, M, N, 9)
+        u = _mat(B, M, N, 9)
         y = L.orthogonalize(u)
         torch.cuda.synchronize()
-        _check(y[[0, 17, 39]], u[[0, 17, 39]], what=(M, N))
+        some = [0, B // 2, B - 1]
+        _check(y[some], u[some], what=(M, N))
+
+
+def test_batch_in_several_parts(gpu_lib):
+    """A batch whose workspace would pass 8 GiB goes through in parts: the
+    matrices on both sides of the cut, and the last."""
+    from moe_layer_router_amd import layer as L, lib
+    B, M, N = 2300, 512, 1000
+    one = lib.moe_orthogonalize_workspace_size(1, M, N)
+    assert lib.moe_orthogonalize_workspace_size(B, M, N) < B * one
+    g = torch.Generator(device="cuda").manual_seed(1)
+    u = torch.randn(B, M, N, generator=g, device="cuda", dtype=torch.float32).to(torch.bfloat16)
+    y = L.orthogonalize(u)
+    torch.cuda.synchronize()
+    assert torch.isfinite(y).all()
+    some = [0, 1500, 1800, B - 2, B - 1]
+    _check(y[some], u[some])
+    # every matrix was done: the squares sum to the number of singular values, roughly (0.68 .. 1.2 each)
+    s = y.float().square().sum((1, 2))
+    assert float(s.min()) > 0.4 * M and float(s.max()) < 1.5 * M
 
 
 @pytest.mark.parametrize("M,N", [(12, 30), (90, 200)])
