@@ -485,7 +485,7 @@ moe_status moe_balance_loss(int32_t T, int32_t E, int32_t top_k, int32_t n_seq, 
  * and y = X in U's orientation: U's singular vectors, with singular values
  * near 1.  (a, b, c) of step i are coeffs[3i .. 3i+2] (host memory, read
  * during the call), or 3.4445, -4.7750, 2.0315 in each step if coeffs is NULL;
- * coefficients that let X, A or a I + b A + c A A grow past 15 are refused
+ * coefficients that let X's singular values grow past 3.8 are refused
  * (MOE_ERR_UNSUPPORTED).  A zero matrix gives zero.
  * u [batch][M][N] row-major (in_dtype BF16 or F32): dw_gate_up [E][2I][H] is
  * batch = 2E gate and up matrices of I x H, dw_down [E][H][I] E matrices, and

@@ -9,8 +9,10 @@
 // formed on and above the diagonal and mirrored.
 //
 // Precision.  The products are FP16 matrix-core products with fp32
-// accumulation on 2^12 times the values of X, A and a I + B (they stay below 8,
-// and FP16 reaches 2^16; a normal FP16 number goes down to 2^-26 of the scale).
+// accumulation, on 2^12 times the values of X and A (below 4 and 15, and FP16
+// reaches 2^16) and on a I + B itself (its small elements are subnormal FP16
+// numbers, which the matrix cores take: 3e-8 beside a), so that the
+// accumulators of (a I + B) X hold 2^12 X'.
 // X is held as an FP16 part hi and the E4M3 code lo of 2^6 times what is left,
 // 15 bits: the step is X' = (a I + B) hi + a lo, the first term one product, the
 // second added in fp32.  One FP16 product has 2^-11 relative rounding per
@@ -60,6 +62,18 @@ struct OrthArgs {
 DEV uint32_t h_bits(float v) { return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v); }
 DEV float h_val(uint32_t b) { return (float)__builtin_bit_cast(_Float16, (uint16_t)b); }
 constexpr float kOrthLoScale = 64.0f;    // (|lo| <= 4 for |X| < 4, half a unit in hi's last place: within E4M3's 448)
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef short v2s __attribute__((ext_vector_type(2)));
+// Two values as packed FP16 (one conversion instruction, to nearest even), and
+// as E4M3 codes of kOrthLoScale times them in half `HI` of a word.
+DEV uint32_t h_pack(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{lo, hi}), v2h));
+}
+template <bool HI>
+DEV v2s lo_pack(v2s old, float a, float b) {
+  return __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(old, a, b, 1.0f / kOrthLoScale, HI);
+}
 
 template <int BF>
 DEV float orth_ld(const void* u, size_t i) {
@@ -158,9 +172,9 @@ constexpr bool orth_sym(int mode) { return mode == ORTH_GRAM || mode == ORTH_POL
 // C[i][j] = sum_k P[i][k] Q[j][k] for each matrix of a batch, P [rows][ld], Q
 // [cols][ld] FP16, K a multiple of 64, and what follows it:
 //   GRAM   A = s C                                  (symmetric)
-//   POLY   B' = c0 2^12 I + c1 A + s C              (symmetric)
-//   STEP   X' = s C + c0 lo as hi, lo, ht
-//   LAST   the result: (s C + c0 lo) / 2^12 as BF16 in U's orientation
+//   POLY   B' = c0 I + c1 A + s C                   (symmetric)
+//   STEP   X' = C + c0 lo as hi, lo, ht
+//   LAST   the result: (C + c0 lo) / 2^12 as BF16 in U's orientation
 struct OrthGemm {
   const uint16_t* p;
   const uint16_t* q;
@@ -261,80 +275,80 @@ DEV void orth_store(const OrthGemm& g, int mat, int i0, int j0, bool mirror, int
   const int rb = i0 + 64 * (w / TL::WN) + 4 * c16, c = j0 + 16 * TL::NJ * (w % TL::WN) + 32 * p + 8 * gq;
   const size_t sq = (size_t)mat * g.rows * g.cols, yb = (size_t)mat * g.m * g.n;
   if (rb >= g.rows || c >= g.cols) return;         // (rows and cols are multiples of 64)
-  uint32_t h[4][8];                                // this lane's 4 rows x 8 columns
+  float v[4][8];                                   // this lane's 4 rows x 8 columns
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const size_t o = sq + (size_t)(rb + i) * g.cols + c;
-    float v[8];
+    const float scale = MODE == ORTH_LAST ? 1.0f / kOrthScale : orth_sym(MODE) ? g.s : 1.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = g.s * acc[i][e >> 2][e & 3];
+    for (int e = 0; e < 8; ++e) v[i][e] = scale * acc[i][e >> 2][e & 3];
     if (MODE == ORTH_POLY) {
       const v4i q = ld16(g.a + o);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        v[e] = __builtin_fmaf(g.c1, h_val((uint32_t)q[e >> 1] >> (16 * (e & 1))), v[e]);
-        if (c + e == rb + i) v[e] += g.c0 * kOrthScale;
+        v[i][e] = __builtin_fmaf(g.c1, h_val((uint32_t)q[e >> 1] >> (16 * (e & 1))), v[i][e]);
+        if (c + e == rb + i) v[i][e] += g.c0;
       }
     }
     if (!orth_sym(MODE)) {
-      const float c0 = g.c0 * (1.0f / kOrthLoScale);
-      typedef float v2f __attribute__((ext_vector_type(2)));
+      const float c0 = g.c0 * scale * (1.0f / kOrthLoScale);
 #pragma unroll
       for (int d = 0; d < 2; ++d) {
         const v2f l0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)lq[i][d], false);
         const v2f l1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)lq[i][d], true);
-        v[4 * d] = __builtin_fmaf(c0, l0[0], v[4 * d]);
-        v[4 * d + 1] = __builtin_fmaf(c0, l0[1], v[4 * d + 1]);
-        v[4 * d + 2] = __builtin_fmaf(c0, l1[0], v[4 * d + 2]);
-        v[4 * d + 3] = __builtin_fmaf(c0, l1[1], v[4 * d + 3]);
+        v[i][4 * d] = __builtin_fmaf(c0, l0[0], v[i][4 * d]);
+        v[i][4 * d + 1] = __builtin_fmaf(c0, l0[1], v[i][4 * d + 1]);
+        v[i][4 * d + 2] = __builtin_fmaf(c0, l1[0], v[i][4 * d + 2]);
+        v[i][4 * d + 3] = __builtin_fmaf(c0, l1[1], v[i][4 * d + 3]);
       }
     }
     if (MODE == ORTH_LAST) {
+      if (!g.tall && rb + i < g.m) {
+        uint16_t* y = g.y + yb + (size_t)(rb + i) * g.n + c;
+        if (c + 8 <= g.n && g.n % 8 == 0) {        // (rows of y start on 16 bytes)
+          st16(y, v4i{(int)bf16x2_rne(v[i][0], v[i][1]), (int)bf16x2_rne(v[i][2], v[i][3]),
+                      (int)bf16x2_rne(v[i][4], v[i][5]), (int)bf16x2_rne(v[i][6], v[i][7])});
+        } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[i][e] = f32_to_bf16_rne(v[e] * (1.0f / kOrthScale));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[i][e] = h_bits(v[e]);
+          for (int e = 0; e < 8; ++e)
+            if (c + e < g.n) y[e] = (uint16_t)f32_to_bf16_rne(v[i][e]);
+        }
+      }
+      continue;
     }
-    const v4i hw = v4i{(int)(h[i][0] | (h[i][1] << 16)), (int)(h[i][2] | (h[i][3] << 16)),
-                       (int)(h[i][4] | (h[i][5] << 16)), (int)(h[i][6] | (h[i][7] << 16))};
+    const v4i hw = v4i{(int)h_pack(v[i][0], v[i][1]), (int)h_pack(v[i][2], v[i][3]), (int)h_pack(v[i][4], v[i][5]),
+                       (int)h_pack(v[i][6], v[i][7])};
     if (orth_sym(MODE)) st16(g.c + o, hw);
     if (MODE == ORTH_STEP) {
       float l[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) l[e] = (v[e] - h_val(h[i][e])) * kOrthLoScale;
-      orth_put<TL>(g.hi + o, hw);
-      orth_put<TL>(g.lo + o, v2u{f32x4_to_e4m3x4(l[0], l[1], l[2], l[3]), f32x4_to_e4m3x4(l[4], l[5], l[6], l[7])});
-    }
-    if (MODE == ORTH_LAST && !g.tall && rb + i < g.m) {
-      uint16_t* y = g.y + yb + (size_t)(rb + i) * g.n + c;
-      if (c + 8 <= g.n && g.n % 8 == 0) {          // (rows of y start on 16 bytes)
-        st16(y, hw);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (c + e < g.n) y[e] = (uint16_t)h[i][e];
+      for (int e = 0; e < 8; ++e) {
+        const int word = hw[e >> 1];               // (a bit cast of the vector's element itself reads element 0)
+        l[e] = v[i][e] - (float)__builtin_bit_cast(v2h, word)[e & 1];
       }
+      const v2s z = v2s{0, 0};
+      orth_put<TL>(g.hi + o, hw);
+      orth_put<TL>(g.lo + o, v2u{__builtin_bit_cast(uint32_t, lo_pack<true>(lo_pack<false>(z, l[0], l[1]), l[2], l[3])),
+                                 __builtin_bit_cast(uint32_t, lo_pack<true>(lo_pack<false>(z, l[4], l[5]), l[6], l[7]))});
     }
   }
   if (MODE == ORTH_STEP || mirror || (MODE == ORTH_LAST && g.tall)) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const v2u t = v2u{h[0][e] | (h[1][e] << 16), h[2][e] | (h[3][e] << 16)};
       if (MODE == ORTH_LAST) {
         if (c + e >= g.n) continue;
         uint16_t* y = g.y + yb + (size_t)(c + e) * g.m + rb;
         if (rb + 4 <= g.m && g.m % 4 == 0) {
-          *reinterpret_cast<v2u*>(y) = t;
+          *reinterpret_cast<v2u*>(y) = v2u{bf16x2_rne(v[0][e], v[1][e]), bf16x2_rne(v[2][e], v[3][e])};
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (rb + i < g.m) y[i] = (uint16_t)h[i][e];
+            if (rb + i < g.m) y[i] = (uint16_t)f32_to_bf16_rne(v[i][e]);
         }
-      } else if (orth_sym(MODE)) {
-        *reinterpret_cast<v2u*>(g.c + sq + (size_t)(c + e) * g.rows + rb) = t;
       } else {
-        orth_put<TL>(g.ht + sq + (size_t)(c + e) * g.rows + rb, t);
+        const v2u t = v2u{h_pack(v[0][e], v[1][e]), h_pack(v[2][e], v[3][e])};
+        if (orth_sym(MODE)) *reinterpret_cast<v2u*>(g.c + sq + (size_t)(c + e) * g.rows + rb) = t;
+        else orth_put<TL>(g.ht + sq + (size_t)(c + e) * g.rows + rb, t);
       }
     }
   }
@@ -427,10 +441,7 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_orth_gemm(OrthGemm g) {
   barrier_vmcnt<(TL::ST - 1) * 2 * PP>();          // the first step has landed
   read_first(lds);
   int stage = 0;
-  for (int s = s0; s < s1; ++s) {
-    const char* st = lds + stage * TL::kStage;
-    const int cur = stage;
-    stage = stage == TL::ST - 1 ? 0 : stage + 1;
+  auto halves = [&](const char* st) {              // the step but for the last NL column subtiles
 #pragma unroll
     for (int j = NL; j < NJ; ++j) qf[j] = frag(st + TL::kSide * 128, qr0, j, 0);
 #pragma unroll
@@ -441,6 +452,11 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_orth_gemm(OrthGemm g) {
     for (int j = 0; j < NJ; ++j) qf[j] = frag(st + TL::kSide * 128, qr0, j, 1);
 #pragma unroll
     for (int j = 0; j < NJ - NL; ++j) mul(j);
+  };
+  for (int s = s0; s < s1 - 1; ++s) {
+    halves(lds + stage * TL::kStage);
+    const int cur = stage;
+    stage = stage == TL::ST - 1 ? 0 : stage + 1;
     // this wave's loads of the next step have landed and its reads of this one
     // are done, and so are every wave's: this stage is free
     barrier_vmcnt<(TL::ST - 2) * 2 * PP>();
@@ -462,6 +478,17 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_orth_gemm(OrthGemm g) {
 #pragma unroll
     for (int j = 0; j < NL; ++j) asm volatile("" : "+v"(qf[j]));
   }
+  // the first half of what is stored below reads its lo parts during the last
+  // step, the second (the operands' registers are free then) during the first
+  constexpr int NP = NJ / 2, NE = NP > 1 ? NP / 2 : 1;
+  v2u lq[NP][4];
+#pragma unroll
+  for (int p = 0; p < NE; ++p) orth_lo<TL, MODE>(g, mat, i0, j0, w, lane, p, lq[p]);
+  halves(lds + stage * TL::kStage);
+#pragma unroll
+  for (int j = NJ - NL; j < NJ; ++j) mul(j);
+#pragma unroll
+  for (int p = NE; p < NP; ++p) orth_lo<TL, MODE>(g, mat, i0, j0, w, lane, p, lq[p]);
   wait_vmcnt<0>();                                 // no load into LDS outlives the workgroup
   if (part >= 0) {
     v4f* dst = reinterpret_cast<v4f*>(g.part + (size_t)part * TL::kPart) + (size_t)w * 4 * NJ * 64 + lane;
@@ -471,9 +498,6 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_orth_gemm(OrthGemm g) {
       for (int j = 0; j < NJ; ++j) dst[(i * NJ + j) * 64] = acc[i][j];
     return;
   }
-  v2u lq[NJ / 2][4];
-#pragma unroll
-  for (int p = 0; p < NJ / 2; ++p) orth_lo<TL, MODE>(g, mat, i0, j0, w, lane, p, lq[p]);
 #pragma unroll
   for (int p = 0; p < NJ / 2; ++p) {
     const v4f a[4][2] = {{acc[0][2 * p], acc[0][2 * p + 1]},

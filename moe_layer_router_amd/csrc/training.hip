@@ -218,9 +218,9 @@ moe_status check_orth(int32_t batch, int32_t M, int32_t N) {
   return MOE_OK;
 }
 
-// Whether X, A and a I + B stay within FP16's range times 2^-12 over the steps: the
-// singular values start in [0, 1], and a step takes [0, s] to its image under
-// the polynomial.
+// Whether X and A stay within the range of their FP16 and E4M3 parts over the
+// steps: the singular values start in [0, 1], and a step takes [0, s] to its
+// image under the polynomial.
 bool orth_in_range(int steps, const float* co) {
   double top = 1;
   for (int k = 0; k < steps; ++k) {
@@ -228,7 +228,7 @@ bool orth_in_range(int steps, const float* co) {
     double next = 0;
     for (int i = 0; i <= 1024; ++i) {
       const double s = top * i / 1024, s2 = s * s, bv = b * s2 + c * s2 * s2, to = std::fabs(s * (a + bv));
-      if (!(std::fabs(a) + std::fabs(bv) < 15) || !(s2 < 15) || !(to < 14)) return false;      // (NaN: false too)
+      if (!(std::fabs(a) + std::fabs(bv) < 1000) || !(to < 3.8)) return false;      // (NaN: false too)
       next = std::max(next, to);
     }
     top = 1.01 * next;                    // (rounding, and the grid's gaps)
@@ -514,8 +514,8 @@ moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dty
       g.a = A;
       g.c = B;
       g.c0 = co[0];
-      g.c1 = co[1];
-      g.s = co[2] / kOrthScale;
+      g.c1 = co[1] / kOrthScale;
+      g.s = co[2] / (kOrthScale * kOrthScale);
       TRY((launch_orth_gemm<ORTH_POLY>(g, nb, di.cus, st)));
       // X' = B' hi + a lo
       g.p = B;
@@ -523,7 +523,6 @@ moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dty
       g.q_stride = xs;
       g.q_bytes = (uint32_t)(xs * 2);
       g.cols = L.np;
-      g.s = 1.0f / kOrthScale;
       g.ht = ht[(k + 1) & 1];
       g.y = static_cast<uint16_t*>(y) + (size_t)b0 * elems;
       if (k + 1 < steps) TRY((launch_orth_gemm<ORTH_STEP>(g, nb, di.cus, st)));
