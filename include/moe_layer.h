@@ -422,8 +422,8 @@ moe_status moe_backward_aux(const moe_desc* d, const void* x, const void* router
  * as there), codes in y and fp32 scales in y_scales [T][H/128], the layout
  * moe_forward takes.  mean and rstd [T] fp32: optional outputs, both or
  * neither, for moe_layer_norm_backward.  1 <= T, H a multiple of 128 up to
- * 16384, eps >= 0; pointers 16-byte aligned; y must not overlap x.  Enqueued
- * on `stream`; errors as moe_forward. */
+ * 16384, eps >= 0, for FP8 output finite x; pointers 16-byte aligned; y must
+ * not overlap x.  Enqueued on `stream`; errors as moe_forward. */
 moe_status moe_layer_norm(int32_t T, int32_t H, int32_t in_dtype, int32_t out_dtype, int32_t scale_mode,
                           const void* x, const float* gamma, const float* beta, float eps, void* y, float* y_scales,
                           float* mean, float* rstd, moe_stream_t stream);
@@ -434,7 +434,7 @@ moe_status moe_layer_norm(int32_t T, int32_t H, int32_t in_dtype, int32_t out_dt
  * x [T][H] (x_dtype BF16 or F32) and gamma, mean, rstd as in the forward
  * call; dy [T][H] (dy_dtype BF16 or F32), e.g. the dx of moe_backward.
  * Outputs (fp32, overwritten): dx [T][H] (dx may be dy where dy is fp32; no
- * other overlap), dgamma [H] and dbeta [H] (each optional, NULL = not
+ * other overlap with x or dy), dgamma [H] and dbeta [H] (each optional, NULL = not
  * computed).  Limits as moe_layer_norm.  workspace: of
  * moe_layer_norm_backward_workspace_size(T, H) bytes (0 for a shape that is
  * refused), not needed when neither dgamma nor dbeta is asked for.
@@ -466,7 +466,7 @@ moe_status moe_layer_norm_backward(int32_t T, int32_t H, int32_t x_dtype, int32_
  * moe_forward's workspace); topk_ids [T][top_k] int32 (ids out of range are
  * clamped, as in moe_permute).  Outputs, overwritten: counts [n_seq][E] int32,
  * probs [n_seq][E] fp32, loss [1] fp32, and dlogits [T][E] fp32 (optional,
- * NULL = not computed; not the logits themselves).  Sums are fp32 (the loss
+ * NULL = not computed; must not overlap logits).  Sums are fp32 (the loss
  * fp64) in a fixed order: identical inputs give identical bits.  1 <= T,
  * 1 <= top_k <= min(E, 16), E <= 1024, T * top_k <= 2^30, 1 <= n_seq <= 2^20.
  * workspace: moe_balance_loss_workspace_size bytes (0 for arguments that are

@@ -3,6 +3,7 @@
 // kernels.hip.
 #pragma once
 #include <hip/hip_runtime.h>
+#include <stdint.h>
 
 #include "moe_layer.h"
 
@@ -19,6 +20,12 @@ struct DevInfo {
 };
 // The current device: MOE_ERR_UNSUPPORTED unless it is a gfx950.
 moe_status device_info(DevInfo* out);
+
+// Whether two buffers share bytes.
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
+  return a && b && a0 < b0 + nb && b0 < a0 + na;
+}
 
 inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 

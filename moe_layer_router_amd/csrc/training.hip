@@ -16,6 +16,8 @@ using namespace moe;
 namespace {
 
 // ----------------------------------------------------------------- layer norm
+size_t float_bytes(int32_t dtype) { return dtype == MOE_DTYPE_F32 ? 4 : dtype == MOE_DTYPE_BF16 ? 2 : 1; }
+
 moe_status check_norm_shape(int32_t T, int32_t H) {
   if (T < 1) return fail(MOE_ERR_INVALID_ARGUMENT, "T must be >= 1 (got %d)", T);
   if (H < 128 || H % 128) return fail(MOE_ERR_INVALID_ARGUMENT, "H must be a positive multiple of 128 (got %d)", H);
@@ -333,6 +335,9 @@ moe_status moe_layer_norm(int32_t T, int32_t H, int32_t in_dtype, int32_t out_dt
   if (!fp8 && y_scales) return fail(MOE_ERR_INVALID_ARGUMENT, "y_scales must be NULL unless the output is FP8");
   TRY(check_ptr(mean, "mean", rstd != nullptr));
   TRY(check_ptr(rstd, "rstd", mean != nullptr));
+  const size_t n = (size_t)T * H;
+  if (overlap(x, n * float_bytes(in_dtype), y, n * float_bytes(out_dtype)))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "y overlaps x");
   DevInfo di;
   TRY(device_info(&di));
   const LnArgs a{x, gamma, beta, y, y_scales, mean, rstd, T, H, eps, fp8 && scale_mode == MOE_INTER_SCALE_POW2};
@@ -363,8 +368,10 @@ moe_status moe_layer_norm_backward(int32_t T, int32_t H, int32_t x_dtype, int32_
   TRY(check_ptr(dx, "dx"));
   TRY(check_ptr(dgamma, "dgamma", false));
   TRY(check_ptr(dbeta, "dbeta", false));
-  if (dx == dy && dy_dtype != MOE_DTYPE_F32)
-    return fail(MOE_ERR_INVALID_ARGUMENT, "dx can be dy only where dy is fp32");
+  const size_t n = (size_t)T * H;
+  if (overlap(dx, n * 4, dy, n * float_bytes(dy_dtype)) && !(dx == dy && dy_dtype == MOE_DTYPE_F32))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "dx overlaps dy (it may only be an fp32 dy itself)");
+  if (overlap(dx, n * 4, x, n * float_bytes(x_dtype))) return fail(MOE_ERR_INVALID_ARGUMENT, "dx overlaps x");
   const bool weights = dgamma || dbeta;
   TRY(check_ptr(workspace, "workspace", weights));
   const size_t need = weights ? moe_layer_norm_backward_workspace_size(T, H) : 0;
@@ -408,7 +415,8 @@ moe_status moe_balance_loss(int32_t T, int32_t E, int32_t top_k, int32_t n_seq, 
   TRY(check_ptr(probs, "probs"));
   TRY(check_ptr(loss, "loss"));
   TRY(check_ptr(dlogits, "dlogits", false));
-  if (dlogits == logits) return fail(MOE_ERR_INVALID_ARGUMENT, "dlogits is logits");
+  if (overlap(dlogits, (size_t)T * E * 4, logits, (size_t)T * E * 4))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "dlogits overlaps logits");
   TRY(check_ptr(workspace, "workspace"));
   const BalLayout L = bal_layout(T, E, top_k, n_seq);
   if (workspace_bytes < L.total)
@@ -454,8 +462,7 @@ moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dty
   TRY(check_ptr(y, "y"));
   TRY(check_ptr(workspace, "workspace"));
   const size_t elems = (size_t)M * N, isz = in_dtype == MOE_DTYPE_BF16 ? 2 : 4;
-  const uintptr_t u0 = (uintptr_t)u, y0 = (uintptr_t)y;
-  if (u0 < y0 + batch * elems * 2 && y0 < u0 + batch * elems * isz)
+  if (overlap(y, batch * elems * 2, u, batch * elems * isz))
     return fail(MOE_ERR_INVALID_ARGUMENT, "y overlaps u");
   const OrthLayout L = orth_layout(batch, M, N);
   if (workspace_bytes < L.total)

@@ -180,8 +180,8 @@ def backward(inputs: dict, topk_ids: torch.Tensor, topk_weights: torch.Tensor, d
 
 
 def logits(out: dict) -> torch.Tensor:
-    """View of the router logits [T, E] (float32, bias included) of a finished
-    forward() call that did the routing itself."""
+    """View of the router logits [T, E] (float32, bias included) of a forward()
+    call that did the routing itself, valid until its workspace is used again."""
     desc, ws = out["desc"], out["workspace"]
     _need(not desc.flags & lib.MOE_FLAG_ROUTING_GIVEN, "the call was given its routing: it has no logits")
     at = lib.moe_get_workspace_regions(desc)["logits"]

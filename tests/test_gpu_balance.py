@@ -80,6 +80,9 @@ def _check(out, l, ids, alpha, off, mask, what=""):
     (65, 63, 4, 3, True), (130, 64, 6, 0, True), (257, 65, 16, 5, False), (300, 128, 8, 4, True), (77, 129, 3, 0, False),
     (1000, 256, 8, 7, True), (90, 257, 8, 2, True), (513, 512, 2, 0, False), (210, 515, 16, 3, True),
     (1500, 1024, 16, 4, True), (40, 1023, 5, 40, False), (900, 70, 3, 300, True), (5000, 16, 4, 64, True), (3, 4, 4, 0, False),
+    # one workgroup does it all (few tokens, at most 4 sequences), and the first that it does not
+    (60, 300, 8, 2, True), (64, 1024, 16, 3, False), (50, 515, 4, 0, True), (512, 128, 4, 2, True),
+    (513, 100, 4, 2, True), (400, 200, 4, 4, False),
 ])
 @pytest.mark.parametrize("grad", [True, False])
 def test_against_definition(gpu_lib, T, E, k, S, masked, grad):
@@ -282,3 +285,29 @@ def test_gradient_through_the_layers_backward(gpu_lib):
         assert err < 1e-3, (k, float(err))
     with pytest.raises(ValueError):
         L.backward(inp, fwd["topk_ids"], fwd["topk_weights"], dy, dlogits=aux[:, :5])
+
+
+def test_offsets_past_32_bits(gpu_lib):
+    """More than 2^31 logits: the gradient of rows at both ends from the counts
+    and the softmax of the rows themselves."""
+    from moe_layer_router_amd import layer as L
+    T, E, k = 2_200_000, 1000, 2
+    l = torch.empty(T, E, device="cuda")
+    l.normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    ids = torch.stack([torch.arange(T, device="cuda") ** 2 % E, torch.arange(T, device="cuda") % 7], 1).to(torch.int32)
+    out = L.balance_loss(l, ids, alpha=1.0)
+    torch.cuda.synchronize()
+    c = torch.bincount(ids.long().reshape(-1), minlength=E)
+    assert torch.equal(out["counts"][0].long(), c)
+    for t in (0, 1_000_003, T - 1):
+        p = torch.softmax(l[t].double(), 0)
+        h = (c - c[l[t].argmax()]).double()
+        ref = E / (k * float(T) ** 2) * p * (h - p @ h)
+        bound = E / (k * float(T) ** 2) * p * (h.abs() + p @ h.abs())
+        assert bool(((out["dlogits"][t].double() - ref).abs() <= 108 * U * bound + 2.0 ** -130).all()), t
+    mean = torch.zeros(E, dtype=torch.float64, device="cuda")
+    for i in range(0, T, 100_000):
+        mean += torch.softmax(l[i:i + 100_000].double(), 1).sum(0)
+    # sums over blocks of about T / 1024 tokens, then over the blocks: (28 + 40 + T / 1024 + 64) roundings
+    err = (out["probs"][0].double() - mean / T).abs() / (mean / T)
+    assert float(err.max()) <= (132 + T / 1024) * U

@@ -240,3 +240,40 @@ def test_wrapper_refusals(gpu_lib):
         L.layer_norm(x, g, want_stats=True, out=r)
     with pytest.raises(ValueError):
         L.layer_norm_backward(x, g, torch.zeros(3, device="cuda"), torch.zeros(4, device="cuda"), x)
+
+
+def test_offsets_past_32_bits(gpu_lib):
+    """More than 2^31 elements: the rows at both ends, forward and backward."""
+    from moe_layer_router_amd import layer as L
+    T, H = 300_000, 7680
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    x.normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    gamma = _vec(H, 1, 1.0)
+    r = L.layer_norm(x, gamma, out_dtype="bf16", want_stats=True)
+    b = L.layer_norm_backward(x, gamma, r["mean"], r["rstd"], x)
+    torch.cuda.synchronize()
+    some = [0, 1, 123_456, T - 2, T - 1]
+    xn = _np(x[some])
+    y, mean, rstd = R.layer_norm(xn, _np(gamma), None, 1e-5)
+    _check(_np(r["y"][some]), y, 1.01 * _y_bound(xn, _np(gamma), None, rstd, y) + 2.0 ** -8 * np.abs(y), "y")
+    m, s = _np(r["mean"][some]), _np(r["rstd"][some])
+    dx, _, _ = R.layer_norm_backward(xn, _np(gamma), m, s, xn)
+    z, g = (xn - m[:, None]) * s[:, None], xn * _np(gamma)
+    bound = C * U * s[:, None] * (np.abs(g) + np.abs(g).mean(1, keepdims=True) +
+                                  np.abs(z) * np.abs(g * z).mean(1, keepdims=True))
+    _check(_np(b["dx"][some]), dx, bound, "dx")
+    ref, mag = torch.zeros(H, dtype=torch.float64, device="cuda"), torch.zeros(H, dtype=torch.float64, device="cuda")
+    for i in range(0, T, 50_000):
+        c = x[i:i + 50_000].double()
+        ref += c.sum(0)
+        mag += c.abs().sum(0)
+    # a workgroup sums its T / 256 rows, then the workgroups' sums are joined
+    assert bool(((b["dbeta"].double() - ref).abs() <= (T / 256 + 64) * U * mag).all())
+
+
+def test_default_stream_by_handle(gpu_lib):
+    from moe_layer_router_amd import layer as L
+    x, gamma = _rows(9, 256, torch.bfloat16, 1), _vec(256, 1, 1.0)
+    a, b = L.layer_norm(x, gamma), L.layer_norm(x, gamma, stream=torch.cuda.default_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(a["y"], b["y"])

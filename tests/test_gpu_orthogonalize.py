@@ -201,3 +201,31 @@ def test_wrapper_refusals(gpu_lib):
               dict(u=u[:0])):
         with pytest.raises(lib.MoeError):
             L.orthogonalize(**{**dict(u=u), **b})
+
+
+@pytest.mark.parametrize("B,M,N", [(40_000, 1024, 60), (3, 16384, 20_000)])
+def test_offsets_past_32_bits(gpu_lib, B, M, N):
+    """Batches of narrow matrices, and of the largest, with elements past 2^31
+    (and bytes of one matrix past 2^29): narrow ones against the definition,
+    large ones by what they must be: U^T Y symmetric (same singular vectors) and Y's
+    singular values in the polynomial's range, on random vectors."""
+    from moe_layer_router_amd import layer as L
+    u = torch.empty(B, M, N, dtype=torch.bfloat16, device="cuda")
+    u.normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    y = L.orthogonalize(u)
+    torch.cuda.synchronize()
+    if M == 1024:
+        some = [0, 20_000, 35_000, B - 1]
+        _check(y[some], u[some])
+        return
+    g = torch.Generator(device="cuda").manual_seed(2)
+    for b in (0, B - 1):
+        v = torch.randn(M, 8, generator=g, device="cuda")
+        uf, yf = u[b].float(), y[b].float()
+        # all singular values between 0.6 and 1.3: |Y^T v| = |v| within that
+        ratio = (yf.t() @ v).norm(dim=0) / v.norm(dim=0)
+        assert float(ratio.min()) > 0.6 and float(ratio.max()) < 1.3
+        # Y U^T = V p(S) S V^T is symmetric
+        a, c = (yf @ (uf.t() @ v)), (uf @ (yf.t() @ v))
+        assert float((a - c).norm() / a.norm()) < 1e-2
+        del uf, yf

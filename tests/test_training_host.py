@@ -15,7 +15,7 @@ INVALID, UNSUPPORTED, SMALL = lib.MOE_ERR_INVALID_ARGUMENT, lib.MOE_ERR_UNSUPPOR
 
 
 def _norm(**over):
-    a = dict(T=4, H=256, i=BF, o=BF, mode=0, x=A, gamma=A, beta=A, eps=1e-5, y=A, ys=None, mean=A, rstd=A)
+    a = dict(T=4, H=256, i=BF, o=BF, mode=0, x=A, gamma=A, beta=A, eps=1e-5, y=2 * A, ys=None, mean=A, rstd=A)
     a.update(over)
     return lib._lib.moe_layer_norm(*a.values(), None)
 
@@ -26,6 +26,7 @@ def _norm(**over):
     (dict(o=FP8, ys=A, mode=7), INVALID), (dict(o=FP8), INVALID), (dict(ys=A), INVALID), (dict(eps=-1.0), INVALID),
     (dict(eps=float("nan")), INVALID), (dict(x=None), INVALID), (dict(gamma=None), INVALID), (dict(y=None), INVALID),
     (dict(beta=A + 4), INVALID), (dict(x=A + 2), INVALID), (dict(mean=None), INVALID), (dict(rstd=None), INVALID),
+    (dict(y=A), INVALID), (dict(y=A + 4 * 256 * 2 - 16), INVALID), (dict(y=A - 16), INVALID),
 ])
 def test_layer_norm_refusals(over, status):
     assert _norm(**over) == status
@@ -45,6 +46,8 @@ def _norm_bwd(**over):
     (dict(rstd=None), INVALID), (dict(dy=None), INVALID), (dict(dx=None), INVALID), (dict(dgamma=A + 8), INVALID),
     (dict(ws=None), INVALID), (dict(ws=None, dgamma=None), INVALID), (dict(nbytes=64), SMALL),
     (dict(o=BF, dx=A), INVALID),             # dx over a BF16 dy
+    (dict(x=4 * A, dx=A + 16), INVALID),     # dx over a part of an fp32 dy
+    (dict(dy=4 * A, dx=A), INVALID),         # dx over x
 ])
 def test_layer_norm_backward_refusals(over, status):
     assert _norm_bwd(**over) == status
@@ -63,7 +66,7 @@ def _balance(**over):
     (dict(E=1025), UNSUPPORTED), (dict(E=64, k=17), UNSUPPORTED), (dict(T=1 << 30), UNSUPPORTED),
     (dict(S=2), INVALID), (dict(S=(1 << 20) + 1, off=A), UNSUPPORTED), (dict(logits=None), INVALID),
     (dict(ids=None), INVALID), (dict(counts=None), INVALID), (dict(probs=None), INVALID), (dict(loss=None), INVALID),
-    (dict(loss=A + 4), INVALID), (dict(dlogits=A), INVALID), (dict(mask=A + 1), INVALID), (dict(ws=None), INVALID),
+    (dict(loss=A + 4), INVALID), (dict(dlogits=A), INVALID), (dict(dlogits=A + 16), INVALID), (dict(mask=A + 1), INVALID), (dict(ws=None), INVALID),
     (dict(nbytes=0), SMALL),
 ])
 def test_balance_loss_refusals(over, status):
