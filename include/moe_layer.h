@@ -496,8 +496,8 @@ moe_status moe_balance_loss(int32_t T, int32_t E, int32_t top_k, int32_t n_seq, 
  * exact iteration in the Frobenius norm, 1.7e-3 of it y's own rounding (default
  * coefficients, 5 steps).  1 <= M, N <= 32768, the smaller <= 16384, 1 <= batch <=
  * 65535, 1 <= steps <= 32, eps > 0; pointers (not coeffs) 16-byte aligned.
- * workspace: moe_orthogonalize_workspace_size bytes (about 10 bytes per
- * element of u, at most 8 GiB or one matrix's; 0 for sizes that are
+ * workspace: moe_orthogonalize_workspace_size bytes (5 to 9 per element of u
+ * and up to 128 MiB, at most 8 GiB or one matrix's; 0 for sizes that are
  * refused).  Enqueued on `stream`; errors as moe_forward. */
 size_t moe_orthogonalize_workspace_size(int32_t batch, int32_t M, int32_t N);
 moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dtype, const void* u, int32_t steps,

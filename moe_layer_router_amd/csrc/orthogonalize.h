@@ -22,11 +22,13 @@
 // Without lo it is up to 2e-2 off (small singular values are lost in the rounding
 // of the large ones), with BF16 products 1e-2 to 1.6e-1.
 //
-// Layout.  Rows and columns are padded with zeros to multiples of 64: hi, lo
-// [mp][np], A, B' = a I + B [mp][mp], and the transposed hi part ht [np][mp] (two,
-// read and written in turn), so that each of the three products has both
-// operands with contiguous K: X X^T from hi and hi, A A from A and A, B' X from
-// B' and ht.
+// Layout.  Rows and columns are padded with zeros to multiples of 64.  X is kept
+// transposed, hi (two, read and written in turn) and lo [np][mp], beside A and
+// B' = a I + B [mp][mp]: then A A from A and A and the step, X'^T = X^T B', from hi
+// and B' have both operands with contiguous K, and only X X^T has its K along the
+// columns, whose tiles are transposed as they are read from LDS.  (With a second
+// copy of X in the other orientation no product needs that, but a step then
+// stores it, 110 of its 600 us at 8 x 2048 x 7168.)
 //
 // Narrow matrices (m <= 64) go another way.  With G = X X^T and P = a + b G + c
 // G^2 a step is X' = P X, G' = P G P: the whole iteration runs on m x m
@@ -54,9 +56,8 @@ struct OrthArgs {
   int tall;                  // M > N: X is the transpose
   float eps;
   double* part;              // [batch][kOrthNormParts]
-  uint16_t* hi;              // [batch][mp][np]
+  uint16_t* hi;              // [batch][np][mp]
   uint8_t* lo;
-  uint16_t* ht;              // [batch][np][mp]
 };
 
 DEV uint32_t h_bits(float v) { return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v); }
@@ -114,8 +115,8 @@ __global__ void __launch_bounds__(256) k_orth_norm(OrthArgs a) {
   if (threadIdx.x == 0) a.part[(size_t)blockIdx.y * kOrthNormParts + blockIdx.x] = red[0];
 }
 
-// X_0 as hi, lo and ht, zeros in the padding: workgroup (x, y, b) does the
-// 64 x 64 tile (y, x) of U's padded matrix b.
+// X_0 as hi and lo, zeros in the padding: workgroup (x, y, b) does the 64 x 64
+// tile (y, x) of U's padded matrix b.
 template <int BF>
 __global__ void __launch_bounds__(256) k_orth_load(OrthArgs a) {
   static_assert(kOrthNormParts == 64, "one part per lane");
@@ -128,11 +129,12 @@ __global__ void __launch_bounds__(256) k_orth_load(OrthArgs a) {
   const double scd = (double)kOrthScale / (sqrt(ss) + (double)a.eps);
   const float sc = scd > 3e38 ? 3e38f : (float)scd;
   const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
-  const size_t ub = (size_t)blockIdx.z * a.M * a.N;
-  const int ldd = a.tall ? a.mp : a.np;      // U's padded row length
-  const size_t xb = (size_t)blockIdx.z * a.mp * a.np;
-  uint16_t* direct = a.tall ? a.ht : a.hi;   // in U's own orientation
-  auto lo_of = [](float v, float h) { return (uint8_t)f32_to_e4m3((v - h) * kOrthLoScale); };
+  const size_t ub = (size_t)blockIdx.z * a.M * a.N, xb = (size_t)blockIdx.z * a.mp * a.np;
+  auto put = [&](size_t o, float x) {
+    const uint32_t h = h_bits(x);
+    a.hi[o] = (uint16_t)h;
+    a.lo[o] = (uint8_t)f32_to_e4m3((x - h_val(h)) * kOrthLoScale);
+  };
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     float v[8];                              // eight rows' loads together
@@ -143,26 +145,15 @@ __global__ void __launch_bounds__(256) k_orth_load(OrthArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int k = ty + 4 * (8 * q + i), r = r0 + k, c = c0 + tx;
-      const float x = v[i] * sc;
-      tile[k][tx] = x;
-      const uint32_t h = h_bits(x);
-      const size_t o = xb + (size_t)r * ldd + c;
-      direct[o] = (uint16_t)h;
-      if (!a.tall) a.lo[o] = lo_of(x, h_val(h));
+      const int k = ty + 4 * (8 * q + i);
+      if (a.tall) put(xb + (size_t)(r0 + k) * a.mp + c0 + tx, v[i] * sc);
+      else tile[k][tx] = v[i] * sc;
     }
   }
+  if (a.tall) return;
   __syncthreads();
-  const int ldt = a.tall ? a.np : a.mp;
 #pragma unroll 4
-  for (int i = ty; i < 64; i += 4) {
-    const int r = r0 + tx, c = c0 + i;       // element (r, c) of U at row c of the transpose
-    const float x = tile[tx][i];
-    const uint32_t h = h_bits(x);
-    const size_t o = xb + (size_t)c * ldt + r;
-    (a.tall ? a.hi : a.ht)[o] = (uint16_t)h;
-    if (a.tall) a.lo[o] = lo_of(x, h_val(h));
-  }
+  for (int i = ty; i < 64; i += 4) put(xb + (size_t)(c0 + i) * a.mp + r0 + tx, tile[tx][i]);
 }
 
 // ------------------------------------------------------------------ products
@@ -170,10 +161,11 @@ enum { ORTH_GRAM = 0, ORTH_POLY = 1, ORTH_STEP = 2, ORTH_LAST = 3 };
 constexpr bool orth_sym(int mode) { return mode == ORTH_GRAM || mode == ORTH_POLY; }
 
 // C[i][j] = sum_k P[i][k] Q[j][k] for each matrix of a batch, P [rows][ld], Q
-// [cols][ld] FP16, K a multiple of 64, and what follows it:
+// [cols][ld] FP16 (GRAM: P = Q [K][ld], C[i][j] = sum_k P[k][i] Q[k][j]), K a
+// multiple of 64, and what follows it:
 //   GRAM   A = s C                                  (symmetric)
 //   POLY   B' = c0 I + c1 A + s C                   (symmetric)
-//   STEP   X' = C + c0 lo as hi, lo, ht
+//   STEP   X'^T = C + c0 lo as hi and lo
 //   LAST   the result: (C + c0 lo) / 2^12 as BF16 in U's orientation
 struct OrthGemm {
   const uint16_t* p;
@@ -182,16 +174,15 @@ struct OrthGemm {
   uint32_t p_bytes, q_bytes;           // of one matrix
   int ldp, ldq;
   int rows, cols, K;                   // padded sizes
-  int ti, tiles;                       // tiles of rows, tiles per matrix
+  int tj, tiles;                       // tiles of columns, tiles per matrix
   int full;                            // tiles (of the batch) worked on whole
   int split, rest;                     // the other `rest` tiles: parts along K of each
   float* part;                         // [rest][split][tile] sums of the parts
   float c0, c1, s;
   uint16_t* c;                         // GRAM: A; POLY: B'
   const uint16_t* a;                   // POLY: A
-  uint16_t* hi;
+  uint16_t* hi;                        // STEP: of X'
   uint8_t* lo;
-  uint16_t* ht;
   uint16_t* y;                         // LAST: [batch][M][N]
   int m, n, tall;
 };
@@ -230,51 +221,111 @@ DEV bool orth_tile(const OrthGemm& g, int t, int* mat, int* i0, int* j0) {
   if (orth_sym(MODE)) {
     orth_tri(l, &i, &j);
   } else {
-    i = l % g.ti;
-    j = l / g.ti;
+    i = l / g.tj;
+    j = l % g.tj;
   }
   *i0 = i * TL::kSide;
   *j0 = j * TL::kSide;
   return orth_sym(MODE) && i < j;
 }
 
+// X's tile in memory, by 32-bit offsets into a matrix's buffer (half the
+// registers of addresses): element offset of this lane's 4 rows x 8 columns, but
+// for i rows and 32 p columns.  What a wave has past the end of the matrix is
+// never stored, and read at the matrix's last rows and columns.
+template <class TL>
+DEV uint32_t orth_at(const OrthGemm& g, int i0, int j0, int w, int lane, int p) {
+  const int r0 = min(i0 + 64 * (w / TL::WN), g.rows - 64);
+  const int c0 = min(j0 + 16 * TL::NJ * (w % TL::WN) + 32 * p, g.cols - 32) - 32 * p;
+  return (uint32_t)(r0 + 4 * (lane & 15)) * (uint32_t)g.cols + (uint32_t)(c0 + 8 * (lane >> 4));
+}
+DEV uint32_t orth_row(const OrthGemm& g, int i, int p) { return (uint32_t)(i * g.cols + 32 * p); }
+template <typename T>
+DEV rsrc_t orth_rsrc(const OrthGemm& g, T* x, int mat) {
+  const size_t n = (size_t)g.rows * g.cols;
+  return make_rsrc(x + mat * n, (uint32_t)(n * sizeof(T)));
+}
+
 // The lo parts of the elements that orth_store finishes, read ahead of it.
 template <class TL, int MODE>
 DEV void orth_lo(const OrthGemm& g, int mat, int i0, int j0, int w, int lane, int p, v2u (&lq)[4]) {
   if (orth_sym(MODE)) return;
-  const int rb = i0 + 64 * (w / TL::WN) + 4 * (lane & 15);
-  const int c = j0 + 16 * TL::NJ * (w % TL::WN) + 32 * p + 8 * (lane >> 4);
+  const uint32_t o = orth_at<TL>(g, i0, j0, w, lane, p);
+  const rsrc_t lo = orth_rsrc(g, g.lo, mat);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    lq[i] = v2u{0u, 0u};
-    if (rb < g.rows && c < g.cols)
-      lq[i] = *reinterpret_cast<const v2u*>(g.lo + (size_t)mat * g.rows * g.cols + (size_t)(rb + i) * g.cols + c);
+  for (int i = 0; i < 4; ++i)
+    lq[i] = __builtin_bit_cast(v2u, __builtin_amdgcn_raw_buffer_load_b64(lo, (int)o, (int)orth_row(g, i, p), 0));
+}
+
+// GRAM: a wave's sums acc[i][j][v] are row 64 wm + 16 i + c16 and column 16 NJ wn +
+// 16 j + 4 gq + v of its tile.  Rows are stored in 8-byte pieces; for the mirror
+// image four lanes exchange their rows 16 i + (4 lanes) for four consecutive ones
+// each, and columns are stored in 8-byte pieces, 128 bytes at a time.
+DEV uint32_t quad_swap1(uint32_t v) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true); }
+DEV uint32_t quad_swap2(uint32_t v) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true); }
+template <class TL>
+DEV void orth_store_gram(const OrthGemm& g, int mat, int i0, int j0, bool mirror, int w, int lane, int p,
+                         const v4f (&acc)[4][2]) {
+  const int c16 = lane & 15, gq = lane >> 4;
+  const int r0 = i0 + 64 * (w / TL::WN), c0 = j0 + 16 * TL::NJ * (w % TL::WN) + 32 * p;
+  if (r0 >= g.rows || c0 >= g.cols) return;        // (as in orth_store)
+  uint16_t* a = g.c + (size_t)mat * g.rows * g.cols;
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    const int c = c0 + 16 * d + 4 * gq;
+    uint32_t x[4][2];                              // rows 16 i + c16, columns c + 2 h and c + 2 h + 1
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) x[i][h] = h_pack(g.s * acc[i][d][2 * h], g.s * acc[i][d][2 * h + 1]);
+      *reinterpret_cast<v2u*>(a + (size_t)(r0 + 16 * i + c16) * g.cols + c) = v2u{x[i][0], x[i][1]};
+    }
+    if (!mirror) continue;
+    const bool b0 = lane & 1, b1 = lane & 2;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // 4 x 4 transpose of (i, lane % 4): by bit 0, then by bit 1 of both
+      uint32_t y[4] = {x[0][h], x[1][h], x[2][h], x[3][h]};
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const uint32_t t = quad_swap1(b0 ? y[i] : y[i + 1]);
+        if (b0) y[i] = t; else y[i + 1] = t;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t t = quad_swap2(b1 ? y[i] : y[i + 2]);
+        if (b1) y[i] = t; else y[i + 2] = t;
+      }
+      // now rows 16 (lane % 4) + 4 (c16 / 4) + i
+      const int r = r0 + 16 * (lane & 3) + (c16 & 12);
+      *reinterpret_cast<v2u*>(a + (size_t)(c + 2 * h) * g.rows + r) =
+          v2u{__builtin_amdgcn_perm(y[1], y[0], 0x05040100), __builtin_amdgcn_perm(y[3], y[2], 0x05040100)};
+      *reinterpret_cast<v2u*>(a + (size_t)(c + 2 * h + 1) * g.rows + r) =
+          v2u{__builtin_amdgcn_perm(y[1], y[0], 0x07060302), __builtin_amdgcn_perm(y[3], y[2], 0x07060302)};
+    }
   }
 }
 
-// Stores of X': past the caches where there is more of it than they hold (the
-// large tiles), so that they leave the operands of the running products in the
-// L2 (8 x 2048 x 7168: 4795 -> 4680 us).
-template <class TL, typename T>
-DEV void orth_put(void* p, const T& v) {
-  if (TL::kSide >= 256) __builtin_nontemporal_store(v, static_cast<T*>(p));
-  else *static_cast<T*>(p) = v;
-}
-
-// A wave's sums acc[i][j][v] are row 64 wm + 4 c16 + i and column 16 NJ wn + 32
-// (j / 2) + 8 gq + 4 (j % 2) + v of its tile (the operands are brought to LDS in
-// that order).  A lane then holds 8 consecutive columns of a row and 4
-// consecutive rows of a column, and both orientations are stored straight
-// from registers: rows in 16-byte pieces, 64 bytes at a time, the transpose
-// in 8-byte pieces, 128 bytes at a time.  This stores the columns of j = 2 p
-// and 2 p + 1.
+// Else acc[i][j][v] is row 64 wm + 4 c16 + i and column 16 NJ wn + 32 (j / 2) + 8 gq +
+// 4 (j % 2) + v of the tile (the operands are brought to LDS in that order).  A
+// lane then holds 8 consecutive columns of a row and 4 consecutive rows of a
+// column, and both orientations are stored straight from registers: rows in
+// 16-byte pieces, 64 bytes at a time, columns (the mirror image, and a result
+// whose orientation is the other) in 8-byte pieces, 128 bytes at a time.  This
+// stores the columns of j = 2 p and 2 p + 1.  (With 64 columns alternating in the
+// same way a row of hi has 128 bytes in two stores and one of lo 64 in one:
+// slower, 4555 -> 4640 us for 8 x 2048 x 7168.)
 template <class TL, int MODE>
 DEV void orth_store(const OrthGemm& g, int mat, int i0, int j0, bool mirror, int w, int lane, int p,
                     const v4f (&acc)[4][2], const v2u (&lq)[4]) {
+  if (MODE == ORTH_GRAM) return orth_store_gram<TL>(g, mat, i0, j0, mirror, w, lane, p, acc);
   const int c16 = lane & 15, gq = lane >> 4;
-  const int rb = i0 + 64 * (w / TL::WN) + 4 * c16, c = j0 + 16 * TL::NJ * (w % TL::WN) + 32 * p + 8 * gq;
+  const int r0 = i0 + 64 * (w / TL::WN), c0 = j0 + 16 * TL::NJ * (w % TL::WN) + 32 * p;
+  if (r0 >= g.rows || c0 >= g.cols) return;        // (whole waves: rows and cols are multiples of 64)
+  const int rb = r0 + 4 * c16, c = c0 + 8 * gq;
+  const uint32_t x = orth_at<TL>(g, i0, j0, w, lane, p);
+  const rsrc_t hi_r = orth_rsrc(g, g.hi, mat), lo_r = orth_rsrc(g, g.lo, mat);
   const size_t sq = (size_t)mat * g.rows * g.cols, yb = (size_t)mat * g.m * g.n;
-  if (rb >= g.rows || c >= g.cols) return;         // (rows and cols are multiples of 64)
   float v[4][8];                                   // this lane's 4 rows x 8 columns
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -303,15 +354,15 @@ DEV void orth_store(const OrthGemm& g, int mat, int i0, int j0, bool mirror, int
       }
     }
     if (MODE == ORTH_LAST) {
-      if (!g.tall && rb + i < g.m) {
-        uint16_t* y = g.y + yb + (size_t)(rb + i) * g.n + c;
-        if (c + 8 <= g.n && g.n % 8 == 0) {        // (rows of y start on 16 bytes)
+      if (g.tall && rb + i < g.n) {
+        uint16_t* y = g.y + yb + (size_t)(rb + i) * g.m + c;
+        if (c + 8 <= g.m && g.m % 8 == 0) {        // (rows of y start on 16 bytes)
           st16(y, v4i{(int)bf16x2_rne(v[i][0], v[i][1]), (int)bf16x2_rne(v[i][2], v[i][3]),
                       (int)bf16x2_rne(v[i][4], v[i][5]), (int)bf16x2_rne(v[i][6], v[i][7])});
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (c + e < g.n) y[e] = (uint16_t)f32_to_bf16_rne(v[i][e]);
+            if (c + e < g.m) y[e] = (uint16_t)f32_to_bf16_rne(v[i][e]);
         }
       }
       continue;
@@ -327,28 +378,31 @@ DEV void orth_store(const OrthGemm& g, int mat, int i0, int j0, bool mirror, int
         l[e] = v[i][e] - (float)__builtin_bit_cast(v2h, word)[e & 1];
       }
       const v2s z = v2s{0, 0};
-      orth_put<TL>(g.hi + o, hw);
-      orth_put<TL>(g.lo + o, v2u{__builtin_bit_cast(uint32_t, lo_pack<true>(lo_pack<false>(z, l[0], l[1]), l[2], l[3])),
-                                 __builtin_bit_cast(uint32_t, lo_pack<true>(lo_pack<false>(z, l[4], l[5]), l[6], l[7]))});
+      const v2u lw = v2u{__builtin_bit_cast(uint32_t, lo_pack<true>(lo_pack<false>(z, l[0], l[1]), l[2], l[3])),
+                         __builtin_bit_cast(uint32_t, lo_pack<true>(lo_pack<false>(z, l[4], l[5]), l[6], l[7]))};
+      // past the caches where there is more of X' than they hold (the large
+      // tiles), so that it leaves the operands of the running products in the L2
+      constexpr int kAux = TL::kSide >= 256 ? 2 : 0;
+      __builtin_amdgcn_raw_buffer_store_b128(hw, hi_r, (int)(2 * x), (int)(2 * orth_row(g, i, p)), kAux);
+      __builtin_amdgcn_raw_buffer_store_b64(lw, lo_r, (int)x, (int)orth_row(g, i, p), kAux);
     }
   }
-  if (MODE == ORTH_STEP || mirror || (MODE == ORTH_LAST && g.tall)) {
+  if (mirror || (MODE == ORTH_LAST && !g.tall)) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       if (MODE == ORTH_LAST) {
-        if (c + e >= g.n) continue;
-        uint16_t* y = g.y + yb + (size_t)(c + e) * g.m + rb;
-        if (rb + 4 <= g.m && g.m % 4 == 0) {
+        if (c + e >= g.m) continue;
+        uint16_t* y = g.y + yb + (size_t)(c + e) * g.n + rb;
+        if (rb + 4 <= g.n && g.n % 4 == 0) {
           *reinterpret_cast<v2u*>(y) = v2u{bf16x2_rne(v[0][e], v[1][e]), bf16x2_rne(v[2][e], v[3][e])};
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (rb + i < g.m) y[i] = (uint16_t)f32_to_bf16_rne(v[i][e]);
+            if (rb + i < g.n) y[i] = (uint16_t)f32_to_bf16_rne(v[i][e]);
         }
       } else {
-        const v2u t = v2u{h_pack(v[0][e], v[1][e]), h_pack(v[2][e], v[3][e])};
-        if (orth_sym(MODE)) *reinterpret_cast<v2u*>(g.c + sq + (size_t)(c + e) * g.rows + rb) = t;
-        else orth_put<TL>(g.ht + sq + (size_t)(c + e) * g.rows + rb, t);
+        *reinterpret_cast<v2u*>(g.c + sq + (size_t)(c + e) * g.rows + rb) =
+            v2u{h_pack(v[0][e], v[1][e]), h_pack(v[2][e], v[3][e])};
       }
     }
   }
@@ -359,6 +413,24 @@ DEV void orth_store(const OrthGemm& g, int mat, int i0, int j0, bool mirror, int
 // 128 bytes (64 K), its 16-byte chunk c at c ^ ((row ^ row / 8) % 8), so that the
 // 16 rows of an operand read fall in distinct banks.
 DEV int orth_swz(int r) { return (r ^ (r >> 3)) & 7; }
+
+// GRAM's tiles: an LDS row is one K of the tile's kSide columns.  An operand is
+// read with the transposing load: lane l of 16 hands in the address of 8 bytes,
+// columns 4 (l % 4) .. + 3 of row l / 4, and gets the 4 rows of column l.  Its 32-byte
+// chunk c is at c ^ orth_swz_t(row), so that the rows of 32 lanes, 0 .. 3 and 8 .. 11
+// (or 4 more, 16 more), fall in distinct banks.
+typedef short v4s __attribute__((ext_vector_type(4)));
+template <class TL>
+DEV int orth_swz_t(int r) {
+  if (TL::kSide == 64) return ((r >> 1) & 1) | ((r >> 2) & 2);      // (two rows in the banks' 256 bytes)
+  return (r & 3) | ((r >> 1) & 4);
+}
+// (restrict: the compiler does not see which loads into LDS the barriers have
+// waited for, and would wait for all of them before each read)
+DEV v4s lds_tr16(const char* __restrict__ p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (__attribute__((address_space(3))) v4s*)(__attribute__((address_space(3))) char*)const_cast<char*>(p));
+}
 
 template <class TL, int MODE>
 __global__ void __launch_bounds__(TL::kThreads, 2) k_orth_gemm(OrthGemm g) {
@@ -372,7 +444,7 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_orth_gemm(OrthGemm g) {
   // tiles; the parts of the others follow
   const int per = (g.full + 7) / 8;
   int t, part = -1;
-  if ((int)blockIdx.x < 8 * per) {
+  if (!orth_sym(MODE) || (int)blockIdx.x < 8 * per) {
     t = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
     if (t >= g.full) return;
   } else {
@@ -382,20 +454,30 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_orth_gemm(OrthGemm g) {
   int mat, i0, j0;
   const bool mirror = orth_tile<TL, MODE>(g, t, &mat, &i0, &j0);
   int s0 = 0, s1 = g.K / 64;
-  if (part >= 0) {
+  if (orth_sym(MODE) && part >= 0) {
     const int ks = part % g.split, n = s1;
     s0 = (int)((long)ks * n / g.split);
     s1 = (int)((long)(ks + 1) * n / g.split);
   }
   const rsrc_t pr = make_rsrc(g.p + mat * g.p_stride, g.p_bytes), qr = make_rsrc(g.q + mat * g.q_stride, g.q_bytes);
 
-  // LDS row r of the P tile is row 64 (r / 64) + 4 (r % 16) + r / 16 % 4, of the
+  constexpr bool TR = MODE == ORTH_GRAM;
+  // (not GRAM:) LDS row r of the P tile is row 64 (r / 64) + 4 (r % 16) + r / 16 % 4, of the
   // Q tile column NC (r / NC) + 32 (j / 2) + 8 (x / 4) + 4 (j % 2) + x % 4 with NC
   // = 16 NJ, j = r % NC / 16, x = r % 16 (see orth_store)
   uint32_t poff[PP], qoff[PP];
 #pragma unroll
   for (int q = 0; q < PP; ++q) {
     const int r = 8 * (q * NW + w) + (lane >> 3), c = (lane & 7) ^ orth_swz(r);
+    if (TR) {
+      constexpr int kRow = TL::kSide * 2;          // bytes of a K
+      const int o = (q * NW + w) * 1024 + lane * 16, k = o / kRow;
+      const int col = 8 * ((o % kRow / 16) ^ (orth_swz_t<TL>(k) << 1));
+      // (columns past the end are never stored: the last ones again)
+      poff[q] = ((uint32_t)k * g.ldp + min(i0 + col, g.rows - 8)) * 2;
+      qoff[q] = ((uint32_t)k * g.ldq + min(j0 + col, g.cols - 8)) * 2;
+      continue;
+    }
     poff[q] = (uint32_t)(i0 + (r & ~63) + 4 * (r & 15) + ((r >> 4) & 3)) * (uint32_t)g.ldp * 2 + 16 * c;
     const int x = r & 15, j = r % (16 * NJ) / 16;
     const int col = r / (16 * NJ) * (16 * NJ) + 32 * (j >> 1) + 8 * (x >> 2) + 4 * (j & 1) + (x & 3);
@@ -403,7 +485,8 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_orth_gemm(OrthGemm g) {
   }
   auto load = [&](int s, int stage) {
     char* st = lds + stage * TL::kStage;
-    const uint32_t k = (uint32_t)min(s, s1 - 1) * 128;         // (past the end: the last step again, never read)
+    // (past the end: the last step again, never read)
+    const uint32_t k = (uint32_t)min(s, s1 - 1) * 128 * (TR ? (uint32_t)g.ldp : 1u);
 #pragma unroll
     for (int q = 0; q < PP; ++q) {
       buf_ld16_lds(pr, st + (q * NW + w) * 1024, poff[q], k);
@@ -419,6 +502,12 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_orth_gemm(OrthGemm g) {
   // operand reads: chunk 4 kh + gq of row r0 + 16 i + c16 (r0: the wave's first)
   const int pr0 = 64 * wm, qr0 = 16 * NJ * wn;
   auto frag = [&](const char* op, int r0, int i, int kh) {
+    if (TR) {                                      // K 32 kh + 8 gq + 0 .. 7 of column r0 + 16 i + c16
+      const int k = 32 * kh + 8 * gq + (c16 >> 2), c = (r0 >> 4) + i;
+      const char* a = op + k * (TL::kSide * 2) + ((c ^ orth_swz_t<TL>(k)) << 5) + 8 * (lane & 3);
+      const v4s x0 = lds_tr16(a), x1 = lds_tr16(a + 4 * TL::kSide * 2);
+      return __builtin_bit_cast(v8h, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
     return lds_ld<v8h>(op, (uint32_t)(r0 + 16 * i + c16) * 128 + (((4 * kh + gq) ^ orth_swz(r0 + 16 * i + c16)) << 4));
   };
   // Every step's first operands are read during the last products of the step
@@ -478,19 +567,18 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_orth_gemm(OrthGemm g) {
 #pragma unroll
     for (int j = 0; j < NL; ++j) asm volatile("" : "+v"(qf[j]));
   }
-  // the first half of what is stored below reads its lo parts during the last
-  // step, the second (the operands' registers are free then) during the first
-  constexpr int NP = NJ / 2, NE = NP > 1 ? NP / 2 : 1;
-  v2u lq[NP][4];
+  // (lo is read during the last step)
+  constexpr int NP = NJ / 2;
+  v2u lq[NP][4] = {};
 #pragma unroll
-  for (int p = 0; p < NE; ++p) orth_lo<TL, MODE>(g, mat, i0, j0, w, lane, p, lq[p]);
+  for (int p = 0; p < NP; ++p) orth_lo<TL, MODE>(g, mat, i0, j0, w, lane, p, lq[p]);
   halves(lds + stage * TL::kStage);
 #pragma unroll
   for (int j = NJ - NL; j < NJ; ++j) mul(j);
-#pragma unroll
-  for (int p = NE; p < NP; ++p) orth_lo<TL, MODE>(g, mat, i0, j0, w, lane, p, lq[p]);
-  wait_vmcnt<0>();                                 // no load into LDS outlives the workgroup
-  if (part >= 0) {
+  __builtin_amdgcn_sched_barrier(0);               // (the operands' registers are free below)
+  // no load into LDS outlives the workgroup (they are older than those of lo)
+  wait_vmcnt<orth_sym(MODE) ? 0 : 4 * NP>();
+  if (orth_sym(MODE) && part >= 0) {
     v4f* dst = reinterpret_cast<v4f*>(g.part + (size_t)part * TL::kPart) + (size_t)w * 4 * NJ * 64 + lane;
 #pragma unroll
     for (int i = 0; i < 4; ++i)

@@ -183,7 +183,7 @@ size_t orth_part_bytes(int batch, int mp, int np) {
 
 struct OrthLayout {
   int m, n, mp, np, chunk;           // short and long side, padded; matrices worked on together
-  size_t part, hi, lo, ht0, ht1, a, b, sums, total;
+  size_t part, hi0, hi1, lo, a, b, sums, total;
   int sq, slabs;                     // narrow matrices: padded side, partial Gram matrices
   size_t q;
 };
@@ -208,14 +208,13 @@ OrthLayout orth_layout(int batch, int M, int N) {
   // fills the GPU
   const size_t sums = std::max({orth_part_bytes<OrthBig>(batch, L.mp, L.np), orth_part_bytes<OrthMid>(batch, L.mp, L.np),
                                 orth_part_bytes<OrthSmall>(batch, L.mp, L.np)});
-  L.chunk = (int)std::min((size_t)batch, std::max((size_t)1, (kOrthChunkBytes - sums) / (3 * x + x / 2 + 2 * q)));
+  L.chunk = (int)std::min((size_t)batch, std::max((size_t)1, (kOrthChunkBytes - sums) / (2 * x + x / 2 + 2 * q)));
   const size_t c = L.chunk;
   size_t o = 0;
   L.part = o; o = align256(o + c * kOrthNormParts * 8);
-  L.hi = o; o = align256(o + c * x);
+  L.hi0 = o; o = align256(o + c * x);
+  L.hi1 = o; o = align256(o + c * x);
   L.lo = o; o = align256(o + c * x / 2);
-  L.ht0 = o; o = align256(o + c * x);
-  L.ht1 = o; o = align256(o + c * x);
   L.a = o; o = align256(o + c * q);
   L.b = o; o = align256(o + c * q);
   L.sums = o; o = align256(o + sums);
@@ -254,9 +253,9 @@ bool orth_in_range(int steps, const float* co) {
 // Tiles of a product, and how many of them are worked on in parts.
 template <class TL, int MODE>
 moe_status launch_orth_gemm(OrthGemm g, int batch, int cus, hipStream_t st) {
-  g.ti = (g.rows + TL::kSide - 1) / TL::kSide;
-  const int tj = (g.cols + TL::kSide - 1) / TL::kSide;
-  g.tiles = orth_sym(MODE) ? tj * (tj + 1) / 2 : g.ti * tj;
+  const int ti = (g.rows + TL::kSide - 1) / TL::kSide;
+  g.tj = (g.cols + TL::kSide - 1) / TL::kSide;
+  g.tiles = orth_sym(MODE) ? ti * (ti + 1) / 2 : ti * g.tj;
   const int total = g.tiles * batch, slots = cus * (160 * 1024 / TL::kLds);
   g.full = total;
   g.split = 1;
@@ -490,10 +489,9 @@ moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dty
     a.tall = M > N;
     a.eps = eps;
     a.part = reinterpret_cast<double*>(ws + L.part);
-    a.hi = reinterpret_cast<uint16_t*>(ws + L.hi);
+    uint16_t* hi[2] = {reinterpret_cast<uint16_t*>(ws + L.hi0), reinterpret_cast<uint16_t*>(ws + L.hi1)};
+    a.hi = hi[0];
     a.lo = reinterpret_cast<uint8_t*>(ws + L.lo);
-    uint16_t* ht[2] = {reinterpret_cast<uint16_t*>(ws + L.ht0), reinterpret_cast<uint16_t*>(ws + L.ht1)};
-    a.ht = ht[0];
     const dim3 norm_grid(kOrthNormParts, nb);
     const dim3 load_grid((a.tall ? L.mp : L.np) / 64, (a.tall ? L.np : L.mp) / 64, nb);
     if (bf) hipLaunchKernelGGL(k_orth_norm<1>, norm_grid, dim3(256), 0, st, a);
@@ -509,12 +507,12 @@ moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dty
       const float* co = coeffs ? coeffs + 3 * k : kOrthCoeffs;
       OrthGemm g{};
       g.part = reinterpret_cast<float*>(ws + L.sums);
-      g.hi = a.hi; g.lo = a.lo; g.m = L.m; g.n = L.n; g.tall = a.tall;
+      g.lo = a.lo; g.m = L.m; g.n = L.n; g.tall = a.tall;
       // A = X X^T: 2^24 times it in the accumulators, 2^12 in A
-      g.p = g.q = a.hi;
+      g.p = g.q = hi[k & 1];
       g.p_stride = g.q_stride = xs;
       g.p_bytes = g.q_bytes = (uint32_t)(xs * 2);
-      g.ldp = g.ldq = L.np;
+      g.ldp = g.ldq = L.mp;
       g.rows = g.cols = L.mp;
       g.K = L.np;
       g.s = 1.0f / kOrthScale;
@@ -524,7 +522,6 @@ moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dty
       g.p = g.q = A;
       g.p_stride = g.q_stride = qs;
       g.p_bytes = g.q_bytes = (uint32_t)(qs * 2);
-      g.ldp = g.ldq = L.mp;
       g.K = L.mp;
       g.a = A;
       g.c = B;
@@ -532,13 +529,13 @@ moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dty
       g.c1 = co[1] / kOrthScale;
       g.s = co[2] / (kOrthScale * kOrthScale);
       TRY((launch_orth_gemm<ORTH_POLY>(g, nb, di.cus, st)));
-      // X' = B' hi + a lo
-      g.p = B;
-      g.q = ht[k & 1];
-      g.q_stride = xs;
-      g.q_bytes = (uint32_t)(xs * 2);
-      g.cols = L.np;
-      g.ht = ht[(k + 1) & 1];
+      // X'^T = hi B' + a lo
+      g.p = hi[k & 1];
+      g.q = B;
+      g.p_stride = xs;
+      g.p_bytes = (uint32_t)(xs * 2);
+      g.rows = L.np;
+      g.hi = hi[(k + 1) & 1];
       g.y = static_cast<uint16_t*>(y) + (size_t)b0 * elems;
       if (k + 1 < steps) TRY((launch_orth_gemm<ORTH_STEP>(g, nb, di.cus, st)));
       else TRY((launch_orth_gemm<ORTH_LAST>(g, nb, di.cus, st)));
