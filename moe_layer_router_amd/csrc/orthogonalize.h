@@ -661,135 +661,173 @@ DEV float orth_x(const OrthNarrow& a, size_t base, int i, int j) {
   return orth_ld<BF>(a.u, base + (a.tall ? (size_t)j * a.m + i : (size_t)i * a.n + j));
 }
 
-// Workgroup (slab, b): the slab's share of U U^T (U^T U if tall) in fp64; 16 x
-// 16 threads, R x R elements each.
+// Products of the narrow path, by fp64 matrix instructions (16 x 16 x 4): the
+// MP x MP result in 16 x 16 tiles, kSide x kSide of them per wave; with MP = 16
+// only the first of the four waves has one.
+typedef double v4d __attribute__((ext_vector_type(4)));
+template <int MP>
+struct OrthF64 {
+  static constexpr int kSide = MP == 64 ? 2 : 1, kWaves = MP / 16 / kSide;      // waves per side
+  v4d acc[kSide][kSide];
+  int i0, j0, r, kk;                   // the wave's first row and column; this lane's row or column of a tile, and its K
+  bool on;
+  DEV void init() {
+    const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    on = w < kWaves * kWaves;
+    i0 = 16 * kSide * (w / kWaves);
+    j0 = 16 * kSide * (w % kWaves);
+    r = lane & 15;
+    kk = lane >> 4;
+    zero();
+  }
+  DEV void zero() {
+#pragma unroll
+    for (int a = 0; a < kSide; ++a)
+#pragma unroll
+      for (int b = 0; b < kSide; ++b) acc[a][b] = v4d{0, 0, 0, 0};
+  }
+  // acc += p q^T over four K: element (i, k) of p at p[i * si + k * sk], and so q
+  DEV void mul4(const double* p, const double* q, int si, int sk) {
+    double pv[kSide], qv[kSide];
+#pragma unroll
+    for (int a = 0; a < kSide; ++a) {
+      pv[a] = p[(i0 + 16 * a + r) * si + kk * sk];
+      qv[a] = q[(j0 + 16 * a + r) * si + kk * sk];
+    }
+#pragma unroll
+    for (int a = 0; a < kSide; ++a)
+#pragma unroll
+      for (int b = 0; b < kSide; ++b) acc[a][b] = __builtin_amdgcn_mfma_f64_16x16x4f64(pv[a], qv[b], acc[a][b], 0, 0, 0);
+  }
+  // f(row, column, element) for each element of this lane
+  template <class F>
+  DEV void each(F&& f) {
+    if (!on) return;
+#pragma unroll
+    for (int a = 0; a < kSide; ++a)
+#pragma unroll
+      for (int b = 0; b < kSide; ++b)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          double x = acc[a][b][v];
+          f(i0 + 16 * a + kk + 4 * v, j0 + 16 * b + r, x);
+          acc[a][b][v] = x;
+        }
+  }
+};
+
+// Workgroup (slab, b): the slab's share of U U^T (U^T U if tall) in fp64, in
+// passes of kOrthSlabCols columns, the next of which is read during a pass.
+// (Rows of a pass in LDS are 17 doubles past a multiple of the 32 that the
+// banks hold: neither the writes along a column nor the reads along a row
+// collide, but for one.)
 template <int BF, int MP>
 __global__ void __launch_bounds__(256) k_orth_gram64(OrthNarrow a) {
-  constexpr int R = MP / 16, KC = kOrthSlabCols;
-  __shared__ double xs[KC][MP + 1];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  constexpr int KC = kOrthSlabCols, LD = MP == 16 ? 17 : MP + 17, NE = KC * MP / 256;
+  __shared__ double xs[KC * LD];
   const int per = (a.n + a.slabs - 1) / a.slabs, j0 = blockIdx.x * per, j1 = min(a.n, j0 + per);
   const size_t base = (size_t)blockIdx.y * a.m * a.n;
-  double acc[R][R];
+  OrthF64<MP> t;
+  t.init();
+  float next[NE];
+  auto at = [&](int e, int* i, int* c) {           // (memory order: along i if tall, else along j)
+    *i = a.tall ? e % MP : e / KC;
+    *c = a.tall ? e / MP : e % KC;
+  };
+  auto load = [&](int jb) {
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int c = 0; c < R; ++c) acc[r][c] = 0;
+    for (int x = 0; x < NE; ++x) {
+      int i, c;
+      at(threadIdx.x + 256 * x, &i, &c);
+      next[x] = i < a.m && jb + c < j1 ? orth_x<BF>(a, base, i, jb + c) : 0.f;
+    }
+  };
+  load(j0);
   for (int jb = j0; jb < j1; jb += KC) {
-    for (int e = threadIdx.x; e < KC * MP; e += 256) {        // (memory order: along i if tall, else along j)
-      const int i = a.tall ? e % MP : e / KC, c = a.tall ? e / MP : e % KC;
-      xs[c][i] = i < a.m && jb + c < j1 ? (double)orth_x<BF>(a, base, i, jb + c) : 0.0;
+#pragma unroll
+    for (int x = 0; x < NE; ++x) {
+      int i, c;
+      at(threadIdx.x + 256 * x, &i, &c);
+      xs[c * LD + i] = (double)next[x];
     }
     __syncthreads();
-#pragma unroll 4
-    for (int c = 0; c < KC; ++c) {
-      double p[R], q[R];
+    load(jb + KC);
+    if (t.on) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        p[r] = xs[c][ty * R + r];
-        q[r] = xs[c][tx + 16 * r];
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int s = 0; s < R; ++s) acc[r][s] = __builtin_fma(p[r], q[s], acc[r][s]);
+      for (int c = 0; c < KC; c += 4) t.mul4(xs + c * LD, xs + c * LD, 1, LD);
     }
     __syncthreads();
   }
   double* out = a.part + ((size_t)blockIdx.y * a.slabs + blockIdx.x) * MP * MP;
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int s = 0; s < R; ++s) out[(ty * R + r) * MP + tx + 16 * s] = acc[r][s];
+  t.each([&](int i, int j, double& v) { out[i * MP + j] = v; });
 }
 
-// LDS matrices of the iteration: [MP][MP + 1] doubles.
+// LDS matrices of the iteration: [MP][MP + 2] doubles (a wave's reads down 16
+// rows fall in distinct banks).
 template <int MP>
 struct OrthSq {
-  static constexpr int kLd = MP + 1, kSize = MP * kLd;
+  static constexpr int kLd = MP + 2, kSize = MP * kLd;
   static constexpr int kLds = 4 * kSize * 8;
 };
-// This thread's R x R elements of p q.
-template <int MP, int R>
-DEV void orth_mul64(const double* p, const double* q, int tx, int ty, double (&acc)[R][R]) {
-  constexpr int LD = OrthSq<MP>::kLd;
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int c = 0; c < R; ++c) acc[r][c] = 0;
-#pragma unroll 4
-  for (int k = 0; k < MP; ++k) {
-    double pv[R], qv[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      pv[r] = p[(ty * R + r) * LD + k];
-      qv[r] = q[k * LD + tx + 16 * r];
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int c = 0; c < R; ++c) acc[r][c] = __builtin_fma(pv[r], qv[c], acc[r][c]);
-  }
-}
 
 // One workgroup per matrix: G from its slabs, the norm from G's trace, the
-// steps, and Q.
+// steps, and Q.  G, P and Q are polynomials of the first G, so symmetric, and
+// they commute: every product is formed as p q^T.
 template <int MP>
 __global__ void __launch_bounds__(256) k_orth_iter64(OrthNarrow a) {
-  constexpr int R = MP / 16, LD = OrthSq<MP>::kLd;
+  constexpr int LD = OrthSq<MP>::kLd;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   double* G = reinterpret_cast<double*>(lds);
   double* P = G + OrthSq<MP>::kSize;
   double* Q = P + OrthSq<MP>::kSize;
   double* T = Q + OrthSq<MP>::kSize;
   __shared__ double s_inv;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const double* part = a.part + (size_t)blockIdx.x * a.slabs * MP * MP;
   for (int e = threadIdx.x; e < MP * MP; e += 256) {
     double s = 0;
+#pragma unroll 8
     for (int p = 0; p < a.slabs; ++p) s += part[(size_t)p * MP * MP + e];
     G[e / MP * LD + e % MP] = s;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double tr = 0;
-    for (int i = 0; i < MP; ++i) tr += G[i * LD + i];
-    s_inv = 1.0 / (sqrt(tr) + (double)a.eps);
+  if (threadIdx.x < 64) {
+    double tr = (int)threadIdx.x < MP ? G[threadIdx.x * (LD + 1)] : 0.0;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) tr += __shfl_xor(tr, d);
+    if (threadIdx.x == 0) s_inv = 1.0 / (sqrt(tr) + (double)a.eps);
   }
   __syncthreads();
   const double inv = s_inv, inv2 = inv * inv;
   for (int e = threadIdx.x; e < MP * MP; e += 256) G[e / MP * LD + e % MP] *= inv2;
   __syncthreads();
-  double acc[R][R];
+  OrthF64<MP> t;
+  t.init();
+  auto mul = [&](const double* p, const double* q) {
+    t.zero();
+    if (!t.on) return;
+#pragma unroll 4
+    for (int k = 0; k < MP; k += 4) t.mul4(p + k, q + k, LD, 1);
+  };
   auto put = [&](double* dst) {
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int c = 0; c < R; ++c) dst[(ty * R + r) * LD + tx + 16 * c] = acc[r][c];
+    t.each([&](int i, int j, double& v) { dst[i * LD + j] = v; });
   };
   for (int k = 0; k < a.steps; ++k) {
     const double ca = a.co[k][0], cb = a.co[k][1], cc = a.co[k][2];
-    orth_mul64<MP, R>(G, G, tx, ty, acc);
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int c = 0; c < R; ++c) {
-        const int i = ty * R + r, j = tx + 16 * c;
-        acc[r][c] = cc * acc[r][c] + cb * G[i * LD + j] + (i == j ? ca : 0.0);
-      }
+    mul(G, G);
+    t.each([&](int i, int j, double& v) { v = cc * v + cb * G[i * LD + j] + (i == j ? ca : 0.0); });
     put(P);
     if (k == 0) put(Q);
     __syncthreads();
     if (k > 0) {
-      orth_mul64<MP, R>(P, Q, tx, ty, acc);
+      mul(P, Q);
       __syncthreads();
       put(Q);
     }
     if (k + 1 < a.steps) {
-      orth_mul64<MP, R>(P, G, tx, ty, acc);
+      mul(P, G);
       put(T);
       __syncthreads();
-      orth_mul64<MP, R>(T, P, tx, ty, acc);
+      mul(T, P);
       put(G);
     }
     __syncthreads();
