@@ -28,6 +28,11 @@
 // in a fixed order (the only atomics count finished workgroups and add
 // integers in LDS).
 //
+// Measured: T = 16384, E = 1024, k = 16, 13 sequences, masked (134 MB): 10.5 + 32 +
+// 9.2 us, the middle kernel at 4.2 TB/s; T = 8192, E = 256, k = 8 (17 MB): 6.8 +
+// 9.5 + 6.0 us, of which 3.3 is the traffic and the rest launches and the chains
+// of dependent loads in them; T = 64, E = 8: 8 us in one launch.
+//
 // Sequence offsets are device data: each is clamped to [0, T], and a
 // sequence that ends before it begins is empty.  With offsets that descend
 // the results are unspecified, but every access stays in range.

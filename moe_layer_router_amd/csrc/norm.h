@@ -13,6 +13,11 @@
 // and chunk, R chunks), so it is read once and the variance is the sum of
 // squared differences from the row's own mean, not a difference of sums.
 // Every sum is fp32.
+//
+// Measured (T = 8192, H = 7168): forward BF16 -> BF16 41 to 45 us (5.2 to 5.7 TB/s; a
+// large copy reaches 5.2), to FP8 53 us (3.3 TB/s, the conversions), backward of
+// BF16 x and fp32 dy with the weight gradients 111 + 5 us (5.2 TB/s).  One token:
+// 3.3 us, a launch.
 #pragma once
 #include "device_common.h"
 #include "quant.h"

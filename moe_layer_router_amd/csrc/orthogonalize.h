@@ -34,10 +34,20 @@
 // G^2 a step is X' = P X, G' = P G P: the whole iteration runs on m x m
 // matrices, and y = Q X_0 with Q the product of the P.  G squares the
 // spread of the singular values, which fp64 carries (its products are cheap
-// at this size, 17 of m x m); the matrix itself is read twice and written
-// once, in three launches.  It is also the accurate way for them: a matrix of
+// at this size, 17 of m x m on the fp64 matrix cores); the matrix itself is read
+// twice and written once, in three launches.  It is also the accurate way for them: a matrix of
 // few rows does not average the roundings of FP16 products (up to 1e-2 at m
 // <= 8, below 2.3e-3 from m = 64 on).
+//
+// Measured (5 steps).  Large matrices are bound by the matrix cores: 8 x 2048 x
+// 7168 takes 4.45 ms, 887 TFLOP/s, where one large FP16 library product reaches
+// 1390: norm 95 us (4.9 TB/s), load 140 (5.9), then per step X X^T 240 + 13 (its
+// parts), the polynomial 88 + 14, the step 550 (the last 485).  A step's products
+// alone take 380 us; its tile ends, where the one workgroup of a CU stores and
+// multiplies nothing, the rest.  Small ones are bound by their 17 to 22 dependent
+// launches of 4 to 6 us: 8 x 256 x 256 75 us, 256 x 7168 131 us.  Narrow: 16 x 64 x
+// 7168 24 + 52 + 33 us, bound by fp64 (its 17 products on one CU each take 2 us at
+// the peak rate, 3 here).
 #pragma once
 #include "device_common.h"
 #include "norm.h"
@@ -662,57 +672,50 @@ DEV float orth_x(const OrthNarrow& a, size_t base, int i, int j) {
 }
 
 // Products of the narrow path, by fp64 matrix instructions (16 x 16 x 4): the
-// MP x MP result in 16 x 16 tiles, kSide x kSide of them per wave; with MP = 16
-// only the first of the four waves has one.
+// MP x MP result in 16 x 16 tiles, 1 x kB of them per wave, of the workgroup's
+// kThreads / 64 waves the first kWi x kWj.
 typedef double v4d __attribute__((ext_vector_type(4)));
 template <int MP>
 struct OrthF64 {
-  static constexpr int kSide = MP == 64 ? 2 : 1, kWaves = MP / 16 / kSide;      // waves per side
-  v4d acc[kSide][kSide];
+  static constexpr int kB = MP == 64 ? 2 : 1, kWi = MP / 16, kWj = MP / 16 / kB;
+  static constexpr int kThreads = kWi * kWj < 4 ? 256 : 64 * kWi * kWj;
+  v4d acc[kB];
   int i0, j0, r, kk;                   // the wave's first row and column; this lane's row or column of a tile, and its K
   bool on;
   DEV void init() {
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    on = w < kWaves * kWaves;
-    i0 = 16 * kSide * (w / kWaves);
-    j0 = 16 * kSide * (w % kWaves);
+    on = w < kWi * kWj;
+    i0 = 16 * (w / kWj);
+    j0 = 16 * kB * (w % kWj);
     r = lane & 15;
     kk = lane >> 4;
     zero();
   }
   DEV void zero() {
 #pragma unroll
-    for (int a = 0; a < kSide; ++a)
-#pragma unroll
-      for (int b = 0; b < kSide; ++b) acc[a][b] = v4d{0, 0, 0, 0};
+    for (int b = 0; b < kB; ++b) acc[b] = v4d{0, 0, 0, 0};
   }
   // acc += p q^T over four K: element (i, k) of p at p[i * si + k * sk], and so q
   DEV void mul4(const double* p, const double* q, int si, int sk) {
-    double pv[kSide], qv[kSide];
+    const double pv = p[(i0 + r) * si + kk * sk];
+    double qv[kB];
 #pragma unroll
-    for (int a = 0; a < kSide; ++a) {
-      pv[a] = p[(i0 + 16 * a + r) * si + kk * sk];
-      qv[a] = q[(j0 + 16 * a + r) * si + kk * sk];
-    }
+    for (int b = 0; b < kB; ++b) qv[b] = q[(j0 + 16 * b + r) * si + kk * sk];
 #pragma unroll
-    for (int a = 0; a < kSide; ++a)
-#pragma unroll
-      for (int b = 0; b < kSide; ++b) acc[a][b] = __builtin_amdgcn_mfma_f64_16x16x4f64(pv[a], qv[b], acc[a][b], 0, 0, 0);
+    for (int b = 0; b < kB; ++b) acc[b] = __builtin_amdgcn_mfma_f64_16x16x4f64(pv, qv[b], acc[b], 0, 0, 0);
   }
   // f(row, column, element) for each element of this lane
   template <class F>
   DEV void each(F&& f) {
     if (!on) return;
 #pragma unroll
-    for (int a = 0; a < kSide; ++a)
+    for (int b = 0; b < kB; ++b)
 #pragma unroll
-      for (int b = 0; b < kSide; ++b)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          double x = acc[a][b][v];
-          f(i0 + 16 * a + kk + 4 * v, j0 + 16 * b + r, x);
-          acc[a][b][v] = x;
-        }
+      for (int v = 0; v < 4; ++v) {
+        double x = acc[b][v];
+        f(i0 + kk + 4 * v, j0 + 16 * b + r, x);
+        acc[b][v] = x;
+      }
   }
 };
 
@@ -722,8 +725,9 @@ struct OrthF64 {
 // banks hold: neither the writes along a column nor the reads along a row
 // collide, but for one.)
 template <int BF, int MP>
-__global__ void __launch_bounds__(256) k_orth_gram64(OrthNarrow a) {
-  constexpr int KC = kOrthSlabCols, LD = MP == 16 ? 17 : MP + 17, NE = KC * MP / 256;
+__global__ void __launch_bounds__(OrthF64<MP>::kThreads) k_orth_gram64(OrthNarrow a) {
+  constexpr int NT = OrthF64<MP>::kThreads;
+  constexpr int KC = kOrthSlabCols, LD = MP == 16 ? 17 : MP + 17, NE = KC * MP / NT;
   __shared__ double xs[KC * LD];
   const int per = (a.n + a.slabs - 1) / a.slabs, j0 = blockIdx.x * per, j1 = min(a.n, j0 + per);
   const size_t base = (size_t)blockIdx.y * a.m * a.n;
@@ -738,7 +742,7 @@ __global__ void __launch_bounds__(256) k_orth_gram64(OrthNarrow a) {
 #pragma unroll
     for (int x = 0; x < NE; ++x) {
       int i, c;
-      at(threadIdx.x + 256 * x, &i, &c);
+      at(threadIdx.x + NT * x, &i, &c);
       next[x] = i < a.m && jb + c < j1 ? orth_x<BF>(a, base, i, jb + c) : 0.f;
     }
   };
@@ -747,7 +751,7 @@ __global__ void __launch_bounds__(256) k_orth_gram64(OrthNarrow a) {
 #pragma unroll
     for (int x = 0; x < NE; ++x) {
       int i, c;
-      at(threadIdx.x + 256 * x, &i, &c);
+      at(threadIdx.x + NT * x, &i, &c);
       xs[c * LD + i] = (double)next[x];
     }
     __syncthreads();
@@ -774,8 +778,8 @@ struct OrthSq {
 // steps, and Q.  G, P and Q are polynomials of the first G, so symmetric, and
 // they commute: every product is formed as p q^T.
 template <int MP>
-__global__ void __launch_bounds__(256) k_orth_iter64(OrthNarrow a) {
-  constexpr int LD = OrthSq<MP>::kLd;
+__global__ void __launch_bounds__(OrthF64<MP>::kThreads) k_orth_iter64(OrthNarrow a) {
+  constexpr int LD = OrthSq<MP>::kLd, NT = OrthF64<MP>::kThreads;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   double* G = reinterpret_cast<double*>(lds);
   double* P = G + OrthSq<MP>::kSize;
@@ -783,7 +787,7 @@ __global__ void __launch_bounds__(256) k_orth_iter64(OrthNarrow a) {
   double* T = Q + OrthSq<MP>::kSize;
   __shared__ double s_inv;
   const double* part = a.part + (size_t)blockIdx.x * a.slabs * MP * MP;
-  for (int e = threadIdx.x; e < MP * MP; e += 256) {
+  for (int e = threadIdx.x; e < MP * MP; e += NT) {
     double s = 0;
 #pragma unroll 8
     for (int p = 0; p < a.slabs; ++p) s += part[(size_t)p * MP * MP + e];
@@ -798,7 +802,7 @@ __global__ void __launch_bounds__(256) k_orth_iter64(OrthNarrow a) {
   }
   __syncthreads();
   const double inv = s_inv, inv2 = inv * inv;
-  for (int e = threadIdx.x; e < MP * MP; e += 256) G[e / MP * LD + e % MP] *= inv2;
+  for (int e = threadIdx.x; e < MP * MP; e += NT) G[e / MP * LD + e % MP] *= inv2;
   __syncthreads();
   OrthF64<MP> t;
   t.init();
@@ -833,7 +837,7 @@ __global__ void __launch_bounds__(256) k_orth_iter64(OrthNarrow a) {
     __syncthreads();
   }
   float* out = a.q + (size_t)blockIdx.x * MP * MP;
-  for (int e = threadIdx.x; e < MP * MP; e += 256) {
+  for (int e = threadIdx.x; e < MP * MP; e += NT) {
     const double v = Q[e / MP * LD + e % MP] * inv;
     // (a tiny norm's scale past fp32: a zero matrix still gives zero)
     out[e] = v > 3e38 ? 3e38f : v < -3e38 ? -3e38f : (float)v;

@@ -291,10 +291,10 @@ moe_status launch_orth_gemm(const OrthGemm& g, int batch, int cus, hipStream_t s
 
 template <int BF, int MP>
 moe_status launch_orth_narrow(const OrthNarrow& a, int batch, hipStream_t st) {
-  hipLaunchKernelGGL((k_orth_gram64<BF, MP>), dim3(a.slabs, batch), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((k_orth_gram64<BF, MP>), dim3(a.slabs, batch), dim3(OrthF64<MP>::kThreads), 0, st, a);
   HIP_TRY(hipGetLastError());
   TRY((set_lds_limit_once<k_orth_iter64<MP>>(OrthSq<MP>::kLds)));
-  hipLaunchKernelGGL(k_orth_iter64<MP>, dim3(batch), dim3(256), OrthSq<MP>::kLds, st, a);
+  hipLaunchKernelGGL(k_orth_iter64<MP>, dim3(batch), dim3(OrthF64<MP>::kThreads), OrthSq<MP>::kLds, st, a);
   HIP_TRY(hipGetLastError());
   const dim3 grid((a.n + kOrthApply - 1) / kOrthApply, batch);
   if (a.tall) hipLaunchKernelGGL((k_orth_apply<BF, MP, 1>), grid, dim3(kOrthApply), 0, st, a);
