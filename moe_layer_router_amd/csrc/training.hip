@@ -166,9 +166,11 @@ constexpr float kOrthCoeffs[3] = {3.4445f, -4.7750f, 2.0315f};
 constexpr int kOrthMaxSteps = 32;
 constexpr size_t kOrthChunkBytes = (size_t)8 << 30;
 // Tile shapes: 256 x 256 (eight waves of 64 x 128, one workgroup per CU), and
-// smaller ones where there are too few of those to fill the GPU.
+// smaller ones where there are too few of those to fill the GPU or they would
+// cover too much that is not there.
 using OrthBig = OrthTile<4, 2, 8, 2>;
 using OrthMid = OrthTile<2, 2, 4, 2>;
+using OrthMidDeep = OrthTile<2, 2, 4, 3>;
 using OrthSmall = OrthTile<1, 2, 2, 3>;
 constexpr int kOrthParts = 512;      // parts of tiles in one launch (at most 128 MiB of sums)
 
@@ -283,9 +285,20 @@ moe_status launch_orth_gemm(OrthGemm g, int batch, int cus, hipStream_t st) {
 template <int MODE>
 moe_status launch_orth_gemm(const OrthGemm& g, int batch, int cus, hipStream_t st) {
   const long big = (long)((g.rows + 255) / 256) * ((g.cols + 255) / 256) * batch;
-  if (big >= cus) return launch_orth_gemm<OrthBig, MODE>(g, batch, cus, st);
-  const long mid = (long)((g.rows + 127) / 128) * ((g.cols + 127) / 128) * batch;
-  if (mid >= cus) return launch_orth_gemm<OrthMid, MODE>(g, batch, cus, st);
+  const long ti = (g.rows + 127) / 128, tj = (g.cols + 127) / 128, mid = ti * tj * batch;
+  // the large tiles unless they cover a quarter more than the middle ones do
+  // (16 x 640 x 1400, a third more: 412 us, with the middle ones 357; 64 x 300 x 700
+  // 432 and 311; 8 x 2048 x 7168, the same: 4.54 ms, with the middle ones 5.00)
+  if (big >= cus && 16 * big <= 5 * mid) return launch_orth_gemm<OrthBig, MODE>(g, batch, cus, st);
+  if (mid >= cus) {
+    // up to one workgroup per CU: a third stage in place of the second workgroup
+    // (4 x 1024 x 1024 348 -> 255 us, 16 x 512 x 2048 458 -> 346; with more tiles 812 ->
+    // 903 for 2048 x 7168), unless K is long enough for parts (X X^T of the same, 136
+    // tiles of K = 7168: 820 in three parts each, 869 whole)
+    const long tiles = orth_sym(MODE) ? ti * (ti + 1) / 2 * batch : mid;
+    if (tiles <= cus && !(orth_sym(MODE) && g.K > 4096)) return launch_orth_gemm<OrthMidDeep, MODE>(g, batch, cus, st);
+    return launch_orth_gemm<OrthMid, MODE>(g, batch, cus, st);
+  }
   return launch_orth_gemm<OrthSmall, MODE>(g, batch, cus, st);
 }
 

@@ -76,18 +76,26 @@ def test_spectra(gpu_lib, B, M, N, kind):
     _check(y, u, what=kind)
 
 
-@pytest.mark.parametrize("B", [40, 12, 3])
-def test_tile_shapes(gpu_lib, B):
-    """Batches for the 256 x 256, the 128 x 128 and the 64 x 64 tiles, with padding
-    and partial tiles on both sides and a partial round split along K, wide
-    and tall."""
+@pytest.mark.parametrize("B,M,N", [
+    (8, 960, 2100),      # 256 x 256 tiles, cut off on both sides
+    (40, 520, 1100),     # 128 x 128 tiles, as the larger ones would cover a third more
+    (7, 576, 1000),      # 128 x 128, up to one per CU (three stages) in the symmetric products
+    (8, 450, 900),       # in all of them
+    (4, 1000, 4300),     # not in X X^T, whose K is long: split
+    (12, 520, 1100),
+    (3, 520, 1100),      # 64 x 64
+])
+def test_tile_shapes(gpu_lib, B, M, N):
+    """Batches for each tile shape and its variants, with padding and partial tiles on
+    both sides and a partial round split along K, wide and tall."""
     from moe_layer_router_amd import layer as L
-    for M, N in ((520, 1100), (1100, 520)):
-        u = _mat(B, M, N, 9)
+    for m, n in ((M, N), (N, M)):
+        u = _mat(B, m, n, 9)
         y = L.orthogonalize(u)
         torch.cuda.synchronize()
-        some = [0, B // 2, B - 1]
-        _check(y[some], u[some], what=(M, N))
+        some = sorted({0, B - 1} if m * n > 10 ** 6 else {0, B // 2, B - 1})
+        _check(y[some], u[some], what=(m, n))
+        assert torch.equal(L.orthogonalize(u), y)
 
 
 def test_batch_in_several_parts(gpu_lib):
@@ -108,7 +116,7 @@ def test_batch_in_several_parts(gpu_lib):
     assert float(s.min()) > 0.4 * M and float(s.max()) < 1.5 * M
 
 
-@pytest.mark.parametrize("B,M,N", [(40, 576, 1088), (40, 1100, 520), (8, 130, 1500), (3, 200, 333)])
+@pytest.mark.parametrize("B,M,N", [(40, 576, 1088), (40, 1100, 520), (8, 960, 2100), (8, 130, 1500), (3, 200, 333)])
 def test_repeated_calls_agree(gpu_lib, B, M, N):
     """Sides that end inside a tile, of each tile shape: the same bits from every call."""
     from moe_layer_router_amd import layer as L
