@@ -13,14 +13,18 @@
 // reaches 2^16) and on a I + B itself (its small elements are subnormal FP16
 // numbers, which the matrix cores take: 3e-8 beside a), so that the
 // accumulators of (a I + B) X hold 2^12 X'.
-// X is held as an FP16 part hi and the E4M3 code lo of 2^6 times what is left,
-// 15 bits: the step is X' = (a I + B) hi + a lo, the first term one product, the
-// second added in fp32.  One FP16 product has 2^-11 relative rounding per
-// operand, eight times less than BF16.  Simulated in fp64 with these roundings,
-// over spectra from flat to 1/r^2, the result is within 1.9e-3 of the exact
-// iteration for sides from 65 on, beside the output's own BF16 rounding (1.7e-3).
-// Without lo it is up to 2e-2 off (small singular values are lost in the rounding
-// of the large ones), with BF16 products 1e-2 to 1.6e-1.
+// X is held as an FP16 part hi and the FP16 rounding lo of what is left, 22 bits:
+// the step is X' = (a I + B) hi + a lo, the first term one product, the second
+// added in fp32.  One FP16 product has 2^-11 relative rounding per operand, eight
+// times less than BF16.  Its roundings in A and B' move singular vectors and
+// values a little; those of X would have full rank, and each step lifts what they put
+// into directions that U lacks by a, 485-fold in 5 steps: hence lo.  Simulated in
+// fp64 with these roundings, 5 steps, the result is within 2.6e-3 of the exact
+// iteration for sides from 65 to 2048, spectra from flat to 1/r^2 and exact ranks from 1 on
+// (within 1.1e-2 for matrices of one magnitude, whose elements all round alike),
+// beside the output's own BF16 rounding (1.7e-3).  With an 8-bit E4M3 lo it is up
+// to 6.8e-3 off after 5 steps and 1.5e-1 after 8 (2048 x 7168 of rank 1), for 1 to 4%
+// less time; without lo up to 2e-2, with BF16 products 1e-2 to 1.6e-1.
 //
 // Layout.  Rows and columns are padded with zeros to multiples of 64.  X is kept
 // transposed, hi (two, read and written in turn) and lo [np][mp], beside A and
@@ -67,23 +71,16 @@ struct OrthArgs {
   float eps;
   double* part;              // [batch][kOrthNormParts]
   uint16_t* hi;              // [batch][np][mp]
-  uint8_t* lo;
+  uint16_t* lo;
 };
 
 DEV uint32_t h_bits(float v) { return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v); }
 DEV float h_val(uint32_t b) { return (float)__builtin_bit_cast(_Float16, (uint16_t)b); }
-constexpr float kOrthLoScale = 64.0f;    // (|lo| <= 4 for |X| < 4, half a unit in hi's last place: within E4M3's 448)
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef float v2f __attribute__((ext_vector_type(2)));
-typedef short v2s __attribute__((ext_vector_type(2)));
-// Two values as packed FP16 (one conversion instruction, to nearest even), and
-// as E4M3 codes of kOrthLoScale times them in half `HI` of a word.
+// Two values as packed FP16 (one conversion instruction, to nearest even).
 DEV uint32_t h_pack(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{lo, hi}), v2h));
-}
-template <bool HI>
-DEV v2s lo_pack(v2s old, float a, float b) {
-  return __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(old, a, b, 1.0f / kOrthLoScale, HI);
 }
 
 template <int BF>
@@ -143,7 +140,7 @@ __global__ void __launch_bounds__(256) k_orth_load(OrthArgs a) {
   auto put = [&](size_t o, float x) {
     const uint32_t h = h_bits(x);
     a.hi[o] = (uint16_t)h;
-    a.lo[o] = (uint8_t)f32_to_e4m3((x - h_val(h)) * kOrthLoScale);
+    a.lo[o] = (uint16_t)h_bits(x - h_val(h));
   };
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
@@ -192,7 +189,7 @@ struct OrthGemm {
   uint16_t* c;                         // GRAM: A; POLY: B'
   const uint16_t* a;                   // POLY: A
   uint16_t* hi;                        // STEP: of X'
-  uint8_t* lo;
+  uint16_t* lo;
   uint16_t* y;                         // LAST: [batch][M][N]
   int m, n, tall;
 };
@@ -258,13 +255,13 @@ DEV rsrc_t orth_rsrc(const OrthGemm& g, T* x, int mat) {
 
 // The lo parts of the elements that orth_store finishes, read ahead of it.
 template <class TL, int MODE>
-DEV void orth_lo(const OrthGemm& g, int mat, int i0, int j0, int w, int lane, int p, v2u (&lq)[4]) {
+DEV void orth_lo(const OrthGemm& g, int mat, int i0, int j0, int w, int lane, int p, v4i (&lq)[4]) {
   if (orth_sym(MODE)) return;
   const uint32_t o = orth_at<TL>(g, i0, j0, w, lane, p);
   const rsrc_t lo = orth_rsrc(g, g.lo, mat);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    lq[i] = __builtin_bit_cast(v2u, __builtin_amdgcn_raw_buffer_load_b64(lo, (int)o, (int)orth_row(g, i, p), 0));
+    lq[i] = buf_ld16(lo, 2 * o, 2 * orth_row(g, i, p));
 }
 
 // GRAM: a wave's sums acc[i][j][v] are row 64 wm + 16 i + c16 and column 16 NJ wn +
@@ -327,7 +324,7 @@ DEV void orth_store_gram(const OrthGemm& g, int mat, int i0, int j0, bool mirror
 // slower, 4555 -> 4640 us for 8 x 2048 x 7168.)
 template <class TL, int MODE>
 DEV void orth_store(const OrthGemm& g, int mat, int i0, int j0, bool mirror, int w, int lane, int p,
-                    const v4f (&acc)[4][2], const v2u (&lq)[4]) {
+                    const v4f (&acc)[4][2], const v4i (&lq)[4]) {
   if (MODE == ORTH_GRAM) return orth_store_gram<TL>(g, mat, i0, j0, mirror, w, lane, p, acc);
   const int c16 = lane & 15, gq = lane >> 4;
   const int r0 = i0 + 64 * (w / TL::WN), c0 = j0 + 16 * TL::NJ * (w % TL::WN) + 32 * p;
@@ -352,15 +349,11 @@ DEV void orth_store(const OrthGemm& g, int mat, int i0, int j0, bool mirror, int
       }
     }
     if (!orth_sym(MODE)) {
-      const float c0 = g.c0 * scale * (1.0f / kOrthLoScale);
+      const float c0 = g.c0 * scale;
 #pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        const v2f l0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)lq[i][d], false);
-        const v2f l1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)lq[i][d], true);
-        v[i][4 * d] = __builtin_fmaf(c0, l0[0], v[i][4 * d]);
-        v[i][4 * d + 1] = __builtin_fmaf(c0, l0[1], v[i][4 * d + 1]);
-        v[i][4 * d + 2] = __builtin_fmaf(c0, l1[0], v[i][4 * d + 2]);
-        v[i][4 * d + 3] = __builtin_fmaf(c0, l1[1], v[i][4 * d + 3]);
+      for (int e = 0; e < 8; ++e) {
+        const int word = lq[i][e >> 1];            // (a bit cast of the vector's element itself reads element 0)
+        v[i][e] = __builtin_fmaf(c0, (float)__builtin_bit_cast(v2h, word)[e & 1], v[i][e]);
       }
     }
     if (MODE == ORTH_LAST) {
@@ -384,17 +377,16 @@ DEV void orth_store(const OrthGemm& g, int mat, int i0, int j0, bool mirror, int
       float l[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int word = hw[e >> 1];               // (a bit cast of the vector's element itself reads element 0)
+        const int word = hw[e >> 1];
         l[e] = v[i][e] - (float)__builtin_bit_cast(v2h, word)[e & 1];
       }
-      const v2s z = v2s{0, 0};
-      const v2u lw = v2u{__builtin_bit_cast(uint32_t, lo_pack<true>(lo_pack<false>(z, l[0], l[1]), l[2], l[3])),
-                         __builtin_bit_cast(uint32_t, lo_pack<true>(lo_pack<false>(z, l[4], l[5]), l[6], l[7]))};
+      const v4i lw = v4i{(int)h_pack(l[0], l[1]), (int)h_pack(l[2], l[3]), (int)h_pack(l[4], l[5]),
+                         (int)h_pack(l[6], l[7])};
       // past the caches where there is more of X' than they hold (the large
       // tiles), so that it leaves the operands of the running products in the L2
       constexpr int kAux = TL::kSide >= 256 ? 2 : 0;
       __builtin_amdgcn_raw_buffer_store_b128(hw, hi_r, (int)(2 * x), (int)(2 * orth_row(g, i, p)), kAux);
-      __builtin_amdgcn_raw_buffer_store_b64(lw, lo_r, (int)x, (int)orth_row(g, i, p), kAux);
+      __builtin_amdgcn_raw_buffer_store_b128(lw, lo_r, (int)(2 * x), (int)(2 * orth_row(g, i, p)), kAux);
     }
   }
   if (mirror || (MODE == ORTH_LAST && !g.tall)) {
@@ -577,17 +569,18 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_orth_gemm(OrthGemm g) {
 #pragma unroll
     for (int j = 0; j < NL; ++j) asm volatile("" : "+v"(qf[j]));
   }
-  // (lo is read during the last step)
-  constexpr int NP = NJ / 2;
-  v2u lq[NP][4] = {};
+  // (the first lo parts are read during the last step, as many as the registers
+  // beside the operands hold; the others as these are used)
+  constexpr int NP = NJ / 2, NA = NP < 2 ? NP : 2;
+  v4i lq[NP][4] = {};
 #pragma unroll
-  for (int p = 0; p < NP; ++p) orth_lo<TL, MODE>(g, mat, i0, j0, w, lane, p, lq[p]);
+  for (int p = 0; p < NA; ++p) orth_lo<TL, MODE>(g, mat, i0, j0, w, lane, p, lq[p]);
   halves(lds + stage * TL::kStage);
 #pragma unroll
   for (int j = NJ - NL; j < NJ; ++j) mul(j);
   __builtin_amdgcn_sched_barrier(0);               // (the operands' registers are free below)
   // no load into LDS outlives the workgroup (they are older than those of lo)
-  wait_vmcnt<orth_sym(MODE) ? 0 : 4 * NP>();
+  wait_vmcnt<orth_sym(MODE) ? 0 : 4 * NA>();
   if (orth_sym(MODE) && part >= 0) {
     v4f* dst = reinterpret_cast<v4f*>(g.part + (size_t)part * TL::kPart) + (size_t)w * 4 * NJ * 64 + lane;
 #pragma unroll
@@ -597,12 +590,13 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_orth_gemm(OrthGemm g) {
     return;
   }
 #pragma unroll
-  for (int p = 0; p < NJ / 2; ++p) {
+  for (int p = 0; p < NP; ++p) {
     const v4f a[4][2] = {{acc[0][2 * p], acc[0][2 * p + 1]},
                          {acc[1][2 * p], acc[1][2 * p + 1]},
                          {acc[2][2 * p], acc[2][2 * p + 1]},
                          {acc[3][2 * p], acc[3][2 * p + 1]}};
     orth_store<TL, MODE>(g, mat, i0, j0, mirror, w, lane, p, a, lq[p]);
+    if (p + NA < NP) orth_lo<TL, MODE>(g, mat, i0, j0, w, lane, p + NA, lq[p + NA]);
   }
 }
 
@@ -644,7 +638,7 @@ __global__ void __launch_bounds__(256) k_orth_join(OrthGemm g) {
       acc[i][0] += sum[k][2 * i][lane];
       acc[i][1] += sum[k][2 * i + 1][lane];
     }
-  v2u lq[4];
+  v4i lq[4];
   orth_lo<TL, MODE>(g, mat, i0, j0, w, lane, p, lq);
   orth_store<TL, MODE>(g, mat, i0, j0, mirror, w, lane, p, acc, lq);
 }

@@ -210,13 +210,13 @@ OrthLayout orth_layout(int batch, int M, int N) {
   // fills the GPU
   const size_t sums = std::max({orth_part_bytes<OrthBig>(batch, L.mp, L.np), orth_part_bytes<OrthMid>(batch, L.mp, L.np),
                                 orth_part_bytes<OrthSmall>(batch, L.mp, L.np)});
-  L.chunk = (int)std::min((size_t)batch, std::max((size_t)1, (kOrthChunkBytes - sums) / (2 * x + x / 2 + 2 * q)));
+  L.chunk = (int)std::min((size_t)batch, std::max((size_t)1, (kOrthChunkBytes - sums) / (3 * x + 2 * q)));
   const size_t c = L.chunk;
   size_t o = 0;
   L.part = o; o = align256(o + c * kOrthNormParts * 8);
   L.hi0 = o; o = align256(o + c * x);
   L.hi1 = o; o = align256(o + c * x);
-  L.lo = o; o = align256(o + c * x / 2);
+  L.lo = o; o = align256(o + c * x);
   L.a = o; o = align256(o + c * q);
   L.b = o; o = align256(o + c * q);
   L.sums = o; o = align256(o + sums);
@@ -234,7 +234,7 @@ moe_status check_orth(int32_t batch, int32_t M, int32_t N) {
   return MOE_OK;
 }
 
-// Whether X and A stay within the range of their FP16 and E4M3 parts over the
+// Whether X and A stay within the range of their FP16 parts over the
 // steps: the singular values start in [0, 1], and a step takes [0, s] to its
 // image under the polynomial.
 bool orth_in_range(int steps, const float* co) {
@@ -504,7 +504,7 @@ moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dty
     a.part = reinterpret_cast<double*>(ws + L.part);
     uint16_t* hi[2] = {reinterpret_cast<uint16_t*>(ws + L.hi0), reinterpret_cast<uint16_t*>(ws + L.hi1)};
     a.hi = hi[0];
-    a.lo = reinterpret_cast<uint8_t*>(ws + L.lo);
+    a.lo = reinterpret_cast<uint16_t*>(ws + L.lo);
     const dim3 norm_grid(kOrthNormParts, nb);
     const dim3 load_grid((a.tall ? L.mp : L.np) / 64, (a.tall ? L.np : L.mp) / 64, nb);
     if (bf) hipLaunchKernelGGL(k_orth_norm<1>, norm_grid, dim3(256), 0, st, a);

@@ -1,0 +1,102 @@
+"""The accuracy that moe_orthogonalize documents, on the updates that strain it
+most: exactly low rank (the gradient of an expert that got few tokens), where
+every direction that the matrix lacks holds nothing but what rounding puts
+there, and matrices of one magnitude, whose elements all round alike.
+
+The matrices are products of integer factors, so that fp32 holds them exactly
+and their rank is exact; the iteration keeps their singular vectors, and the
+reference follows in 64 bits from the factors' QR and the scalar polynomial.
+
+Bounds (relative, Frobenius), for the wide path (sides above 64).  A step's roundings
+are those of FP16 operands, half a step 2^-11 = 4.9e-4 of an element at most,
+2.8e-4 in the root mean square: of A (in the polynomial 4.8 + 2 * 2.0 times), of
+B' (its diagonal, 2 to 4, at most 2^-10 from its place) and of the FP16 part of X in
+X X^T.  Simulated with these rounding points in 64 bits: 2.6e-3 after 5 steps and
+4.1e-3 after 8 for rank 1 to 64, 1.1e-2 and 1.4e-2 for matrices of one magnitude.  With
+the BF16 rounding of y, 2^-8 / sqrt(3) = 2.3e-3 at most and independent: 4e-3
+(documented) >= sqrt(2.6^2 + 2.3^2) = 3.5e-3; 6e-3 for 8 steps; 1.3e-2 and 1.6e-2.
+
+Beside it, in directions that U lacks, what the sums' own rounding leaves, lifted by
+a = 3.4445 in each step that follows, as in an fp32 iteration.  A step's sum over m
+terms is m / 32 additions of fp32 numbers, each off by up to 2^-24 of the sum, at
+random sqrt(m / 32) 2^-24 together; behind K steps, with P = a^K, the sum over the steps
+is P / a * 1.41 * sqrt(m / 32) 2^-24 = P sqrt(m) 2^-27.8, and X_0's 22 bits (half a step 2^-23
+at most, 2^-23.8 at random) add P 2^-23.8, which is below P sqrt(m) 2^-26.8 from m = 65 on:
+together P sqrt(m) 2^-26 (3.3e-4 after 5 steps at m = 2048, within the 4e-3; 1.3e-2 after 8)."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import training as R
+
+pytestmark = pytest.mark.gpu
+
+
+def _poly(s, steps, coeffs=None):
+    for i in range(steps):
+        a, b, c = R.NS_COEFFS if coeffs is None else coeffs[i]
+        s = a * s + b * s ** 3 + c * s ** 5
+    return s
+
+
+def low_rank(M, N, r, seed):
+    """(U exact in fp32, function of the steps: the exact result)."""
+    rng = np.random.default_rng(seed)
+    p, q = np.rint(4 * rng.normal(size=(M, r))), np.rint(4 * rng.normal(size=(N, r)))
+    qp, rp = np.linalg.qr(p)
+    qq, rq = np.linalg.qr(q)
+    a, s, b = np.linalg.svd(rp @ rq.T)
+    s /= np.linalg.norm(s) + 1e-7
+    u = (p @ q.T).astype(np.float32)
+    assert np.array_equal(u, p @ q.T)
+    return torch.from_numpy(u).cuda(), lambda steps: ((qp @ a) * _poly(s, steps)) @ (b @ qq.T)
+
+
+def _error(y, ref):
+    got = y.cpu().double().numpy()
+    assert np.all(np.isfinite(got))
+    return np.linalg.norm(got - ref) / np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("M,N,ranks", [(65, 65, (1, 4)), (96, 160, (1, 3)), (300, 200, (1, 16)), (256, 512, (1, 2, 64)),
+                                       (1024, 4096, (1, 2, 16)), (2048, 1024, (1, 8)), (2048, 7168, (1, 2, 16))])
+def test_low_rank(gpu_lib, M, N, ranks):
+    from moe_layer_router_amd import layer as L
+    for r in ranks:
+        u, exact = low_rank(M, N, r, M + r)
+        for steps, bound in ((5, 4e-3), (8, 6e-3), (10, 8e-3)):
+            lifted = R.NS_COEFFS[0] ** steps * min(M, N) ** 0.5 * 2.0 ** -26 if steps > 5 else 0
+            e = _error(L.orthogonalize(u, steps=steps), exact(steps))
+            assert e <= bound + lifted, (r, steps, e)
+
+
+@pytest.mark.parametrize("M,N", [(65, 65), (127, 345), (350, 733), (200, 333), (2048, 1024)])
+def test_elements_of_one_magnitude(gpu_lib, M, N):
+    from moe_layer_router_amd import layer as L
+    rng = np.random.default_rng(1)
+    for u in (np.ones((M, N)), np.sign(rng.normal(size=(M, 1))) * np.sign(rng.normal(size=(1, N)))):
+        v = u / np.sqrt(M * N)
+        for steps, bound in ((5, 1.3e-2), (8, 1.6e-2)):
+            s = _poly(np.sqrt(M * N) / (np.sqrt(M * N) + 1e-7), steps)
+            e = _error(L.orthogonalize(torch.from_numpy(u.astype(np.float32)).cuda(), steps=steps), s * v)
+            assert e <= bound, (steps, e)
+
+
+def test_the_cut_between_parts_of_a_batch(gpu_lib):
+    """Rank-1 matrices around the cut of a batch that goes through in two parts."""
+    from moe_layer_router_amd import layer as L, lib
+    M, N, B = 1024, 4096, 400
+    per = lib.moe_orthogonalize_workspace_size(2, M, N) - lib.moe_orthogonalize_workspace_size(1, M, N)
+    assert lib.moe_orthogonalize_workspace_size(B, M, N) == lib.moe_orthogonalize_workspace_size(2 * B, M, N)
+    cut = (8 << 30) // per
+    some = [0, 1] + [i for i in range(cut - 12, cut + 3)] + [B - 1]
+    assert cut + 3 < B
+    u = torch.randn(B, M, N, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    exact = {}
+    for i in some:
+        u[i], exact[i] = low_rank(M, N, 1, i)
+    y = L.orthogonalize(u)
+    torch.cuda.synchronize()
+    for i in some:
+        assert _error(y[i], exact[i](5)) <= 4e-3, i
