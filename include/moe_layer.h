@@ -491,15 +491,16 @@ moe_status moe_balance_loss(int32_t T, int32_t E, int32_t top_k, int32_t n_seq, 
  * batch = 2E gate and up matrices of I x H, dw_down [E][H][I] E matrices, and
  * dw_router one.  y [batch][M][N] BF16 (output, must not overlap u).  The
  * products are FP16 matrix-core products with fp32 accumulation on scaled
- * values, X is held in 22 bits and the norm in fp64 (all of it in fp64 where the
- * smaller of M and N is at most 64).  With the default coefficients and 5 steps y
+ * values, X is held in 22 bits and the norm in fp64.  With the default coefficients and 5 steps y
  * is within 4e-3 of the exact iteration in the Frobenius norm, 1.7e-3 of it y's
  * own rounding, for matrices of any rank, and within 1.3e-2 for those of one magnitude,
  * whose elements all round alike; after 8 steps within 6e-3 and 1.6e-2.  What
  * rounding leaves in directions that U lacks, each step lifts by its a, as in an
  * fp32 iteration: with P the product of the steps' |a|, up to P sqrt(min(M, N))
  * 2^-26 more (with the default coefficients and 2048 rows 3e-4 after 5 steps, 1.3e-2
- * after 8, 5e-1 after 11).
+ * after 8, 5e-1 after 11).  Where the smaller of M and N is at most 64 all of it is
+ * in fp64 and y is the exact iteration's result, rounded, for any steps; only
+ * singular values below 2^-22 of the norm, rounding in an fp32 U, are lifted 2^22-fold at most.
  * 1 <= M, N <= 32768, the smaller <= 16384, 1 <= batch <=
  * 65535, 1 <= steps <= 32, eps > 0; pointers (not coeffs) 16-byte aligned.
  * workspace: moe_orthogonalize_workspace_size bytes (5 to 9 per element of u

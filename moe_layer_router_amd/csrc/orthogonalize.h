@@ -42,6 +42,13 @@
 // twice and written once, in three launches.  It is also the accurate way for them: a matrix of
 // few rows does not average the roundings of FP16 products (up to 1e-2 at m
 // <= 8, below 2.3e-3 from m = 64 on).
+// Where U lacks a direction, G holds rounding of either sign there, and a step
+// multiplies it by a^2.  A negative one would grow past 1 after 16 default steps, and P
+// with it, without end.  So G starts with 2^-44 on its diagonal: above its
+// rounding (about 1e-15) and that of each P G P (2^-53 |P|^2, while the shift has grown as much), it
+// stays positive and ends near 1 like any other value.  To the singular values that
+// is sqrt(s^2 + 2^-44): those below 2^-22 of the norm, rounding in an fp32 U, are lifted
+// 2^22-fold at most, and no other is off by more than 2^-45 / s.
 //
 // Measured (5 steps).  Large matrices are bound by the matrix cores: 8 x 2048 x
 // 7168 takes 4.45 ms, 887 TFLOP/s, where one large FP16 library product reaches
@@ -647,15 +654,15 @@ __global__ void __launch_bounds__(256) k_orth_join(OrthGemm g) {
 constexpr int kOrthNarrow = 64;          // largest m of the narrow kernels
 constexpr int kOrthSlabs = 16;           // partial Gram matrices per matrix
 constexpr int kOrthSlabCols = 32;        // columns of X per pass of a slab
-constexpr int kOrthApply = 128;          // columns of X per workgroup of the last kernel
 
 struct OrthNarrow {
   const void* u;             // [batch][M][N]
   int m, n, tall, slabs, steps;
+  int tiles;                 // of 16 columns, for each wave of the last kernel
   float eps;
   float co[32][3];
   double* part;              // [batch][slabs][MP][MP]
-  float* q;                  // [batch][MP][MP]: Q / (|U|_F + eps)
+  double* q;                 // [batch][MP][MP]: Q / (|U|_F + eps)
   uint16_t* y;
 };
 
@@ -770,7 +777,8 @@ struct OrthSq {
 
 // One workgroup per matrix: G from its slabs, the norm from G's trace, the
 // steps, and Q.  G, P and Q are polynomials of the first G, so symmetric, and
-// they commute: every product is formed as p q^T.
+// they commute: every product is formed as p q^T.  G is kept exactly symmetric: an
+// antisymmetric part would grow with G's smallest values (9e-5 of y after 16 steps).
 template <int MP>
 __global__ void __launch_bounds__(OrthF64<MP>::kThreads) k_orth_iter64(OrthNarrow a) {
   constexpr int LD = OrthSq<MP>::kLd, NT = OrthF64<MP>::kThreads;
@@ -796,7 +804,11 @@ __global__ void __launch_bounds__(OrthF64<MP>::kThreads) k_orth_iter64(OrthNarro
   }
   __syncthreads();
   const double inv = s_inv, inv2 = inv * inv;
-  for (int e = threadIdx.x; e < MP * MP; e += NT) G[e / MP * LD + e % MP] *= inv2;
+  constexpr double kShift = 1.0 / (1ull << 44);
+  for (int e = threadIdx.x; e < MP * MP; e += NT) {
+    double& v = G[e / MP * LD + e % MP];
+    v = v * inv2 + (e / MP == e % MP ? kShift : 0.0);
+  }
   __syncthreads();
   OrthF64<MP> t;
   t.init();
@@ -826,53 +838,73 @@ __global__ void __launch_bounds__(OrthF64<MP>::kThreads) k_orth_iter64(OrthNarro
       put(T);
       __syncthreads();
       mul(T, P);
-      put(G);
+      t.each([&](int i, int j, double& v) {        // (exactly symmetric: one triangle, mirrored)
+        if (i <= j) G[i * LD + j] = G[j * LD + i] = v;
+      });
     }
     __syncthreads();
   }
-  float* out = a.q + (size_t)blockIdx.x * MP * MP;
-  for (int e = threadIdx.x; e < MP * MP; e += NT) {
-    const double v = Q[e / MP * LD + e % MP] * inv;
-    // (a tiny norm's scale past fp32: a zero matrix still gives zero)
-    out[e] = v > 3e38 ? 3e38f : v < -3e38 ? -3e38f : (float)v;
-  }
+  double* out = a.q + (size_t)blockIdx.x * MP * MP;
+  for (int e = threadIdx.x; e < MP * MP; e += NT) out[e] = Q[e / MP * LD + e % MP] * inv;
 }
 
-// y = Q U: one column of X per thread, its m elements in registers, Q through
-// the scalar cache (every thread of the grid's matrix reads the same
-// element).  A tall matrix's columns are rows in memory: a workgroup's are one
-// contiguous run, staged through LDS both ways.
+// y = Q U in fp64 (where U lacks a direction Q holds up to 2^22, of which nothing may be
+// left in y), by fp64 matrix instructions: a wave keeps 16 rows of Q in registers
+// (lane r + 16 kk: row r, K from KS kk on) and goes through tiles of 16 columns of
+// X, the next one's loads in flight; waves side by side have the other rows of Q or
+// the next columns.  A tall matrix's columns are rows in memory: its product is
+// formed transposed, so that 16 lanes store consecutive elements either way.
+// (A call on 16 x 64 x 7168 105 us, with vector fp64 and Q through the scalar cache 147.)
 template <int BF, int MP, int TALL>
-__global__ void __launch_bounds__(kOrthApply) k_orth_apply(OrthNarrow a) {
-  __shared__ float st[TALL ? kOrthApply * (MP + 1) : 1];
-  typedef const __attribute__((address_space(4))) float KFloat;
-  KFloat* q = (KFloat*)(uintptr_t)(a.q + (size_t)blockIdx.y * MP * MP);
-  const int j0 = blockIdx.x * kOrthApply, j = j0 + (int)threadIdx.x;
-  const size_t base = (size_t)blockIdx.y * a.m * a.n;
-  const int cols = min(kOrthApply, a.n - j0);
-  float x[MP];
-  if (TALL) {
-    for (int e = threadIdx.x; e < cols * a.m; e += kOrthApply)
-      st[e / a.m * (MP + 1) + e % a.m] = orth_ld<BF>(a.u, base + (size_t)j0 * a.m + e);
-    __syncthreads();
+__global__ void __launch_bounds__(256) k_orth_apply(OrthNarrow a) {
+  constexpr int NI = MP / 16, CW = 4 / NI, KS = MP / 4;
+  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, kk = lane >> 4;
+  const int i0 = 16 * (w % NI), m = a.m, n = a.n;
+  const size_t base = (size_t)blockIdx.y * m * n;
+  const double* q = a.q + (size_t)blockIdx.y * MP * MP + (i0 + r) * MP + KS * kk;
+  double qv[KS];
 #pragma unroll
-    for (int i = 0; i < MP; ++i) x[i] = i < a.m && j < a.n ? st[threadIdx.x * (MP + 1) + i] : 0.f;
-  } else {
+  for (int s = 0; s < KS; ++s) qv[s] = q[s];
+  float x[KS];
+  auto load = [&](int j0) {
+    const int j = j0 + r;
+    // (this lane's elements line up in 16-byte pieces: 16 x 7168 x 64 115 us a call, one by one 151)
+    if (TALL && KS >= 8 && m == MP) {
 #pragma unroll
-    for (int i = 0; i < MP; ++i) x[i] = i < a.m && j < a.n ? orth_ld<BF>(a.u, base + (size_t)i * a.n + j) : 0.f;
-  }
-  for (int i = 0; i < a.m; ++i) {
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int s = 0; s + 8 <= KS; s += 8) {
+        float v[8];
+        ln_unpack<BF ? LN_BF16 : LN_F32>(
+            ln_load<BF ? LN_BF16 : LN_F32>(a.u, base + (size_t)min(j, n - 1) * m + KS * kk + s), v);
 #pragma unroll
-    for (int k = 0; k < MP; ++k) s[k & 3] = __builtin_fmaf(q[i * MP + k], x[k], s[k & 3]);
-    const float v = (s[0] + s[1]) + (s[2] + s[3]);
-    if (TALL) st[threadIdx.x * (MP + 1) + i] = v;             // (this thread's own row: x is in registers)
-    else if (j < a.n) a.y[base + (size_t)i * a.n + j] = (uint16_t)f32_to_bf16_rne(v);
-  }
-  if (TALL) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < cols * a.m; e += kOrthApply)
-      a.y[base + (size_t)j0 * a.m + e] = (uint16_t)f32_to_bf16_rne(st[e / a.m * (MP + 1) + e % a.m]);
+        for (int e = 0; e < 8; ++e) x[s + e] = v[e];
+      }
+      return;
+    }
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int k = KS * kk + s;
+      x[s] = k < m && j < n ? orth_ld<BF>(a.u, base + (TALL ? (size_t)j * m + k : (size_t)k * n + j)) : 0.f;
+    }
+  };
+  int j0 = 16 * (blockIdx.x * a.tiles * CW + w / NI);
+  const int j1 = min(n, 16 * (int)((blockIdx.x + 1) * a.tiles * CW));
+  if (j0 < j1) load(j0);
+  for (; j0 < j1; j0 += 16 * CW) {
+    double xv[KS];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) xv[s] = (double)x[s];
+    if (j0 + 16 * CW < j1) load(j0 + 16 * CW);
+    v4d acc = v4d{0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+      acc = TALL ? __builtin_amdgcn_mfma_f64_16x16x4f64(xv[s], qv[s], acc, 0, 0, 0)
+                 : __builtin_amdgcn_mfma_f64_16x16x4f64(qv[s], xv[s], acc, 0, 0, 0);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int i = i0 + (TALL ? r : kk + 4 * v), j = j0 + (TALL ? kk + 4 * v : r);
+      if (i < m && j < n)
+        a.y[base + (TALL ? (size_t)j * m + i : (size_t)i * n + j)] = (uint16_t)f32_to_bf16_rne((float)acc[v]);
+    }
   }
 }
 

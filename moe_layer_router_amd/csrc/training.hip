@@ -202,7 +202,7 @@ OrthLayout orth_layout(int batch, int M, int N) {
     L.chunk = batch;
     const size_t e = (size_t)L.sq * L.sq * batch;
     L.q = align256(L.slabs * e * 8);
-    L.total = L.q + align256(e * 4);
+    L.total = L.q + align256(e * 8);
     return L;
   }
   const size_t x = (size_t)L.mp * L.np * 2, q = (size_t)L.mp * L.mp * 2;
@@ -303,23 +303,27 @@ moe_status launch_orth_gemm(const OrthGemm& g, int batch, int cus, hipStream_t s
 }
 
 template <int BF, int MP>
-moe_status launch_orth_narrow(const OrthNarrow& a, int batch, hipStream_t st) {
+moe_status launch_orth_narrow(OrthNarrow a, int batch, int cus, hipStream_t st) {
   hipLaunchKernelGGL((k_orth_gram64<BF, MP>), dim3(a.slabs, batch), dim3(OrthF64<MP>::kThreads), 0, st, a);
   HIP_TRY(hipGetLastError());
   TRY((set_lds_limit_once<k_orth_iter64<MP>>(OrthSq<MP>::kLds)));
   hipLaunchKernelGGL(k_orth_iter64<MP>, dim3(batch), dim3(OrthF64<MP>::kThreads), OrthSq<MP>::kLds, st, a);
   HIP_TRY(hipGetLastError());
-  const dim3 grid((a.n + kOrthApply - 1) / kOrthApply, batch);
-  if (a.tall) hipLaunchKernelGGL((k_orth_apply<BF, MP, 1>), grid, dim3(kOrthApply), 0, st, a);
-  else hipLaunchKernelGGL((k_orth_apply<BF, MP, 0>), grid, dim3(kOrthApply), 0, st, a);
+  // a wave's tiles share its reads of Q, as far as there are four workgroups per CU
+  constexpr int kCols = 16 * 4 / (MP / 16);       // columns of the workgroup's waves side by side
+  const long passes = (a.n + kCols - 1) / kCols;
+  a.tiles = (int)std::max(1L, std::min(8L, passes * batch / (4L * cus)));
+  const dim3 grid((unsigned)((passes + a.tiles - 1) / a.tiles), batch);
+  if (a.tall) hipLaunchKernelGGL((k_orth_apply<BF, MP, 1>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((k_orth_apply<BF, MP, 0>), grid, dim3(256), 0, st, a);
   HIP_TRY(hipGetLastError());
   return MOE_OK;
 }
 template <int BF>
-moe_status launch_orth_narrow(const OrthNarrow& a, int sq, int batch, hipStream_t st) {
-  if (sq == 16) return launch_orth_narrow<BF, 16>(a, batch, st);
-  if (sq == 32) return launch_orth_narrow<BF, 32>(a, batch, st);
-  return launch_orth_narrow<BF, 64>(a, batch, st);
+moe_status launch_orth_narrow(const OrthNarrow& a, int sq, int batch, int cus, hipStream_t st) {
+  if (sq == 16) return launch_orth_narrow<BF, 16>(a, batch, cus, st);
+  if (sq == 32) return launch_orth_narrow<BF, 32>(a, batch, cus, st);
+  return launch_orth_narrow<BF, 64>(a, batch, cus, st);
 }
 
 }  // namespace
@@ -490,9 +494,9 @@ moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dty
     for (int k = 0; k < steps; ++k)
       for (int i = 0; i < 3; ++i) a.co[k][i] = coeffs ? coeffs[3 * k + i] : kOrthCoeffs[i];
     a.part = reinterpret_cast<double*>(ws);
-    a.q = reinterpret_cast<float*>(ws + L.q);
+    a.q = reinterpret_cast<double*>(ws + L.q);
     a.y = static_cast<uint16_t*>(y);
-    return bf ? launch_orth_narrow<1>(a, L.sq, batch, st) : launch_orth_narrow<0>(a, L.sq, batch, st);
+    return bf ? launch_orth_narrow<1>(a, L.sq, batch, di.cus, st) : launch_orth_narrow<0>(a, L.sq, batch, di.cus, st);
   }
   for (int b0 = 0; b0 < batch; b0 += L.chunk) {
     const int nb = std::min(L.chunk, batch - b0);
