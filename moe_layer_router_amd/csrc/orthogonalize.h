@@ -139,16 +139,12 @@ __global__ void __launch_bounds__(256) k_orth_load(OrthArgs a) {
   double ss = a.part[(size_t)blockIdx.z * kOrthNormParts + tx];
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) ss += __shfl_xor(ss, d);
-  // (a zero matrix stays zero: the scale is finite)
-  const double scd = (double)kOrthScale / (sqrt(ss) + (double)a.eps);
-  const float sc = scd > 3e38 ? 3e38f : (float)scd;
+  // (in two factors, as the norm's reciprocal may leave fp32; a zero matrix stays
+  // zero, eps being positive)
+  int se;
+  const float sc = (float)frexp((double)kOrthScale / (sqrt(ss) + (double)a.eps), &se);
   const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
   const size_t ub = (size_t)blockIdx.z * a.M * a.N, xb = (size_t)blockIdx.z * a.mp * a.np;
-  auto put = [&](size_t o, float x) {
-    const uint32_t h = h_bits(x);
-    a.hi[o] = (uint16_t)h;
-    a.lo[o] = (uint16_t)h_bits(x - h_val(h));
-  };
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     float v[8];                              // eight rows' loads together
@@ -158,16 +154,25 @@ __global__ void __launch_bounds__(256) k_orth_load(OrthArgs a) {
       v[i] = r < a.M && c < a.N ? orth_ld<BF>(a.u, ub + (size_t)r * a.N + c) : 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int k = ty + 4 * (8 * q + i);
-      if (a.tall) put(xb + (size_t)(r0 + k) * a.mp + c0 + tx, v[i] * sc);
-      else tile[k][tx] = v[i] * sc;
-    }
+    for (int i = 0; i < 8; ++i) tile[ty + 4 * (8 * q + i)][tx] = ldexpf(v[i], se) * sc;
   }
-  if (a.tall) return;
   __syncthreads();
-#pragma unroll 4
-  for (int i = ty; i < 64; i += 4) put(xb + (size_t)(c0 + i) * a.mp + r0 + tx, tile[tx][i]);
+  // 8 consecutive elements of a row of X^T at a time: column k of the tile, or a row if tall
+  const size_t o0 = xb + (a.tall ? (size_t)r0 * a.mp + c0 : (size_t)c0 * a.mp + r0);
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int k = (threadIdx.x >> 3) + 32 * q, e0 = 8 * (threadIdx.x & 7);
+    v4i h, l;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const float x0 = a.tall ? tile[k][e0 + e] : tile[e0 + e][k], x1 = a.tall ? tile[k][e0 + e + 1] : tile[e0 + e + 1][k];
+      const uint32_t w = h_pack(x0, x1);
+      h[e / 2] = (int)w;
+      l[e / 2] = (int)h_pack(x0 - h_val(w & 0xFFFFu), x1 - h_val(w >> 16));
+    }
+    st16(a.hi + o0 + (size_t)k * a.mp + e0, h);
+    st16(a.lo + o0 + (size_t)k * a.mp + e0, l);
+  }
 }
 
 // ------------------------------------------------------------------ products

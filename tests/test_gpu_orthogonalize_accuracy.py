@@ -100,3 +100,16 @@ def test_the_cut_between_parts_of_a_batch(gpu_lib):
     torch.cuda.synchronize()
     for i in some:
         assert _error(y[i], exact[i](5)) <= 4e-3, i
+
+
+def test_norms_at_the_ends_of_fp32(gpu_lib):
+    """Norms whose reciprocals leave fp32: tiny ones with a tiny eps, and the largest."""
+    from moe_layer_router_amd import layer as L
+    rng = np.random.default_rng(3)
+    for M, N in ((96, 160), (300, 70)):
+        base = rng.normal(size=(M, N)).astype(np.float32)
+        base /= np.abs(base).max()
+        for scale in (2.0 ** -126, 2.0 ** -140, 2.0 ** 127):
+            u = (base.astype(np.float64) * scale).astype(np.float32)
+            y = L.orthogonalize(torch.from_numpy(u).cuda(), eps=1e-44)
+            assert _error(y, R.orthogonalize(u, 5, None, float(np.float32(1e-44)))) <= 4e-3, (M, N, scale)
