@@ -163,19 +163,19 @@ def backward(inputs: dict, topk_ids: torch.Tensor, topk_weights: torch.Tensor, d
     desc = desc_from_inputs(inputs, k, layout="row_major")
     E, I = desc.E, desc.I
     dev = x.device
-    f32 = dict(dtype=torch.float32, device=dev)
-    if out is None:
-        out = dict(dx=torch.empty(T, H, **f32), dw_gate_up=torch.empty(E, 2 * I, H, **f32),
-                   dw_down=torch.empty(E, H, I, **f32), dw_router=torch.empty(E, H, **f32),
-                   dbias=torch.empty(E, **f32) if want_dbias else None)
-    ws = (workspace or Workspace(dev)).get(lib.moe_backward_workspace_size(desc))
     if dlogits is not None:
-        _need(dlogits.shape == (T, E) and dlogits.dtype == torch.float32 and dlogits.device == dev,
-              f"dlogits must be float32 [{T}, {E}] on {dev}")
-        dlogits = dlogits.contiguous()
-    lib.moe_backward_aux(desc, x, inputs["router_w"], inputs["w_gate_up"].contiguous(), inputs["w_down"].contiguous(),
-                         topk_ids.contiguous(), topk_weights.contiguous(), dy.contiguous(), dlogits, out["dx"],
-                         out["dw_gate_up"], out["dw_down"], out["dw_router"], out["dbias"], ws, stream)
+        _is(dlogits, "dlogits", (T, E), _F32, dev)
+    with _on(dev, stream):
+        f32 = dict(dtype=torch.float32, device=dev)
+        if out is None:
+            out = dict(dx=torch.empty(T, H, **f32), dw_gate_up=torch.empty(E, 2 * I, H, **f32),
+                       dw_down=torch.empty(E, H, I, **f32), dw_router=torch.empty(E, H, **f32),
+                       dbias=torch.empty(E, **f32) if want_dbias else None)
+        ws = (workspace or Workspace(dev)).get(lib.moe_backward_workspace_size(desc))
+        lib.moe_backward_aux(desc, _dense(x), _dense(inputs["router_w"]), _dense(inputs["w_gate_up"]),
+                             _dense(inputs["w_down"]), _dense(topk_ids), _dense(topk_weights), _dense(dy),
+                             None if dlogits is None else _dense(dlogits), out["dx"], out["dw_gate_up"],
+                             out["dw_down"], out["dw_router"], out["dbias"], ws)
     return out
 
 
