@@ -171,7 +171,7 @@ def backward(inputs: dict, topk_ids: torch.Tensor, topk_weights: torch.Tensor, d
             out = dict(dx=torch.empty(T, H, **f32), dw_gate_up=torch.empty(E, 2 * I, H, **f32),
                        dw_down=torch.empty(E, H, I, **f32), dw_router=torch.empty(E, H, **f32),
                        dbias=torch.empty(E, **f32) if want_dbias else None)
-        ws = (workspace or Workspace(dev)).get(lib.moe_backward_workspace_size(desc))
+        ws = _scratch(workspace, dev, lib.moe_backward_workspace_size(desc))
         lib.moe_backward_aux(desc, _dense(x), _dense(inputs["router_w"]), _dense(inputs["w_gate_up"]),
                              _dense(inputs["w_down"]), _dense(topk_ids), _dense(topk_weights), _dense(dy),
                              None if dlogits is None else _dense(dlogits), out["dx"], out["dw_gate_up"],
@@ -203,8 +203,18 @@ def _on(device, stream):
     if stream is not None:
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(stream, device)
+        _need(stream.device == device, f"stream must be one of {device} (got one of {stream.device})")
         return torch.cuda.stream(stream)
     return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _scratch(workspace, device, nbytes):
+    """The caller's workspace, or one of the call's own; on the call's device."""
+    if workspace is None:
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    ws = workspace.get(nbytes)
+    _need(ws.device == device, f"workspace must be on {device} (got {ws.device})")
+    return ws
 
 
 def _dense(t):
@@ -301,8 +311,7 @@ def layer_norm_backward(x: torch.Tensor, gamma: torch.Tensor, mean: torch.Tensor
                     _is(out[name], name, (H,), _F32, dev, True)
         ws = None
         if want_weights:
-            nbytes = lib.moe_layer_norm_backward_workspace_size(T, H)
-            ws = (workspace or Workspace(dev)).get(nbytes)
+            ws = _scratch(workspace, dev, lib.moe_layer_norm_backward_workspace_size(T, H))
         lib.moe_layer_norm_backward(_dense(x), _dense(gamma), _dense(mean), _dense(rstd), _dense(dy), out["dx"],
                                     out["dgamma"], out["dbeta"], ws)
     return out
@@ -340,8 +349,7 @@ def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, alpha: float = 1.
                                     ("probs", (S, E), torch.float32), ("dlogits", (T, E), torch.float32)):
                 if out[name] is not None:
                     _is(out[name], name, shape, (dt,), dev, True)
-        nbytes = lib.moe_balance_loss_workspace_size(T, E, topk_ids.shape[1], S)
-        ws = (workspace or Workspace(dev)).get(nbytes)
+        ws = _scratch(workspace, dev, lib.moe_balance_loss_workspace_size(T, E, topk_ids.shape[1], S))
         lib.moe_balance_loss(_dense(logits), _dense(topk_ids if topk_ids.dtype == torch.int32 else topk_ids.to(torch.int32)),
                              None if seq_offsets is None else _dense(seq_offsets.to(torch.int32)),
                              None if token_mask is None else _dense(token_mask), alpha, out["counts"], out["probs"],
@@ -420,6 +428,6 @@ def orthogonalize(u: torch.Tensor, steps: int = 5, coeffs=None, eps: float = 1e-
             _is(out, "out", u.shape, (torch.bfloat16,), dev, True)
         v = _dense(u)
         v, y = (v, out) if u.dim() == 3 else (v[None], out[None])
-        ws = (workspace or Workspace(dev)).get(lib.moe_orthogonalize_workspace_size(*v.shape))
+        ws = _scratch(workspace, dev, lib.moe_orthogonalize_workspace_size(*v.shape))
         lib.moe_orthogonalize(v, steps, coeffs, eps, y, ws)
     return out

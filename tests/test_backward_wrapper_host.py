@@ -19,10 +19,9 @@ def test_copies_and_buffers_belong_to_the_stream_of_the_call(monkeypatch):
         yield
         where.pop()
 
-    class Seen(L.Workspace):
-        def get(self, nbytes):
-            assert where == [stream]
-            return torch.empty(256, dtype=torch.uint8)
+    def scratch(workspace, device, nbytes):
+        assert where == [stream] and workspace is None and device == torch.device("cpu")
+        return torch.empty(256, dtype=torch.uint8)
 
     def aux(desc, x, router_w, w_gate_up, w_down, ids, w, dy, dlogits, dx, dgu, dd, dr, db, ws, s=None):
         assert where == [stream] and s is None         # the context's own stream
@@ -34,7 +33,7 @@ def test_copies_and_buffers_belong_to_the_stream_of_the_call(monkeypatch):
     monkeypatch.setattr(torch.Tensor, "contiguous", lambda t: (where == [stream] or t.is_contiguous() or 1 / 0) and
                         contiguous(t))
     monkeypatch.setattr(L, "_on", on)
-    monkeypatch.setattr(L, "Workspace", Seen)
+    monkeypatch.setattr(L, "_scratch", scratch)
     monkeypatch.setattr(lib, "moe_backward_aux", aux)
     bf = dict(dtype=torch.bfloat16)
     inputs = dict(x=torch.randn(T, 2 * H).to(torch.bfloat16)[:, ::2], router_w=torch.zeros(E, H, **bf),
