@@ -421,8 +421,10 @@ moe_status moe_backward_aux(const moe_desc* d, const void* x, const void* router
  * FP8_E4M3: the fp32 values quantised as moe_quantize_input does (scale_mode
  * as there), codes in y and fp32 scales in y_scales [T][H/128], the layout
  * moe_forward takes.  mean and rstd [T] fp32: optional outputs, both or
- * neither, for moe_layer_norm_backward.  1 <= T, H a multiple of 128 up to
- * 16384, eps >= 0, for FP8 output finite x; pointers 16-byte aligned; y must
+ * neither, for moe_layer_norm_backward.  NaN and infinity in a row of x make its
+ * y NaN; with FP8 output (no code for it) its scales are NaN, and so are a block's
+ * where gamma or beta is not finite, whatever the codes.  1 <= T, H a multiple of 128 up to
+ * 16384, eps >= 0; pointers 16-byte aligned; y must
  * not overlap x.  Enqueued on `stream`; errors as moe_forward. */
 moe_status moe_layer_norm(int32_t T, int32_t H, int32_t in_dtype, int32_t out_dtype, int32_t scale_mode,
                           const void* x, const float* gamma, const float* beta, float eps, void* y, float* y_scales,

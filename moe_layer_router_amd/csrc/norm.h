@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(ln_threads(TPR)) k_layer_norm(LnArgs a) {
   const long step = (long)gridDim.x * RPW;
   long t = (long)blockIdx.x * RPW + threadIdx.x / TPR;
   float ga[R][8], be[R][8];
+  float bad[R];              // FP8: NaN where gamma or beta of the block is not finite, else 0
   LnRaw<IN> raw[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -135,6 +136,12 @@ __global__ void __launch_bounds__(ln_threads(TPR)) k_layer_norm(LnArgs a) {
     for (int i = 0; i < 8; ++i) {
       if (c >= nch) ga[r][i] = 0.f;
       if (c >= nch || !a.beta) be[r][i] = 0.f;
+    }
+    bad[r] = 0.f;
+    if (OUT == LN_FP8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) bad[r] += ga[r][i] * 0.f + be[r][i] * 0.f;
+      bad[r] = row_sum16(bad[r]);
     }
   }
   const float inv_h = 1.0f / (float)H;
@@ -194,6 +201,9 @@ __global__ void __launch_bounds__(ln_threads(TPR)) k_layer_norm(LnArgs a) {
         mx = row_max16(mx);
         float sc, inv;
         block_scale(mx, a.pow2 != 0, &sc, &inv);
+        // (the maximum and E4M3's clamp drop NaN: it goes into the scale; rstd is
+        // NaN where the row holds NaN or infinity, infinite where 0 / 0 follows)
+        sc += bad[r] + (rstd - rstd);
         if (c < nch) {
           *reinterpret_cast<v2u*>(static_cast<uint8_t*>(a.y) + e0) =
               v2u{f32x4_to_e4m3x4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv),
