@@ -321,8 +321,8 @@ def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, alpha: float = 1.
                  token_mask: torch.Tensor = None, want_grad: bool = True, workspace: Workspace = None, stream=None,
                  out: dict = None) -> dict:
     """Load-balance loss of a routing (moe_balance_loss): logits [T, E] float32
-    and topk_ids [T, k] as route() returns them, seq_offsets [S + 1] integers
-    (None: one sequence), token_mask [T] bool or uint8 (None: every token
+    and topk_ids [T, k] int32 or int64 as route() returns them, seq_offsets
+    [S + 1] int32 or int64 (None: one sequence; both clamped to their range), token_mask [T] bool or uint8 (None: every token
     counts).  Returns dict(loss [1] float32, counts [S, E] int32, probs [S, E]
     float32, dlogits [T, E] float32 or, without want_grad, None); `out`, a
     previous result, is reused."""
@@ -350,8 +350,12 @@ def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, alpha: float = 1.
                 if out[name] is not None:
                     _is(out[name], name, shape, (dt,), dev, True)
         ws = _scratch(workspace, dev, lib.moe_balance_loss_workspace_size(T, E, topk_ids.shape[1], S))
-        lib.moe_balance_loss(_dense(logits), _dense(topk_ids if topk_ids.dtype == torch.int32 else topk_ids.to(torch.int32)),
-                             None if seq_offsets is None else _dense(seq_offsets.to(torch.int32)),
+        # (the library clamps 32-bit values: wider ones must not wrap round into the range)
+        if topk_ids.dtype == torch.int64:
+            topk_ids = topk_ids.clamp(0, E - 1).to(torch.int32)
+        if seq_offsets is not None and seq_offsets.dtype == torch.int64:
+            seq_offsets = seq_offsets.clamp(0, T).to(torch.int32)
+        lib.moe_balance_loss(_dense(logits), _dense(topk_ids), None if seq_offsets is None else _dense(seq_offsets),
                              None if token_mask is None else _dense(token_mask), alpha, out["counts"], out["probs"],
                              out["loss"], out["dlogits"], ws)
     return out
