@@ -505,9 +505,11 @@ moe_status moe_balance_loss(int32_t T, int32_t E, int32_t top_k, int32_t n_seq, 
  * singular values below 2^-22 of the norm, rounding in an fp32 U, are lifted 2^22-fold at most.
  * 1 <= M, N <= 32768, the smaller <= 16384, 1 <= batch <=
  * 65535, 1 <= steps <= 32, eps > 0; pointers (not coeffs) 16-byte aligned.
- * workspace: moe_orthogonalize_workspace_size bytes (5 to 9 per element of u
- * and up to 128 MiB, at most 8 GiB or one matrix's; 0 for sizes that are
- * refused).  Enqueued on `stream`; errors as moe_forward. */
+ * workspace: moe_orthogonalize_workspace_size bytes (0 for sizes that are
+ * refused).  With m <= n the sides of a matrix rounded up to multiples of 64: 6 m n + 4
+ * m^2 + 512 bytes per matrix, for as many matrices at a time as 8 GiB hold (one at
+ * least), and up to 128 MiB of partial sums.  Where the smaller side is at most 64: 8 (p + 1) s^2
+ * per matrix of the batch, s the smaller side rounded up to 16, 32 or 64, p = min(16, n / 64).  Enqueued on `stream`; errors as moe_forward. */
 size_t moe_orthogonalize_workspace_size(int32_t batch, int32_t M, int32_t N);
 moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dtype, const void* u, int32_t steps,
                              const float* coeffs, float eps, void* y, void* workspace, size_t workspace_bytes,
