@@ -9,6 +9,7 @@ microbenchmarks).
 """
 
 import os
+import signal
 import subprocess
 import sys
 import tempfile
@@ -38,9 +39,19 @@ def build(verbose: bool = False) -> str:
         # one object per source, compiled side by side
         outs = [os.path.join(objs, os.path.basename(s) + ".o") for s in SOURCES]
         cmds = [[HIPCC, *FLAGS, "-c", s, "-o", o] for s, o in zip(SOURCES, outs)]
-        procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True) for c in cmds]
-        for c, p in zip(cmds, procs):
-            _finish(c, *p.communicate(), p.returncode, verbose)
+        procs = []
+        try:
+            for c in cmds:
+                procs.append(subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True,
+                                              start_new_session=True))
+            for c, p in zip(cmds, procs):
+                _finish(c, *p.communicate(), p.returncode, verbose)
+        finally:
+            # one failed: the others, with the compilers they started, end with it
+            for p in procs:
+                if p.poll() is None:
+                    os.killpg(p.pid, signal.SIGKILL)
+                    p.communicate()
         link = [HIPCC, *LINK_FLAGS, *outs, "-o", tmp]
         r = subprocess.run(link, capture_output=True, text=True)
         _finish(link, r.stdout, r.stderr, r.returncode, verbose)
