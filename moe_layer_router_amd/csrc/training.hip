@@ -123,13 +123,11 @@ moe_status check_balance(int32_t T, int32_t E, int32_t k, int32_t S) {
 
 template <int L, int NJ, int VEC, int GRAD>
 moe_status launch_bal(const BalArgs& a, const BalLayout& G, hipStream_t st) {
-  // one workgroup while it does the tokens in at most 8 passes and 2^15 logits, else three
-  // kernels (a call, one against three: E = 8 and 64, T = 512 15 us and 16, T = 768 19 and
-  // 16; E = 128, T = 256 14 and 17, T = 512 21 and 17; E = 256, T = 128 13 and 17, T =
-  // 256 19 and 17; E = 512, T = 64 14 and 18, T = 128 22 and 18; E = 1024, T = 16 11 and 19, T = 64 20 and 20)
+  // one workgroup while it does the tokens in at most 8 passes and 2^16 logits
+  // (a call of T = 512, E = 64: 15 us against 21; T = 512, E = 256: 31 against 21)
   constexpr int NT = L == 16 ? 1024 : 512;
   using One = BalTokens<L, NJ, VEC, GRAD, NT>;
-  if (a.S <= kBalSegs && a.T <= 8 * One::G && a.T * a.E <= 1 << 15) {
+  if (a.S <= kBalSegs && a.T <= 8 * One::G && a.T * a.E <= 1 << 16) {
     hipLaunchKernelGGL((k_bal_one<L, NJ, VEC, GRAD, NT>), dim3(1), dim3(NT), One::kLds + kBalSegs * a.E * 4, st, a);
     HIP_TRY(hipGetLastError());
     return MOE_OK;
