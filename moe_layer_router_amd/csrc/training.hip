@@ -123,8 +123,12 @@ moe_status check_balance(int32_t T, int32_t E, int32_t k, int32_t S) {
 
 template <int L, int NJ, int VEC, int GRAD>
 moe_status launch_bal(const BalArgs& a, const BalLayout& G, hipStream_t st) {
-  // one workgroup while it does the tokens in at most 8 passes and 2^16 logits
-  // (a call of T = 512, E = 64: 15 us against 21; T = 512, E = 256: 31 against 21)
+  // one workgroup while it does the tokens in at most 8 passes and 2^16 logits, else three
+  // kernels.  On the GPU alone the border is at 2^15 (one against three: E = 64, T = 512
+  // 15 us and 16, T = 768 20 and 16; E = 128, T = 256 14 and 16, T = 512 21 and 17; E = 256,
+  // T = 128 14 and 17, T = 256 20 and 17; E = 1024, T = 16 10 and 19, T = 64 20 and 19), but
+  // a call that allocates its outputs takes the host 21 to 24 us with three launches (T =
+  // 512, E = 128: 21 and 24; E = 256: 31 and 24).
   constexpr int NT = L == 16 ? 1024 : 512;
   using One = BalTokens<L, NJ, VEC, GRAD, NT>;
   if (a.S <= kBalSegs && a.T <= 8 * One::G && a.T * a.E <= 1 << 16) {
@@ -292,11 +296,16 @@ moe_status launch_orth_gemm(const OrthGemm& g, int batch, int cus, hipStream_t s
   if (big >= cus && 16 * big <= 5 * mid) return launch_orth_gemm<OrthBig, MODE>(g, batch, cus, st);
   if (mid >= cus) {
     // up to one workgroup per CU: a third stage in place of the second workgroup
-    // (4 x 1024 x 1024 348 -> 255 us, 16 x 512 x 2048 458 -> 346; with more tiles 812 ->
-    // 903 for 2048 x 7168), unless K is long enough for parts (X X^T of the same, 136
-    // tiles of K = 7168: 820 in three parts each, 869 whole)
+    // (4 x 1024 x 1024 337 -> 241 us, 20 x 450 x 900 379 -> 270; with more tiles 812 ->
+    // 903 for 2048 x 7168), unless a product is one matrix's, would leave a third of the CUs
+    // idle and has a K long enough for parts (whole tiles against three parts each, 136
+    // tiles of 2048 rows: K = 4160 614 us and 590, 7168 860 and 797, 14336 1386 and
+    // 1244).  The parts of a batch's matrices share less in the L2s (4 x 1024 x 8192
+    // 935 and 996), and with fewer CUs idle they gain nothing (2700 x 8192 1331 and
+    // 1352, 25 x 450 x 9000 1994 and 2262).
     const long tiles = orth_sym(MODE) ? ti * (ti + 1) / 2 * batch : mid;
-    if (tiles <= cus && !(orth_sym(MODE) && g.K > 4096)) return launch_orth_gemm<OrthMidDeep, MODE>(g, batch, cus, st);
+    const bool parts = orth_sym(MODE) && batch == 1 && 3 * tiles <= 2 * cus && g.K > 4096;
+    if (tiles <= cus && !parts) return launch_orth_gemm<OrthMidDeep, MODE>(g, batch, cus, st);
     return launch_orth_gemm<OrthMid, MODE>(g, batch, cus, st);
   }
   return launch_orth_gemm<OrthSmall, MODE>(g, batch, cus, st);
