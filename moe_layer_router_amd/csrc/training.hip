@@ -127,8 +127,8 @@ moe_status launch_bal(const BalArgs& a, const BalLayout& G, hipStream_t st) {
   // kernels.  On the GPU alone the border is at 2^15 (one against three: E = 64, T = 512
   // 15 us and 16, T = 768 20 and 16; E = 128, T = 256 14 and 16, T = 512 21 and 17; E = 256,
   // T = 128 14 and 17, T = 256 20 and 17; E = 1024, T = 16 10 and 19, T = 64 20 and 19), but
-  // a call that allocates its outputs takes the host 21 to 24 us with three launches (T =
-  // 512, E = 128: 21 and 24; E = 256: 31 and 24).
+  // a call that allocates its outputs takes the host 21 us with three launches (T = 512: E
+  // = 64 16 and 21, E = 128 21 and 21, E = 256 31 and 21; T = 64, E = 1024 20 and 21).
   constexpr int NT = L == 16 ? 1024 : 512;
   using One = BalTokens<L, NJ, VEC, GRAD, NT>;
   if (a.S <= kBalSegs && a.T <= 8 * One::G && a.T * a.E <= 1 << 16) {

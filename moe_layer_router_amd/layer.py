@@ -19,15 +19,16 @@ def pack_weights(inputs: dict, top_k: int = 1, stream=None) -> dict:
     desc = desc_from_inputs(inputs, top_k, layout="row_major")
     fp4 = desc.weight_dtype == lib.MOE_DTYPE_FP4_E2M1
     out = dict(inputs)
-    for which, w, sc in ((lib.MOE_WEIGHTS_GATE_UP, "w_gate_up", "w_gate_up_scales"),
-                         (lib.MOE_WEIGHTS_DOWN, "w_down", "w_down_scales")):
-        dst = torch.empty_like(inputs[w])
-        dst_sc = torch.empty_like(inputs[sc]) if fp4 else None
-        lib.moe_pack_weights(desc, which, inputs[w].contiguous(), inputs[sc].contiguous() if fp4 else None,
-                             dst, dst_sc, stream)
-        out[w] = dst
-        if fp4:
-            out[sc] = dst_sc
+    with _on(inputs["x"].device, stream):
+        for which, w, sc in ((lib.MOE_WEIGHTS_GATE_UP, "w_gate_up", "w_gate_up_scales"),
+                             (lib.MOE_WEIGHTS_DOWN, "w_down", "w_down_scales")):
+            dst = torch.empty_like(inputs[w])
+            dst_sc = torch.empty_like(inputs[sc]) if fp4 else None
+            lib.moe_pack_weights(desc, which, inputs[w].contiguous(), inputs[sc].contiguous() if fp4 else None,
+                                 dst, dst_sc)
+            out[w] = dst
+            if fp4:
+                out[sc] = dst_sc
     out["weights_packed"] = True
     return out
 
@@ -81,23 +82,24 @@ def forward(inputs: dict, top_k: int, mode: str = "mega", workspace: Workspace =
     desc = desc_from_inputs(inputs, top_k, mode, flags, inter_scale=inter_scale)
     dev = inputs["x"].device
     T, H, E, k = desc.T, desc.H, desc.E, desc.top_k
-    if out is None:
-        out = dict(y=torch.empty(T, H, dtype=torch.bfloat16, device=dev),
-                   topk_ids=torch.empty(T, k, dtype=torch.int32, device=dev),
-                   topk_weights=torch.empty(T, k, dtype=torch.float32, device=dev),
-                   expert_offsets=torch.empty(E + 1, dtype=torch.int32, device=dev) if want_perm else None,
-                   perm=torch.empty(T * k, dtype=torch.int32, device=dev) if want_perm else None)
-    if routing is not None:
-        out["topk_ids"].copy_(routing[0])
-        out["topk_weights"].copy_(routing[1])
-    ws = (workspace or Workspace(dev)).get(lib.moe_workspace_size(desc))
-    if trace:      # rows of workgroups that do not run must read as unused
-        reg = lib.moe_get_workspace_regions(desc)
-        ws[reg["trace"]: reg["trace"] + lib.MOE_TRACE_GROUPS * lib.MOE_TRACE_FIELDS * 8].zero_()
-    lib.moe_forward(desc, inputs["x"], inputs.get("x_scales"), inputs["router_w"], inputs.get("router_bias"),
-                    inputs["w_gate_up"], inputs.get("w_gate_up_scales"), inputs["w_down"],
-                    inputs.get("w_down_scales"), out["y"], out["topk_ids"], out["topk_weights"],
-                    out["expert_offsets"], out["perm"], ws, stream)
+    with _on(dev, stream):
+        if out is None:
+            out = dict(y=torch.empty(T, H, dtype=torch.bfloat16, device=dev),
+                       topk_ids=torch.empty(T, k, dtype=torch.int32, device=dev),
+                       topk_weights=torch.empty(T, k, dtype=torch.float32, device=dev),
+                       expert_offsets=torch.empty(E + 1, dtype=torch.int32, device=dev) if want_perm else None,
+                       perm=torch.empty(T * k, dtype=torch.int32, device=dev) if want_perm else None)
+        if routing is not None:
+            out["topk_ids"].copy_(routing[0])
+            out["topk_weights"].copy_(routing[1])
+        ws = _scratch(workspace, dev, lib.moe_workspace_size(desc))
+        if trace:      # rows of workgroups that do not run must read as unused
+            reg = lib.moe_get_workspace_regions(desc)
+            ws[reg["trace"]: reg["trace"] + lib.MOE_TRACE_GROUPS * lib.MOE_TRACE_FIELDS * 8].zero_()
+        lib.moe_forward(desc, inputs["x"], inputs.get("x_scales"), inputs["router_w"], inputs.get("router_bias"),
+                        inputs["w_gate_up"], inputs.get("w_gate_up_scales"), inputs["w_down"],
+                        inputs.get("w_down_scales"), out["y"], out["topk_ids"], out["topk_weights"],
+                        out["expert_offsets"], out["perm"], ws)
     out["workspace"] = ws
     out["desc"] = desc
     return out
@@ -122,9 +124,10 @@ def quantize_input(x: torch.Tensor, scale_mode: str = "f32", stream=None):
     """Per-token FP8 quantisation of [T, H] BF16 / fp32 activations
     (moe_quantize_input): returns (codes uint8 [T, H], scales float32 [T, H/128])."""
     T, H = x.shape
-    xq = torch.empty(T, H, dtype=torch.uint8, device=x.device)
-    xs = torch.empty(T, H // 128, dtype=torch.float32, device=x.device)
-    lib.moe_quantize_input(x.contiguous(), xq, xs, scale_mode, stream)
+    with _on(x.device, stream):
+        xq = torch.empty(T, H, dtype=torch.uint8, device=x.device)
+        xs = torch.empty(T, H // 128, dtype=torch.float32, device=x.device)
+        lib.moe_quantize_input(x.contiguous(), xq, xs, scale_mode)
     return xq, xs
 
 
@@ -133,17 +136,19 @@ def quantize_e5m6(x: torch.Tensor, scale_mode: str = "f32", stream=None):
     [T, H] bfloat16 / float32 tensor: (codes [T, 3H/2] uint8, scales
     [T, H/128] float32)."""
     T, H = x.shape
-    xq = torch.empty(T, H // 2 * 3, dtype=torch.uint8, device=x.device)
-    xs = torch.empty(T, H // 128, dtype=torch.float32, device=x.device)
-    lib.moe_quantize_e5m6(x.contiguous(), xq, xs, scale_mode, stream)
+    with _on(x.device, stream):
+        xq = torch.empty(T, H // 2 * 3, dtype=torch.uint8, device=x.device)
+        xs = torch.empty(T, H // 128, dtype=torch.float32, device=x.device)
+        lib.moe_quantize_e5m6(x.contiguous(), xq, xs, scale_mode)
     return xq, xs
 
 
 def dequantize_e5m6(xq: torch.Tensor, xs: torch.Tensor, stream=None) -> torch.Tensor:
     """float32 [T, H] values of E5M6 codes and their scales (moe_dequantize_e5m6)."""
     T, H = xq.shape[0], xq.shape[1] // 3 * 2
-    out = torch.empty(T, H, dtype=torch.float32, device=xq.device)
-    lib.moe_dequantize_e5m6(xq.contiguous(), xs.contiguous(), out, stream)
+    with _on(xq.device, stream):
+        out = torch.empty(T, H, dtype=torch.float32, device=xq.device)
+        lib.moe_dequantize_e5m6(xq.contiguous(), xs.contiguous(), out)
     return out
 
 
@@ -390,12 +395,13 @@ def route(inputs: dict, top_k: int, E: int, I: int = 128, workspace: Workspace =
     act = "bf16" if x.dtype == torch.bfloat16 else "fp8"
     desc = lib.make_desc(T, H, E, I, top_k, act, "bf16" if act == "bf16" else "fp8")
     dev = x.device
-    out = dict(logits=torch.empty(T, E, dtype=torch.float32, device=dev),
-               topk_ids=torch.empty(T, top_k, dtype=torch.int32, device=dev),
-               topk_weights=torch.empty(T, top_k, dtype=torch.float32, device=dev))
-    ws = (workspace or Workspace(dev)).get(lib.moe_route_workspace_size(desc))
-    lib.moe_route(desc, x, inputs.get("x_scales"), inputs["router_w"], inputs.get("router_bias"),
-                  out["logits"], out["topk_ids"], out["topk_weights"], ws, stream)
+    with _on(dev, stream):
+        out = dict(logits=torch.empty(T, E, dtype=torch.float32, device=dev),
+                   topk_ids=torch.empty(T, top_k, dtype=torch.int32, device=dev),
+                   topk_weights=torch.empty(T, top_k, dtype=torch.float32, device=dev))
+        ws = _scratch(workspace, dev, lib.moe_route_workspace_size(desc))
+        lib.moe_route(desc, x, inputs.get("x_scales"), inputs["router_w"], inputs.get("router_bias"),
+                      out["logits"], out["topk_ids"], out["topk_weights"], ws)
     return out
 
 
@@ -404,12 +410,13 @@ def permute(topk_ids: torch.Tensor, E: int, H: int = 128, I: int = 128, workspac
     T, k = topk_ids.shape
     desc = lib.make_desc(T, H, E, I, k, "fp8", "fp8")
     dev = topk_ids.device
-    out = dict(expert_offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
-               perm=torch.empty(T * k, dtype=torch.int32, device=dev),
-               row_of=torch.empty(T * k, dtype=torch.int32, device=dev))
-    ws = (workspace or Workspace(dev)).get(lib.moe_permute_workspace_size(desc))
-    lib.moe_permute(desc, topk_ids.to(torch.int32).contiguous(), out["expert_offsets"], out["perm"],
-                    out["row_of"], ws, stream)
+    with _on(dev, stream):
+        out = dict(expert_offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
+                   perm=torch.empty(T * k, dtype=torch.int32, device=dev),
+                   row_of=torch.empty(T * k, dtype=torch.int32, device=dev))
+        ws = _scratch(workspace, dev, lib.moe_permute_workspace_size(desc))
+        lib.moe_permute(desc, topk_ids.to(torch.int32).contiguous(), out["expert_offsets"], out["perm"],
+                        out["row_of"], ws)
     return out
 
 
