@@ -404,8 +404,8 @@ moe_status moe_backward(const moe_desc* d, const void* x, const void* router_w, 
 /* moe_backward with an additional gradient of the router logits, dlogits
  * [T][E] fp32 (NULL = moe_backward), such as moe_balance_loss gives:
  *   dl[t][e] = the layer's (above, at the selected experts) + dlogits[t][e]
- * goes into dW_router, dbias and dx.  Everything else as moe_backward (the
- * same workspace). */
+ * goes into dW_router, dbias and dx, the sum in the same two BF16 parts.  No
+ * output may overlap dlogits.  Everything else as moe_backward (the same workspace). */
 moe_status moe_backward_aux(const moe_desc* d, const void* x, const void* router_w, const void* w_gate_up,
                             const void* w_down, const int32_t* topk_ids, const float* topk_weights, const void* dy,
                             const float* dlogits, float* dx, float* dw_gate_up, float* dw_down, float* dw_router,
@@ -423,9 +423,10 @@ moe_status moe_backward_aux(const moe_desc* d, const void* x, const void* router
  * moe_forward takes.  mean and rstd [T] fp32: optional outputs, both or
  * neither, for moe_layer_norm_backward.  NaN and infinity in a row of x make its
  * y NaN; with FP8 output (no code for it) its scales are NaN, and so are a block's
- * where gamma or beta is not finite, whatever the codes.  1 <= T, H a multiple of 128 up to
- * 16384, eps >= 0; pointers 16-byte aligned; y must
- * not overlap x.  Enqueued on `stream`; errors as moe_forward. */
+ * where gamma or beta is not finite, whatever the codes.  The squares of a row's
+ * deviations must fit fp32 (deviations up to 2^63 / sqrt(H), with eps = 0 from 2^-62
+ * on): past it rstd is 0 or infinite.  1 <= T, H a multiple of 128 up to 16384, eps >=
+ * 0; pointers 16-byte aligned; outputs must overlap neither each other nor an input.  Enqueued on `stream`; errors as moe_forward. */
 moe_status moe_layer_norm(int32_t T, int32_t H, int32_t in_dtype, int32_t out_dtype, int32_t scale_mode,
                           const void* x, const float* gamma, const float* beta, float eps, void* y, float* y_scales,
                           float* mean, float* rstd, moe_stream_t stream);
@@ -435,9 +436,9 @@ moe_status moe_layer_norm(int32_t T, int32_t H, int32_t in_dtype, int32_t out_dt
  *   dgamma = sum_t dy[t] * z[t],  dbeta = sum_t dy[t]
  * x [T][H] (x_dtype BF16 or F32) and gamma, mean, rstd as in the forward
  * call; dy [T][H] (dy_dtype BF16 or F32), e.g. the dx of moe_backward.
- * Outputs (fp32, overwritten): dx [T][H] (dx may be dy where dy is fp32; no
- * other overlap with x or dy), dgamma [H] and dbeta [H] (each optional, NULL = not
- * computed).  Limits as moe_layer_norm.  workspace: of
+ * Outputs (fp32, overwritten): dx [T][H] (dx may be dy where dy is fp32), dgamma
+ * [H] and dbeta [H] (each optional, NULL = not computed); no other overlap of outputs,
+ * inputs and workspace.  Limits as moe_layer_norm.  workspace: of
  * moe_layer_norm_backward_workspace_size(T, H) bytes (0 for a shape that is
  * refused), not needed when neither dgamma nor dbeta is asked for.
  * Enqueued on `stream`. */
@@ -468,9 +469,12 @@ moe_status moe_layer_norm_backward(int32_t T, int32_t H, int32_t x_dtype, int32_
  * moe_forward's workspace); topk_ids [T][top_k] int32 (ids out of range are
  * clamped, as in moe_permute).  Outputs, overwritten: counts [n_seq][E] int32,
  * probs [n_seq][E] fp32, loss [1] fp32, and dlogits [T][E] fp32 (optional,
- * NULL = not computed; must not overlap logits).  Sums are fp32 (the loss
- * fp64) in a fixed order: identical inputs give identical bits.  1 <= T,
- * 1 <= top_k <= min(E, 16), E <= 1024, T * top_k <= 2^30, 1 <= n_seq <= 2^20.
+ * NULL = not computed); outputs, inputs and workspace must not overlap.  Sums are
+ * fp32 (the loss fp64) in a fixed order: identical inputs give identical bits.  1 <= T,
+ * 1 <= top_k <= min(E, 16), E <= 1024, T * top_k <= 2^30, 1 <= n_seq <= 2^20.  The time
+ * grows with n_seq from a few hundred on (up to 1024 workgroups each go through all
+ * sequences, one through the empty ones: T = 65536, E = 64 takes 53 us for 16
+ * sequences, 0.44 ms for 4096, 6.3 ms for 65536, 0.3 s for 2^20 of which most are empty).
  * workspace: moe_balance_loss_workspace_size bytes (0 for arguments that are
  * refused).  Enqueued on `stream`; errors as moe_forward. */
 size_t moe_balance_loss_workspace_size(int32_t T, int32_t E, int32_t top_k, int32_t n_seq);
@@ -491,25 +495,31 @@ moe_status moe_balance_loss(int32_t T, int32_t E, int32_t top_k, int32_t n_seq, 
  * (MOE_ERR_UNSUPPORTED).  A zero matrix gives zero.
  * u [batch][M][N] row-major (in_dtype BF16 or F32): dw_gate_up [E][2I][H] is
  * batch = 2E gate and up matrices of I x H, dw_down [E][H][I] E matrices, and
- * dw_router one.  y [batch][M][N] BF16 (output, must not overlap u).  The
- * products are FP16 matrix-core products with fp32 accumulation on scaled
- * values, X is held in 22 bits and the norm in fp64.  With the default coefficients and 5 steps y
- * is within 4e-3 of the exact iteration in the Frobenius norm, 1.7e-3 of it y's
- * own rounding, for matrices of any rank, and within 1.3e-2 for those of one magnitude,
- * whose elements all round alike; after 8 steps within 6e-3 and 1.6e-2.  What
- * rounding leaves in directions that U lacks, each step lifts by its a, as in an
- * fp32 iteration: with P the product of the steps' |a|, up to P sqrt(min(M, N))
- * 2^-26 more (with the default coefficients and 2048 rows 3e-4 after 5 steps, 1.3e-2
- * after 8, 5e-1 after 11).  Where the smaller of M and N is at most 64 all of it is
- * in fp64 and y is the exact iteration's result, rounded, for any steps; only
- * singular values below 2^-22 of the norm, rounding in an fp32 U, are lifted 2^22-fold at most.
- * 1 <= M, N <= 32768, the smaller <= 16384, 1 <= batch <=
- * 65535, 1 <= steps <= 32, eps > 0; pointers (not coeffs) 16-byte aligned.
+ * dw_router one.  y [batch][M][N] BF16 (output, overwritten).
+ * Accuracy.  Where the smaller of M and N is above 64 the products are FP16
+ * matrix-core products with fp32 accumulation on scaled values, X is held in 22 bits
+ * and the norm in fp64.  With the default coefficients and 5 steps y is within 4e-3 of
+ * the exact iteration in the Frobenius norm, 1.7e-3 of it y's own rounding, for
+ * matrices of any rank, and within 1.3e-2 for those of one magnitude, whose elements
+ * all round alike; after 8 steps within 6e-3 and 1.6e-2, after 32 within 1e-2 for
+ * full rank.  What rounding leaves in directions that U lacks, each step lifts by its
+ * a, as in an fp32 iteration: with P the product of the steps' |a|, up to P sqrt(min(M,
+ * N)) 2^-26 more (with the default coefficients and 2048 rows 3e-4 after 5 steps,
+ * 1.3e-2 after 8, 5e-1 after 11; y's singular values stay within the polynomial's
+ * range).  These hold for |U|_F from eps / 1024 on: further below eps X's FP16 parts run
+ * out of small numbers.  Where the smaller side is at most 64 all of it is in fp64
+ * and y is the exact iteration's result, rounded, for any steps; only singular values below
+ * 2^-22 of the norm, rounding in an fp32 U, are lifted 2^22-fold at most.  NaN and
+ * infinity stay within their matrix.
+ * 1 <= M, N <= 32768, the smaller <= 16384, 1 <= batch <= 65535, 1 <= steps <= 32,
+ * eps > 0; pointers (not coeffs) 16-byte aligned; y and the workspace must overlap
+ * neither each other nor u.
  * workspace: moe_orthogonalize_workspace_size bytes (0 for sizes that are
- * refused).  With m <= n the sides of a matrix rounded up to multiples of 64: 6 m n + 4
- * m^2 + 512 bytes per matrix, for as many matrices at a time as 8 GiB hold (one at
- * least), and up to 128 MiB of partial sums.  Where the smaller side is at most 64: 8 (p + 1) s^2
- * per matrix of the batch, s the smaller side rounded up to 16, 32 or 64, p = min(16, n / 64).  Enqueued on `stream`; errors as moe_forward. */
+ * refused).  With m <= n the sides of a matrix rounded up to multiples of 64: 6 m n +
+ * 4 m^2 + 512 bytes per matrix, for as many matrices at a time as 8 GiB hold (one
+ * at least), and up to 128 MiB of partial sums.  Where the smaller side is at most 64:
+ * 8 (p + 1) s^2 per matrix of the batch, s the smaller side rounded up to 16, 32 or
+ * 64, p = min(16, n / 64).  Enqueued on `stream`; errors as moe_forward. */
 size_t moe_orthogonalize_workspace_size(int32_t batch, int32_t M, int32_t N);
 moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dtype, const void* u, int32_t steps,
                              const float* coeffs, float eps, void* y, void* workspace, size_t workspace_bytes,

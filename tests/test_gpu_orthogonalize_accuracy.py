@@ -40,17 +40,23 @@ def _poly(s, steps, coeffs=None):
     return s
 
 
-def low_rank(M, N, r, seed):
-    """(U exact in fp32, function of the steps: the exact result)."""
+def low_rank(M, N, r, seed, ratio=None):
+    """(U exact in fp32, function of the steps: the exact result); its eps is
+    1e-7, or ratio |U|, as exact.eps."""
     rng = np.random.default_rng(seed)
     p, q = np.rint(4 * rng.normal(size=(M, r))), np.rint(4 * rng.normal(size=(N, r)))
     qp, rp = np.linalg.qr(p)
     qq, rq = np.linalg.qr(q)
     a, s, b = np.linalg.svd(rp @ rq.T)
-    s /= np.linalg.norm(s) + 1e-7
+    eps = 1e-7 if ratio is None else float(np.float32(ratio * np.linalg.norm(s)))
+    s /= np.linalg.norm(s) + eps
     u = (p @ q.T).astype(np.float32)
     assert np.array_equal(u, p @ q.T)
-    return torch.from_numpy(u).cuda(), lambda steps: ((qp @ a) * _poly(s, steps)) @ (b @ qq.T)
+
+    def exact(steps):
+        return ((qp @ a) * _poly(s, steps)) @ (b @ qq.T)
+    exact.eps = eps
+    return torch.from_numpy(u).cuda(), exact
 
 
 def _error(y, ref):
@@ -113,3 +119,41 @@ def test_norms_at_the_ends_of_fp32(gpu_lib):
             u = (base.astype(np.float64) * scale).astype(np.float32)
             y = L.orthogonalize(torch.from_numpy(u).cuda(), eps=1e-44)
             assert _error(y, R.orthogonalize(u, 5, None, float(np.float32(1e-44)))) <= 4e-3, (M, N, scale)
+
+
+@pytest.mark.parametrize("M,N", [(65, 65), (96, 200), (256, 512)])
+def test_many_steps(gpu_lib, M, N):
+    """Full rank: the roundings of each step (7e-3 after 32 steps in the simulation
+    above) and y's stay within 1e-2.  Low rank: what is lifted ends in the
+    polynomial's range, singular values up to 1.2 and their roundings."""
+    from moe_layer_router_amd import layer as L
+    rng = np.random.default_rng(5)
+    u = torch.from_numpy(rng.normal(size=(M, N)).astype(np.float32)).cuda()
+    low, _ = low_rank(M, N, 1, 7)
+    for steps in (16, 32):
+        assert _error(L.orthogonalize(u, steps=steps), R.orthogonalize(u.cpu().numpy(), steps)) <= 1e-2, steps
+        y = L.orthogonalize(low, steps=steps).cpu().double().numpy()
+        assert np.all(np.isfinite(y)) and np.linalg.norm(y, 2) <= 1.25, steps
+
+
+@pytest.mark.parametrize("M,N", [(96, 160), (2048, 7168)])
+def test_norms_below_eps(gpu_lib, M, N):
+    """|U| = eps / 1024: X_0's elements are small FP16 numbers."""
+    from moe_layer_router_amd import layer as L
+    for r in (1, 16):
+        u, exact = low_rank(M, N, r, 3, 1024)
+        assert _error(L.orthogonalize(u, eps=exact.eps), exact(5)) <= 4e-3, r
+
+
+@pytest.mark.parametrize("M,N", [(65, 65), (130, 100), (200, 333), (256, 1000), (512, 300), (960, 2100)])
+def test_full_rank(gpu_lib, M, N):
+    """Gaussian matrices and singular values 1 / r, held to the documented bounds."""
+    from moe_layer_router_amd import layer as L
+    g = np.random.default_rng(M).normal(size=(M, N))
+    a, s, b = np.linalg.svd(g, full_matrices=False)
+    for u in (g, (a / np.arange(1, len(s) + 1)) @ b):
+        for dtype in (torch.float32, torch.bfloat16):
+            t = torch.from_numpy(u).to(dtype).cuda()
+            for steps, bound in ((5, 4e-3), (8, 6e-3)):
+                ref = R.orthogonalize(t.double().cpu().numpy(), steps)
+                assert _error(L.orthogonalize(t, steps=steps), ref) <= bound, (dtype, steps)
