@@ -15,9 +15,10 @@
 // Every sum is fp32.
 //
 // Measured (T = 8192, H = 7168): forward BF16 -> BF16 41 to 45 us (5.2 to 5.7 TB/s; a
-// large copy reaches 5.2), to FP8 53 us (3.3 TB/s, the conversions), backward of
-// BF16 x and fp32 dy with the weight gradients 111 + 5 us (5.2 TB/s).  One token:
-// 3.3 us, a launch.
+// large copy reaches 5.2), to FP8 52 to 55 us (3.2 TB/s; with as many elements at H =
+// 4096 39 to 42: its vector instructions, 1.7 times those of BF16 output, take 0.7 of
+// the SIMDs' time by the counters), backward of BF16 x and fp32 dy with the weight
+// gradients 112 + 5 us (5.2 TB/s).  One token: 3.6 us, a launch.
 #pragma once
 #include "device_common.h"
 #include "quant.h"

@@ -51,14 +51,14 @@
 // 2^22-fold at most, and no other is off by more than 2^-45 / s.
 //
 // Measured (5 steps).  Large matrices are bound by the matrix cores: 8 x 2048 x
-// 7168 takes 4.45 ms, 887 TFLOP/s, where one large FP16 library product reaches
-// 1390: norm 95 us (4.9 TB/s), load 140 (5.9), then per step X X^T 240 + 13 (its
-// parts), the polynomial 88 + 14, the step 550 (the last 485).  A step's products
+// 7168 takes 4.5 to 4.8 ms, by card, 820 to 875 TFLOP/s, where one large FP16 library
+// product reaches 1390: norm 96 us (4.9 TB/s), load 220 (4.3), then per step X X^T 248 + 13
+// (its parts), the polynomial 89 + 15, the step 547 (the last 491).  A step's products
 // alone take 380 us; its tile ends, where the one workgroup of a CU stores and
 // multiplies nothing, the rest.  Small ones are bound by their 17 to 22 dependent
-// launches of 4 to 6 us: 8 x 256 x 256 75 us, 256 x 7168 131 us.  Narrow: 16 x 64 x
-// 7168 24 + 52 + 33 us, bound by fp64 (its 17 products on one CU each take 2 us at
-// the peak rate, 3 here).
+// launches of 4 to 6 us: 8 x 256 x 256 76 us, 256 x 7168 135 us.  Narrow: 16 x 64 x
+// 7168 23 + 53 + 32 us, bound by fp64 (its 17 products on one CU each take 2 us at
+// the peak rate, 3 here; the last kernel's product 12 of its 32).
 #pragma once
 #include "device_common.h"
 #include "norm.h"
@@ -332,8 +332,8 @@ DEV void orth_store_gram(const OrthGemm& g, int mat, int i0, int j0, bool mirror
 // 16-byte pieces, 64 bytes at a time, columns (the mirror image, and a result
 // whose orientation is the other) in 8-byte pieces, 128 bytes at a time.  This
 // stores the columns of j = 2 p and 2 p + 1.  (With 64 columns alternating in the
-// same way a row of hi has 128 bytes in two stores and one of lo 64 in one:
-// slower, 4555 -> 4640 us for 8 x 2048 x 7168.)
+// same way a row has 128 bytes in two stores: slower, 4555 -> 4640 us for 8 x 2048
+// x 7168, measured with a lo of 8 bits.)
 template <class TL, int MODE>
 DEV void orth_store(const OrthGemm& g, int mat, int i0, int j0, bool mirror, int w, int lane, int p,
                     const v4f (&acc)[4][2], const v4i (&lq)[4]) {

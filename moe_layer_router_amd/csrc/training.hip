@@ -291,13 +291,13 @@ moe_status launch_orth_gemm(const OrthGemm& g, int batch, int cus, hipStream_t s
   const long big = (long)((g.rows + 255) / 256) * ((g.cols + 255) / 256) * batch;
   const long ti = (g.rows + 127) / 128, tj = (g.cols + 127) / 128, mid = ti * tj * batch;
   // the large tiles unless they cover a quarter more than the middle ones do
-  // (16 x 640 x 1400, a third more: 412 us, with the middle ones 357; 64 x 300 x 700
-  // 432 and 311; 8 x 2048 x 7168, the same: 4.54 ms, with the middle ones 5.00)
+  // (16 x 640 x 1400, a third more: 429 us, with the middle ones 363; 64 x 300 x 700
+  // 441 and 317; 8 x 2048 x 7168, the same: 4.62 ms, with the middle ones 5.15)
   if (big >= cus && 16 * big <= 5 * mid) return launch_orth_gemm<OrthBig, MODE>(g, batch, cus, st);
   if (mid >= cus) {
     // up to one workgroup per CU: a third stage in place of the second workgroup
-    // (4 x 1024 x 1024 337 -> 241 us, 20 x 450 x 900 379 -> 270; with more tiles 812 ->
-    // 903 for 2048 x 7168), unless a product is one matrix's, would leave a third of the CUs
+    // (4 x 1024 x 1024 337 -> 241 us, 20 x 450 x 900 379 -> 270; with more tiles 796 ->
+    // 946 for 2048 x 7168), unless a product is one matrix's, would leave a third of the CUs
     // idle and has a K long enough for parts (whole tiles against three parts each, 136
     // tiles of 2048 rows: K = 4160 614 us and 590, 7168 860 and 797, 14336 1386 and
     // 1244).  The parts of a batch's matrices share less in the L2s (4 x 1024 x 8192
