@@ -1,5 +1,6 @@
-"""The backward pass on a stream that is not the current one, fed strided and
-misaligned views, while the current stream allocates and writes."""
+"""The layer, its backward pass and its conversions on a stream that is not the
+current one, fed strided and misaligned views, while the current stream allocates and
+writes."""
 
 import pytest
 import torch
@@ -36,3 +37,34 @@ def test_side_stream_with_views(gpu_lib):
             for k in ref:
                 assert torch.equal(got[k], ref[k]), k
             del junk
+
+
+def test_the_layer_and_its_conversions_on_a_side_stream(gpu_lib):
+    from moe_layer_router_amd import layer as L
+    cfg = gen.LayerConfig("side", 200, 512, 16, 4, 256, "fp8", "fp8")
+    raw = to_dev(gen.make_inputs(cfg, seed=3))
+    h = torch.randn(cfg.T, cfg.H, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).cuda()
+    strided = h.t().contiguous().t()
+
+    def run(s, x):
+        inp = L.pack_weights(raw, stream=s)
+        q, qs = L.quantize_input(x, stream=s)
+        e, es = L.quantize_e5m6(x, stream=s)
+        d = L.dequantize_e5m6(e, es, stream=s)
+        f = L.forward({**inp, "x": q.view(inp["x"].dtype), "x_scales": qs}, cfg.k, stream=s)
+        r = L.route({**inp, "x": q.view(inp["x"].dtype), "x_scales": qs}, cfg.k, cfg.E, stream=s)
+        p = L.permute(r["topk_ids"], cfg.E, stream=s)
+        g = L.forward({**inp, "x": q.view(inp["x"].dtype), "x_scales": qs}, cfg.k, stream=s,
+                      routing=(r["topk_ids"], r["topk_weights"]))
+        return [q, qs, d, f["y"], f["topk_ids"], r["logits"], r["topk_weights"], p["perm"], p["expert_offsets"], g["y"]]
+
+    ref = run(None, h)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for s in (side, side.cuda_stream):
+        got = run(s, strided)
+        junk = [torch.full((1 << 22,), -1.0, device="cuda") for _ in range(16)]
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(got, ref)):
+            assert torch.equal(a, b), i
+        del junk
