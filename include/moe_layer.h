@@ -483,6 +483,76 @@ moe_status moe_balance_loss(int32_t T, int32_t E, int32_t top_k, int32_t n_seq, 
                             float alpha, int32_t* counts, float* probs, float* loss, float* dlogits, void* workspace,
                             size_t workspace_bytes, moe_stream_t stream);
 
+/* Selection of experts from router logits by scores of their own, where
+ * moe_route's (a softmax over the selected logits) is not the model's rule: a
+ * bias that evens the experts' load without touching the weights, groups of
+ * experts (of one device, say) of which a token uses a few, weights that need
+ * not add up to one.  For each token, from logits l [T][E] fp32 (moe_route's
+ * output, or the logits region of a workspace):
+ *   s[e] = sigmoid(l[e])  or  softmax(l)[e] over all E
+ *   c[e] = s[e] + bias[e]                       (bias [E] fp32, NULL = zero)
+ *   the n_group groups are E / n_group consecutive experts each; a group's
+ *     score is the sum of its group_top (1 or 2) largest c; the topk_group
+ *     best groups stay (ties to the lower group; n_group = 1: all experts)
+ *   topk_ids     = the top_k experts by c among them, descending, ties to the
+ *     lower index; without a bias by l, which s follows
+ *   topk_weights = scale * s[id] / sum of s over the selected (renormalize),
+ *     or scale * s[id]
+ * Scores, group scores and what is compared are those of 64-bit arithmetic, so
+ * that near-ties are not decided by fp32 rounding; weights are fp32 (with
+ * renormalize also where all scores underflow).  A NaN is ordered as -infinity;
+ * it makes the weights NaN that it enters.  With renormalize, selected scores
+ * that are all zero (logits of -infinity) give zero weights; with softmax a row
+ * of -infinity has zero scores.  A bias of -infinity takes an expert out as
+ * long as others are left.  Output goes to moe_forward with
+ * MOE_FLAG_ROUTING_GIVEN.
+ * T >= 1, 1 <= E <= 1024, 1 <= top_k <= 16, n_group <= 64 dividing E, top_k <=
+ * topk_group * E / n_group, group_top at most a group's size, scale finite;
+ * pointers 16-byte aligned; outputs overlap neither each other nor an input.
+ * Enqueued on `stream`; errors as moe_forward. */
+typedef enum moe_scoring {
+  MOE_SCORING_SOFTMAX = 0,
+  MOE_SCORING_SIGMOID = 1
+} moe_scoring;
+typedef struct moe_selection {
+  int32_t T, E, top_k;
+  int32_t scoring;       /* moe_scoring                                     */
+  int32_t n_group;       /* 1 = no groups                                   */
+  int32_t topk_group;
+  int32_t group_top;     /* 1 or 2                                          */
+  int32_t renormalize;   /* nonzero: divide by the sum of the selected s    */
+  float scale;
+} moe_selection;
+moe_status moe_select_experts(const moe_selection* s, const float* logits, const float* bias, int32_t* topk_ids,
+                              float* topk_weights, moe_stream_t stream);
+
+/* Gradient of sum(dweights * topk_weights) in the logits, the selection held
+ * fixed (so the bias and the groups have none): with d_j = scale dweights_j,
+ * and with renormalize d_j = scale (dweights_j - sum_i q_i dweights_i) / sum_i
+ * s_i, q = s / sum s over the selected,
+ *   sigmoid:  dlogits[id_j] = d_j s_j (1 - s_j)
+ *   softmax:  dlogits[e]    = s_e ([e = id_j] d_j - sum_i s_i d_i)
+ * and zero elsewhere.  topk_ids [T][top_k] (clamped to [0, E); an id that stands
+ * twice has both entries' sum) and dweights [T][top_k] fp32; dlogits [T][E] fp32
+ * (output, overwritten), meant for moe_backward_aux where another kernel made
+ * dweights; moe_backward_selected does the whole.  Limits and errors as
+ * moe_select_experts; the groups are checked and not used. */
+moe_status moe_select_experts_backward(const moe_selection* s, const float* logits, const int32_t* topk_ids,
+                                       const float* dweights, float* dlogits, moe_stream_t stream);
+
+/* moe_backward_aux for a layer whose routing moe_select_experts made: topk_ids and
+ * topk_weights are its output for `logits` [T][E] fp32, the router's x W_r^T + bias,
+ * and the router's gradient goes through that selection,
+ *   dl = moe_select_experts_backward(dw) (+ dlogits),  dw as in moe_backward,
+ * into dw_router, dbias and dx.  s->T, s->E and s->top_k are the descriptor's.
+ * Everything else as moe_backward_aux (the same workspace). */
+moe_status moe_backward_selected(const moe_desc* d, const moe_selection* s, const void* x, const void* router_w,
+                                 const void* w_gate_up, const void* w_down, const float* logits,
+                                 const int32_t* topk_ids, const float* topk_weights, const void* dy,
+                                 const float* dlogits, float* dx, float* dw_gate_up, float* dw_down,
+                                 float* dw_router, float* dbias, void* workspace, size_t workspace_bytes,
+                                 moe_stream_t stream);
+
 /* Newton-Schulz orthogonalisation of the updates of weight matrices, the
  * matrix step of the Muon optimiser for the gradients (or momenta) of the
  * layer's matrices: for each of the `batch` matrices U (M x N)

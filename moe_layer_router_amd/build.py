@@ -18,7 +18,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB_DIR = PKG
 LIB = os.path.join(LIB_DIR, "libmoe_layer.so")
-SOURCES = [os.path.join(PKG, "csrc", f) for f in ("kernels.hip", "training.hip", "peaks.hip")]
+SOURCES = [os.path.join(PKG, "csrc", f) for f in ("kernels.hip", "training.hip", "select.hip", "peaks.hip")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -9,6 +9,7 @@
 // streaming and MFMA work of different work items running side by side.
 #include "kernels.h"
 #include "backward.h"
+#include "select_host.h"
 
 namespace moe {
 
@@ -1219,18 +1220,13 @@ size_t moe_backward_workspace_size(const moe_desc* d) {
   return bwd_layout(d).total;
 }
 
-moe_status moe_backward(const moe_desc* d, const void* x, const void* router_w, const void* w_gate_up,
-                        const void* w_down, const int32_t* topk_ids, const float* topk_weights, const void* dy,
-                        float* dx, float* dw_gate_up, float* dw_down, float* dw_router, float* dbias,
-                        void* workspace, size_t workspace_bytes, moe_stream_t stream) {
-  return moe_backward_aux(d, x, router_w, w_gate_up, w_down, topk_ids, topk_weights, dy, nullptr, dx, dw_gate_up,
-                          dw_down, dw_router, dbias, workspace, workspace_bytes, stream);
-}
-
-moe_status moe_backward_aux(const moe_desc* d, const void* x, const void* router_w, const void* w_gate_up,
-                            const void* w_down, const int32_t* topk_ids, const float* topk_weights, const void* dy,
-                            const float* dlogits, float* dx, float* dw_gate_up, float* dw_down, float* dw_router,
-                            float* dbias, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+// The backward pass; the router's gradient through its own softmax over the
+// selection, or (s not NULL) through moe_select_experts.
+static moe_status backward_impl(const moe_desc* d, const moe_selection* s, const void* x, const void* router_w,
+                                const void* w_gate_up, const void* w_down, const float* logits,
+                                const int32_t* topk_ids, const float* topk_weights, const void* dy,
+                                const float* dlogits, float* dx, float* dw_gate_up, float* dw_down, float* dw_router,
+                                float* dbias, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
   TRY(check_bwd_desc(d));
   TRY(check_ptr(x, "x"));
   TRY(check_ptr(router_w, "router_w"));
@@ -1246,6 +1242,12 @@ moe_status moe_backward_aux(const moe_desc* d, const void* x, const void* router
   TRY(check_ptr(dw_router, "dw_router"));
   TRY(check_ptr(dbias, "dbias", false));
   TRY(check_ptr(workspace, "workspace"));
+  SelArgs sel{};
+  if (s) {
+    TRY(select_bwd_args(s, logits, topk_ids, &sel));
+    if (s->T != d->T || s->E != d->E || s->top_k != d->top_k)
+      return fail(MOE_ERR_INVALID_ARGUMENT, "the selection's T, E and top_k are not the descriptor's");
+  }
   const BwdLayout B = bwd_layout(d);
   if (workspace_bytes < B.total)
     return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, needs %zu", workspace_bytes, B.total);
@@ -1271,12 +1273,12 @@ moe_status moe_backward_aux(const moe_desc* d, const void* x, const void* router
   float* dxr = reinterpret_cast<float*>(ws + B.dxr);
 
   // counters, then the dense logit gradients (the additional ones or zero;
-  // the layer's own are written at the selected entries)
+  // the layer's own are written at the selected entries; a selection's gradient writes all of them)
   hipLaunchKernelGGL(k_zero, dim3(16), dim3(256), 0, st, p.err, (p.zero_bytes + 256) / 4);
   HIP_TRY(hipGetLastError());
-  if (dlogits)
+  if (!s && dlogits)
     hipLaunchKernelGGL(k_bwd_split, dim3(di.cus * 4), dim3(256), 0, st, dlogits, (size_t)T * E, dl_hi, dl_lo);
-  else
+  else if (!s)
     hipLaunchKernelGGL(k_bwd_zero, dim3(di.cus * 4), dim3(256), 0, st, reinterpret_cast<uint32_t*>(dl_hi),
                        (B.dxr - B.dl) / 4);      // both parts
   HIP_TRY(hipGetLastError());
@@ -1337,9 +1339,14 @@ moe_status moe_backward_aux(const moe_desc* d, const void* x, const void* router
   TRY(launch_bwd_gemm(g, up(I, kBwdBM), up(H, kBwdBN), E, st));
   g.c_trans = 0;
   // router: logit gradients, bias, W_r and the router's share of dx
-  hipLaunchKernelGGL(k_bwd_router, dim3(up(T, 256)), dim3(256), 0, st, topk_ids, topk_weights, dws, dlogits, T, E, k,
-                     dl_hi, dl_lo);
-  HIP_TRY(hipGetLastError());
+  if (s) {
+    sel.dw = dws; sel.aux = dlogits; sel.hi = dl_hi; sel.lo = dl_lo;
+    TRY(launch_select_bwd(sel, di.cus, st));
+  } else {
+    hipLaunchKernelGGL(k_bwd_router, dim3(up(T, 256)), dim3(256), 0, st, topk_ids, topk_weights, dws, dlogits, T, E, k,
+                       dl_hi, dl_lo);
+    HIP_TRY(hipGetLastError());
+  }
   if (dbias) {
     hipLaunchKernelGGL(k_bwd_dbias, dim3(E), dim3(256), 0, st, dl_hi, dl_lo, T, E, dbias);
     HIP_TRY(hipGetLastError());
@@ -1356,6 +1363,33 @@ moe_status moe_backward_aux(const moe_desc* d, const void* x, const void* router
   hipLaunchKernelGGL(k_bwd_dx, dim3(up((long)T * (H / 4), 256)), dim3(256), 0, st, dXr, p.row_of, dxr, T, H, k, dx);
   HIP_TRY(hipGetLastError());
   return MOE_OK;
+}
+
+moe_status moe_backward(const moe_desc* d, const void* x, const void* router_w, const void* w_gate_up,
+                        const void* w_down, const int32_t* topk_ids, const float* topk_weights, const void* dy,
+                        float* dx, float* dw_gate_up, float* dw_down, float* dw_router, float* dbias,
+                        void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  return moe_backward_aux(d, x, router_w, w_gate_up, w_down, topk_ids, topk_weights, dy, nullptr, dx, dw_gate_up,
+                          dw_down, dw_router, dbias, workspace, workspace_bytes, stream);
+}
+
+moe_status moe_backward_aux(const moe_desc* d, const void* x, const void* router_w, const void* w_gate_up,
+                            const void* w_down, const int32_t* topk_ids, const float* topk_weights, const void* dy,
+                            const float* dlogits, float* dx, float* dw_gate_up, float* dw_down, float* dw_router,
+                            float* dbias, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  return backward_impl(d, nullptr, x, router_w, w_gate_up, w_down, nullptr, topk_ids, topk_weights, dy, dlogits, dx,
+                       dw_gate_up, dw_down, dw_router, dbias, workspace, workspace_bytes, stream);
+}
+
+moe_status moe_backward_selected(const moe_desc* d, const moe_selection* s, const void* x, const void* router_w,
+                                 const void* w_gate_up, const void* w_down, const float* logits,
+                                 const int32_t* topk_ids, const float* topk_weights, const void* dy,
+                                 const float* dlogits, float* dx, float* dw_gate_up, float* dw_down,
+                                 float* dw_router, float* dbias, void* workspace, size_t workspace_bytes,
+                                 moe_stream_t stream) {
+  if (!s) return fail(MOE_ERR_INVALID_ARGUMENT, "selection is NULL");
+  return backward_impl(d, s, x, router_w, w_gate_up, w_down, logits, topk_ids, topk_weights, dy, dlogits, dx,
+                       dw_gate_up, dw_down, dw_router, dbias, workspace, workspace_bytes, stream);
 }
 
 const char* moe_status_string(moe_status s) {

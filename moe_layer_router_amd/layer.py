@@ -71,13 +71,23 @@ class Workspace:
 
 def forward(inputs: dict, top_k: int, mode: str = "mega", workspace: Workspace = None,
             routing=None, want_perm: bool = True, stream=None, out=None, inter_scale: str = "f32",
-            trace: bool = False) -> dict:
+            trace: bool = False, selection: dict = None) -> dict:
     """Run the layer on inputs whose weights went through pack_weights().
     routing=(topk_ids, topk_weights) feeds given routing
-    (MOE_FLAG_ROUTING_GIVEN).  Returns dict(y, topk_ids, topk_weights,
-    expert_offsets, perm)."""
+    (MOE_FLAG_ROUTING_GIVEN); selection=dict(scoring=, bias=, ...), the keyword
+    arguments of select_experts, routes by that instead of the layer's own rule.
+    Returns dict(y, topk_ids, topk_weights, expert_offsets, perm), with a
+    selection the router's logits [T, E] too."""
     if not inputs.get("weights_packed"):
         raise ValueError("forward() needs MFMA-tiled weights: pass the inputs through pack_weights() first")
+    if selection is not None:
+        _need(routing is None, "routing and selection exclude each other")
+        routed = route(inputs, top_k, inputs["w_gate_up"].shape[0], stream=stream)
+        chosen = select_experts(routed["logits"], top_k, stream=stream, **selection)
+        out = forward(inputs, top_k, mode, workspace, (chosen["topk_ids"], chosen["topk_weights"]), want_perm, stream,
+                      out, inter_scale, trace)
+        out["logits"] = routed["logits"]
+        return out
     flags = (lib.MOE_FLAG_ROUTING_GIVEN if routing is not None else 0) | (lib.MOE_FLAG_TRACE if trace else 0)
     desc = desc_from_inputs(inputs, top_k, mode, flags, inter_scale=inter_scale)
     dev = inputs["x"].device
@@ -154,11 +164,12 @@ def dequantize_e5m6(xq: torch.Tensor, xs: torch.Tensor, stream=None) -> torch.Te
 
 def backward(inputs: dict, topk_ids: torch.Tensor, topk_weights: torch.Tensor, dy: torch.Tensor,
              workspace: Workspace = None, stream=None, want_dbias: bool = True, out: dict = None,
-             dlogits: torch.Tensor = None) -> dict:
+             dlogits: torch.Tensor = None, selection: dict = None, logits: torch.Tensor = None) -> dict:
     """Gradients of a BF16 layer (moe_backward) for the routing a forward
     call returned, from row-major weights (inputs as generated, not packed).
     dlogits: an additional gradient of the router logits [T, E] float32
-    (balance_loss's; moe_backward_aux).  Returns dict(dx, dw_gate_up, dw_down,
+    (balance_loss's; moe_backward_aux).  selection and logits: those of a
+    forward() call that routed by select_experts (moe_backward_selected).  Returns dict(dx, dw_gate_up, dw_down,
     dw_router, dbias), fp32 (`out`, a previous result, is reused)."""
     if inputs.get("weights_packed"):
         raise ValueError("backward() reads the row-major weights: pass the inputs before pack_weights()")
@@ -170,6 +181,10 @@ def backward(inputs: dict, topk_ids: torch.Tensor, topk_weights: torch.Tensor, d
     dev = x.device
     if dlogits is not None:
         _is(dlogits, "dlogits", (T, E), _F32, dev)
+    _need((selection is None) == (logits is None), "selection and logits belong together")
+    if selection is not None:
+        _is(logits, "logits", (T, E), _F32, dev)
+        sel = lib.make_selection(T, E, k, **{n: v for n, v in selection.items() if n != "bias"})
     with _on(dev, stream):
         f32 = dict(dtype=torch.float32, device=dev)
         if out is None:
@@ -177,10 +192,13 @@ def backward(inputs: dict, topk_ids: torch.Tensor, topk_weights: torch.Tensor, d
                        dw_down=torch.empty(E, H, I, **f32), dw_router=torch.empty(E, H, **f32),
                        dbias=torch.empty(E, **f32) if want_dbias else None)
         ws = _scratch(workspace, dev, lib.moe_backward_workspace_size(desc))
-        lib.moe_backward_aux(desc, _dense(x), _dense(inputs["router_w"]), _dense(inputs["w_gate_up"]),
-                             _dense(inputs["w_down"]), _dense(topk_ids), _dense(topk_weights), _dense(dy),
-                             None if dlogits is None else _dense(dlogits), out["dx"], out["dw_gate_up"],
-                             out["dw_down"], out["dw_router"], out["dbias"], ws)
+        weights = (_dense(x), _dense(inputs["router_w"]), _dense(inputs["w_gate_up"]), _dense(inputs["w_down"]))
+        rest = (_dense(topk_ids), _dense(topk_weights), _dense(dy), None if dlogits is None else _dense(dlogits),
+                out["dx"], out["dw_gate_up"], out["dw_down"], out["dw_router"], out["dbias"], ws)
+        if selection is None:
+            lib.moe_backward_aux(desc, *weights, *rest)
+        else:
+            lib.moe_backward_selected(desc, sel, *weights, _dense(logits), *rest)
     return out
 
 
@@ -363,6 +381,57 @@ def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, alpha: float = 1.
         lib.moe_balance_loss(_dense(logits), _dense(topk_ids), None if seq_offsets is None else _dense(seq_offsets),
                              None if token_mask is None else _dense(token_mask), alpha, out["counts"], out["probs"],
                              out["loss"], out["dlogits"], ws)
+    return out
+
+
+def select_experts(logits: torch.Tensor, top_k: int, scoring: str = "sigmoid", bias: torch.Tensor = None,
+                   n_group: int = 1, topk_group: int = 1, group_top: int = 2, renormalize: bool = True,
+                   scale: float = 1.0, stream=None, out: dict = None) -> dict:
+    """Experts by scores of router logits [T, E] float32 (moe_select_experts):
+    scoring "sigmoid" or "softmax", bias [E] float32 added for the selection
+    alone, topk_group of n_group groups by the sum of their group_top largest.
+    Returns dict(topk_ids [T, top_k] int32, topk_weights [T, top_k] float32),
+    which forward(routing=...) takes; `out`, a previous result, is reused."""
+    _matrix(logits, "logits", _F32)
+    T, E = logits.shape
+    dev = logits.device
+    if bias is not None:
+        _is(bias, "bias", (E,), _F32, dev)
+    _need(scoring in lib.SCORINGS, f"unknown scoring {scoring!r}")
+    sel = lib.make_selection(T, E, top_k, scoring, n_group, topk_group, group_top, renormalize, scale)
+    with _on(dev, stream):
+        if out is None:
+            out = dict(topk_ids=torch.empty(T, max(top_k, 0), dtype=torch.int32, device=dev),
+                       topk_weights=torch.empty(T, max(top_k, 0), dtype=torch.float32, device=dev))
+        else:
+            _is(out["topk_ids"], "out['topk_ids']", (T, top_k), (torch.int32,), dev, True)
+            _is(out["topk_weights"], "out['topk_weights']", (T, top_k), _F32, dev, True)
+        lib.moe_select_experts(sel, _dense(logits), None if bias is None else _dense(bias), out["topk_ids"],
+                               out["topk_weights"])
+    return out
+
+
+def select_experts_backward(logits: torch.Tensor, topk_ids: torch.Tensor, dweights: torch.Tensor,
+                            scoring: str = "sigmoid", renormalize: bool = True, scale: float = 1.0, stream=None,
+                            out: torch.Tensor = None) -> torch.Tensor:
+    """Gradient of select_experts in the logits (moe_select_experts_backward)
+    for its topk_ids [T, k] int32 and the gradient dweights [T, k] float32 of its
+    topk_weights: dlogits [T, E] float32, `out` if given."""
+    _matrix(logits, "logits", _F32)
+    T, E = logits.shape
+    dev = logits.device
+    _need(isinstance(topk_ids, torch.Tensor) and topk_ids.dim() == 2, "topk_ids must be [T, k]")
+    k = topk_ids.shape[1]
+    _is(topk_ids, "topk_ids", (T, k), (torch.int32,), dev)
+    _is(dweights, "dweights", (T, k), _F32, dev)
+    _need(scoring in lib.SCORINGS, f"unknown scoring {scoring!r}")
+    sel = lib.make_selection(T, E, k, scoring, 1, 1, 1, renormalize, scale)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(T, E, dtype=torch.float32, device=dev)
+        else:
+            _is(out, "out", (T, E), _F32, dev, True)
+        lib.moe_select_experts_backward(sel, _dense(logits), _dense(topk_ids), _dense(dweights), out)
     return out
 
 

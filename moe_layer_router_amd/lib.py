@@ -53,6 +53,10 @@ MOE_INTER_SCALE_POW2 = 1
 # moe_weight_scale
 MOE_WSCALE_BLOCK = 0
 MOE_WSCALE_CHANNEL = 1
+# moe_scoring
+MOE_SCORING_SOFTMAX = 0
+MOE_SCORING_SIGMOID = 1
+SCORINGS = {"softmax": MOE_SCORING_SOFTMAX, "sigmoid": MOE_SCORING_SIGMOID}
 # moe_peak_kind
 MOE_PEAK_KINDS = {"mfma16_fp8_fp8": 0, "mfma16_fp4_fp8": 1, "mfma16_fp4_fp4": 2, "mfma16_bf16": 3,
                   "mfma32_fp8_fp8": 4, "mfma32_fp4_fp8": 5}
@@ -70,6 +74,11 @@ class MoeDesc(ctypes.Structure):
                 ("weight_dtype", ctypes.c_int32), ("mode", ctypes.c_int32), ("flags", ctypes.c_int32),
                 ("weight_layout", ctypes.c_int32), ("inter_scale", ctypes.c_int32),
                 ("weight_scale", ctypes.c_int32)]
+
+
+class MoeSelection(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "E", "top_k", "scoring", "n_group", "topk_group", "group_top",
+                                              "renormalize")] + [("scale", ctypes.c_float)]
 
 
 class MoeWorkspaceRegions(ctypes.Structure):
@@ -125,6 +134,13 @@ _lib.moe_orthogonalize_workspace_size.argtypes = [ctypes.c_int32] * 3
 _lib.moe_orthogonalize.restype = ctypes.c_int
 _lib.moe_orthogonalize.argtypes = [ctypes.c_int32] * 4 + [_P, ctypes.c_int32, _P, ctypes.c_float, _P, _P,
                                                           ctypes.c_size_t, _P]
+_lib.moe_select_experts.restype = ctypes.c_int
+_lib.moe_select_experts.argtypes = [ctypes.POINTER(MoeSelection)] + [_P] * 5
+_lib.moe_select_experts_backward.restype = ctypes.c_int
+_lib.moe_select_experts_backward.argtypes = [ctypes.POINTER(MoeSelection)] + [_P] * 5
+_lib.moe_backward_selected.restype = ctypes.c_int
+_lib.moe_backward_selected.argtypes = [ctypes.POINTER(MoeDesc), ctypes.POINTER(MoeSelection)] + [_P] * 15 + \
+    [ctypes.c_size_t, _P]
 _lib.moe_forward_static.restype = ctypes.c_int
 _lib.moe_forward_static.argtypes = [ctypes.POINTER(MoeDesc)] + [_P] * 13 + [_P]
 _lib.moe_route.restype = ctypes.c_int
@@ -345,6 +361,33 @@ def moe_orthogonalize(u, steps, coeffs, eps, y, workspace, stream=None):
                                   _nbytes(workspace), _stream(stream)), "moe_orthogonalize")
 
 
+def make_selection(T, E, top_k, scoring="sigmoid", n_group=1, topk_group=1, group_top=2, renormalize=True,
+                   scale=1.0) -> MoeSelection:
+    return MoeSelection(T, E, top_k, SCORINGS.get(scoring, scoring), n_group, topk_group, group_top,
+                        1 if renormalize else 0, scale)
+
+
+def moe_select_experts(sel, logits, bias, topk_ids, topk_weights, stream=None):
+    """logits [T, E] float32, bias [E] float32 or None; topk_ids [T, k] int32, topk_weights [T, k] float32."""
+    _check(_lib.moe_select_experts(ctypes.byref(sel), _ptr(logits), _ptr(bias), _ptr(topk_ids), _ptr(topk_weights),
+                                   _stream(stream)), "moe_select_experts")
+
+
+def moe_select_experts_backward(sel, logits, topk_ids, dweights, dlogits, stream=None):
+    """logits, dlogits [T, E] float32; topk_ids [T, k] int32, dweights [T, k] float32."""
+    _check(_lib.moe_select_experts_backward(ctypes.byref(sel), _ptr(logits), _ptr(topk_ids), _ptr(dweights),
+                                            _ptr(dlogits), _stream(stream)), "moe_select_experts_backward")
+
+
+def moe_backward_selected(desc, sel, x, router_w, w_gate_up, w_down, logits, topk_ids, topk_weights, dy, dlogits, dx,
+                          dw_gate_up, dw_down, dw_router, dbias, workspace, stream=None):
+    nbytes = _nbytes(workspace) if workspace is not None else 0
+    _check(_lib.moe_backward_selected(ctypes.byref(desc), ctypes.byref(sel), _ptr(x), _ptr(router_w), _ptr(w_gate_up),
+                                      _ptr(w_down), _ptr(logits), _ptr(topk_ids), _ptr(topk_weights), _ptr(dy),
+                                      _ptr(dlogits), _ptr(dx), _ptr(dw_gate_up), _ptr(dw_down), _ptr(dw_router),
+                                      _ptr(dbias), _ptr(workspace), nbytes, _stream(stream)), "moe_backward_selected")
+
+
 def moe_route(desc, x, x_scales, router_w, router_bias, logits, topk_ids, topk_weights, workspace,
               stream=None):
     st = _lib.moe_route(ctypes.byref(desc), _ptr(x), _ptr(x_scales), _ptr(router_w), _ptr(router_bias),
@@ -386,4 +429,5 @@ def exported_symbols():
             "moe_peak_mfma_flops", "moe_peak_mfma", "moe_peak_hbm_read", "moe_backward_workspace_size",
             "moe_backward", "moe_quantize_e5m6", "moe_dequantize_e5m6", "moe_backward_aux", "moe_layer_norm",
             "moe_layer_norm_backward_workspace_size", "moe_layer_norm_backward", "moe_balance_loss_workspace_size",
-            "moe_balance_loss", "moe_orthogonalize_workspace_size", "moe_orthogonalize"]
+            "moe_balance_loss", "moe_orthogonalize_workspace_size", "moe_orthogonalize", "moe_select_experts",
+            "moe_select_experts_backward", "moe_backward_selected"]

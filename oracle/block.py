@@ -1,0 +1,72 @@
+"""fp64 numpy definitions of the operators that stand beside the routed
+experts in a block: the selection of experts by scores, a bias and groups
+with its gradient, linear layers with an epilogue and their gradient, and the
+AdamW step.  Written from the formulas in include/moe_layer.h, a token or an
+element at a time where that is short, without the device code's groupings or
+orders of sums."""
+
+import math
+
+import numpy as np
+
+from . import formats as F
+
+
+# ------------------------------------------------------------------ selection
+def scores(row, scoring):
+    """s of one token's fp64 logits."""
+    if scoring == "sigmoid":
+        with np.errstate(over="ignore"):
+            return 1.0 / (1.0 + np.exp(-row))
+    m = row.max()
+    if m == -np.inf:
+        return np.zeros_like(row)
+    e = np.exp(row - m)
+    return e / e.sum()
+
+
+def _best(keys, n):
+    """The n largest by key, descending, ties to the lower index; NaN as -infinity."""
+    keys = [-math.inf if math.isnan(v) else float(v) for v in keys]
+    return sorted(range(len(keys)), key=lambda i: (-keys[i], i))[:n]
+
+
+def select_experts(logits, k, scoring="sigmoid", bias=None, n_group=1, topk_group=1, group_top=2, renormalize=True,
+                   scale=1.0):
+    """(ids [T, k], weights [T, k])."""
+    logits = np.asarray(logits, np.float64)
+    T, E = logits.shape
+    per = E // n_group
+    ids, w = np.zeros((T, k), np.int64), np.zeros((T, k))
+    for t in range(T):
+        s = scores(logits[t], scoring)
+        c = s if bias is None else s + np.asarray(bias, np.float64)
+        order = logits[t] if bias is None else c
+        groups = [-np.sort(-np.where(np.isnan(g), -np.inf, g))[:group_top].sum() for g in c.reshape(n_group, per)]
+        kept = _best(groups, topk_group)
+        members = sorted(e for g in kept for e in range(g * per, g * per + per))
+        ids[t] = [members[i] for i in _best(order[members], k)]
+        w[t] = s[ids[t]]
+        if renormalize:
+            w[t] = w[t] / w[t].sum() if w[t].sum() != 0 else 0.0
+    return ids, scale * w
+
+
+def select_experts_backward(logits, ids, dw, scoring="sigmoid", renormalize=True, scale=1.0):
+    """dlogits [T, E] by the chain rule through every s of the token."""
+    logits, dw = np.asarray(logits, np.float64), np.asarray(dw, np.float64)
+    T, E = logits.shape
+    out = np.zeros((T, E))
+    for t in range(T):
+        s = scores(logits[t], scoring)
+        sel = np.clip(ids[t], 0, E - 1)
+        z = s[sel].sum()
+        ds = np.zeros(E)
+        for j, e in enumerate(sel):
+            if renormalize:
+                # w_i = scale s_i / z:  dw_i / ds_e = scale ([i = j] / z - s_i / z^2), i over the slots
+                ds[e] += scale * (dw[t, j] - (dw[t] * s[sel]).sum() / z) / z if z else 0.0
+            else:
+                ds[e] += scale * dw[t, j]
+        out[t] = ds * s * (1 - s) if scoring == "sigmoid" else s * (ds - (s * ds).sum())
+    return out

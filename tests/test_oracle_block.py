@@ -1,0 +1,48 @@
+"""The fp64 definitions of the operators beside the routed experts, pinned:
+worked examples, gradients against central differences, statements that hold
+for any input."""
+
+import numpy as np
+import pytest
+
+from oracle import block as B
+
+
+def test_selection_worked_example():
+    # groups {0, 1} {2, 3} {4, 5}; c = s + bias
+    l = np.log(np.array([[0.6, 0.2, 0.5, 0.5, 0.1, 0.65]]) / (1 - np.array([[0.6, 0.2, 0.5, 0.5, 0.1, 0.65]])))
+    ids, w = B.select_experts(l, 2, n_group=3, topk_group=1, group_top=2)
+    assert ids.tolist() == [[2, 3]] and np.allclose(w, 0.5)          # 1.0 beats 0.8 and 0.75; a tie by index
+    ids, w = B.select_experts(l, 2, n_group=3, topk_group=1, group_top=1)
+    assert ids.tolist() == [[5, 4]] and np.allclose(w, [[0.65 / 0.75, 0.1 / 0.75]])
+    bias = np.array([0, 0.5, -0.3, -0.3, 0.0, 0.0])
+    ids, w = B.select_experts(l, 3, bias=bias, n_group=3, topk_group=2, group_top=2, renormalize=False, scale=2.0)
+    assert ids.tolist() == [[1, 5, 0]] and np.allclose(w, [[0.4, 1.3, 1.2]])     # the bias is not in the weights
+
+
+def test_selection_of_empty_rows_and_nan():
+    l = np.array([[-np.inf] * 4, [1.0, np.nan, -np.inf, 2.0]])
+    for scoring in ("softmax", "sigmoid"):
+        with np.errstate(invalid="ignore"):
+            ids, w = B.select_experts(l, 3, scoring)
+        assert ids.tolist() == [[0, 1, 2], [3, 0, 1]] and np.all(w[0] == 0)
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_selection_gradient_against_differences(scoring, renorm):
+    rng = np.random.default_rng(0)
+    l, dw = rng.normal(size=(3, 7)), rng.normal(size=(3, 3))
+    ids = np.array([[6, 0, 3], [1, 2, 4], [5, 5, 1]])                # one id twice
+
+    def f(x):
+        total = 0.0
+        for t in range(3):
+            s = B.scores(x[t], scoring)[ids[t]]
+            total += (dw[t] * 1.7 * (s / s.sum() if renorm else s)).sum()
+        return total
+    g = B.select_experts_backward(l, ids, dw, scoring, renorm, 1.7)
+    for i in np.ndindex(*l.shape):
+        h = np.zeros_like(l)
+        h[i] = 1e-5
+        assert abs((f(l + h) - f(l - h)) / 2e-5 - g[i]) < 1e-8
