@@ -595,6 +595,58 @@ moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dty
                              const float* coeffs, float eps, void* y, void* workspace, size_t workspace_bytes,
                              moe_stream_t stream);
 
+/* One AdamW step over many tensors, of a layer or of a whole model: for each
+ * element, in fp32, with t = step (1 for the first) and c_i = 1 - beta_i^t,
+ *   g  = grad_scale * grad
+ *   m' = beta1 m + (1 - beta1) g,   v' = beta2 v + (1 - beta2) g^2
+ *   w' = w - lr weight_decay w - lr (m' / c1) / (sqrt(v' / c2) + eps)
+ * `tensors` is host memory, read during the call.  A tensor's n elements (0: it
+ * is passed over) lie densely: param fp32 or BF16, grad fp32 or BF16 (read
+ * only), m and v states of state_dtype.  With `master` (fp32 weights of BF16 ones) w is
+ * read from it, and w' goes there and, rounded to nearest, to param.  BF16
+ * weights without master weights are rounded stochastically.
+ * States: fp32; or FP8_E4M3, one byte per element, with m_scales and v_scales
+ * [ceil(n / 128)] fp32: m is code * scale of its 128 elements, v the square of
+ * code * scale.  A step writes scale = largest magnitude / 448 (1 for a block of
+ * zeros, and one below 2^-100 becomes zeros; NaN where something is not finite)
+ * and rounds to the code above or below stochastically, a nonzero root of v never
+ * to zero.  Zero codes with scales of 1 are the states before the first step.
+ * Stochastic rounding adds 16 random bits, a hash of (seed, t, the tensor's place in
+ * the call, the element's index), to what is dropped: the same call gives the same bits.
+ * grad_scale, lr_dev, step_dev: optional scalars in device memory (NULL: 1, lr,
+ * step), read when the kernels run, for captured graphs; step_dev must be >= 1.  If grad_scale is
+ * not finite nothing is written: a step whose gradients overflowed is left out.
+ * 0 <= beta < 1, eps from 2^-100 to 2^100, n <= 2^40, |g| up to 2^63 (v' beyond is
+ * infinite); tensors 16-byte aligned (scalars to their size); what is written
+ * overlaps nothing else (a tensor stands in the list once).  No workspace; one launch for
+ * each 48 tensors of one kind.  Enqueued on `stream`; errors as moe_forward, of arguments
+ * before anything is enqueued. */
+typedef struct moe_adamw_tensor {
+  void* param;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scales;       /* FP8_E4M3 states, else NULL */
+  float* v_scales;
+  float* master;         /* optional, BF16 weights only */
+  int64_t n;
+  int32_t param_dtype;   /* MOE_DTYPE_F32 or MOE_DTYPE_BF16 */
+  int32_t grad_dtype;
+  float weight_decay;
+  int32_t reserved;      /* 0 */
+} moe_adamw_tensor;
+typedef struct moe_adamw_options {
+  double lr, beta1, beta2, eps;
+  int64_t step;
+  const float* grad_scale;
+  const float* lr_dev;
+  const int64_t* step_dev;
+  int32_t state_dtype;   /* MOE_DTYPE_F32 or MOE_DTYPE_FP8_E4M3 */
+  uint32_t seed;
+} moe_adamw_options;
+moe_status moe_adamw(int32_t n_tensors, const moe_adamw_tensor* tensors, const moe_adamw_options* options,
+                     moe_stream_t stream);
+
 const char* moe_status_string(moe_status s);
 const char* moe_last_error(void);
 

@@ -511,3 +511,120 @@ def orthogonalize(u: torch.Tensor, steps: int = 5, coeffs=None, eps: float = 1e-
         ws = _scratch(workspace, dev, lib.moe_orthogonalize_workspace_size(*v.shape))
         lib.moe_orthogonalize(v, steps, coeffs, eps, y, ws)
     return out
+
+
+class AdamW:
+    """AdamW over a list of dense tensors on one GPU (moe_adamw), updated in place.
+
+    params: float32 or bfloat16 tensors.  masters: None, or a list with the
+    float32 weights of each bfloat16 one (entries may be None: those are rounded
+    stochastically).  state "f32" or "fp8": the moments' type; states: None
+    (zeros are allocated), or a list of dict(m=, v=) float32, or dict(m=, v=,
+    m_scales=, v_scales=) with uint8 E4M3 codes and float32 scales [ceil(n / 128)],
+    v's being its root's.  weight_decay: a number, or one per tensor.  seed: of the
+    stochastic rounding.  count: steps done before.  capturable: the count is a
+    tensor on the GPU (int64 [1]), so that a captured step() counts and corrects its
+    bias at every replay; lr may then be a float32 tensor [1] there too.
+    The tensors are kept, not their addresses; `states`, `masters` and `count`
+    are what a checkpoint needs."""
+
+    def __init__(self, params, masters=None, states=None, state: str = None, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay=0.0, seed: int = 0, count: int = 0, capturable: bool = False):
+        self.params = list(params)
+        _need(len(self.params) > 0, "params must not be empty")
+        dev = self.params[0].device
+        for p in self.params:
+            _need(isinstance(p, torch.Tensor) and p.is_cuda and p.dtype in _FLOATS,
+                  "params must be tensors on a GPU, torch.bfloat16 or torch.float32")
+        n = len(self.params)
+        self.device = dev
+        self.masters = [None] * n if masters is None else list(masters)
+        self.weight_decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else [float(d) for d in weight_decay]
+        if state is None:
+            state = "fp8" if states and "m_scales" in states[0] else "f32"
+        _need(state in ("f32", "fp8"), f"unknown state {state!r}")
+        self.state = state
+        self.states = [self._zeros(p) for p in self.params] if states is None else list(states)
+        _need(len(self.masters) == n and len(self.weight_decay) == n and len(self.states) == n,
+              "masters, states and weight_decay must have one entry per tensor")
+        self.betas, self.eps, self.seed = (float(betas[0]), float(betas[1])), float(eps), int(seed)
+        _need(0 <= self.seed < 1 << 32, "seed must be in [0, 2^32)")
+        self.capturable = capturable
+        self.count = torch.tensor([count], dtype=torch.int64, device=dev) if capturable else int(count)
+        self._table, self._at = None, None
+
+    def _zeros(self, p):
+        dt = torch.uint8 if self.state == "fp8" else torch.float32
+        s = {k: torch.zeros(p.shape, dtype=dt, device=p.device) for k in ("m", "v")}
+        if self.state == "fp8":
+            for k in ("m_scales", "v_scales"):
+                s[k] = torch.ones((p.numel() + 127) // 128, dtype=torch.float32, device=p.device)
+        return s
+
+    def _kept(self):
+        """The tensors that a step writes, None for those that are not there."""
+        names = ("m", "v", "m_scales", "v_scales") if self.state == "fp8" else ("m", "v")
+        return [t for p, w, s in zip(self.params, self.masters, self.states) for t in (p, w, *[s[k] for k in names])]
+
+    def _fill(self):
+        """The table of the call but for the gradients."""
+        self._table = (lib.MoeAdamwTensor * len(self.params))()
+        f8 = self.state == "fp8"
+        for i, (p, w, s) in enumerate(zip(self.params, self.masters, self.states)):
+            n = p.numel()
+            _is(p, f"params[{i}]", p.shape, _FLOATS, self.device, True)
+            if w is not None:
+                _need(p.dtype == torch.bfloat16, f"params[{i}] is float32: it has no master weights")
+                _is(w, f"masters[{i}]", p.shape, _F32, self.device, True)
+            for k in ("m", "v"):
+                _is(s[k], f"states[{i}]['{k}']", p.shape, (torch.uint8,) if f8 else _F32, self.device, True)
+                if f8:
+                    _is(s[k + "_scales"], f"states[{i}]['{k}_scales']", ((n + 127) // 128,), _F32, self.device, True)
+            t = self._table[i]
+            t.param, t.m, t.v, t.n = p.data_ptr(), s["m"].data_ptr(), s["v"].data_ptr(), n
+            t.master = None if w is None else w.data_ptr()
+            if f8:
+                t.m_scales, t.v_scales = s["m_scales"].data_ptr(), s["v_scales"].data_ptr()
+            t.param_dtype = lib.MOE_DTYPE_BF16 if p.dtype == torch.bfloat16 else lib.MOE_DTYPE_F32
+            t.weight_decay = self.weight_decay[i]
+
+    def step(self, grads, lr, grad_scale: torch.Tensor = None, stream=None):
+        """One step with the gradients `grads` (bfloat16 or float32 tensors of the
+        params' shapes, in their order).  grad_scale: a float32 tensor [1] on the
+        GPU that they are multiplied by (a clipping or unscaling factor); if it is
+        not finite nothing is updated (the count goes on)."""
+        dev = self.device
+        _need(len(grads) == len(self.params), "grads must have one entry per tensor")
+        with _on(dev, stream):
+            # (tensors whose memory was exchanged since the last step, as by .data or .to, are looked at again)
+            at = [None if t is None else t.data_ptr() for t in self._kept()]
+            if at != self._at:
+                self._fill()
+                self._at = at
+            table, dense = self._table, []
+            for i, (g, p) in enumerate(zip(grads, self.params)):
+                _is(g, f"grads[{i}]", p.shape, _FLOATS, dev)
+                g = _dense(g)
+                dense.append(g)
+                table[i].grad = g.data_ptr()
+                table[i].grad_dtype = lib.MOE_DTYPE_F32 if g.dtype == torch.float32 else lib.MOE_DTYPE_BF16
+            o = lib.MoeAdamwOptions()
+            o.beta1, o.beta2 = self.betas
+            o.eps, o.seed = self.eps, self.seed
+            o.state_dtype = lib.MOE_DTYPE_FP8_E4M3 if self.state == "fp8" else lib.MOE_DTYPE_F32
+            if isinstance(lr, torch.Tensor):
+                _is(lr, "lr", (1,), _F32, dev)
+                o.lr_dev = lr.data_ptr()
+            else:
+                o.lr = lr
+            if grad_scale is not None:
+                _is(grad_scale, "grad_scale", (1,), _F32, dev)
+                o.grad_scale = grad_scale.data_ptr()
+            if self.capturable:
+                self.count.add_(1)
+                o.step_dev = self.count.data_ptr()
+            else:
+                o.step = self.count + 1
+            lib.moe_adamw(table, o)
+            if not self.capturable:
+                self.count += 1

@@ -81,6 +81,18 @@ class MoeSelection(ctypes.Structure):
                                               "renormalize")] + [("scale", ctypes.c_float)]
 
 
+class MoeAdamwTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "m", "v", "m_scales", "v_scales", "master")] + \
+        [("n", ctypes.c_int64), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+         ("weight_decay", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class MoeAdamwOptions(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps")] + [("step", ctypes.c_int64)] + \
+        [(n, ctypes.c_void_p) for n in ("grad_scale", "lr_dev", "step_dev")] + \
+        [("state_dtype", ctypes.c_int32), ("seed", ctypes.c_uint32)]
+
+
 class MoeWorkspaceRegions(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in
                 ("logits", "perm", "row_of", "offsets", "inter", "inter_scales", "staging", "trace", "total")]
@@ -141,6 +153,8 @@ _lib.moe_select_experts_backward.argtypes = [ctypes.POINTER(MoeSelection)] + [_P
 _lib.moe_backward_selected.restype = ctypes.c_int
 _lib.moe_backward_selected.argtypes = [ctypes.POINTER(MoeDesc), ctypes.POINTER(MoeSelection)] + [_P] * 15 + \
     [ctypes.c_size_t, _P]
+_lib.moe_adamw.restype = ctypes.c_int
+_lib.moe_adamw.argtypes = [ctypes.c_int32, ctypes.POINTER(MoeAdamwTensor), ctypes.POINTER(MoeAdamwOptions), _P]
 _lib.moe_forward_static.restype = ctypes.c_int
 _lib.moe_forward_static.argtypes = [ctypes.POINTER(MoeDesc)] + [_P] * 13 + [_P]
 _lib.moe_route.restype = ctypes.c_int
@@ -388,6 +402,11 @@ def moe_backward_selected(desc, sel, x, router_w, w_gate_up, w_down, logits, top
                                       _ptr(dbias), _ptr(workspace), nbytes, _stream(stream)), "moe_backward_selected")
 
 
+def moe_adamw(tensors, options, stream=None):
+    """tensors: a ctypes array of MoeAdamwTensor; options: a MoeAdamwOptions."""
+    _check(_lib.moe_adamw(len(tensors), tensors, ctypes.byref(options), _stream(stream)), "moe_adamw")
+
+
 def moe_route(desc, x, x_scales, router_w, router_bias, logits, topk_ids, topk_weights, workspace,
               stream=None):
     st = _lib.moe_route(ctypes.byref(desc), _ptr(x), _ptr(x_scales), _ptr(router_w), _ptr(router_bias),
@@ -430,4 +449,4 @@ def exported_symbols():
             "moe_backward", "moe_quantize_e5m6", "moe_dequantize_e5m6", "moe_backward_aux", "moe_layer_norm",
             "moe_layer_norm_backward_workspace_size", "moe_layer_norm_backward", "moe_balance_loss_workspace_size",
             "moe_balance_loss", "moe_orthogonalize_workspace_size", "moe_orthogonalize", "moe_select_experts",
-            "moe_select_experts_backward", "moe_backward_selected"]
+            "moe_select_experts_backward", "moe_backward_selected", "moe_adamw"]

@@ -70,3 +70,36 @@ def select_experts_backward(logits, ids, dw, scoring="sigmoid", renormalize=True
                 ds[e] += scale * dw[t, j]
         out[t] = ds * s * (1 - s) if scoring == "sigmoid" else s * (ds - (s * ds).sum())
     return out
+
+
+# --------------------------------------------------------------------- AdamW
+def mix(x):
+    """The 32-bit mixing function of the stochastic rounding, on Python ints or uint64 arrays."""
+    x = x & 0xFFFFFFFF
+    x = x ^ (x >> 15)
+    x = (x * 0x6A09E667) & 0xFFFFFFFF
+    x = x ^ (x >> 13)
+    x = (x * 0xBB67AE85) & 0xFFFFFFFF
+    return x ^ (x >> 16)
+
+
+def dice(n, seed, t, index):
+    """16 random bits per element for m, for v and for the weight: three arrays [n]."""
+    key = mix(mix(seed ^ (t * 0x9E3779B9 & 0xFFFFFFFF)) + index * 0xA54FF53B)
+    i = np.arange(n, dtype=np.uint64)
+    h = mix(i * np.uint64(0x9E3779B1) + np.uint64(key))
+    return h & 0xFFFF, h >> np.uint64(16), ((h * np.uint64(0x3C6EF373)) & np.uint64(0xFFFFFFFF)) >> np.uint64(16)
+
+
+def state_values(codes, scales):
+    """The numbers that E4M3 codes [n] with a scale per 128 stand for."""
+    return F.e4m3_decode(np.asarray(codes)) * np.repeat(np.asarray(scales, np.float64), 128)[:len(codes)]
+
+
+def adamw(w, g, m, v, t, lr, betas=(0.9, 0.999), eps=1e-8, decay=0.0, grad_scale=1.0):
+    """(w', m', v') of fp64 arrays after step t."""
+    g = grad_scale * g
+    m = betas[0] * m + (1 - betas[0]) * g
+    v = betas[1] * v + (1 - betas[1]) * g * g
+    update = (m / (1 - betas[0] ** t)) / (np.sqrt(v / (1 - betas[1] ** t)) + eps)
+    return w - lr * decay * w - lr * update, m, v

@@ -93,3 +93,66 @@ def test_select_wrappers_refuse():
         L.select_experts_backward(x, torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2))
     with pytest.raises(ValueError, match="exclude"):
         L.forward({"weights_packed": True}, 2, routing=(x, x), selection={})
+
+
+BF, F32, FP8, FP4 = lib.MOE_DTYPE_BF16, lib.MOE_DTYPE_F32, lib.MOE_DTYPE_FP8_E4M3, lib.MOE_DTYPE_FP4_E2M1
+
+
+def _adamw(tensors=({},), n_tensors=None, f8=False, table=True, options=True, **over):
+    o = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, step=1, grad_scale=None, lr_dev=None, step_dev=None,
+             state_dtype=FP8 if f8 else F32, seed=0)
+    o.update(over)
+    ts = (lib.MoeAdamwTensor * max(1, len(tensors)))()
+    for i, t in enumerate(tensors):
+        b = A * 16 * (i + 1)
+        d = dict(param=b, grad=b + A, m=b + 2 * A, v=b + 3 * A, m_scales=b + 4 * A if f8 else None,
+                 v_scales=b + 5 * A if f8 else None, master=None, n=1000, param_dtype=F32, grad_dtype=F32,
+                 weight_decay=0.0, reserved=0)
+        d.update(t)
+        ts[i] = lib.MoeAdamwTensor(*d.values())
+    opts = lib.MoeAdamwOptions(*o.values())
+    return lib._lib.moe_adamw(len(tensors) if n_tensors is None else n_tensors, ts if table else None,
+                              ctypes.byref(opts) if options else None, None)
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(n_tensors=-1), INVALID), (dict(n_tensors=(1 << 24) + 1), UNSUPPORTED), (dict(table=False), INVALID),
+    (dict(options=False), INVALID), (dict(beta1=1.0), INVALID), (dict(beta1=-0.1), INVALID), (dict(beta2=1.0), INVALID),
+    (dict(beta2=NAN), INVALID), (dict(eps=0.0), INVALID), (dict(eps=-1.0), INVALID), (dict(eps=NAN), INVALID),
+    (dict(eps=INF), INVALID), (dict(lr=NAN), INVALID), (dict(lr=INF), INVALID), (dict(step=0), INVALID),
+    (dict(step=-3), INVALID), (dict(state_dtype=BF), UNSUPPORTED), (dict(state_dtype=9), UNSUPPORTED),
+    (dict(grad_scale=A + 2), INVALID), (dict(lr_dev=A + 1), INVALID), (dict(step_dev=A + 4), INVALID),
+    (dict(tensors=[dict(n=-1)]), INVALID), (dict(tensors=[dict(n=(1 << 40) + 1)]), UNSUPPORTED),
+    (dict(tensors=[dict(param_dtype=FP8)]), UNSUPPORTED), (dict(tensors=[dict(grad_dtype=FP4)]), UNSUPPORTED),
+    (dict(tensors=[dict(weight_decay=INF)]), INVALID), (dict(tensors=[dict(master=A)]), INVALID),
+    (dict(tensors=[dict(m_scales=A)]), INVALID), (dict(tensors=[dict(m_scales=None)], f8=True), INVALID),
+    (dict(tensors=[dict(v_scales=None)], f8=True), INVALID), (dict(tensors=[dict(param=None)]), INVALID),
+    (dict(tensors=[dict(grad=None)]), INVALID), (dict(tensors=[dict(m=None)]), INVALID),
+    (dict(tensors=[dict(v=None)]), INVALID), (dict(tensors=[dict(param=A + 4)]), INVALID),
+    (dict(tensors=[dict(grad=A + 8)]), INVALID), (dict(tensors=[dict(param_dtype=BF, master=A + 4)]), INVALID),
+    (dict(tensors=[{}, dict(param=A * 16)]), INVALID),                     # one tensor twice
+    (dict(tensors=[{}, dict(grad=A * 16 + 16)]), INVALID),                 # a gradient that is another's weights
+    (dict(tensors=[dict(m=A * 18, v=A * 18 + 3984)]), INVALID),            # the last bytes of m
+    (dict(tensors=[dict(grad=A * 16)]), INVALID), (dict(tensors=[dict(m_scales=A * 16 + 16)], f8=True), INVALID),
+])
+def test_adamw_refusals(over, status):
+    assert _adamw(**over) == status
+    assert lib.moe_last_error() != ""
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: the call must end at the missing device")
+def test_adamw_shared_gradients_are_no_overlap():
+    """Past its checks of the arguments a call without a GPU fails at the device."""
+    for ts in ([dict(grad=A), dict(grad=A)], [dict(n=0, param=None, grad=None, m=None, v=None)],
+               [dict(m=A * 18, v=A * 18 + 4000)]):
+        assert _adamw(ts) not in (INVALID, lib.MOE_ERR_WORKSPACE_TOO_SMALL)
+
+
+def test_adamw_wrapper_refuses():
+    with pytest.raises(ValueError, match="not be empty"):
+        L.AdamW([])
+    with pytest.raises(ValueError, match="on a GPU"):
+        L.AdamW([torch.zeros(4)])

@@ -46,3 +46,26 @@ def test_selection_gradient_against_differences(scoring, renorm):
         h = np.zeros_like(l)
         h[i] = 1e-5
         assert abs((f(l + h) - f(l - h)) / 2e-5 - g[i]) < 1e-8
+
+
+def test_adamw_worked_example_and_first_step():
+    w, m, v = B.adamw(np.array([1.0]), np.array([2.0]), np.array([0.5]), np.array([3.0]), 2, 0.1, (0.5, 0.75), 1.0, 0.2)
+    assert m[0] == 1.25 and v[0] == 3.25
+    assert np.isclose(w[0], 1 - 0.02 - 0.1 * (1.25 / 0.75) / (np.sqrt(3.25 / 0.4375) + 1))
+    # the first step from zero states moves every weight by lr, whatever its gradient's size
+    g = np.array([1e-3, -5.0, 7e4])
+    w, _, _ = B.adamw(np.zeros(3), g, np.zeros(3), np.zeros(3), 1, 0.01, eps=1e-30)
+    assert np.allclose(w, -0.01 * np.sign(g))
+
+
+def test_stochastic_bits_are_uniform_and_differ():
+    """Means, and correlations between fields, neighbours, steps, tensors and seeds, within 5 standard deviations."""
+    n = 1 << 18
+    fields = [f.astype(np.float64) / 65536 for args in ((0, 1, 0), (0, 2, 0), (0, 1, 1), (9, 1, 0)) for f in B.dice(n, *args)]
+    for f in fields:
+        assert abs(f.mean() - 0.5) < 5 / np.sqrt(12 * n) + 2.0 ** -17
+        for lag in (1, 2, 8, 128, 2048):
+            assert abs(np.corrcoef(f[:-lag], f[lag:])[0, 1]) < 5 / np.sqrt(n - lag)
+    for i, a in enumerate(fields):
+        for b in fields[:i]:
+            assert abs(np.corrcoef(a, b)[0, 1]) < 5 / np.sqrt(n)
