@@ -617,7 +617,7 @@ moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dty
  * step), read when the kernels run, for captured graphs; step_dev must be >= 1.  If grad_scale is
  * not finite nothing is written: a step whose gradients overflowed is left out.
  * 0 <= beta < 1, eps from 2^-100 to 2^100, n <= 2^40, |g| up to 2^63 (v' beyond is
- * infinite); tensors 16-byte aligned (scalars to their size); what is written
+ * infinite); tensors 16-byte aligned, scales and scalars to their size; what is written
  * overlaps nothing else (a tensor stands in the list once).  No workspace; one launch for
  * each 48 tensors of one kind.  Enqueued on `stream`; errors as moe_forward, of arguments
  * before anything is enqueued. */

@@ -87,6 +87,14 @@ DEV uint32_t row_max16_u32(uint32_t v) {
   return v;
 }
 
+// b x + a y with every operation rounded on its own, as the formulas are read one operation at a time: a sum
+// fused with a product may differ in the last bit, which can decide a stochastic rounding.
+DEV float adam_mean(float b, float x, float a, float y) {
+#pragma clang fp contract(off)
+  const float p = b * x, q = a * y;
+  return p + q;
+}
+
 // 8 elements from i on (those at n and past it zero).
 template <int BF>
 DEV void adam_load(const void* p, int64_t i, int64_t n, float (&v)[8]) {
@@ -133,7 +141,7 @@ DEV void adam_store_fp8(void* p, float* scales, int64_t i, int64_t n, const floa
   mx = row_max16_u32(mx);
   const float amax = __uint_as_float(mx);
   const bool tiny = mx < 0x0D800000u;              // 2^-100
-  const float s = mx >= 0x7F800000u ? __builtin_nanf("") : tiny ? 1.0f : amax / 448.0f;
+  const float s = mx >= 0x7F800000u ? __builtin_nanf("") : tiny ? 1.0f : amax * (1.0f / 448.0f);
   const float inv = tiny ? 0.0f : 1.0f / s;
   uint32_t w[2] = {0, 0};
 #pragma unroll
@@ -200,8 +208,8 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw(const AdamArgs a) {
     for (int e = 0; e < 8; ++e) {
       const float x = g[e] * gs;
       if (S8) v[e] *= v[e];
-      m[e] = __builtin_fmaf(a.b1, m[e], a.a1 * x);
-      v[e] = __builtin_fmaf(a.b2, v[e], a.a2 * (x * x));
+      m[e] = adam_mean(a.b1, m[e], a.a1, x);
+      v[e] = adam_mean(a.b2, v[e], a.a2, x * x);
       root[e] = sqrtf(v[e]);
       const float u = m[e] * __builtin_amdgcn_rcpf(__builtin_fmaf(root[e], rs, a.eps));
       w[e] = __builtin_fmaf(-step, u, __builtin_fmaf(shrink, w[e], w[e]));

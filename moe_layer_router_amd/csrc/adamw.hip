@@ -43,8 +43,8 @@ moe_status check_tensors(int32_t count, const moe_adamw_tensor* ts, int32_t stat
     TRY(check_ptr(t.grad, "grad", some));
     TRY(check_ptr(t.m, "m", some));
     TRY(check_ptr(t.v, "v", some));
-    TRY(check_ptr(t.m_scales, "m_scales", some && f8));
-    TRY(check_ptr(t.v_scales, "v_scales", some && f8));
+    if (some && f8 && (!t.m_scales || !t.v_scales || (uintptr_t)t.m_scales % 4 || (uintptr_t)t.v_scales % 4))
+      return fail(MOE_ERR_INVALID_ARGUMENT, "tensor %d: m_scales and v_scales must be there, 4-byte aligned", i);
     TRY(check_ptr(t.master, "master", false));
     if (!some) continue;
     const auto add = [&](const void* p, size_t bytes, bool written) {

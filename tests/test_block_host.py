@@ -129,7 +129,7 @@ NAN, INF = float("nan"), float("inf")
     (dict(tensors=[dict(param_dtype=FP8)]), UNSUPPORTED), (dict(tensors=[dict(grad_dtype=FP4)]), UNSUPPORTED),
     (dict(tensors=[dict(weight_decay=INF)]), INVALID), (dict(tensors=[dict(master=A)]), INVALID),
     (dict(tensors=[dict(m_scales=A)]), INVALID), (dict(tensors=[dict(m_scales=None)], f8=True), INVALID),
-    (dict(tensors=[dict(v_scales=None)], f8=True), INVALID), (dict(tensors=[dict(param=None)]), INVALID),
+    (dict(tensors=[dict(v_scales=None)], f8=True), INVALID), (dict(tensors=[dict(v_scales=A + 2)], f8=True), INVALID), (dict(tensors=[dict(param=None)]), INVALID),
     (dict(tensors=[dict(grad=None)]), INVALID), (dict(tensors=[dict(m=None)]), INVALID),
     (dict(tensors=[dict(v=None)]), INVALID), (dict(tensors=[dict(param=A + 4)]), INVALID),
     (dict(tensors=[dict(grad=A + 8)]), INVALID), (dict(tensors=[dict(param_dtype=BF, master=A + 4)]), INVALID),

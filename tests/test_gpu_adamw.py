@@ -340,6 +340,25 @@ def test_adamw_wrapper(gpu_lib):
     L.AdamW([torch.zeros(0, device="cuda"), w]).step([torch.zeros(0, device="cuda"), g], 0.0)
 
 
+def test_adamw_scales_in_one_buffer(gpu_lib):
+    """Scales of several tensors one after another: only the first lies on 16 bytes."""
+    from moe_layer_router_amd import layer as L
+    sizes = [130, 200, 1000, 90]
+    params, grads, _, states = _tensors(sizes, "f32", False, "f32", "fp8")
+    other = [p.clone() for p in params]
+    flat = torch.cat([s[k] for k in ("m_scales", "v_scales") for s in states])
+    views, at = [], 0
+    for k in ("m_scales", "v_scales"):
+        for s in states:
+            views.append(flat[at:at + s[k].numel()])
+            at += s[k].numel()
+    shared = [dict(m=s["m"].clone(), v=s["v"].clone(), m_scales=views[i], v_scales=views[4 + i]) for i, s in enumerate(states)]
+    L.AdamW(params, states=states).step(grads, 1e-2)
+    L.AdamW(other, states=shared).step(grads, 1e-2)
+    for i in range(4):
+        assert torch.equal(params[i], other[i]) and all(torch.equal(states[i][k], shared[i][k]) for k in states[i])
+
+
 def test_adamw_offsets_past_32_bits(gpu_lib):
     """2^31 + 1000 elements: byte offsets past 2^33, element indices past 2^31."""
     from moe_layer_router_amd import layer as L
