@@ -595,6 +595,48 @@ moe_status moe_orthogonalize(int32_t batch, int32_t M, int32_t N, int32_t in_dty
                              const float* coeffs, float eps, void* y, void* workspace, size_t workspace_bytes,
                              moe_stream_t stream);
 
+/* Linear layer with what follows it, as a shared expert beside the routed ones or
+ * a dense block has them:
+ *   z = x W^T + bias,  y = act(z) + residual       (sums and act in fp32)
+ * x [T][K] BF16, w [R][K] BF16 with R = N, bias [R] fp32 (NULL = zero), residual
+ * [T][N] of residual_dtype (NULL = zero; it may be y itself, of one type), y [T][N] of y_dtype.  MOE_ACT_SWIGLU: R = 2N,
+ * rows 0..N-1 of W are the gate, N..2N-1 up, and y = SiLU(z_gate) z_up + residual,
+ * as in the layer's experts.  pre [T][R] of pre_dtype (optional output): z, for
+ * moe_linear_backward.  dtypes BF16 (rounded to nearest) or F32.
+ * T >= 1; K and N positive multiples of 8, K and R up to 131072; pointers 16-byte
+ * aligned; outputs and workspace overlap neither each other nor an input (but for the
+ * residual that is y).  workspace: moe_linear_workspace_size bytes (0 for sizes that are
+ * refused; at most 128 MiB).  Enqueued on `stream`; errors as moe_forward. */
+typedef enum moe_act {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_GELU = 2,        /* z (1 + erf(z / sqrt 2)) / 2                          */
+  MOE_ACT_GELU_TANH = 3,   /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2    */
+  MOE_ACT_SILU = 4,        /* z / (1 + exp(-z))                                    */
+  MOE_ACT_SWIGLU = 5
+} moe_act;
+size_t moe_linear_workspace_size(int32_t T, int32_t K, int32_t N, int32_t act);
+moe_status moe_linear(int32_t T, int32_t K, int32_t N, int32_t act, const void* x, const void* w, const float* bias,
+                      const void* residual, int32_t residual_dtype, void* y, int32_t y_dtype, void* pre,
+                      int32_t pre_dtype, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* Gradients of moe_linear: with dy [T][N] of dy_dtype and z = pre [T][R] of
+ * pre_dtype (not read without an activation; relu's derivative at 0 is 0),
+ *   dz = dy act'(z)  (SwiGLU: dz_gate = dy z_up SiLU'(z_gate), dz_up = dy SiLU(z_gate))
+ *   dx = dz W,  dW = dz^T x,  dbias = sum_t dz
+ * and the residual's gradient is dy.  dx [T][K] of dx_dtype, dw [R][K] fp32, dbias [R]
+ * fp32: each optional (NULL = not computed; x is needed for dw, w for dx), overwritten.
+ * dz enters the matrix cores as two BF16 parts (within 2^-17 of the fp32 value),
+ * or as it is where it is a BF16 dy; sums are fp32 in a fixed order.  Limits as moe_linear; no
+ * overlap of outputs, workspace and inputs.  workspace:
+ * moe_linear_backward_workspace_size bytes (0 for sizes that are refused): 4 T R,
+ * up to 256 rows of R sums and up to 128 MiB.  Enqueued on `stream`. */
+size_t moe_linear_backward_workspace_size(int32_t T, int32_t K, int32_t N, int32_t act);
+moe_status moe_linear_backward(int32_t T, int32_t K, int32_t N, int32_t act, const void* x, const void* w,
+                               const void* pre, int32_t pre_dtype, const void* dy, int32_t dy_dtype, void* dx,
+                               int32_t dx_dtype, float* dw, float* dbias, void* workspace, size_t workspace_bytes,
+                               moe_stream_t stream);
+
 /* One AdamW step over many tensors, of a layer or of a whole model: for each
  * element, in fp32, with t = step (1 for the first) and c_i = 1 - beta_i^t,
  *   g  = grad_scale * grad

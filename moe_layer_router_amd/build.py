@@ -5,7 +5,7 @@
 produces moe_layer_router_amd/libmoe_layer.so from csrc/kernels.hip (the
 layer), csrc/training.hip (the operators around it: layer norm, the balance
 loss, Newton-Schulz orthogonalisation), csrc/select.hip (selection of
-experts), csrc/adamw.hip (the optimiser) and csrc/peaks.hip (peak-rate
+experts), csrc/linear.hip (linear layers with an epilogue), csrc/adamw.hip (the optimiser) and csrc/peaks.hip (peak-rate
 microbenchmarks).
 """
 
@@ -19,7 +19,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB_DIR = PKG
 LIB = os.path.join(LIB_DIR, "libmoe_layer.so")
-SOURCES = [os.path.join(PKG, "csrc", f) for f in ("kernels.hip", "training.hip", "select.hip", "adamw.hip", "peaks.hip")]
+SOURCES = [os.path.join(PKG, "csrc", f) for f in ("kernels.hip", "training.hip", "select.hip", "linear.hip", "adamw.hip", "peaks.hip")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -1,0 +1,252 @@
+// Linear layers with an epilogue and their gradients (linear.h), as C entry points.
+#include "host.h"
+#include "linear.h"
+
+#include <algorithm>
+#include <atomic>
+
+using namespace moe;
+
+namespace {
+
+using LinBig = LinTile<4, 2, 8, 2>;        // 256 x 256, eight waves of 64 x 128, one workgroup per CU
+using LinMid = LinTile<2, 2, 4, 2>;        // 128 x 128, two workgroups per CU
+using LinSmall = LinTile<1, 2, 2, 3>;      // 64 x 64
+constexpr int kLinMaxDim = 1 << 17;        // (offsets in a tile's 256 rows of two parts fit 32 bits)
+
+template <auto K>
+moe_status set_lds_limit_once(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  HIP_TRY(hipGetDevice(&dev));
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (done.load(std::memory_order_relaxed) & bit)) return MOE_OK;
+  TRY(set_lds_limit(K, bytes));
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return MOE_OK;
+}
+
+size_t lin_bytes_of(int32_t dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
+bool lin_float(int32_t dtype) { return dtype == MOE_DTYPE_F32 || dtype == MOE_DTYPE_BF16; }
+
+moe_status check_linear(int32_t T, int32_t K, int32_t N, int32_t act) {
+  if (T < 1) return fail(MOE_ERR_INVALID_ARGUMENT, "T must be >= 1 (got %d)", T);
+  if (K < 8 || K % 8) return fail(MOE_ERR_INVALID_ARGUMENT, "K must be a positive multiple of 8 (got %d)", K);
+  if (N < 8 || N % 8) return fail(MOE_ERR_INVALID_ARGUMENT, "N must be a positive multiple of 8 (got %d)", N);
+  if (act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU) return fail(MOE_ERR_INVALID_ARGUMENT, "unknown act %d", act);
+  if (K > kLinMaxDim || (act == MOE_ACT_SWIGLU ? 2 * (long)N : N) > kLinMaxDim)
+    return fail(MOE_ERR_UNSUPPORTED, "K and the rows of W up to %d are supported (got %d, N = %d)", kLinMaxDim, K, N);
+  return MOE_OK;
+}
+int lin_rows(int N, int act) { return act == MOE_ACT_SWIGLU ? 2 * N : N; }
+
+// Bytes for the sums of tiles worked on in parts, whichever tiles are taken (that depends on the device).
+template <class TL>
+size_t lin_part_bytes(long rows, int cols, long K, int parts, bool gated) {
+  const long mt = TL::kSide / parts, nt = gated ? TL::kSide / 2 : TL::kSide;
+  const long tiles = ((rows + mt - 1) / mt) * ((cols + nt - 1) / nt), split = K / 256;
+  return split < 2 ? 0 : (size_t)std::min((long)kLinParts, tiles * split) * TL::kPart * 4;
+}
+size_t lin_parts(long rows, int cols, long K, int parts, bool gated) {
+  return std::max({lin_part_bytes<LinBig>(rows, cols, K, parts, gated), lin_part_bytes<LinMid>(rows, cols, K, parts, gated),
+                   lin_part_bytes<LinSmall>(rows, cols, K, parts, gated)});
+}
+
+template <class TL, int PT, int QT, int PARTS, int GATED>
+moe_status launch_tiles(LinGemm g, int cus, hipStream_t st) {
+  constexpr int MT = TL::kSide / PARTS, NT = GATED ? TL::kSide / 2 : TL::kSide;
+  g.tj = (g.cols + NT - 1) / NT;
+  const long total = (g.rows + MT - 1) / MT * g.tj, slots = (long)cus * std::max(1, 160 * 1024 / TL::kLds);
+  if (total > 0x7FFFFFFFl - 16) return fail(MOE_ERR_UNSUPPORTED, "the output has too many tiles");
+  g.full = total;
+  g.split = 1;
+  g.rest = 0;
+  // what does not fill a whole round of the GPU is split along k, as far as the slots and 256-k parts go
+  const long rest = total % slots;
+  const long split = rest ? std::min({slots / rest, g.K / 256, (long)kLinParts / rest}) : 1;
+  if (split >= 2) {
+    g.full = total - rest;
+    g.split = (int)split;
+    g.rest = (int)rest;
+  }
+  constexpr auto kernel = k_linear<TL, PT, QT, PARTS, GATED>;
+  TRY(set_lds_limit_once<kernel>(TL::kLds));
+  const unsigned grid = (unsigned)((g.full + 7) / 8 * 8 + (long)g.rest * g.split);
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(TL::kThreads), TL::kLds, st, g);
+  HIP_TRY(hipGetLastError());
+  if (g.rest) {
+    hipLaunchKernelGGL((k_linear_join<TL, PARTS, GATED>), dim3((unsigned)((long)g.rest * MT * NT / 8 / 256)), dim3(256), 0, st, g);
+    HIP_TRY(hipGetLastError());
+  }
+  return MOE_OK;
+}
+
+template <int PT, int QT, int PARTS, int GATED>
+moe_status launch_product(const LinGemm& g, int cus, hipStream_t st) {
+  const auto tiles = [&](long side) {
+    const long mt = side / PARTS, nt = GATED ? side / 2 : side;
+    return ((g.rows + mt - 1) / mt) * ((g.cols + nt - 1) / nt);
+  };
+  const long big = tiles(256), mid = tiles(128);
+  if (big >= cus && 16 * big <= 5 * mid) return launch_tiles<LinBig, PT, QT, PARTS, GATED>(g, cus, st);
+  if (mid >= cus) return launch_tiles<LinMid, PT, QT, PARTS, GATED>(g, cus, st);
+  return launch_tiles<LinSmall, PT, QT, PARTS, GATED>(g, cus, st);
+}
+
+// Slabs of rows for the sums over the tokens.
+constexpr int kLinSlabs = 256;
+int lin_slab(long T) { return (int)std::max(16l, ((T + kLinSlabs - 1) / kLinSlabs + 3) / 4 * 4); }
+
+struct LinBwdLayout {
+  size_t dz, part, sums, total;
+};
+LinBwdLayout lin_bwd_layout(long T, int K, int N, int act) {
+  const int R = lin_rows(N, act);
+  LinBwdLayout L{};
+  size_t o = 0;
+  L.dz = o; o = align256(o + (size_t)T * R * 4);
+  L.part = o; o = align256(o + (size_t)((T + lin_slab(T) - 1) / lin_slab(T)) * R * 4);
+  L.sums = o;
+  size_t sums = 0;
+  for (int parts = 1; parts <= 2; ++parts)
+    sums = std::max({sums, lin_parts(T, K, R, parts, false), lin_parts(R, K, T, parts, false)});
+  L.total = align256(o + sums);
+  return L;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_linear_workspace_size(int32_t T, int32_t K, int32_t N, int32_t act) {
+  if (check_linear(T, K, N, act) != MOE_OK) return 0;
+  return std::max((size_t)256, lin_parts(T, N, K, 1, act == MOE_ACT_SWIGLU));
+}
+
+moe_status moe_linear(int32_t T, int32_t K, int32_t N, int32_t act, const void* x, const void* w, const float* bias,
+                      const void* residual, int32_t residual_dtype, void* y, int32_t y_dtype, void* pre,
+                      int32_t pre_dtype, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  TRY(check_linear(T, K, N, act));
+  if (!lin_float(y_dtype) || (residual && !lin_float(residual_dtype)) || (pre && !lin_float(pre_dtype)))
+    return fail(MOE_ERR_UNSUPPORTED, "y, residual and pre must be MOE_DTYPE_BF16 or MOE_DTYPE_F32");
+  TRY(check_ptr(x, "x"));
+  TRY(check_ptr(w, "w"));
+  TRY(check_ptr(bias, "bias", false));
+  TRY(check_ptr(residual, "residual", false));
+  TRY(check_ptr(y, "y"));
+  TRY(check_ptr(pre, "pre", false));
+  TRY(check_ptr(workspace, "workspace"));
+  const int R = lin_rows(N, act);
+  const size_t need = moe_linear_workspace_size(T, K, N, act);
+  if (workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  const size_t nx = (size_t)T * K * 2, nw = (size_t)R * K * 2, nb = (size_t)R * 4;
+  const size_t nr = (size_t)T * N * lin_bytes_of(residual_dtype), ny = (size_t)T * N * lin_bytes_of(y_dtype);
+  const size_t np = (size_t)T * R * lin_bytes_of(pre_dtype);
+  const struct { const void* p; size_t n; } in[] = {{x, nx}, {w, nw}, {bias, nb}, {residual, nr}}, out[] = {{y, ny}, {pre, np}, {workspace, need}};
+  for (int i = 0; i < 3; ++i) {
+    for (const auto& v : in) {
+      // (an element of the residual is read where its y is written, by the same thread)
+      if (i == 0 && v.p == residual && residual == y && residual_dtype == y_dtype) continue;
+      if (overlap(out[i].p, out[i].n, v.p, v.n)) return fail(MOE_ERR_INVALID_ARGUMENT, "an output or the workspace overlaps an input");
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "y, pre and the workspace must not overlap");
+  }
+  DevInfo di;
+  TRY(device_info(&di));
+  LinGemm g{};
+  g.p = static_cast<const uint16_t*>(x);
+  g.q = static_cast<const uint16_t*>(w);
+  g.ldp = g.ldq = K;
+  g.rows = T; g.cols = N; g.K = K;
+  g.part = static_cast<float*>(workspace);
+  g.e.bias = bias; g.e.res = residual; g.e.y = y; g.e.pre = pre;
+  g.e.act = act; g.e.n = N;
+  g.e.y_f32 = y_dtype == MOE_DTYPE_F32; g.e.res_f32 = residual_dtype == MOE_DTYPE_F32; g.e.pre_f32 = pre_dtype == MOE_DTYPE_F32;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return act == MOE_ACT_SWIGLU ? launch_product<0, 0, 1, 1>(g, di.cus, st) : launch_product<0, 0, 1, 0>(g, di.cus, st);
+}
+
+size_t moe_linear_backward_workspace_size(int32_t T, int32_t K, int32_t N, int32_t act) {
+  if (check_linear(T, K, N, act) != MOE_OK) return 0;
+  return lin_bwd_layout(T, K, N, act).total;
+}
+
+moe_status moe_linear_backward(int32_t T, int32_t K, int32_t N, int32_t act, const void* x, const void* w,
+                               const void* pre, int32_t pre_dtype, const void* dy, int32_t dy_dtype, void* dx,
+                               int32_t dx_dtype, float* dw, float* dbias, void* workspace, size_t workspace_bytes,
+                               moe_stream_t stream) {
+  TRY(check_linear(T, K, N, act));
+  if (!lin_float(dy_dtype) || (dx && !lin_float(dx_dtype)) || (act != MOE_ACT_NONE && !lin_float(pre_dtype)))
+    return fail(MOE_ERR_UNSUPPORTED, "dy, dx and pre must be MOE_DTYPE_BF16 or MOE_DTYPE_F32");
+  if (!dx && !dw && !dbias) return fail(MOE_ERR_INVALID_ARGUMENT, "no gradient is asked for");
+  TRY(check_ptr(x, "x", dw != nullptr));
+  TRY(check_ptr(w, "w", dx != nullptr));
+  TRY(check_ptr(pre, "pre", act != MOE_ACT_NONE));
+  TRY(check_ptr(dy, "dy"));
+  TRY(check_ptr(dx, "dx", false));
+  TRY(check_ptr(dw, "dw", false));
+  TRY(check_ptr(dbias, "dbias", false));
+  TRY(check_ptr(workspace, "workspace"));
+  const int R = lin_rows(N, act);
+  const LinBwdLayout L = lin_bwd_layout(T, K, N, act);
+  if (workspace_bytes < L.total)
+    return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, needs %zu", workspace_bytes, L.total);
+  const struct { const void* p; size_t n; } in[] = {{dw ? x : nullptr, (size_t)T * K * 2}, {dx ? w : nullptr, (size_t)R * K * 2},
+      {act != MOE_ACT_NONE ? pre : nullptr, (size_t)T * R * lin_bytes_of(pre_dtype)}, {dy, (size_t)T * N * lin_bytes_of(dy_dtype)}},
+      out[] = {{dx, (size_t)T * K * lin_bytes_of(dx_dtype)}, {dw, (size_t)R * K * 4}, {dbias, (size_t)R * 4}, {workspace, L.total}};
+  for (int i = 0; i < 4; ++i) {
+    for (const auto& v : in)
+      if (overlap(out[i].p, out[i].n, v.p, v.n)) return fail(MOE_ERR_INVALID_ARGUMENT, "an output or the workspace overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "the outputs and the workspace must not overlap");
+  }
+  DevInfo di;
+  TRY(device_info(&di));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  uint16_t* dz = reinterpret_cast<uint16_t*>(ws + L.dz);
+  float* sums = reinterpret_cast<float*>(ws + L.part);
+  const bool whole = act == MOE_ACT_NONE && dy_dtype == MOE_DTYPE_BF16;      // dz is dy: one part
+  const bool want_dz = !whole && (dx || dw);
+  if (want_dz || dbias) {
+    LinDz a{};
+    a.dy = dy; a.pre = act == MOE_ACT_NONE ? nullptr : pre;
+    a.dz = want_dz ? dz : nullptr; a.part = dbias ? sums : nullptr;
+    a.T = T; a.n = N; a.act = act; a.dy_f32 = dy_dtype == MOE_DTYPE_F32; a.pre_f32 = pre_dtype == MOE_DTYPE_F32;
+    a.slab = lin_slab(T);
+    const int slabs = (int)((T + a.slab - 1) / a.slab);
+    const dim3 grid((N / 8 + 63) / 64, slabs);
+    if (act == MOE_ACT_SWIGLU) hipLaunchKernelGGL(k_linear_dz<1>, grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL(k_linear_dz<0>, grid, dim3(256), 0, st, a);
+    HIP_TRY(hipGetLastError());
+    if (dbias) {
+      hipLaunchKernelGGL(k_linear_dbias, dim3((R + 63) / 64), dim3(256), 0, st, sums, slabs, R, dbias);
+      HIP_TRY(hipGetLastError());
+    }
+  }
+  LinGemm g{};
+  g.p = whole ? static_cast<const uint16_t*>(dy) : dz;
+  g.ldp = whole ? R : 2l * R;
+  g.part = reinterpret_cast<float*>(ws + L.sums);
+  if (dx) {
+    g.q = static_cast<const uint16_t*>(w);
+    g.ldq = K;
+    g.rows = T; g.cols = K; g.K = R;
+    g.e.y = dx; g.e.n = K; g.e.y_f32 = dx_dtype == MOE_DTYPE_F32;
+    TRY((whole ? launch_product<0, 1, 1, 0>(g, di.cus, st) : launch_product<0, 1, 2, 0>(g, di.cus, st)));
+  }
+  if (dw) {
+    g.q = static_cast<const uint16_t*>(x);
+    g.ldq = K;
+    g.rows = R; g.cols = K; g.K = T;
+    g.e.y = dw; g.e.n = K; g.e.y_f32 = 1;
+    TRY((whole ? launch_product<1, 1, 1, 0>(g, di.cus, st) : launch_product<1, 1, 2, 0>(g, di.cus, st)));
+  }
+  return MOE_OK;
+}
+
+}  // extern "C"

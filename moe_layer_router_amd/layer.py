@@ -513,6 +513,89 @@ def orthogonalize(u: torch.Tensor, steps: int = 5, coeffs=None, eps: float = 1e-
     return out
 
 
+_BF16 = (torch.bfloat16,)
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor = None, act: str = "none",
+           residual: torch.Tensor = None, out_dtype: str = "bf16", pre_dtype: str = None,
+           workspace: Workspace = None, stream=None, out: dict = None) -> dict:
+    """Linear layer with bias, activation and residual (moe_linear): x [T, K] and
+    w [N, K] bfloat16 ([2N, K], gate and up, for act "swiglu"), bias [N] ([2N])
+    float32, residual [T, N] bfloat16 or float32; act "none", "relu", "gelu",
+    "gelu_tanh", "silu" or "swiglu".  Returns dict(y [T, N] of out_dtype, pre):
+    pre is what the activation took, [T, N] ([T, 2N]) of pre_dtype "bf16" or "f32"
+    for linear_backward, or None.  `out`, a previous result, is reused (its y may
+    be the residual)."""
+    _matrix(x, "x", _BF16)
+    T, K = x.shape
+    dev = x.device
+    _need(act in lib.ACTS, f"unknown act {act!r}")
+    _need(out_dtype in ("bf16", "f32") and pre_dtype in (None, "bf16", "f32"),
+          f"unknown out_dtype {out_dtype!r} or pre_dtype {pre_dtype!r}")
+    _need(isinstance(w, torch.Tensor) and w.dim() == 2 and (act != "swiglu" or w.shape[0] % 2 == 0),
+          "w must be [N, K], for swiglu [2N, K]")
+    R = w.shape[0]
+    N = R // 2 if act == "swiglu" else R
+    _is(w, "w", (R, K), _BF16, dev)
+    if bias is not None:
+        _is(bias, "bias", (R,), _F32, dev)
+    if residual is not None:
+        _is(residual, "residual", (T, N), _FLOATS, dev)
+    with _on(dev, stream):
+        if out is None:
+            out = dict(y=torch.empty(T, N, dtype=_OUT_DTYPES[out_dtype], device=dev),
+                       pre=None if pre_dtype is None else torch.empty(T, R, dtype=_OUT_DTYPES[pre_dtype], device=dev))
+        else:
+            _is(out["y"], "out['y']", (T, N), (_OUT_DTYPES[out_dtype],), dev, True)
+            _need((out["pre"] is not None) == (pre_dtype is not None), "out does not fit the call")
+            if pre_dtype is not None:
+                _is(out["pre"], "out['pre']", (T, R), (_OUT_DTYPES[pre_dtype],), dev, True)
+        ws = _scratch(workspace, dev, lib.moe_linear_workspace_size(T, K, N, act))
+        lib.moe_linear(_dense(x), _dense(w), None if bias is None else _dense(bias),
+                       None if residual is None else _dense(residual), out["y"], out["pre"], act, ws)
+    return out
+
+
+def linear_backward(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, act: str = "none", pre: torch.Tensor = None,
+                    dx_dtype: str = "f32", want_dx: bool = True, want_dw: bool = True, want_dbias: bool = False,
+                    workspace: Workspace = None, stream=None, out: dict = None) -> dict:
+    """Gradients of linear (moe_linear_backward) for dy [T, N] bfloat16 or
+    float32 and the pre that linear returned (needed with an activation).
+    Returns dict(dx [T, K] of dx_dtype, dw float32 of w's shape, dbias float32),
+    None where not wanted; the residual's gradient is dy.  `out`, a previous
+    result, is reused."""
+    _matrix(x, "x", _BF16)
+    T, K = x.shape
+    dev = x.device
+    _need(act in lib.ACTS, f"unknown act {act!r}")
+    _need(dx_dtype in ("bf16", "f32"), f"unknown dx_dtype {dx_dtype!r}")
+    _need(isinstance(w, torch.Tensor) and w.dim() == 2 and (act != "swiglu" or w.shape[0] % 2 == 0),
+          "w must be [N, K], for swiglu [2N, K]")
+    R = w.shape[0]
+    N = R // 2 if act == "swiglu" else R
+    _is(w, "w", (R, K), _BF16, dev)
+    _is(dy, "dy", (T, N), _FLOATS, dev)
+    _need(act == "none" or pre is not None, f"act {act!r} needs pre")
+    if act != "none":
+        _is(pre, "pre", (T, R), _FLOATS, dev)
+    with _on(dev, stream):
+        f32 = dict(dtype=torch.float32, device=dev)
+        if out is None:
+            out = dict(dx=torch.empty(T, K, dtype=_OUT_DTYPES[dx_dtype], device=dev) if want_dx else None,
+                       dw=torch.empty(R, K, **f32) if want_dw else None,
+                       dbias=torch.empty(R, **f32) if want_dbias else None)
+        else:
+            for name, shape, wanted, dts in (("dx", (T, K), want_dx, (_OUT_DTYPES[dx_dtype],)),
+                                             ("dw", (R, K), want_dw, _F32), ("dbias", (R,), want_dbias, _F32)):
+                _need((out[name] is not None) == wanted, "out does not fit the call")
+                if wanted:
+                    _is(out[name], name, shape, dts, dev, True)
+        ws = _scratch(workspace, dev, lib.moe_linear_backward_workspace_size(T, K, N, act))
+        lib.moe_linear_backward(_dense(x), _dense(w), None if act == "none" else _dense(pre), _dense(dy), out["dx"],
+                                out["dw"], out["dbias"], act, ws)
+    return out
+
+
 class AdamW:
     """AdamW over a list of dense tensors on one GPU (moe_adamw), updated in place.
 

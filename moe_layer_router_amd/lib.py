@@ -57,6 +57,8 @@ MOE_WSCALE_CHANNEL = 1
 MOE_SCORING_SOFTMAX = 0
 MOE_SCORING_SIGMOID = 1
 SCORINGS = {"softmax": MOE_SCORING_SOFTMAX, "sigmoid": MOE_SCORING_SIGMOID}
+# moe_act
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "swiglu": 5}
 # moe_peak_kind
 MOE_PEAK_KINDS = {"mfma16_fp8_fp8": 0, "mfma16_fp4_fp8": 1, "mfma16_fp4_fp4": 2, "mfma16_bf16": 3,
                   "mfma32_fp8_fp8": 4, "mfma32_fp4_fp8": 5}
@@ -153,6 +155,16 @@ _lib.moe_select_experts_backward.argtypes = [ctypes.POINTER(MoeSelection)] + [_P
 _lib.moe_backward_selected.restype = ctypes.c_int
 _lib.moe_backward_selected.argtypes = [ctypes.POINTER(MoeDesc), ctypes.POINTER(MoeSelection)] + [_P] * 15 + \
     [ctypes.c_size_t, _P]
+_lib.moe_linear_workspace_size.restype = ctypes.c_size_t
+_lib.moe_linear_workspace_size.argtypes = [ctypes.c_int32] * 4
+_lib.moe_linear.restype = ctypes.c_int
+_lib.moe_linear.argtypes = [ctypes.c_int32] * 4 + [_P] * 4 + [ctypes.c_int32, _P] * 2 + [ctypes.c_int32, _P,
+                                                                                        ctypes.c_size_t, _P]
+_lib.moe_linear_backward_workspace_size.restype = ctypes.c_size_t
+_lib.moe_linear_backward_workspace_size.argtypes = [ctypes.c_int32] * 4
+_lib.moe_linear_backward.restype = ctypes.c_int
+_lib.moe_linear_backward.argtypes = [ctypes.c_int32] * 4 + [_P] * 3 + [ctypes.c_int32, _P] * 2 + \
+    [ctypes.c_int32] + [_P] * 3 + [ctypes.c_size_t, _P]
 _lib.moe_adamw.restype = ctypes.c_int
 _lib.moe_adamw.argtypes = [ctypes.c_int32, ctypes.POINTER(MoeAdamwTensor), ctypes.POINTER(MoeAdamwOptions), _P]
 _lib.moe_forward_static.restype = ctypes.c_int
@@ -402,6 +414,34 @@ def moe_backward_selected(desc, sel, x, router_w, w_gate_up, w_down, logits, top
                                       _ptr(dbias), _ptr(workspace), nbytes, _stream(stream)), "moe_backward_selected")
 
 
+def moe_linear_workspace_size(T: int, K: int, N: int, act) -> int:
+    return _lib.moe_linear_workspace_size(T, K, N, ACTS.get(act, act))
+
+
+def moe_linear(x, w, bias, residual, y, pre, act, workspace, stream=None):
+    """x [T, K], w [R, K] bfloat16; bias [R] float32 or None; residual (or None), y [T, N], pre (or None) [T, R]
+    bfloat16 or float32."""
+    T, K = x.shape
+    kind = lambda t: MOE_DTYPE_BF16 if t is None else _float_dtype(t)
+    _check(_lib.moe_linear(T, K, y.shape[1], ACTS.get(act, act), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual),
+                           kind(residual), _ptr(y), kind(y), _ptr(pre), kind(pre), _ptr(workspace),
+                           _nbytes(workspace), _stream(stream)), "moe_linear")
+
+
+def moe_linear_backward_workspace_size(T: int, K: int, N: int, act) -> int:
+    return _lib.moe_linear_backward_workspace_size(T, K, N, ACTS.get(act, act))
+
+
+def moe_linear_backward(x, w, pre, dy, dx, dw, dbias, act, workspace, stream=None):
+    """x [T, K], w [R, K] bfloat16; pre (or None) [T, R], dy [T, N], dx (or None) [T, K] bfloat16 or float32; dw [R, K],
+    dbias [R] (or None) float32."""
+    T, K = x.shape
+    kind = lambda t: MOE_DTYPE_BF16 if t is None else _float_dtype(t)
+    _check(_lib.moe_linear_backward(T, K, dy.shape[1], ACTS.get(act, act), _ptr(x), _ptr(w), _ptr(pre), kind(pre),
+                                    _ptr(dy), kind(dy), _ptr(dx), kind(dx), _ptr(dw), _ptr(dbias), _ptr(workspace),
+                                    _nbytes(workspace), _stream(stream)), "moe_linear_backward")
+
+
 def moe_adamw(tensors, options, stream=None):
     """tensors: a ctypes array of MoeAdamwTensor; options: a MoeAdamwOptions."""
     _check(_lib.moe_adamw(len(tensors), tensors, ctypes.byref(options), _stream(stream)), "moe_adamw")
@@ -449,4 +489,5 @@ def exported_symbols():
             "moe_backward", "moe_quantize_e5m6", "moe_dequantize_e5m6", "moe_backward_aux", "moe_layer_norm",
             "moe_layer_norm_backward_workspace_size", "moe_layer_norm_backward", "moe_balance_loss_workspace_size",
             "moe_balance_loss", "moe_orthogonalize_workspace_size", "moe_orthogonalize", "moe_select_experts",
-            "moe_select_experts_backward", "moe_backward_selected", "moe_adamw"]
+            "moe_select_experts_backward", "moe_backward_selected", "moe_adamw", "moe_linear_workspace_size",
+            "moe_linear", "moe_linear_backward_workspace_size", "moe_linear_backward"]

@@ -103,3 +103,51 @@ def adamw(w, g, m, v, t, lr, betas=(0.9, 0.999), eps=1e-8, decay=0.0, grad_scale
     v = betas[1] * v + (1 - betas[1]) * g * g
     update = (m / (1 - betas[0] ** t)) / (np.sqrt(v / (1 - betas[1] ** t)) + eps)
     return w - lr * decay * w - lr * update, m, v
+
+
+# -------------------------------------------------------------- linear layers
+def act(z, name):
+    z = np.asarray(z, np.float64)
+    if name == "relu":
+        return np.maximum(z, 0)
+    if name == "gelu":
+        return z * 0.5 * np.vectorize(math.erfc, otypes=[np.float64])(-z / math.sqrt(2))
+    if name == "gelu_tanh":
+        return 0.5 * z * (1 + np.tanh(math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)))
+    if name == "silu":
+        return z / (1 + np.exp(-z))
+    return z
+
+
+def act_grad(z, name):
+    z = np.asarray(z, np.float64)
+    if name == "relu":
+        return (z > 0).astype(np.float64)
+    if name == "gelu":
+        return 0.5 * np.vectorize(math.erfc, otypes=[np.float64])(-z / math.sqrt(2)) + \
+            z * np.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    if name == "gelu_tanh":
+        c = math.sqrt(2 / math.pi)
+        t = np.tanh(c * (z + 0.044715 * z ** 3))
+        return 0.5 * (1 + t) + 0.5 * z * (1 - t * t) * c * (1 + 3 * 0.044715 * z * z)
+    if name == "silu":
+        s = 1 / (1 + np.exp(-z))
+        return s + z * s * (1 - s)
+    return np.ones_like(z)
+
+
+def activate(z, name):
+    """act(z); SwiGLU of gate and up side by side."""
+    if name == "swiglu":
+        n = z.shape[1] // 2
+        return act(z[:, :n], "silu") * z[:, n:]
+    return act(z, name)
+
+
+def activate_grad(z, dy, name):
+    """dz."""
+    if name == "swiglu":
+        n = z.shape[1] // 2
+        g, u = z[:, :n], z[:, n:]
+        return np.concatenate([dy * u * act_grad(g, "silu"), dy * act(g, "silu")], axis=1)
+    return dy * act_grad(z, name)

@@ -156,3 +156,64 @@ def test_adamw_wrapper_refuses():
         L.AdamW([])
     with pytest.raises(ValueError, match="on a GPU"):
         L.AdamW([torch.zeros(4)])
+
+
+def _linear(**over):
+    a = dict(T=10, K=64, N=24, act=0, x=A, w=2 * A, bias=3 * A, res=4 * A, rd=BF, y=5 * A, yd=BF, pre=6 * A, pd=BF,
+             ws=16 * A, nbytes=1 << 20)
+    a.update(over)
+    return lib._lib.moe_linear(*a.values(), None)
+
+
+SHAPES = [(dict(T=0), INVALID), (dict(T=-1), INVALID), (dict(K=0), INVALID), (dict(K=60), INVALID), (dict(N=0), INVALID),
+          (dict(N=20), INVALID), (dict(K=-8), INVALID), (dict(act=6), INVALID), (dict(act=-1), INVALID),
+          (dict(K=131080), UNSUPPORTED), (dict(N=131080), UNSUPPORTED), (dict(N=65544, act=5), UNSUPPORTED)]
+
+
+@pytest.mark.parametrize("over,status", SHAPES + [
+    (dict(yd=FP8), UNSUPPORTED), (dict(rd=FP8), UNSUPPORTED), (dict(pd=FP4), UNSUPPORTED), (dict(x=None), INVALID),
+    (dict(w=None), INVALID), (dict(y=None), INVALID), (dict(ws=None), INVALID), (dict(x=A + 2), INVALID),
+    (dict(bias=A + 4), INVALID), (dict(res=A + 8), INVALID), (dict(pre=A + 1), INVALID), (dict(nbytes=0), SMALL),
+    (dict(y=A), INVALID), (dict(y=2 * A + 24 * 64 * 2 - 16), INVALID), (dict(y=3 * A), INVALID), (dict(y=4 * A + 16), INVALID),
+    (dict(y=4 * A, yd=F32), INVALID), (dict(pre=4 * A), INVALID), (dict(pre=5 * A), INVALID), (dict(ws=A - 128), INVALID),
+    (dict(ws=5 * A), INVALID), (dict(pre=16 * A), INVALID),
+])
+def test_linear_refusals(over, status):
+    assert _linear(**over) == status
+    assert lib.moe_last_error() != ""
+
+
+def _linear_bwd(**over):
+    a = dict(T=10, K=64, N=24, act=2, x=A, w=2 * A, pre=3 * A, pd=BF, dy=4 * A, dyd=BF, dx=5 * A, dxd=BF, dw=6 * A,
+             db=7 * A, ws=16 * A, nbytes=1 << 24)
+    a.update(over)
+    return lib._lib.moe_linear_backward(*a.values(), None)
+
+
+@pytest.mark.parametrize("over,status", SHAPES + [
+    (dict(dyd=FP8), UNSUPPORTED), (dict(dxd=FP8), UNSUPPORTED), (dict(pd=FP4), UNSUPPORTED), (dict(x=None), INVALID),
+    (dict(w=None), INVALID), (dict(pre=None), INVALID), (dict(dy=None), INVALID), (dict(dx=None, dw=None, db=None), INVALID),
+    (dict(dx=A + 2), INVALID), (dict(dw=A + 4), INVALID), (dict(db=A + 8), INVALID), (dict(nbytes=64), SMALL),
+    (dict(dx=A), INVALID), (dict(dx=4 * A), INVALID), (dict(dw=2 * A), INVALID), (dict(dw=5 * A), INVALID),
+    (dict(db=3 * A), INVALID), (dict(db=6 * A + 64), INVALID), (dict(ws=4 * A), INVALID), (dict(ws=7 * A), INVALID),
+])
+def test_linear_backward_refusals(over, status):
+    assert _linear_bwd(**over) == status
+    assert lib.moe_last_error() != ""
+
+
+def test_linear_workspace_sizes():
+    for f in (lib.moe_linear_workspace_size, lib.moe_linear_backward_workspace_size):
+        assert f(0, 64, 64, "none") == 0 and f(1, 60, 64, "none") == 0 and f(1, 64, 65544, "swiglu") == 0
+        assert 0 < f(1, 8, 8, "none") < 1 << 16
+    assert lib.moe_linear_workspace_size(8192, 7168, 2048, "swiglu") <= 128 << 20
+    T, K, N = 8192, 7168, 2048
+    assert lib.moe_linear_backward_workspace_size(T, K, N, "swiglu") <= 4 * T * 2 * N + 256 * 2 * N * 4 + (128 << 20) + 1024
+
+
+def test_linear_wrappers_refuse():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="on a GPU"):
+        L.linear(x, x)
+    with pytest.raises(ValueError, match="on a GPU"):
+        L.linear_backward(x, x, x)

@@ -69,3 +69,19 @@ def test_stochastic_bits_are_uniform_and_differ():
     for i, a in enumerate(fields):
         for b in fields[:i]:
             assert abs(np.corrcoef(a, b)[0, 1]) < 5 / np.sqrt(n)
+
+
+@pytest.mark.parametrize("name", ["none", "relu", "gelu", "gelu_tanh", "silu", "swiglu"])
+def test_activations_against_differences_and_known_values(name):
+    rng = np.random.default_rng(1)
+    z, dy = rng.normal(size=(3, 8)) * 2, rng.normal(size=(3, 4 if name == "swiglu" else 8))
+    g = B.activate_grad(z, dy, name)
+    for i in np.ndindex(*z.shape):
+        h = np.zeros_like(z)
+        h[i] = 1e-5
+        assert abs(((B.activate(z + h, name) - B.activate(z - h, name)) * dy).sum() / 2e-5 - g[i]) < 1e-8
+    one = np.array([[1.0, 2.0]])
+    known = dict(none=1.0, relu=1.0, gelu=0.8413447460685429, gelu_tanh=0.8411919906082768, silu=0.7310585786300049,
+                 swiglu=2 * 0.7310585786300049)
+    assert abs(B.activate(one, name)[0, 0] - known[name]) < 1e-12
+    assert B.activate(np.zeros((1, 2)), name)[0, 0] == 0
