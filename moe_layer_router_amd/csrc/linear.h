@@ -6,9 +6,10 @@
 // All three products are C[i][j] = sum_k P(i, k) Q(j, k) of BF16 operands on the matrix cores with
 // fp32 sums; they differ in which operands lie along k in memory: x and W do in z, dz does and W does not in
 // dx, neither does in dW.  An operand along k is read from LDS 8 k at a time, one across it by the transposing load.
-// dz is an fp32 value: it enters as two BF16 parts (hi = bf16(dz), lo = bf16(dz - hi): within 2^-17 of it),
-// each with a product of its own into the same sum; one BF16 rounding would be 2^-9.  Where dz is the
-// BF16 dy itself (no activation) there is one part.
+// dz is an fp32 value: it enters as BF16 parts (bf16(dz), bf16 of what is left, and so on), each with a
+// product of its own into the same sum.  Three hold all 24 bits, for fp32 results; two (within 2^-17) do for a BF16 dx, whose
+// own rounding is 2^-8.  (Two parts for fp32 results take two thirds of the time and leave an error of 2.5e-6 in
+// the Frobenius norm where the fp32 sums alone leave 4e-7 to 1.6e-6.)  Where dz is the BF16 dy itself (no activation) there is one.
 #pragma once
 #include "elements.h"
 
@@ -18,17 +19,21 @@ constexpr int kLinParts = 512;             // tiles' parts along k in one launch
 
 enum { LIN_NONE = 0, LIN_RELU = 1, LIN_GELU = 2, LIN_GELU_TANH = 3, LIN_SILU = 4, LIN_SWIGLU = 5 };
 
-// WM x WN waves, each 4 x NJ subtiles of 16 x 16 of 64 WM rows and as many columns in LDS, 64 k at a
-// time, ST steps in LDS.
+// WM x WN waves with NJ subtiles of 16 columns each, 64 k at a time, ST steps in LDS.  A wave has 4 subtiles of 16 rows in LDS; with P in
+// parts 2 subtiles of rows, times the parts.
 template <int WM_, int WN_, int NJ_, int ST_>
 struct LinTile {
-  static constexpr int WM = WM_, WN = WN_, NJ = NJ_, ST = ST_, NW = WM * WN, kThreads = 64 * NW, kSide = 64 * WM;
-  static constexpr int kStage = 2 * kSide * 128;                        // bytes of a step's operands
-  static constexpr int kPitch = kSide + 4;                              // floats between rows of sums in LDS
-  static constexpr int kSums = 16 * WM * kPitch * 4;
-  static constexpr int kLds = ST * kStage > kSums ? ST * kStage : kSums;
-  static constexpr size_t kPart = (size_t)kSide * kSide;                // fp32 sums of one part
-  static_assert(16 * NJ * WN == kSide, "square tiles");
+  static constexpr int WM = WM_, WN = WN_, NJ = NJ_, ST = ST_, NW = WM * WN, kThreads = 64 * NW;
+  static constexpr int kCols = 16 * NJ * WN;
+  static constexpr int kPitch = kCols + 4;                              // floats between rows of sums in LDS
+  static constexpr int subs(int parts) { return parts == 1 ? 4 : 2 * parts; }
+  static constexpr int prows(int parts) { return 16 * subs(parts) * WM; }          // rows of P in LDS
+  static constexpr int rows(int parts) { return (parts == 1 ? 64 : 32) * WM; }     // of the output's tile
+  static constexpr int stage(int parts) { return (prows(parts) + kCols) * 128; }   // bytes of a step's operands
+  static constexpr int lds(int parts) {
+    return ST * stage(parts) > 16 * WM * kPitch * 4 ? ST * stage(parts) : 16 * WM * kPitch * 4;
+  }
+  static constexpr size_t sums(int parts) { return (size_t)rows(parts) * kCols; }  // of one part along k
 };
 
 struct LinEpi {
@@ -44,6 +49,7 @@ struct LinGemm {
   const uint16_t* p;                       // along k: [rows][ldp], across: [K][ldp]
   const uint16_t* q;
   long ldp, ldq;                           // elements
+  int pch;                                 // parts of P in memory: 8 elements of each in turn
   long rows;
   int cols;                                // of the output
   long K;
@@ -162,9 +168,10 @@ DEV void lin_finish(const LinEpi& e, long row, int col, float (&v)[8], float (&u
 // fall in distinct banks.  Across k it is one k of the tile's columns, its 32-byte chunk c at c ^ lin_swz_t(k), so that the 8 k
 // of 32 lanes do.
 DEV int lin_swz(int r) { return (r ^ (r >> 3)) & 7; }
-template <int SIDE>
+template <int COLS>
 DEV int lin_swz_t(int r) {
-  if (SIDE == 64) return ((r >> 1) & 1) | ((r >> 2) & 2);      // (two k in the banks' 256 bytes)
+  static_assert(COLS % 64 == 0, "whole groups of 4 chunks");
+  if (COLS % 128) return ((r >> 1) & 1) | ((r >> 2) & 2);      // (every second k starts in the middle of the banks' 256 bytes)
   return (r & 3) | ((r >> 1) & 4);
 }
 typedef short v4s __attribute__((ext_vector_type(4)));
@@ -174,17 +181,31 @@ DEV v4s lin_tr16(const char* __restrict__ p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
       (__attribute__((address_space(3))) v4s*)(__attribute__((address_space(3))) char*)const_cast<char*>(p));
 }
+// Operand read from a tile in LDS: k 32 kh + 8 (lane / 16) .. + 7 of row r0 + 16 i + lane % 16.
+template <int COLS, bool TR>
+DEV v8bf lin_frag(const char* op, int r0, int i, int kh, int lane) {
+  const int c16 = lane & 15, gq = lane >> 4;
+  if (TR) {
+    const int k = 32 * kh + 8 * gq + (c16 >> 2), c = (r0 >> 4) + i;
+    const char* a = op + k * (2 * COLS) + ((c ^ lin_swz_t<COLS>(k)) << 5) + 8 * (lane & 3);
+    const v4s x0 = lin_tr16(a), x1 = lin_tr16(a + 4 * 2 * COLS);
+    return __builtin_bit_cast(v8bf, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+  const int r = r0 + 16 * i + c16;
+  return lds_ld<v8bf>(op, (uint32_t)r * 128 + (((4 * kh + gq) ^ lin_swz(r)) << 4));
+}
 DEV uint32_t lin_bytes(long n) { return (uint32_t)(n < 0x7FFFFF00l ? n : 0x7FFFFF00l); }
 constexpr uint32_t kLinNowhere = 0x7FFFFFF0u;                  // past every buffer's end
 
-// PT, QT: the operand lies across k.  PARTS: P is two parts, 8 elements of hi and 8 of lo alternating in memory; in LDS a
-// wave's 64 rows are 32 of hi (its subtiles 0 and 1) and the same of lo.
-// GATED: the tile's columns are kSide / 2 of the gate and the same of up, q [2 cols][ldq].
+// PT, QT: the operand lies across k.  PARTS: P's, in memory 8 elements of each in turn; in LDS a wave's rows are its
+// two subtiles of the first part, then of the next.
+// GATED: the tile's columns are kCols / 2 of the gate and the same of up, q [2 cols][ldq].
 template <class TL, int PT, int QT, int PARTS, int GATED>
 __global__ void __launch_bounds__(TL::kThreads, 2) k_linear(LinGemm g) {
-  constexpr int NJ = TL::NJ, NW = TL::NW, S = TL::kSide, PP = S / 8 / NW, NI = 4 / PARTS;
-  constexpr int MT = S / PARTS, NT = GATED ? S / 2 : S;        // rows and columns of the output's tile
-  static_assert(S % (8 * NW) == 0, "whole 1 KB pieces per wave");
+  constexpr int NJ = TL::NJ, NW = TL::NW, S = TL::kCols, SP = TL::prows(PARTS), IP = TL::subs(PARTS);
+  constexpr int NI = PARTS == 1 ? 4 : 2, PP = SP / 8 / NW, QP = S / 8 / NW, kStage = TL::stage(PARTS);
+  constexpr int MT = TL::rows(PARTS), NT = GATED ? S / 2 : S;  // rows and columns of the output's tile
+  static_assert(SP % (8 * NW) == 0 && S % (8 * NW) == 0, "whole 1 KB pieces per wave");
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c16 = lane & 15, gq = lane >> 4, wm = w / TL::WN, wn = w % TL::WN;
@@ -211,25 +232,35 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_linear(LinGemm g) {
   }
 
   // byte offsets of this lane's 16 bytes of each 1 KB piece, from the step's first byte of the operand
-  uint32_t poff[PP], qoff[PP];
-  int pk[PP], qk[PP];                              // along k: the chunk's first k in the step
+  uint32_t poff[PP], qoff[QP];
+  int pk[PP], qk[QP];                              // along k: the chunk's first k in the step
 #pragma unroll
   for (int n = 0; n < PP; ++n) {
-    const int r = 8 * (n * NW + w) + (lane >> 3), c = (lane & 7) ^ lin_swz(r);
-    const int o = (n * NW + w) * 1024 + lane * 16, k = o / (2 * S), cc = (o % (2 * S) / 16) ^ (lin_swz_t<S>(k) << 1);
-    pk[n] = qk[n] = 8 * c;
+    const int o = (n * NW + w) * 1024 + lane * 16;
     if (!PT) {
-      const int row = PARTS == 1 ? r : 32 * (r / 64) + (r & 31);
-      poff[n] = (uint32_t)row * (uint32_t)g.ldp * 2 + (PARTS == 1 ? 16 * c : 32 * c + (r >> 5 & 1) * 16);
+      const int r = o / 128, c = (lane & 7) ^ lin_swz(r), sub = r % (16 * IP) / 16;
+      const int row = PARTS == 1 ? r : r / (16 * IP) * 32 + 16 * (sub & 1) + (r & 15);
+      pk[n] = 8 * c;
+      poff[n] = (uint32_t)row * (uint32_t)g.ldp * 2 + 16 * (c * g.pch + (PARTS == 1 ? 0 : sub >> 1));
     } else {
       // (columns past the end are never stored: the last ones again)
-      const int col = PARTS == 1 ? 8 * cc : 32 * (cc / 8) + 8 * (cc & 3);
+      const int k = o / (2 * SP), cc = (o % (2 * SP) / 16) ^ (lin_swz_t<SP>(k) << 1), sub = cc % (2 * IP) / 2;
+      const int col = PARTS == 1 ? 8 * cc : cc / (2 * IP) * 32 + 16 * (sub & 1) + 8 * (cc & 1);
       const uint32_t at = (uint32_t)(min(i0 + col, g.rows - 8) / 8);
-      poff[n] = (uint32_t)k * (uint32_t)g.ldp * 2 + (PARTS == 1 ? 16 * at : 32 * at + (cc >> 2 & 1) * 16);
+      pk[n] = 0;
+      poff[n] = (uint32_t)k * (uint32_t)g.ldp * 2 + 16 * (at * g.pch + (PARTS == 1 ? 0 : sub >> 1));
     }
+  }
+#pragma unroll
+  for (int n = 0; n < QP; ++n) {
+    const int o = (n * NW + w) * 1024 + lane * 16;
     if (!QT) {
+      const int r = o / 128, c = (lane & 7) ^ lin_swz(r);
+      qk[n] = 8 * c;
       qoff[n] = (uint32_t)(GATED ? r % NT : r) * (uint32_t)g.ldq * 2 + 16 * c;
     } else {
+      const int k = o / (2 * S), cc = (o % (2 * S) / 16) ^ (lin_swz_t<S>(k) << 1);
+      qk[n] = 0;
       qoff[n] = (uint32_t)k * (uint32_t)g.ldq * 2 + 2 * (uint32_t)min(j0 + 8 * cc, g.cols - 8);
     }
   }
@@ -237,7 +268,8 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_linear(LinGemm g) {
   const uint16_t* qb = QT ? g.q : g.q + (long)j0 * g.ldq;
   const uint32_t pn = lin_bytes((g.rows - i0) * g.ldp * 2), qn = lin_bytes((long)(g.cols - j0) * g.ldq * 2);
   auto load = [&](int step, int stage) {
-    char* st = lds + stage * TL::kStage;
+    char* ps = lds + stage * kStage;
+    char* qs = ps + SP * 128;
     const int s = min(step, s1 - 1);               // (past the end: the last step again, never read)
     const long left = g.K - 64l * s;               // k from this step on
     const rsrc_t pr = PT ? make_rsrc(pb + 64l * s * g.ldp, lin_bytes(min(left, 64l) * g.ldp * 2))
@@ -245,20 +277,21 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_linear(LinGemm g) {
     const rsrc_t qr = QT ? make_rsrc(qb + 64l * s * g.ldq, lin_bytes(min(left, 64l) * g.ldq * 2))
                          : make_rsrc(qb, qn);
     const rsrc_t ur = make_rsrc(GATED ? qb + (long)g.cols * g.ldq : qb, qn);
-    const uint32_t pa = PT ? 0 : (uint32_t)s * 128 * PARTS, qa = QT ? 0 : (uint32_t)s * 128;
+    const uint32_t pa = PT ? 0 : (uint32_t)s * 128 * g.pch, qa = QT ? 0 : (uint32_t)s * 128;
     if ((PT && QT) || left >= 64) {
 #pragma unroll
-      for (int n = 0; n < PP; ++n) {
-        buf_ld16_lds(pr, st + (n * NW + w) * 1024, poff[n], pa);
-        buf_ld16_lds(GATED && 8 * (n * NW + w) >= NT ? ur : qr, st + S * 128 + (n * NW + w) * 1024, qoff[n], qa);
-      }
+      for (int n = 0; n < PP; ++n) buf_ld16_lds(pr, ps + (n * NW + w) * 1024, poff[n], pa);
+#pragma unroll
+      for (int n = 0; n < QP; ++n)
+        buf_ld16_lds(GATED && 8 * (n * NW + w) >= NT ? ur : qr, qs + (n * NW + w) * 1024, qoff[n], qa);
     } else {                                       // k past the end are zeros
 #pragma unroll
-      for (int n = 0; n < PP; ++n) {
-        buf_ld16_lds(pr, st + (n * NW + w) * 1024, PT || pk[n] < left ? poff[n] + pa : kLinNowhere, 0);
-        buf_ld16_lds(GATED && 8 * (n * NW + w) >= NT ? ur : qr, st + S * 128 + (n * NW + w) * 1024,
+      for (int n = 0; n < PP; ++n)
+        buf_ld16_lds(pr, ps + (n * NW + w) * 1024, PT || pk[n] < left ? poff[n] + pa : kLinNowhere, 0);
+#pragma unroll
+      for (int n = 0; n < QP; ++n)
+        buf_ld16_lds(GATED && 8 * (n * NW + w) >= NT ? ur : qr, qs + (n * NW + w) * 1024,
                      QT || qk[n] < left ? qoff[n] + qa : kLinNowhere, 0);
-      }
     }
   };
 
@@ -267,36 +300,26 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_linear(LinGemm g) {
   for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  // operand reads: k 32 kh + 8 gq .. + 7 of row r0 + 16 i + c16 (r0: the wave's first)
-  const int pr0 = 64 * wm, qr0 = 16 * NJ * wn;
-  auto frag = [&](const char* op, bool tr, int r0, int i, int kh) {
-    if (tr) {
-      const int k = 32 * kh + 8 * gq + (c16 >> 2), c = (r0 >> 4) + i;
-      const char* a = op + k * (2 * S) + ((c ^ lin_swz_t<S>(k)) << 5) + 8 * (lane & 3);
-      const v4s x0 = lin_tr16(a), x1 = lin_tr16(a + 4 * 2 * S);
-      return __builtin_bit_cast(v8bf, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
-    }
-    return lds_ld<v8bf>(op, (uint32_t)(r0 + 16 * i + c16) * 128 + (((4 * kh + gq) ^ lin_swz(r0 + 16 * i + c16)) << 4));
-  };
-  auto pfrag = [&](const char* st, int i, int kh) { return frag(st, PT, pr0, i, kh); };
-  auto qfrag = [&](const char* st, int j, int kh) { return frag(st + S * 128, QT, qr0, j, kh); };
+  const int pr0 = 16 * IP * wm, qr0 = 16 * NJ * wn;
+  auto pfrag = [&](const char* st, int i, int kh) { return lin_frag<SP, PT != 0>(st, pr0, i, kh, lane); };
+  auto qfrag = [&](const char* st, int j, int kh) { return lin_frag<S, QT != 0>(st + SP * 128, qr0, j, kh, lane); };
   // A step's first operands are read during the last products of the step before, behind the barrier: their
   // LDS latency is covered by products.
   constexpr int NL = NJ >= 4 ? 2 : 1;              // column subtiles left behind the barrier, and read ahead
-  v8bf pf[4], qf[NJ];
+  v8bf pf[IP], qf[NJ];
   auto read_first = [&](const char* st) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pf[i] = pfrag(st, i, 0);
+    for (int i = 0; i < IP; ++i) pf[i] = pfrag(st, i, 0);
 #pragma unroll
     for (int j = 0; j < NL; ++j) qf[j] = qfrag(st, j, 0);
   };
   auto mul = [&](int j) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i % NI][j] = mfma_bf16(qf[j], pf[i], acc[i % NI][j]);
+    for (int i = 0; i < IP; ++i) acc[i % NI][j] = mfma_bf16(qf[j], pf[i], acc[i % NI][j]);
   };
 #pragma unroll
   for (int s = 0; s < TL::ST; ++s) load(s0 + s, s);
-  barrier_vmcnt<(TL::ST - 1) * 2 * PP>();          // the first step has landed
+  barrier_vmcnt<(TL::ST - 1) * (PP + QP)>();          // the first step has landed
   read_first(lds);
   int stage = 0;
   auto halves = [&](const char* st) {              // the step but for the last NL column subtiles
@@ -305,38 +328,38 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_linear(LinGemm g) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) mul(j);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pf[i] = pfrag(st, i, 1);
+    for (int i = 0; i < IP; ++i) pf[i] = pfrag(st, i, 1);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) qf[j] = qfrag(st, j, 1);
 #pragma unroll
     for (int j = 0; j < NJ - NL; ++j) mul(j);
   };
   for (int s = s0; s < s1 - 1; ++s) {
-    halves(lds + stage * TL::kStage);
+    halves(lds + stage * kStage);
     const int cur = stage;
     stage = stage == TL::ST - 1 ? 0 : stage + 1;
     // this wave's loads of the next step have landed and its reads of this one are done, and so are every
     // wave's: this stage is free
-    barrier_vmcnt<(TL::ST - 2) * 2 * PP>();
+    barrier_vmcnt<(TL::ST - 2) * (PP + QP)>();
     load(s + TL::ST, cur);
-    v8bf pl[4], ql[NL];
+    v8bf pl[IP], ql[NL];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pl[i] = pf[i];
+    for (int i = 0; i < IP; ++i) pl[i] = pf[i];
 #pragma unroll
     for (int j = 0; j < NL; ++j) ql[j] = qf[NJ - NL + j];
-    read_first(lds + stage * TL::kStage);
+    read_first(lds + stage * kStage);
     __builtin_amdgcn_sched_barrier(0);             // (these reads are issued before the products below)
 #pragma unroll
     for (int j = 0; j < NL; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i % NI][NJ - NL + j] = mfma_bf16(ql[j], pl[i], acc[i % NI][NJ - NL + j]);
+      for (int i = 0; i < IP; ++i) acc[i % NI][NJ - NL + j] = mfma_bf16(ql[j], pl[i], acc[i % NI][NJ - NL + j]);
     // (and stay in this step: the compiler would move them to the next one's start)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(pf[i]));
+    for (int i = 0; i < IP; ++i) asm volatile("" : "+v"(pf[i]));
 #pragma unroll
     for (int j = 0; j < NL; ++j) asm volatile("" : "+v"(qf[j]));
   }
-  halves(lds + stage * TL::kStage);
+  halves(lds + stage * kStage);
 #pragma unroll
   for (int j = NJ - NL; j < NJ; ++j) mul(j);
   wait_vmcnt<0>();                                 // no load into LDS is in flight below
@@ -358,7 +381,7 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_linear(LinGemm g) {
       ln_load_f32(sums, (size_t)lr * TL::kPitch + col, v);
       if (GATED) ln_load_f32(sums, (size_t)lr * TL::kPitch + NT + col, u);
       if (part >= 0) {
-        float* dst = g.part + (size_t)part * TL::kPart;
+        float* dst = g.part + (size_t)part * TL::sums(PARTS);
         ln_store_f32(dst, (size_t)tr * S + col, v);
         if (GATED) ln_store_f32(dst, (size_t)tr * S + NT + col, u);
         continue;
@@ -371,7 +394,7 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_linear(LinGemm g) {
 // The tiles worked on in parts: 8 columns of a row per thread, the parts added in order.
 template <class TL, int PARTS, int GATED>
 __global__ void __launch_bounds__(256) k_linear_join(LinGemm g) {
-  constexpr int S = TL::kSide, MT = S / PARTS, NT = GATED ? S / 2 : S;
+  constexpr int S = TL::kCols, MT = TL::rows(PARTS), NT = GATED ? S / 2 : S;
   const int n = blockIdx.x * 256 + threadIdx.x;    // (MT NT / 8 of a tile: whole workgroups)
   const int r = n / (MT * (NT / 8)), l = n % (MT * (NT / 8)), tr = l / (NT / 8), col = 8 * (l % (NT / 8));
   const long t = g.full + r, row = t / g.tj * MT + tr;
@@ -379,7 +402,7 @@ __global__ void __launch_bounds__(256) k_linear_join(LinGemm g) {
   if (row >= g.rows || c >= g.cols) return;
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, u[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   for (int k = 0; k < g.split; ++k) {
-    const float* src = g.part + ((size_t)r * g.split + k) * TL::kPart + (size_t)tr * S + col;
+    const float* src = g.part + ((size_t)r * g.split + k) * TL::sums(PARTS) + (size_t)tr * S + col;
     float x[8];
     ln_load_f32(src, 0, x);
 #pragma unroll
@@ -397,23 +420,25 @@ __global__ void __launch_bounds__(256) k_linear_join(LinGemm g) {
 struct LinDz {
   const void* dy;                          // [T][n]
   const void* pre;                         // [T][R]
-  uint16_t* dz;                            // [T][R / 8][hi 8, lo 8], or NULL
+  uint16_t* dz;                            // [T][R / 8][parts][8], or NULL
   float* part;                             // [slabs][R] sums of dz over a slab's rows, or NULL
   long T;
   int n, act, dy_f32, pre_f32;
   int slab;                                // rows of a slab
+  int parts;                               // of dz: 2 or 3
 };
 
-DEV void lin_split_store(uint16_t* dz, size_t chunk, const float (&v)[8]) {
-  float l[8];
-  uint32_t h[8];
+DEV void lin_split_store(uint16_t* dz, size_t chunk, int parts, float (&v)[8]) {
+  uint16_t* at = dz + chunk * 8 * parts;
+  for (int p = 0; p < parts; ++p) {
+    uint32_t h[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    h[e] = f32_to_bf16_rne(v[e]);
-    l[e] = v[e] - bf16_to_f32(h[e]);
+    for (int e = 0; e < 8; ++e) {
+      h[e] = f32_to_bf16_rne(v[e]);
+      v[e] -= bf16_to_f32(h[e]);
+    }
+    st16(at + 8 * p, v4i{(int)(h[0] | h[1] << 16), (int)(h[2] | h[3] << 16), (int)(h[4] | h[5] << 16), (int)(h[6] | h[7] << 16)});
   }
-  st16(dz + chunk * 16, v4i{(int)(h[0] | h[1] << 16), (int)(h[2] | h[3] << 16), (int)(h[4] | h[5] << 16), (int)(h[6] | h[7] << 16)});
-  lin_store8(dz, 0, chunk * 16 + 8, l);
 }
 
 // Workgroup (x, y): 512 columns of y (8 per lane), slab y's rows (wave w every fourth).
@@ -439,13 +464,13 @@ __global__ void __launch_bounds__(256) k_linear_dz(LinDz a) {
           u[e] = dy * z[e] * s;
           su[e] += u[e];
         }
-        if (a.dz) lin_split_store(a.dz, ((size_t)t * R + a.n + col) / 8, u);
+        if (a.dz) lin_split_store(a.dz, ((size_t)t * R + a.n + col) / 8, a.parts, u);
       } else if (a.pre) {
         lin_act_grad(a.act, z, d);
       }
-      if (a.dz) lin_split_store(a.dz, ((size_t)t * R + col) / 8, d);
 #pragma unroll
       for (int e = 0; e < 8; ++e) sg[e] += d[e];
+      if (a.dz) lin_split_store(a.dz, ((size_t)t * R + col) / 8, a.parts, d);
     }
   }
   if (!a.part) return;

@@ -4,14 +4,16 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 using namespace moe;
 
 namespace {
 
-using LinBig = LinTile<4, 2, 8, 2>;        // 256 x 256, eight waves of 64 x 128, one workgroup per CU
-using LinMid = LinTile<2, 2, 4, 2>;        // 128 x 128, two workgroups per CU
-using LinSmall = LinTile<1, 2, 2, 3>;      // 64 x 64
+using LinBig = LinTile<4, 2, 8, 2>;        // 256 columns, eight waves, one workgroup per CU
+using LinMid = LinTile<2, 2, 4, 2>;        // 128 columns, two workgroups per CU
+using LinSmall = LinTile<1, 2, 2, 3>;      // 64 columns
+using LinSmallParts = LinTile<2, 1, 4, 2>; // the same, and as many rows of P in parts
 constexpr int kLinMaxDim = 1 << 17;        // (offsets in a tile's 256 rows of two parts fit 32 bits)
 
 template <auto K>
@@ -43,20 +45,21 @@ int lin_rows(int N, int act) { return act == MOE_ACT_SWIGLU ? 2 * N : N; }
 // Bytes for the sums of tiles worked on in parts, whichever tiles are taken (that depends on the device).
 template <class TL>
 size_t lin_part_bytes(long rows, int cols, long K, int parts, bool gated) {
-  const long mt = TL::kSide / parts, nt = gated ? TL::kSide / 2 : TL::kSide;
+  const long mt = TL::rows(parts), nt = gated ? TL::kCols / 2 : TL::kCols;
   const long tiles = ((rows + mt - 1) / mt) * ((cols + nt - 1) / nt), split = K / 256;
-  return split < 2 ? 0 : (size_t)std::min((long)kLinParts, tiles * split) * TL::kPart * 4;
+  return split < 2 ? 0 : (size_t)std::min((long)kLinParts, tiles * split) * TL::sums(parts) * 4;
 }
 size_t lin_parts(long rows, int cols, long K, int parts, bool gated) {
   return std::max({lin_part_bytes<LinBig>(rows, cols, K, parts, gated), lin_part_bytes<LinMid>(rows, cols, K, parts, gated),
-                   lin_part_bytes<LinSmall>(rows, cols, K, parts, gated)});
+                   parts == 1 ? lin_part_bytes<LinSmall>(rows, cols, K, parts, gated)
+                              : lin_part_bytes<LinSmallParts>(rows, cols, K, parts, gated)});
 }
 
 template <class TL, int PT, int QT, int PARTS, int GATED>
 moe_status launch_tiles(LinGemm g, int cus, hipStream_t st) {
-  constexpr int MT = TL::kSide / PARTS, NT = GATED ? TL::kSide / 2 : TL::kSide;
+  constexpr int MT = TL::rows(PARTS), NT = GATED ? TL::kCols / 2 : TL::kCols, kLds = TL::lds(PARTS);
   g.tj = (g.cols + NT - 1) / NT;
-  const long total = (g.rows + MT - 1) / MT * g.tj, slots = (long)cus * std::max(1, 160 * 1024 / TL::kLds);
+  const long total = (g.rows + MT - 1) / MT * g.tj, slots = (long)cus * (160 * 1024 / kLds);
   if (total > 0x7FFFFFFFl - 16) return fail(MOE_ERR_UNSUPPORTED, "the output has too many tiles");
   g.full = total;
   g.split = 1;
@@ -70,9 +73,9 @@ moe_status launch_tiles(LinGemm g, int cus, hipStream_t st) {
     g.rest = (int)rest;
   }
   constexpr auto kernel = k_linear<TL, PT, QT, PARTS, GATED>;
-  TRY(set_lds_limit_once<kernel>(TL::kLds));
+  TRY(set_lds_limit_once<kernel>(kLds));
   const unsigned grid = (unsigned)((g.full + 7) / 8 * 8 + (long)g.rest * g.split);
-  hipLaunchKernelGGL(kernel, dim3(grid), dim3(TL::kThreads), TL::kLds, st, g);
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(TL::kThreads), kLds, st, g);
   HIP_TRY(hipGetLastError());
   if (g.rest) {
     hipLaunchKernelGGL((k_linear_join<TL, PARTS, GATED>), dim3((unsigned)((long)g.rest * MT * NT / 8 / 256)), dim3(256), 0, st, g);
@@ -83,14 +86,14 @@ moe_status launch_tiles(LinGemm g, int cus, hipStream_t st) {
 
 template <int PT, int QT, int PARTS, int GATED>
 moe_status launch_product(const LinGemm& g, int cus, hipStream_t st) {
-  const auto tiles = [&](long side) {
-    const long mt = side / PARTS, nt = GATED ? side / 2 : side;
+  const auto tiles = [&](long mt, long nt) {
+    if (GATED) nt /= 2;
     return ((g.rows + mt - 1) / mt) * ((g.cols + nt - 1) / nt);
   };
-  const long big = tiles(256), mid = tiles(128);
+  const long big = tiles(LinBig::rows(PARTS), LinBig::kCols), mid = tiles(LinMid::rows(PARTS), LinMid::kCols);
   if (big >= cus && 16 * big <= 5 * mid) return launch_tiles<LinBig, PT, QT, PARTS, GATED>(g, cus, st);
   if (mid >= cus) return launch_tiles<LinMid, PT, QT, PARTS, GATED>(g, cus, st);
-  return launch_tiles<LinSmall, PT, QT, PARTS, GATED>(g, cus, st);
+  return launch_tiles<std::conditional_t<PARTS == 1, LinSmall, LinSmallParts>, PT, QT, PARTS, GATED>(g, cus, st);
 }
 
 // Slabs of rows for the sums over the tokens.
@@ -104,11 +107,11 @@ LinBwdLayout lin_bwd_layout(long T, int K, int N, int act) {
   const int R = lin_rows(N, act);
   LinBwdLayout L{};
   size_t o = 0;
-  L.dz = o; o = align256(o + (size_t)T * R * 4);
+  L.dz = o; o = align256(o + (size_t)T * R * 6);
   L.part = o; o = align256(o + (size_t)((T + lin_slab(T) - 1) / lin_slab(T)) * R * 4);
   L.sums = o;
   size_t sums = 0;
-  for (int parts = 1; parts <= 2; ++parts)
+  for (int parts = 1; parts <= 3; ++parts)
     sums = std::max({sums, lin_parts(T, K, R, parts, false), lin_parts(R, K, T, parts, false)});
   L.total = align256(o + sums);
   return L;
@@ -160,6 +163,7 @@ moe_status moe_linear(int32_t T, int32_t K, int32_t N, int32_t act, const void* 
   g.p = static_cast<const uint16_t*>(x);
   g.q = static_cast<const uint16_t*>(w);
   g.ldp = g.ldq = K;
+  g.pch = 1;
   g.rows = T; g.cols = N; g.K = K;
   g.part = static_cast<float*>(workspace);
   g.e.bias = bias; g.e.res = residual; g.e.y = y; g.e.pre = pre;
@@ -212,12 +216,15 @@ moe_status moe_linear_backward(int32_t T, int32_t K, int32_t N, int32_t act, con
   float* sums = reinterpret_cast<float*>(ws + L.part);
   const bool whole = act == MOE_ACT_NONE && dy_dtype == MOE_DTYPE_BF16;      // dz is dy: one part
   const bool want_dz = !whole && (dx || dw);
+  // parts of dz in memory: three for fp32 results, two for BF16 ones
+  const int parts = whole ? 1 : dw || (dx && dx_dtype == MOE_DTYPE_F32) ? 3 : 2;
   if (want_dz || dbias) {
     LinDz a{};
     a.dy = dy; a.pre = act == MOE_ACT_NONE ? nullptr : pre;
     a.dz = want_dz ? dz : nullptr; a.part = dbias ? sums : nullptr;
     a.T = T; a.n = N; a.act = act; a.dy_f32 = dy_dtype == MOE_DTYPE_F32; a.pre_f32 = pre_dtype == MOE_DTYPE_F32;
     a.slab = lin_slab(T);
+    a.parts = parts;
     const int slabs = (int)((T + a.slab - 1) / a.slab);
     const dim3 grid((N / 8 + 63) / 64, slabs);
     if (act == MOE_ACT_SWIGLU) hipLaunchKernelGGL(k_linear_dz<1>, grid, dim3(256), 0, st, a);
@@ -230,21 +237,23 @@ moe_status moe_linear_backward(int32_t T, int32_t K, int32_t N, int32_t act, con
   }
   LinGemm g{};
   g.p = whole ? static_cast<const uint16_t*>(dy) : dz;
-  g.ldp = whole ? R : 2l * R;
+  g.ldp = (long)parts * R;
+  g.pch = parts;
   g.part = reinterpret_cast<float*>(ws + L.sums);
   if (dx) {
     g.q = static_cast<const uint16_t*>(w);
     g.ldq = K;
     g.rows = T; g.cols = K; g.K = R;
     g.e.y = dx; g.e.n = K; g.e.y_f32 = dx_dtype == MOE_DTYPE_F32;
-    TRY((whole ? launch_product<0, 1, 1, 0>(g, di.cus, st) : launch_product<0, 1, 2, 0>(g, di.cus, st)));
+    TRY((whole ? launch_product<0, 1, 1, 0>(g, di.cus, st)
+               : dx_dtype == MOE_DTYPE_F32 ? launch_product<0, 1, 3, 0>(g, di.cus, st) : launch_product<0, 1, 2, 0>(g, di.cus, st)));
   }
   if (dw) {
     g.q = static_cast<const uint16_t*>(x);
     g.ldq = K;
     g.rows = R; g.cols = K; g.K = T;
     g.e.y = dw; g.e.n = K; g.e.y_f32 = 1;
-    TRY((whole ? launch_product<1, 1, 1, 0>(g, di.cus, st) : launch_product<1, 1, 2, 0>(g, di.cus, st)));
+    TRY((whole ? launch_product<1, 1, 1, 0>(g, di.cus, st) : launch_product<1, 1, 3, 0>(g, di.cus, st)));
   }
   return MOE_OK;
 }

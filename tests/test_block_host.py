@@ -208,7 +208,7 @@ def test_linear_workspace_sizes():
         assert 0 < f(1, 8, 8, "none") < 1 << 16
     assert lib.moe_linear_workspace_size(8192, 7168, 2048, "swiglu") <= 128 << 20
     T, K, N = 8192, 7168, 2048
-    assert lib.moe_linear_backward_workspace_size(T, K, N, "swiglu") <= 4 * T * 2 * N + 256 * 2 * N * 4 + (128 << 20) + 1024
+    assert lib.moe_linear_backward_workspace_size(T, K, N, "swiglu") <= 6 * T * 2 * N + 256 * 2 * N * 4 + (128 << 20) + 1024
 
 
 def test_linear_wrappers_refuse():

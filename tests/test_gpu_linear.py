@@ -334,6 +334,7 @@ def test_linear_in_a_graph(gpu_lib):
 def test_offsets_past_32_bits(gpu_lib):
     """x, dz and y past 2^32 bytes: the last rows are right."""
     from moe_layer_router_amd import layer as L
+    torch.manual_seed(2)
     T, K, N = 300_000, 8200, 8
     x = torch.zeros(T, K, device="cuda", dtype=torch.bfloat16)
     w = torch.randn(N, K, device="cuda").to(torch.bfloat16)
@@ -342,7 +343,8 @@ def test_offsets_past_32_bits(gpu_lib):
     y = L.linear(x, w, out_dtype="f32")["y"]
     ref = _mm(x[rows], w.t())
     assert float((y[rows].double() - ref).abs().max()) <= (K / 32 + 40) * U * float(_mm(x[rows].abs(), w.abs().t()).max())
-    assert float(y.abs().sum() - y[rows].abs().sum()) == 0
+    y[rows] = 0
+    assert float(y.abs().max()) == 0
     dy = torch.zeros(T, N, device="cuda")
     dy[rows] = torch.randn(len(rows), N, device="cuda")
     d = L.linear_backward(x, w, dy, dx_dtype="bf16")
