@@ -5,7 +5,8 @@
 //   ids = the k experts by c (without a bias: by l) among them, ties to the lower index
 //   w_j = scale s_j / sum_i s_i   (or scale s_j)
 // Two experts' c may differ by less than fp32 resolves, and a wrong order there sends
-// a token elsewhere: c, group scores and their comparisons are fp64.
+// a token elsewhere: the order is that of fp64.  fp32 decides where its error cannot matter, in all but
+// about one in a hundred tokens; the others are done again in fp64.
 //
 // One wave per token.
 #pragma once
@@ -40,90 +41,300 @@ DEV double sel_sum(double v) {
   return v;
 }
 
-// A token's k experts in fp64, expert j of them in lane j.  Lane l holds experts
-// l + 64 i; `buf`: E doubles of LDS of this wave's own.
+// Lane l holds experts 256 (i / 4) + 4 l + i % 4: four in a row, so that a load takes 16 bytes, and a
+// group's lie in neighbouring lanes.
+DEV int sel_expert(int lane, int i) { return 256 * (i >> 2) + 4 * lane + (i & 3); }
+// (buffer loads: a uniform base and 32-bit offsets; zeros past the row's end)
 template <int NV>
-DEV int sel_exact(const SelArgs& a, const float (&l)[NV], double* buf) {
-  const int lane = threadIdx.x & 63;
-  const bool need = a.bias || a.groups > 1;        // (the logits' order is the scores')
-  uint64_t alive = 0;
+DEV void sel_load(const float* row, int E, int lane, float (&l)[NV]) {
+  const rsrc_t r = make_rsrc(row, (uint32_t)E * 4);
+  if (E % 4 == 0) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (lane + 64 * i < a.E) alive |= 1ull << i;
-  double c[NV];
-  if (need) {
-    float mx = -__builtin_inff();
-    double sum = 0;
-    if (!a.sigmoid) {
+    for (int q = 0; q < NV / 4; ++q) {
+      const v4i v = buf_ld16(r, 16 * lane, 1024 * q);
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (alive >> i & 1) mx = fmaxf(mx, l[i]);
-      mx = sel_max(mx);
+      for (int j = 0; j < 4; ++j) l[4 * q + j] = __int_as_float(v[j]);
     }
+  } else {                                         // (rows start on 4 bytes)
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      // (a row of -infinity: no score at all)
-      if (a.sigmoid) c[i] = 1.0 / (1.0 + exp(-(double)l[i]));
-      else c[i] = mx == -__builtin_inff() && l[i] == mx ? 0.0 : exp((double)l[i] - (double)mx);
-      if (alive >> i & 1) sum += c[i];
-    }
-    if (!a.sigmoid) {
-      sum = sel_sum(sum);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) c[i] = sum == 0.0 ? 0.0 : c[i] / sum;
-    }
-    if (a.bias) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) c[i] += (double)a.bias[min(lane + 64 * i, a.E - 1)];
-    }
+    for (int i = 0; i < NV; ++i) l[i] = buf_ldf(r, 16 * lane + 4 * (i & 3), 1024 * (i >> 2));
   }
+}
+
+// What the fp64 functions take of a call.
+struct SelRule {
+  const float* bias;
+  int E, k, sigmoid, groups, keep, top;
+};
+// fp64 scores of a row.  softmax: its largest logit and the sum of the exponentials (a row of -infinity: no score at all).
+struct SelRow {
+  const float* l;
+  float mx;
+  double sum;
+};
+DEV SelRow sel_row64(const SelRule& a, const float* row) {
+  SelRow r{row, -__builtin_inff(), 1.0};
+  if (a.sigmoid) return r;
+  const int lane = threadIdx.x & 63;
+#pragma unroll 4
+  for (int e = lane; e < a.E; e += 64) r.mx = fmaxf(r.mx, row[e]);
+  r.mx = sel_max(r.mx);
+  r.sum = 0;
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += 64) r.sum += row[e] == -__builtin_inff() ? 0.0 : exp((double)row[e] - (double)r.mx);
+  r.sum = sel_sum(r.sum);
+  return r;
+}
+DEV double sel_choice64(const SelRule& a, const SelRow& r, int e) {
+  const float l = r.l[e];
+  double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : r.sum == 0.0 || l == -__builtin_inff() ? 0.0 : exp((double)l - (double)r.mx) / r.sum;
+  return a.bias ? s + (double)a.bias[e] : s;
+}
+
+// A token's k experts in fp64 for whatever there is in its row, expert j of them in lane j.  Few tokens get here: small
+// code rather than fast.  `buf`: E doubles of LDS of this wave's own.
+__device__ __noinline__ int sel_exact(SelRule a, const float* row, double* buf) {
+  const int lane = threadIdx.x & 63, n = a.E / a.groups;
+  uint64_t kept = ~0ull;
+  if (a.bias || a.groups > 1) {                    // (else the logits' order is the scores')
+    const SelRow r = sel_row64(a, row);
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 64) buf[e] = sel_choice64(a, r, e);
+  }
+  __builtin_amdgcn_wave_barrier();
   if (a.groups > 1) {
-    const int n = a.E / a.groups;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (alive >> i & 1) buf[lane + 64 * i] = c[i];
-    __builtin_amdgcn_wave_barrier();
     double m1 = -__builtin_inf(), m2 = m1;
     if (lane < a.groups) {
+#pragma unroll 4
       for (int e = 0; e < n; ++e) {
         const double v = buf[lane * n + e];        // (NaN: never larger)
         if (v > m1) { m2 = m1; m1 = v; }
         else if (v > m2) m2 = v;
       }
     }
-    __builtin_amdgcn_wave_barrier();
     const uint64_t score = lane < a.groups ? f64_order_key(a.top == 2 ? m1 + m2 : m1) : 0;
     int rank = 0;
     for (int g = 0; g < a.groups; ++g) {
       const uint64_t o = (uint64_t)__shfl((unsigned long long)score, g);
       rank += o > score || (o == score && g < lane);
     }
-    const uint64_t kept = __ballot(lane < a.groups && rank < a.keep);
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (!(kept >> (min(lane + 64 * i, a.E - 1) / n) & 1)) alive &= ~(1ull << i);
+    kept = __ballot(lane < a.groups && rank < a.keep);
   }
-  uint64_t key[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) key[i] = alive >> i & 1 ? f64_order_key(a.bias ? c[i] : (double)l[i]) : 0;
+  __builtin_amdgcn_wave_barrier();
+  uint64_t* key = reinterpret_cast<uint64_t*>(buf);
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += 64)
+    key[e] = a.groups > 1 && !(kept >> (e / n) & 1) ? 0 : f64_order_key(a.bias ? buf[e] : (double)row[e]);
   int mine = 0;
+#pragma unroll 1
   for (int j = 0; j < a.k; ++j) {
-    uint64_t best = key[0];
+    uint64_t best = 0;
+    int at = 1 << 30;                              // the lowest index of that key
+#pragma unroll 4
+    for (int e = lane; e < a.E; e += 64) {
+      const uint64_t v = key[e];
+      if (v > best) { best = v; at = e; }
+    }
+    const uint64_t top = sel_max64(best);
+    if (best != top) at = 1 << 30;
 #pragma unroll
-    for (int i = 1; i < NV; ++i) best = key[i] > best ? key[i] : best;
-    best = sel_max64(best);
-    int e = 1 << 30;                               // the lowest index of that key
-#pragma unroll
-    for (int i = NV - 1; i >= 0; --i)
-      if (key[i] == best) e = lane + 64 * i;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) e = min(e, __shfl_xor(e, d));
-    if (lane == j) mine = e;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (lane + 64 * i == e) key[i] = 0;
+    for (int d = 1; d < 64; d <<= 1) at = min(at, __shfl_xor(at, d));
+    if (lane == j) mine = at;
+    if ((at & 63) == lane) key[at] = 0;
   }
+  __builtin_amdgcn_wave_barrier();
   return mine;
+}
+
+// The same in fp32, where its rounding cannot change the result; false where it might.
+//   - sigmoid: c has an error of 4 units u = 2^-24 of s (the exponential's argument |l| u, weighted with s (1 - s) |l| <= 0.23, its
+//     function 2 u, weighted with 1/4, the sum and the reciprocal) and one of c.  softmax: the argument's grows with the distance to
+//     the largest logit, 2.5 u each, and the sum's is common to all: under 32 u for the experts in question.  Two c (or group
+//     scores) are told apart only if they differ by more than tol = 8 u or 32 u of their magnitudes.
+//   - A value that k to k + 4 of the 64 lanes' largest c reach is found by bisection.  The k best are among the experts that reach it,
+//     some 1.3 k of up to 1024 (those of lanes with two of them).  They go to LDS, one to a lane, and are ranked by counting.
+// Candidates too near to each other are ranked again by fp64 scores of their own.  A NaN, group scores too near to each other or
+// too many candidates (few lanes with experts left) leave it all to sel_exact.
+struct SelCand {
+  float c[68];
+  v2u le[64];                // logit, expert
+  float sc[20];
+  v2u sle[20];
+};
+DEV float sel_wave_max(float v) { return max_row_groups(row_max16(v)); }
+DEV float sel_wave_min(float v) { return -sel_wave_max(-v); }
+// The other lanes' value at distance d = 1, 2, 4, 8 (any lane of the other half of 2 d), 16, 32.
+DEV float sel_other(float v, int d) {
+  switch (d) {
+    case 1: return dpp_mov<0xB1>(v);
+    case 2: return dpp_mov<0x4E>(v);
+    case 4: return dpp_mov<0x141>(v);
+    case 8: return dpp_mov<0x140>(v);
+    default: return __shfl_xor(v, d);
+  }
+}
+
+// The m candidates of a token ranked again by their fp64 scores (without bias or groups: by the logits).
+__device__ __noinline__ int sel_near(SelRule a, const float* row, SelCand* q, int m) {
+  const int lane = threadIdx.x & 63;
+  const v2u le = q->le[lane];
+  const int mine = lane < m ? (int)le[1] : 0;
+  uint64_t key = 0;
+  if (a.bias) {
+    const SelRow r = sel_row64(a, row);
+    const double c = sel_choice64(a, r, mine);
+    if (lane < m) key = f64_order_key(c);
+  } else if (lane < m) {
+    key = f64_order_key((double)__uint_as_float(le[0]));
+  }
+  int rank = 0;
+  for (int j = 0; j < m; ++j) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)key, j);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(key >> 32), j);
+    const uint64_t o = (uint64_t)hi << 32 | lo;
+    rank += o > key || (o == key && __builtin_amdgcn_readlane(mine, j) < mine);
+  }
+  if (lane < m && rank < a.k) q->sle[rank] = le;
+  __builtin_amdgcn_wave_barrier();
+  const int id = (int)q->sle[min(lane, 15)][1];
+  __builtin_amdgcn_wave_barrier();
+  return id;
+}
+
+enum { SEL_CLEAR = 0, SEL_NEAR = 1, SEL_ALL = 2 };   // done; candidates too near; all in fp64
+template <int NV>
+DEV int sel_fast(const SelArgs& a, int lane, const float (&l)[NV], float bmax, float mx, float inv, float* buf, SelCand& q,
+                 int* count, float* lj, int* id) {
+  const float nan = __builtin_nanf("");
+  float c[NV], b[NV];
+  if (a.bias) sel_load<NV>(a.bias, a.E, lane, b);
+  uint64_t bad = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float s = l[i];
+    if (a.bias || a.groups > 1) {
+      s = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-l[i])) : __expf(l[i] - mx) * inv;
+      if (a.bias) s += b[i];
+    }
+    c[i] = s;
+    bad |= __ballot(!(s < __builtin_inff()));
+    if (sel_expert(lane, i) >= a.E) c[i] = nan;          // (compared with: false)
+  }
+  if (bad) return SEL_ALL;
+  if (a.keep < a.groups) {
+    const int n = a.E / a.groups, lg = a.lanes_log2, L = 1 << lg, g = lane >> lg;
+    float m1 = -__builtin_inff(), m2 = m1;         // the two largest
+    if (NV == 4 && a.direct) {                     // a group's experts are those of its lanes
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        m2 = fmaxf(m2, fminf(m1, c[i]));
+        m1 = fmaxf(m1, c[i]);
+      }
+    } else {
+      if (a.E % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; i += 4)
+          if (sel_expert(lane, i) < a.E) *reinterpret_cast<v4f*>(buf + sel_expert(lane, i)) = v4f{c[i], c[i + 1], c[i + 2], c[i + 3]};
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (sel_expert(lane, i) < a.E) buf[sel_expert(lane, i)] = c[i];
+      }
+      __builtin_amdgcn_wave_barrier();
+      if (g < a.groups) {
+        for (int e = lane & (L - 1); e < n; e += L) {
+          const float v = buf[g * n + e];
+          m2 = fmaxf(m2, fminf(m1, v));
+          m1 = fmaxf(m1, v);
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+    for (int d = 1; d < L; d <<= 1) {
+      const float o1 = sel_other(m1, d), o2 = sel_other(m2, d);
+      m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
+      m1 = fmaxf(m1, o1);
+    }
+    const float score = g < a.groups ? (a.top == 2 ? m1 + m2 : m1) : nan;
+    int rank = 0;
+    for (int h = 0; h < a.groups; ++h)
+      rank += __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(score), h << lg)) > score;
+    const bool in = g < a.groups && rank < a.keep;
+    const uint64_t kept = __ballot(in), last = __ballot(rank == a.keep - 1 && g < a.groups), next = __ballot(rank == a.keep && g < a.groups);
+    // (equal scores share a rank, and the one behind it is missing)
+    if (!last || !next) return SEL_ALL;
+    const float lo = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(score), __builtin_ctzll(last)));
+    const float hi = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(score), __builtin_ctzll(next)));
+    if (!(lo - hi > a.tol * (fabsf(lo) + fabsf(hi) + 4.0f * bmax))) return SEL_ALL;
+    if (NV == 4 && a.direct) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] = in ? c[i] : nan;
+    } else {
+      const float per = 1.0f / (float)n;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        // (e / n: the quotient is at least 1 / 2048 away from the next whole number)
+        const int of = (int)(((float)sel_expert(lane, i) + 0.5f) * per);
+        if (!(kept >> (of << lg & 63) & 1)) c[i] = nan;
+      }
+    }
+  }
+  float t = c[0];
+#pragma unroll
+  for (int i = 1; i < NV; ++i) t = fmaxf(t, c[i]);
+  // bisection of the lanes' largest, as ordered integers (0: a lane without experts)
+  const uint32_t tk = t == t ? f32_order_key(t) : 0;
+  float from = -__builtin_inff();
+  if (__popcll(__ballot(tk > 0)) >= a.k) {
+    uint32_t lo = 1, hi = 0xFFFFFFFFu;             // at least k lanes reach lo, fewer hi
+    for (int i = 0; i < 24; ++i) {
+      const uint32_t mid = lo + ((hi - lo) >> 1);
+      const int in = __popcll(__ballot(tk >= mid));
+      if (in >= a.k) lo = mid; else hi = mid;
+      if (in >= a.k && in <= a.k + 4) break;
+    }
+    from = f32_from_order_key(lo);
+    from -= 4.0f * a.tol * (fabsf(from) + bmax);
+    if (!(from == from)) from = -__builtin_inff();
+  }
+  int m = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const bool in = c[i] >= from;
+    const uint64_t who = __ballot(in);
+    const int at = m + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+    if (in && at < 64) {
+      q.c[at] = c[i];
+      q.le[at] = v2u{__float_as_uint(l[i]), (uint32_t)sel_expert(lane, i)};
+    }
+    m += __popcll(who);
+  }
+  *count = m;
+  if (m > 64 || m < a.k) return SEL_ALL;
+  if (lane < 4) q.c[m + lane] = nan;
+  if (lane < 20) q.sc[lane] = nan;
+  __builtin_amdgcn_wave_barrier();
+  const float mine = lane < m ? q.c[lane] : nan;
+  const v2u le = q.le[lane];
+  int rank = 0;
+  for (int j = 0; j < m; j += 4) {
+    const v4f o = *reinterpret_cast<const v4f*>(q.c + j);
+    rank += (o[0] > mine) + (o[1] > mine) + (o[2] > mine) + (o[3] > mine);
+  }
+  if (lane < m && rank <= a.k) {
+    q.sc[rank] = mine;
+    q.sle[rank] = le;
+  }
+  __builtin_amdgcn_wave_barrier();
+  const int r = min(lane, 16);
+  const float x = q.sc[r], y = q.sc[r + 1];        // (equal ones share a place: the next stays NaN)
+  const v2u win = q.sle[r];
+  __builtin_amdgcn_wave_barrier();
+  const bool exact = !a.bias && a.groups == 1;     // (logits themselves)
+  const bool clear = x - y > (exact ? 0.f : a.tol * (fabsf(x) + fabsf(y) + 2.0f * bmax)) || (r == a.k - 1 && m == a.k);
+  *lj = __uint_as_float(win[0]);
+  *id = (int)win[1];
+  return __ballot(lane < a.k && !clear) ? SEL_NEAR : SEL_CLEAR;
 }
 
 // The scores of the selected experts (lane j < k: expert j, its logit lj), but for a factor
@@ -134,38 +345,57 @@ DEV int sel_exact(const SelArgs& a, const float (&l)[NV], double* buf) {
 DEV float sel_scores16(bool sigmoid, bool live, float lj) {
   const float b = sigmoid ? fminf(lj, 0.f) : lj;
   const float m = row_max16(live ? b : -__builtin_inff());
-  const float e = m == -__builtin_inff() && b == m ? 0.f : expf(b - m);
-  return !live ? 0.f : sigmoid ? e / (1.0f + expf(-fabsf(lj))) : e;
+  const float e = m == -__builtin_inff() && b == m ? 0.f : __expf(b - m);
+  return !live ? 0.f : sigmoid ? e * __builtin_amdgcn_rcpf(1.0f + __expf(-fabsf(lj))) : e;
 }
 
 template <int NV>
-__global__ void __launch_bounds__(64 * kSelWaves) k_select(SelArgs a) {
-  __shared__ double buf[kSelWaves][64 * NV];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  for (long t = (long)blockIdx.x * kSelWaves + w; t < a.T; t += (long)gridDim.x * kSelWaves) {
-    const float* row = a.logits + t * a.E;
-    float l[NV];
+__global__ void __launch_bounds__(64 * kSelWaves, NV == 4 ? 8 : 4) k_select(SelArgs a) {
+  __shared__ __attribute__((aligned(16))) double buf[kSelWaves][64 * NV];
+  __shared__ __attribute__((aligned(16))) SelCand cand[kSelWaves];
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float bmax = 0.f;                                // of the finite ones
+  if (a.bias) {
+    float b[NV];
+    sel_load<NV>(a.bias, a.E, threadIdx.x & 63, b);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) l[i] = row[min(lane + 64 * i, a.E - 1)];
-    const int e = sel_exact<NV>(a, l, buf[w]);
+    for (int i = 0; i < NV; ++i) bmax = fmaxf(bmax, fabsf(b[i]) < __builtin_inff() ? fabsf(b[i]) : 0.f);
+    bmax = sel_wave_max(bmax);
+  }
+  const SelRule rule{a.bias, a.E, a.k, a.sigmoid, a.groups, a.keep, a.top};
+  const bool dense = !a.sigmoid && (!a.renorm || a.bias || a.groups > 1);          // softmax over all experts
+  for (long t = (long)blockIdx.x * kSelWaves + w; t < a.T; t += (long)gridDim.x * kSelWaves) {
+    // (opaque: what depends on the lane alone is formed again for each token, cheaper than the registers to keep it)
+    const int lane = (int)opaque(threadIdx.x & 63);
+    const float* row = a.logits + t * a.E;
+    float l[NV], mx = 0.f, sum = 0.f;
+    sel_load<NV>(row, a.E, lane, l);
+    if (dense) {
+      mx = -__builtin_inff();
+#pragma unroll
+      for (int i = 0; i < NV; ++i) mx = fmaxf(mx, sel_expert(lane, i) < a.E ? l[i] : mx);
+      mx = sel_wave_max(mx);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) sum += sel_expert(lane, i) < a.E ? __expf(l[i] - mx) : 0.f;
+      sum = wave_sum(sum);
+    }
+    int e, m;
+    float lj;
     const bool live = lane < a.k;
-    const float lj = row[live ? e : 0];
+    const int state = sel_fast<NV>(a, lane, l, bmax, mx, __builtin_amdgcn_rcpf(sum), reinterpret_cast<float*>(buf[w]), cand[w], &m, &lj, &e);
+    if (state != SEL_CLEAR) {
+      e = state == SEL_NEAR ? sel_near(rule, row, &cand[w], m) : sel_exact(rule, row, buf[w]);
+      lj = row[live ? e : 0];
+    }
     float s;
     if (a.renorm) {
       s = sel_scores16(a.sigmoid, live, lj);
-      const float sum = row_sum16(s);
-      s = sum == 0.f ? 0.f : s / sum;
+      const float z = row_sum16(s);
+      s = z == 0.f ? 0.f : s * __builtin_amdgcn_rcpf(z);
     } else if (a.sigmoid) {
-      s = 1.0f / (1.0f + expf(-lj));
+      s = __builtin_amdgcn_rcpf(1.0f + __expf(-lj));
     } else {
-      float mx = l[0], sum = 0.f;
-#pragma unroll
-      for (int i = 1; i < NV; ++i) mx = fmaxf(mx, l[i]);
-      mx = sel_max(mx);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) sum += lane + 64 * i < a.E ? expf(l[i] - mx) : 0.f;
-      sum = wave_sum(sum);
-      s = mx == -__builtin_inff() ? 0.f : expf(lj - mx) / sum;
+      s = mx == -__builtin_inff() ? 0.f : __expf(lj - mx) * __builtin_amdgcn_rcpf(sum);
     }
     if (live) {
       a.ids[t * a.k + lane] = e;

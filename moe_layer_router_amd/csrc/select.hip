@@ -41,6 +41,14 @@ SelArgs sel_args(const moe_selection* s) {
   a.sigmoid = s->scoring == MOE_SCORING_SIGMOID;
   a.groups = s->n_group; a.keep = s->topk_group; a.top = s->group_top;
   a.renorm = s->renormalize != 0;
+  while (s->n_group << (a.lanes_log2 + 1) <= 64) ++a.lanes_log2;
+  const int per = s->E / s->n_group, lanes = per / 4;
+  if (s->E <= 256 && per % 4 == 0 && (lanes & (lanes - 1)) == 0) {
+    a.direct = 1;
+    a.lanes_log2 = 0;
+    while (1 << a.lanes_log2 < lanes) ++a.lanes_log2;
+  }
+  a.tol = a.sigmoid ? 0x1p-21f : 0x1p-19f;
   a.scale = s->scale;
   return a;
 }
@@ -105,8 +113,6 @@ moe_status moe_select_experts(const moe_selection* s, const float* logits, const
   SelArgs a = sel_args(s);
   a.logits = logits; a.bias = bias; a.ids = topk_ids; a.w = topk_weights;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (a.E <= 64) return launch_select<1>(a, di.cus, st);
-  if (a.E <= 128) return launch_select<2>(a, di.cus, st);
   if (a.E <= 256) return launch_select<4>(a, di.cus, st);
   if (a.E <= 512) return launch_select<8>(a, di.cus, st);
   return launch_select<16>(a, di.cus, st);

@@ -14,6 +14,9 @@ struct SelArgs {
   float* w;                  // [T][k]
   long T;
   int E, k, sigmoid, groups, keep, top, renorm;
+  int lanes_log2;            // lanes that share a group, as a power of two
+  int direct;                // E <= 256, and a group is 4 experts of each of those lanes
+  float tol;                 // what fp32 scores are compared up to, relative
   float scale;
   // backward
   const int32_t* ids_in;
