@@ -72,6 +72,7 @@ struct SelRow {
   float mx;
   double sum;
 };
+template <int UNROLL>
 DEV SelRow sel_row64(const SelRule& a, const float* row) {
   SelRow r{row, -__builtin_inff(), 1.0};
   if (a.sigmoid) return r;
@@ -80,7 +81,7 @@ DEV SelRow sel_row64(const SelRule& a, const float* row) {
   for (int e = lane; e < a.E; e += 64) r.mx = fmaxf(r.mx, row[e]);
   r.mx = sel_max(r.mx);
   r.sum = 0;
-#pragma unroll 1
+#pragma unroll UNROLL
   for (int e = lane; e < a.E; e += 64) r.sum += row[e] == -__builtin_inff() ? 0.0 : exp((double)row[e] - (double)r.mx);
   r.sum = sel_sum(r.sum);
   return r;
@@ -97,7 +98,7 @@ __device__ __noinline__ int sel_exact(SelRule a, const float* row, double* buf) 
   const int lane = threadIdx.x & 63, n = a.E / a.groups;
   uint64_t kept = ~0ull;
   if (a.bias || a.groups > 1) {                    // (else the logits' order is the scores')
-    const SelRow r = sel_row64(a, row);
+    const SelRow r = sel_row64<1>(a, row);
 #pragma unroll 1
     for (int e = lane; e < a.E; e += 64) buf[e] = sel_choice64(a, r, e);
   }
@@ -146,6 +147,9 @@ __device__ __noinline__ int sel_exact(SelRule a, const float* row, double* buf) 
   return mine;
 }
 
+// exp(v) by the instruction for 2^v: within 2 units, and the argument's rounding; what is below 2^-126 is zero.
+DEV float sel_exp(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504f); }
+
 // The same in fp32, where its rounding cannot change the result; false where it might.
 //   - sigmoid: c has an error of 4 units u = 2^-24 of s (the exponential's argument |l| u, weighted with s (1 - s) |l| <= 0.23, its
 //     function 2 u, weighted with 1/4, the sum and the reciprocal) and one of c.  softmax: the argument's grows with the distance to
@@ -157,36 +161,35 @@ __device__ __noinline__ int sel_exact(SelRule a, const float* row, double* buf) 
 // too many candidates (few lanes with experts left) leave it all to sel_exact.
 struct SelCand {
   float c[68];
-  v2u le[64];                // logit, expert
-  float sc[20];
-  v2u sle[20];
+  int e[64];
+  float sc[20];              // by rank
+  int se[20];
 };
 DEV float sel_wave_max(float v) { return max_row_groups(row_max16(v)); }
 DEV float sel_wave_min(float v) { return -sel_wave_max(-v); }
-// The other lanes' value at distance d = 1, 2, 4, 8 (any lane of the other half of 2 d), 16, 32.
-DEV float sel_other(float v, int d) {
-  switch (d) {
-    case 1: return dpp_mov<0xB1>(v);
-    case 2: return dpp_mov<0x4E>(v);
-    case 4: return dpp_mov<0x141>(v);
-    case 8: return dpp_mov<0x140>(v);
-    default: return __shfl_xor(v, d);
-  }
+// The two largest of a set, from those of its halves.
+DEV void sel_top2(float& m1, float& m2, float o1, float o2) {
+  m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
+  m1 = fmaxf(m1, o1);
+}
+// The two largest over L lanes in a row, from those of each.
+DEV void sel_lanes_top2(float& m1, float& m2, int L) {
+  if (L > 1) sel_top2(m1, m2, dpp_mov<0xB1>(m1), dpp_mov<0xB1>(m2));
+  if (L > 2) sel_top2(m1, m2, dpp_mov<0x4E>(m1), dpp_mov<0x4E>(m2));
+  if (L > 4) sel_top2(m1, m2, dpp_mov<0x141>(m1), dpp_mov<0x141>(m2));
+  if (L > 8) sel_top2(m1, m2, dpp_mov<0x140>(m1), dpp_mov<0x140>(m2));
+  if (L > 16) sel_top2(m1, m2, __shfl_xor(m1, 16), __shfl_xor(m2, 16));
+  if (L > 32) sel_top2(m1, m2, __shfl_xor(m1, 32), __shfl_xor(m2, 32));
 }
 
 // The m candidates of a token ranked again by their fp64 scores (without bias or groups: by the logits).
+template <int NV>
 __device__ __noinline__ int sel_near(SelRule a, const float* row, SelCand* q, int m) {
   const int lane = threadIdx.x & 63;
-  const v2u le = q->le[lane];
-  const int mine = lane < m ? (int)le[1] : 0;
-  uint64_t key = 0;
-  if (a.bias) {
-    const SelRow r = sel_row64(a, row);
-    const double c = sel_choice64(a, r, mine);
-    if (lane < m) key = f64_order_key(c);
-  } else if (lane < m) {
-    key = f64_order_key((double)__uint_as_float(le[0]));
-  }
+  const int mine = lane < m ? q->e[lane] : 0;
+  double c = row[mine];
+  if (a.bias) c = sel_choice64(a, sel_row64<NV / 4>(a, row), mine);
+  const uint64_t key = lane < m ? f64_order_key(c) : 0;
   int rank = 0;
   for (int j = 0; j < m; ++j) {
     const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)key, j);
@@ -194,35 +197,34 @@ __device__ __noinline__ int sel_near(SelRule a, const float* row, SelCand* q, in
     const uint64_t o = (uint64_t)hi << 32 | lo;
     rank += o > key || (o == key && __builtin_amdgcn_readlane(mine, j) < mine);
   }
-  if (lane < m && rank < a.k) q->sle[rank] = le;
+  if (lane < m && rank < a.k) q->se[rank] = mine;
   __builtin_amdgcn_wave_barrier();
-  const int id = (int)q->sle[min(lane, 15)][1];
+  const int id = q->se[min(lane, 15)];
   __builtin_amdgcn_wave_barrier();
   return id;
 }
 
 enum { SEL_CLEAR = 0, SEL_NEAR = 1, SEL_ALL = 2 };   // done; candidates too near; all in fp64
-template <int NV>
-DEV int sel_fast(const SelArgs& a, int lane, const float (&l)[NV], float bmax, float mx, float inv, float* buf, SelCand& q,
-                 int* count, float* lj, int* id) {
-  const float nan = __builtin_nanf("");
-  float c[NV], b[NV];
-  if (a.bias) sel_load<NV>(a.bias, a.E, lane, b);
-  uint64_t bad = 0;
+template <int NV, int GROUPED>
+DEV int sel_fast(const SelArgs& a, int lane, float (&c)[NV], float bmax, float* buf, SelCand& q, int* count, int* id) {
+  const float nan = __builtin_nanf("");            // (an expert that is out: no comparison holds)
+  if (a.bias) {
+    float b[NV];
+    sel_load<NV>(a.bias, a.E, lane, b);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float s = l[i];
-    if (a.bias || a.groups > 1) {
-      s = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-l[i])) : __expf(l[i] - mx) * inv;
-      if (a.bias) s += b[i];
-    }
-    c[i] = s;
-    bad |= __ballot(!(s < __builtin_inff()));
-    if (sel_expert(lane, i) >= a.E) c[i] = nan;          // (compared with: false)
+    for (int i = 0; i < NV; ++i) c[i] += b[i];
   }
-  if (bad) return SEL_ALL;
-  if (a.keep < a.groups) {
+  if (a.E != 64 * NV) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (sel_expert(lane, i) >= a.E) c[i] = nan;
+  }
+  if (GROUPED) {
     const int n = a.E / a.groups, lg = a.lanes_log2, L = 1 << lg, g = lane >> lg;
+    int fine = 0;                                  // (minima and maxima pass over a NaN)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) fine += __popcll(__ballot(c[i] < __builtin_inff()));
+    if (fine != a.E) return SEL_ALL;
     float m1 = -__builtin_inff(), m2 = m1;         // the two largest
     if (NV == 4 && a.direct) {                     // a group's experts are those of its lanes
 #pragma unroll
@@ -250,11 +252,7 @@ DEV int sel_fast(const SelArgs& a, int lane, const float (&l)[NV], float bmax, f
       }
       __builtin_amdgcn_wave_barrier();
     }
-    for (int d = 1; d < L; d <<= 1) {
-      const float o1 = sel_other(m1, d), o2 = sel_other(m2, d);
-      m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
-      m1 = fmaxf(m1, o1);
-    }
+    sel_lanes_top2(m1, m2, L);
     const float score = g < a.groups ? (a.top == 2 ? m1 + m2 : m1) : nan;
     int rank = 0;
     for (int h = 0; h < a.groups; ++h)
@@ -282,40 +280,45 @@ DEV int sel_fast(const SelArgs& a, int lane, const float (&l)[NV], float bmax, f
   float t = c[0];
 #pragma unroll
   for (int i = 1; i < NV; ++i) t = fmaxf(t, c[i]);
-  // bisection of the lanes' largest, as ordered integers (0: a lane without experts)
-  const uint32_t tk = t == t ? f32_order_key(t) : 0;
+  // Bisection of the lanes' largest, between what one lane of each of 16 sets at least reaches and the largest of all.
+  if (!(t == t)) t = -__builtin_inff();
+  float lo = max_row_groups(t), hi = row_max16(lo);
+  lo = -row_max16(-lo);
   float from = -__builtin_inff();
-  if (__popcll(__ballot(tk > 0)) >= a.k) {
-    uint32_t lo = 1, hi = 0xFFFFFFFFu;             // at least k lanes reach lo, fewer hi
-    for (int i = 0; i < 24; ++i) {
-      const uint32_t mid = lo + ((hi - lo) >> 1);
-      const int in = __popcll(__ballot(tk >= mid));
+  if (lo == from && __popcll(__ballot(t > from)) >= a.k)       // (a set without experts: the least of the lanes that have some)
+    lo = sel_wave_min(t > from ? t : __builtin_inff());
+  if (lo > from) {
+    for (int i = 0; i < 16; ++i) {
+      const float mid = 0.5f * lo + 0.5f * hi;
+      const int in = __popcll(__ballot(t >= mid));
       if (in >= a.k) lo = mid; else hi = mid;
       if (in >= a.k && in <= a.k + 4) break;
     }
-    from = f32_from_order_key(lo);
-    from -= 4.0f * a.tol * (fabsf(from) + bmax);
-    if (!(from == from)) from = -__builtin_inff();
+    from = lo - 4.0f * a.tol * (fabsf(lo) + bmax);
   }
   int m = 0;
+  int* be = reinterpret_cast<int*>(buf) + 64 * NV;             // candidates: c, and their experts
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const bool in = c[i] >= from;
     const uint64_t who = __ballot(in);
     const int at = m + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
-    if (in && at < 64) {
-      q.c[at] = c[i];
-      q.le[at] = v2u{__float_as_uint(l[i]), (uint32_t)sel_expert(lane, i)};
+    if (in) {
+      buf[at] = c[i];
+      be[at] = sel_expert(lane, i);
     }
     m += __popcll(who);
   }
   *count = m;
   if (m > 64 || m < a.k) return SEL_ALL;
-  if (lane < 4) q.c[m + lane] = nan;
+  __builtin_amdgcn_wave_barrier();
+  const float mine = lane < m ? buf[lane] : nan;
+  const int me = be[lane];
+  q.c[lane] = mine;
+  if (lane < 4) q.c[64 + lane] = nan;
+  q.e[lane] = me;
   if (lane < 20) q.sc[lane] = nan;
   __builtin_amdgcn_wave_barrier();
-  const float mine = lane < m ? q.c[lane] : nan;
-  const v2u le = q.le[lane];
   int rank = 0;
   for (int j = 0; j < m; j += 4) {
     const v4f o = *reinterpret_cast<const v4f*>(q.c + j);
@@ -323,17 +326,15 @@ DEV int sel_fast(const SelArgs& a, int lane, const float (&l)[NV], float bmax, f
   }
   if (lane < m && rank <= a.k) {
     q.sc[rank] = mine;
-    q.sle[rank] = le;
+    q.se[rank] = me;
   }
   __builtin_amdgcn_wave_barrier();
   const int r = min(lane, 16);
   const float x = q.sc[r], y = q.sc[r + 1];        // (equal ones share a place: the next stays NaN)
-  const v2u win = q.sle[r];
+  *id = q.se[r];
   __builtin_amdgcn_wave_barrier();
-  const bool exact = !a.bias && a.groups == 1;     // (logits themselves)
+  const bool exact = !a.bias && !GROUPED;          // (logits themselves)
   const bool clear = x - y > (exact ? 0.f : a.tol * (fabsf(x) + fabsf(y) + 2.0f * bmax)) || (r == a.k - 1 && m == a.k);
-  *lj = __uint_as_float(win[0]);
-  *id = (int)win[1];
   return __ballot(lane < a.k && !clear) ? SEL_NEAR : SEL_CLEAR;
 }
 
@@ -345,11 +346,12 @@ DEV int sel_fast(const SelArgs& a, int lane, const float (&l)[NV], float bmax, f
 DEV float sel_scores16(bool sigmoid, bool live, float lj) {
   const float b = sigmoid ? fminf(lj, 0.f) : lj;
   const float m = row_max16(live ? b : -__builtin_inff());
-  const float e = m == -__builtin_inff() && b == m ? 0.f : __expf(b - m);
-  return !live ? 0.f : sigmoid ? e * __builtin_amdgcn_rcpf(1.0f + __expf(-fabsf(lj))) : e;
+  const float e = m == -__builtin_inff() && b == m ? 0.f : sel_exp(b - m);
+  return !live ? 0.f : sigmoid ? e * __builtin_amdgcn_rcpf(1.0f + sel_exp(-fabsf(lj))) : e;
 }
 
-template <int NV>
+// GROUPED: some groups are left out.
+template <int NV, int SIGMOID, int GROUPED>
 __global__ void __launch_bounds__(64 * kSelWaves, NV == 4 ? 8 : 4) k_select(SelArgs a) {
   __shared__ __attribute__((aligned(16))) double buf[kSelWaves][64 * NV];
   __shared__ __attribute__((aligned(16))) SelCand cand[kSelWaves];
@@ -362,40 +364,52 @@ __global__ void __launch_bounds__(64 * kSelWaves, NV == 4 ? 8 : 4) k_select(SelA
     for (int i = 0; i < NV; ++i) bmax = fmaxf(bmax, fabsf(b[i]) < __builtin_inff() ? fabsf(b[i]) : 0.f);
     bmax = sel_wave_max(bmax);
   }
-  const SelRule rule{a.bias, a.E, a.k, a.sigmoid, a.groups, a.keep, a.top};
-  const bool dense = !a.sigmoid && (!a.renorm || a.bias || a.groups > 1);          // softmax over all experts
+  const SelRule rule{a.bias, a.E, a.k, SIGMOID, a.groups, a.keep, a.top};
+  const bool scored = a.bias || GROUPED;      // (else the logits' order is the scores')
+  const bool dense = !SIGMOID && (!a.renorm || scored);      // softmax over all experts
   for (long t = (long)blockIdx.x * kSelWaves + w; t < a.T; t += (long)gridDim.x * kSelWaves) {
     // (opaque: what depends on the lane alone is formed again for each token, cheaper than the registers to keep it)
     const int lane = (int)opaque(threadIdx.x & 63);
     const float* row = a.logits + t * a.E;
-    float l[NV], mx = 0.f, sum = 0.f;
-    sel_load<NV>(row, a.E, lane, l);
+    float c[NV], mx = 0.f, inv = 0.f;              // logits, then scores, then c
+    sel_load<NV>(row, a.E, lane, c);
     if (dense) {
-      mx = -__builtin_inff();
+      if (a.E != 64 * NV) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) mx = fmaxf(mx, sel_expert(lane, i) < a.E ? l[i] : mx);
+        for (int i = 0; i < NV; ++i)
+          if (sel_expert(lane, i) >= a.E) c[i] = -__builtin_inff();
+      }
+      mx = c[0];
+#pragma unroll
+      for (int i = 1; i < NV; ++i) mx = fmaxf(mx, c[i]);
       mx = sel_wave_max(mx);
+      float sum = 0.f;
+      float e[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) sum += sel_expert(lane, i) < a.E ? __expf(l[i] - mx) : 0.f;
-      sum = wave_sum(sum);
+      for (int i = 0; i < NV; ++i) sum += e[i] = sel_exp(c[i] - mx);
+      inv = __builtin_amdgcn_rcpf(wave_sum(sum));
+      if (scored) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) c[i] = e[i] * inv;
+      }
+    } else if (scored) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) c[i] = __builtin_amdgcn_rcpf(1.0f + sel_exp(-c[i]));
     }
     int e, m;
-    float lj;
     const bool live = lane < a.k;
-    const int state = sel_fast<NV>(a, lane, l, bmax, mx, __builtin_amdgcn_rcpf(sum), reinterpret_cast<float*>(buf[w]), cand[w], &m, &lj, &e);
-    if (state != SEL_CLEAR) {
-      e = state == SEL_NEAR ? sel_near(rule, row, &cand[w], m) : sel_exact(rule, row, buf[w]);
-      lj = row[live ? e : 0];
-    }
+    const int state = sel_fast<NV, GROUPED>(a, lane, c, bmax, reinterpret_cast<float*>(buf[w]), cand[w], &m, &e);
+    if (state != SEL_CLEAR) e = state == SEL_NEAR ? sel_near<NV>(rule, row, &cand[w], m) : sel_exact(rule, row, buf[w]);
+    const float lj = row[live ? e : 0];
     float s;
     if (a.renorm) {
-      s = sel_scores16(a.sigmoid, live, lj);
+      s = sel_scores16(SIGMOID, live, lj);
       const float z = row_sum16(s);
       s = z == 0.f ? 0.f : s * __builtin_amdgcn_rcpf(z);
-    } else if (a.sigmoid) {
-      s = __builtin_amdgcn_rcpf(1.0f + __expf(-lj));
+    } else if (SIGMOID) {
+      s = __builtin_amdgcn_rcpf(1.0f + sel_exp(-lj));
     } else {
-      s = mx == -__builtin_inff() ? 0.f : __expf(lj - mx) * __builtin_amdgcn_rcpf(sum);
+      s = mx == -__builtin_inff() ? 0.f : sel_exp(lj - mx) * inv;
     }
     if (live) {
       a.ids[t * a.k + lane] = e;

@@ -57,7 +57,14 @@ unsigned sel_grid(long T, int cus) { return (unsigned)std::min((T + kSelWaves - 
 
 template <int NV>
 moe_status launch_select(const SelArgs& a, int cus, hipStream_t st) {
-  hipLaunchKernelGGL(k_select<NV>, dim3(sel_grid(a.T, cus)), dim3(64 * kSelWaves), 0, st, a);
+  const dim3 grid(sel_grid(a.T, cus)), wg(64 * kSelWaves);
+  if (a.keep < a.groups) {
+    if (a.sigmoid) hipLaunchKernelGGL((k_select<NV, 1, 1>), grid, wg, 0, st, a);
+    else hipLaunchKernelGGL((k_select<NV, 0, 1>), grid, wg, 0, st, a);
+  } else {
+    if (a.sigmoid) hipLaunchKernelGGL((k_select<NV, 1, 0>), grid, wg, 0, st, a);
+    else hipLaunchKernelGGL((k_select<NV, 0, 0>), grid, wg, 0, st, a);
+  }
   HIP_TRY(hipGetLastError());
   return MOE_OK;
 }
