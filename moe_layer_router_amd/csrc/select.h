@@ -425,108 +425,150 @@ __global__ void __launch_bounds__(64 * kSelWaves, NV == 4 ? 8 : 4) k_select(SelA
 // The differences cancel (1 - s of a sure expert, dw against its mean): they are formed in
 // fp64, which only the k selected experts need.
 // An expert that stands twice among a token's ids has the sum of both entries.
+//
+// A wave does four tokens at a time: their selected experts in the four rows of 16 lanes, their rows of E one after another.
+template <int CTRL>
+DEV double dpp_movd(double v) {
+  const uint64_t x = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)x, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(x >> 32), CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 DEV double sel_row_sum16(double v) {
-#pragma unroll
-  for (int d = 1; d < 16; d <<= 1) v += __shfl_xor(v, d);
-  return v;
+  v += dpp_movd<0xB1>(v);
+  v += dpp_movd<0x4E>(v);
+  v += dpp_movd<0x141>(v);
+  return v + dpp_movd<0x140>(v);
+}
+DEV double sel_row_max16(double v) {
+  v = fmax(v, dpp_movd<0xB1>(v));
+  v = fmax(v, dpp_movd<0x4E>(v));
+  v = fmax(v, dpp_movd<0x141>(v));
+  return fmax(v, dpp_movd<0x140>(v));
 }
 
-// Lane j < k: the id and the gradient of its logit (softmax without renorm: d_j s_j alone, and
-// *inner the sum of them over the token, which every expert's has to lose times its s).
-DEV void sel_grad16(const SelArgs& a, long t, const float* row, float mx, double sum, int* id, double* g, double* inner) {
-  const int lane = threadIdx.x & 63;
-  const bool live = lane < a.k;
-  const size_t f = (size_t)t * a.k + (live ? lane : 0);
-  *id = min(max(a.ids_in[f], 0), a.E - 1);
-  const double d = live ? (double)a.scale * a.dw[f] : 0.0;
-  const double lj = row[*id];
+// Lane j of a row: the id (-1: none, or an earlier slot has it) and the gradient of its logit lj, d = scale dw.  Softmax without renorm: d_j s_j
+// alone, s = exp(lj - mx) / sum, and *inner the sum of them over the token, which every expert's has to lose times its s.
+DEV void sel_grad16(const SelArgs& a, bool live, double d, double lj, double mx, double sum, int* id, double* g, double* inner) {
   double v = 0;
   *inner = 0;
   if (a.renorm) {
-    double b = a.sigmoid ? fmin(lj, 0.0) : lj, m = live ? b : -__builtin_inf();
-#pragma unroll
-    for (int x = 1; x < 16; x <<= 1) m = fmax(m, __shfl_xor(m, x));
+    const double b = a.sigmoid ? fmin(lj, 0.0) : lj, m = sel_row_max16(live ? b : -__builtin_inf());
     double s = m == -__builtin_inf() && b == m ? 0.0 : exp(b - m);
-    if (a.sigmoid) s /= 1.0 + exp(-fabs(lj));
+    const double f = a.sigmoid ? exp(-fabs(lj)) : 0.0;         // s (1 - s) = f / (1 + f)^2
+    if (a.sigmoid) s /= 1.0 + f;
     if (!live) s = 0;
     const double z = sel_row_sum16(s), q = z == 0.0 ? 0.0 : s / z;
-    v = q * (d - sel_row_sum16(q * d));
-    if (a.sigmoid) v *= 1.0 / (1.0 + exp(lj));     // 1 - s
+    v = q * (d - sel_row_sum16(live ? q * d : 0.0));
+    if (a.sigmoid) v *= lj > 0.0 ? f / (1.0 + f) : 1.0 / (1.0 + f);
   } else if (a.sigmoid) {
-    const double e = exp(-fabs(lj));               // s (1 - s)
-    v = d * (e / ((1.0 + e) * (1.0 + e)));
+    const double f = exp(-fabs(lj));
+    v = d * (f / ((1.0 + f) * (1.0 + f)));
   } else {
-    const double s = sum == 0.0 ? 0.0 : exp(lj - (double)mx) / sum;
+    const double s = sum == 0.0 ? 0.0 : exp(lj - mx) / sum;
     v = s * d;
     *inner = sel_row_sum16(live ? v : 0.0);
   }
   // the first of equal ids takes the others' share
-  double total = 0;
-  bool first = live;
-  for (int j = 0; j < a.k; ++j) {
-    const int o = __shfl(*id, j);
-    const double ov = __shfl(v, j);
-    if (o == *id) {
-      total += ov;
-      if (j < lane) first = false;
+  const int lane = threadIdx.x & 63, j = lane & 15;
+  if (!live) *id = -1 - j;                         // (no two of them alike)
+  bool twice = false;
+#define SEL_ROR(N) twice |= __builtin_amdgcn_mov_dpp(*id, 0x120 + N, 0xF, 0xF, false) == *id
+  SEL_ROR(1); SEL_ROR(2); SEL_ROR(3); SEL_ROR(4); SEL_ROR(5); SEL_ROR(6); SEL_ROR(7); SEL_ROR(8);
+#undef SEL_ROR
+  if (__ballot(twice)) {
+    double total = 0;
+    bool first = true;
+    for (int i = 0; i < 16; ++i) {
+      const int o = __shfl(*id, (lane & 48) + i);
+      const double ov = __shfl(v, (lane & 48) + i);
+      if (o == *id) {
+        total += ov;
+        first = first && i >= j;
+      }
     }
+    v = total;
+    if (!first) *id = -1;
   }
-  if (!first) *id = -1;
-  *g = total;
-  *inner = __shfl(*inner, 0);
+  *g = v;
 }
 
-template <int NV, int SPLIT>
+// DENSE: softmax scores without renorm: every expert of a token has a gradient.
+template <int NV, int SPLIT, int DENSE>
 __global__ void __launch_bounds__(64 * kSelWaves) k_select_bwd(SelArgs a) {
-  __shared__ float buf[kSelWaves][64 * NV];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const bool dense = !a.sigmoid && !a.renorm;
-  for (long t = (long)blockIdx.x * kSelWaves + w; t < a.T; t += (long)gridDim.x * kSelWaves) {
-    const float* row = a.logits + t * a.E;
-    float l[NV], mx = 0.f;
-    double sum = 0;
-    if (dense) {
+  __shared__ __attribute__((aligned(16))) float buf[kSelWaves][64 * NV];
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, j = lane & 15;
+  for (long t0 = ((long)blockIdx.x * kSelWaves + w) * 4; t0 < a.T; t0 += (long)gridDim.x * kSelWaves * 4) {
+    const long t = min(t0 + (lane >> 4), a.T - 1);
+    const bool live = j < a.k;
+    const size_t f = (size_t)t * a.k + (live ? j : 0);
+    int id = min(max(a.ids_in[f], 0), a.E - 1);
+    const double d = live ? (double)a.scale * a.dw[f] : 0.0;
+    const float lj = a.logits[t * a.E + id];
+    float mx = 0.f, sum = 0.f;
+    float l[DENSE ? 4 : 1][NV];                    // logits, then their exponentials
+    if (DENSE) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) l[i] = row[min(lane + 64 * i, a.E - 1)];
-      mx = l[0];
+      for (int r = 0; r < 4; ++r) sel_load<NV>(a.logits + min(t0 + r, a.T - 1) * a.E, a.E, lane, l[DENSE * r]);
 #pragma unroll
-      for (int i = 1; i < NV; ++i) mx = fmaxf(mx, l[i]);
-      mx = sel_max(mx);
+      for (int r = 0; r < 4; ++r) {
+        float(&e)[NV] = l[DENSE * r];
+        if (a.E != 64 * NV) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        l[i] = mx == -__builtin_inff() ? 0.f : expf(l[i] - mx);
-        if (lane + 64 * i < a.E) sum += l[i];
+          for (int i = 0; i < NV; ++i)
+            if (sel_expert(lane, i) >= a.E) e[i] = -__builtin_inff();
+        }
+        float m = e[0], s = 0.f;
+#pragma unroll
+        for (int i = 1; i < NV; ++i) m = fmaxf(m, e[i]);
+        m = sel_wave_max(m);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) s += e[i] = m == -__builtin_inff() ? 0.f : sel_exp(e[i] - m);
+        s = wave_sum(s);
+        if (lane >> 4 == r) { mx = m; sum = s; }
       }
-      sum = sel_sum(sum);
     }
-    int id;
     double g, inner;
-    sel_grad16(a, t, row, mx, sum, &id, &g, &inner);
-    const float scale = dense && sum != 0.0 ? (float)(-inner / sum) : 0.f;
+    sel_grad16(a, live, d, lj, mx, sum, &id, &g, &inner);
+    const double s = DENSE && sum != 0.f ? exp((double)lj - (double)mx) / sum : 0.0;
+    const float at_id = (float)(g - s * inner), scale = sum == 0.f ? 0.f : (float)(-inner / sum);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) buf[w][lane + 64 * i] = dense ? scale * l[i] : 0.f;
-    __builtin_amdgcn_wave_barrier();
-    if (id >= 0) {
-      const double s = dense ? (sum == 0.0 ? 0.0 : exp((double)row[id] - (double)mx) / sum) : 0.0;
-      buf[w][id] = (float)(g - s * inner);
-    }
-    __builtin_amdgcn_wave_barrier();
+    for (int r = 0; r < 4; ++r) {
+      if (t0 + r >= a.T) break;
+      float v[NV];
+      const float c = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(scale), 16 * r));
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = lane + 64 * i;
-      if (e >= a.E) continue;
-      const size_t o = (size_t)t * a.E + e;
-      float v = buf[w][e];
-      if (!SPLIT) {
-        a.dl[o] = v;
-        continue;
+      for (int i = 0; i < NV; ++i) v[i] = DENSE ? c * l[DENSE * r][i] : 0.f;
+#pragma unroll
+      for (int q = 0; q < NV / 4; ++q)
+        *reinterpret_cast<v4f*>(buf[w] + sel_expert(lane, 4 * q)) = v4f{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      __builtin_amdgcn_wave_barrier();
+      if (lane >> 4 == r && id >= 0) buf[w][id] = at_id;
+      __builtin_amdgcn_wave_barrier();
+      const size_t o0 = (size_t)(t0 + r) * a.E;
+      if (SPLIT) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int e = lane + 64 * i;
+          if (e >= a.E) continue;
+          float x = buf[w][e];
+          if (a.aux) x += a.aux[o0 + e];
+          const uint32_t h = f32_to_bf16_rne(x);
+          a.hi[o0 + e] = (uint16_t)h;
+          a.lo[o0 + e] = (uint16_t)f32_to_bf16_rne(x - bf16_to_f32(h));
+        }
+      } else if (a.E % 4 == 0) {
+#pragma unroll
+        for (int q = 0; q < NV / 4; ++q)
+          if (sel_expert(lane, 4 * q) < a.E)
+            *reinterpret_cast<v4f*>(a.dl + o0 + sel_expert(lane, 4 * q)) = *reinterpret_cast<const v4f*>(buf[w] + sel_expert(lane, 4 * q));
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (lane + 64 * i < a.E) a.dl[o0 + lane + 64 * i] = buf[w][lane + 64 * i];
       }
-      if (a.aux) v += a.aux[o];
-      const uint32_t h = f32_to_bf16_rne(v);
-      a.hi[o] = (uint16_t)h;
-      a.lo[o] = (uint16_t)f32_to_bf16_rne(v - bf16_to_f32(h));
+      __builtin_amdgcn_wave_barrier();
     }
-    __builtin_amdgcn_wave_barrier();
   }
 }
 

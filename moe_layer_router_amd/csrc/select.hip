@@ -69,14 +69,12 @@ moe_status launch_select(const SelArgs& a, int cus, hipStream_t st) {
   return MOE_OK;
 }
 
-template <int SPLIT>
+template <int SPLIT, int DENSE>
 moe_status launch_bwd(const SelArgs& a, int cus, hipStream_t st) {
-  const dim3 grid(sel_grid(a.T, cus)), wg(64 * kSelWaves);
-  if (a.E <= 64) hipLaunchKernelGGL((k_select_bwd<1, SPLIT>), grid, wg, 0, st, a);
-  else if (a.E <= 128) hipLaunchKernelGGL((k_select_bwd<2, SPLIT>), grid, wg, 0, st, a);
-  else if (a.E <= 256) hipLaunchKernelGGL((k_select_bwd<4, SPLIT>), grid, wg, 0, st, a);
-  else if (a.E <= 512) hipLaunchKernelGGL((k_select_bwd<8, SPLIT>), grid, wg, 0, st, a);
-  else hipLaunchKernelGGL((k_select_bwd<16, SPLIT>), grid, wg, 0, st, a);
+  const dim3 grid(sel_grid((a.T + 3) / 4, cus)), wg(64 * kSelWaves);
+  if (a.E <= 256) hipLaunchKernelGGL((k_select_bwd<4, SPLIT, DENSE>), grid, wg, 0, st, a);
+  else if (a.E <= 512) hipLaunchKernelGGL((k_select_bwd<8, SPLIT, DENSE>), grid, wg, 0, st, a);
+  else hipLaunchKernelGGL((k_select_bwd<16, SPLIT, DENSE>), grid, wg, 0, st, a);
   HIP_TRY(hipGetLastError());
   return MOE_OK;
 }
@@ -86,7 +84,8 @@ moe_status launch_bwd(const SelArgs& a, int cus, hipStream_t st) {
 namespace moe {
 
 moe_status launch_select_bwd(const SelArgs& a, int cus, hipStream_t st) {
-  return a.hi ? launch_bwd<1>(a, cus, st) : launch_bwd<0>(a, cus, st);
+  if (!a.sigmoid && !a.renorm) return a.hi ? launch_bwd<1, 1>(a, cus, st) : launch_bwd<0, 1>(a, cus, st);
+  return a.hi ? launch_bwd<1, 0>(a, cus, st) : launch_bwd<0, 0>(a, cus, st);
 }
 
 moe_status select_bwd_args(const moe_selection* s, const float* logits, const int32_t* topk_ids, SelArgs* out) {
