@@ -629,7 +629,8 @@ moe_status moe_linear(int32_t T, int32_t K, int32_t N, int32_t act, const void* 
  * dz enters the matrix cores as three BF16 parts (the fp32 value; for a BF16 dx two,
  * within 2^-17 of it), or as it is where it is a BF16 dy; sums are fp32 in a fixed order.  Limits as moe_linear; no
  * overlap of outputs, workspace and inputs.  workspace:
- * moe_linear_backward_workspace_size bytes (0 for sizes that are refused): 6 T R,
+ * moe_linear_backward_workspace_size bytes (0 for sizes that are refused): 6 T R
+ * (R rounded up to 64),
  * up to 256 rows of R sums and up to 128 MiB.  Enqueued on `stream`. */
 size_t moe_linear_backward_workspace_size(int32_t T, int32_t K, int32_t N, int32_t act);
 moe_status moe_linear_backward(int32_t T, int32_t K, int32_t N, int32_t act, const void* x, const void* w,

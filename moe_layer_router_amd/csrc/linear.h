@@ -49,7 +49,7 @@ struct LinGemm {
   const uint16_t* p;                       // along k: [rows][ldp], across: [K][ldp]
   const uint16_t* q;
   long ldp, ldq;                           // elements
-  int pch;                                 // parts of P in memory: 8 elements of each in turn
+  int pch;                                 // parts of P in memory: 64 elements of each in turn
   long rows;
   int cols;                                // of the output
   long K;
@@ -60,7 +60,9 @@ struct LinGemm {
   LinEpi e;
 };
 
-DEV float lin_sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+// exp(v) by the instruction for 2^v: within 2 units, and the argument's rounding; what is below 2^-126 is zero.
+DEV float lin_exp(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504f); }
+DEV float lin_sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + lin_exp(-z)); }
 
 // act(z), elementwise.
 DEV void lin_act(int act, float (&v)[8]) {
@@ -95,7 +97,7 @@ DEV void lin_act_grad(int act, const float (&z)[8], float (&d)[8]) {
     case LIN_GELU:
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        d[e] *= 0.5f * (1.0f + erff(z[e] * 0.70710678f)) + z[e] * 0.39894228f * __expf(-0.5f * z[e] * z[e]);
+        d[e] *= 0.5f * (1.0f + erff(z[e] * 0.70710678f)) + z[e] * 0.39894228f * lin_exp(-0.5f * z[e] * z[e]);
       break;
     case LIN_GELU_TANH:
 #pragma unroll
@@ -197,7 +199,7 @@ DEV v8bf lin_frag(const char* op, int r0, int i, int kh, int lane) {
 DEV uint32_t lin_bytes(long n) { return (uint32_t)(n < 0x7FFFFF00l ? n : 0x7FFFFF00l); }
 constexpr uint32_t kLinNowhere = 0x7FFFFFF0u;                  // past every buffer's end
 
-// PT, QT: the operand lies across k.  PARTS: P's, in memory 8 elements of each in turn; in LDS a wave's rows are its
+// PT, QT: the operand lies across k.  PARTS: P's, in memory 64 elements of each in turn; in LDS a wave's rows are its
 // two subtiles of the first part, then of the next.
 // GATED: the tile's columns are kCols / 2 of the gate and the same of up, q [2 cols][ldq].
 template <class TL, int PT, int QT, int PARTS, int GATED>
@@ -241,14 +243,14 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_linear(LinGemm g) {
       const int r = o / 128, c = (lane & 7) ^ lin_swz(r), sub = r % (16 * IP) / 16;
       const int row = PARTS == 1 ? r : r / (16 * IP) * 32 + 16 * (sub & 1) + (r & 15);
       pk[n] = 8 * c;
-      poff[n] = (uint32_t)row * (uint32_t)g.ldp * 2 + 16 * (c * g.pch + (PARTS == 1 ? 0 : sub >> 1));
+      poff[n] = (uint32_t)row * (uint32_t)g.ldp * 2 + 16 * c + (PARTS == 1 ? 0 : 128 * (sub >> 1));
     } else {
       // (columns past the end are never stored: the last ones again)
       const int k = o / (2 * SP), cc = (o % (2 * SP) / 16) ^ (lin_swz_t<SP>(k) << 1), sub = cc % (2 * IP) / 2;
       const int col = PARTS == 1 ? 8 * cc : cc / (2 * IP) * 32 + 16 * (sub & 1) + 8 * (cc & 1);
-      const uint32_t at = (uint32_t)(min(i0 + col, g.rows - 8) / 8);
+      const uint32_t at = (uint32_t)min(i0 + col, g.rows - 8);
       pk[n] = 0;
-      poff[n] = (uint32_t)k * (uint32_t)g.ldp * 2 + 16 * (at * g.pch + (PARTS == 1 ? 0 : sub >> 1));
+      poff[n] = (uint32_t)k * (uint32_t)g.ldp * 2 + (PARTS == 1 ? 2 * at : 128 * ((at >> 6) * g.pch + (sub >> 1)) + 2 * (at & 63));
     }
   }
 #pragma unroll
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(256) k_linear_join(LinGemm g) {
 struct LinDz {
   const void* dy;                          // [T][n]
   const void* pre;                         // [T][R]
-  uint16_t* dz;                            // [T][R / 8][parts][8], or NULL
+  uint16_t* dz;                            // [T][ceil(R / 64)][parts][64], or NULL
   float* part;                             // [slabs][R] sums of dz over a slab's rows, or NULL
   long T;
   int n, act, dy_f32, pre_f32;
@@ -428,16 +430,16 @@ struct LinDz {
   int parts;                               // of dz: 2 or 3
 };
 
-DEV void lin_split_store(uint16_t* dz, size_t chunk, int parts, float (&v)[8]) {
-  uint16_t* at = dz + chunk * 8 * parts;
-  for (int p = 0; p < parts; ++p) {
+DEV void lin_split_store(const LinDz& a, long t, int R, int col, float (&v)[8]) {
+  uint16_t* at = a.dz + ((size_t)t * ((R + 63) / 64) + col / 64) * 64 * a.parts + (col & 63);
+  for (int p = 0; p < a.parts; ++p) {
     uint32_t h[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       h[e] = f32_to_bf16_rne(v[e]);
       v[e] -= bf16_to_f32(h[e]);
     }
-    st16(at + 8 * p, v4i{(int)(h[0] | h[1] << 16), (int)(h[2] | h[3] << 16), (int)(h[4] | h[5] << 16), (int)(h[6] | h[7] << 16)});
+    st16(at + 64 * p, v4i{(int)(h[0] | h[1] << 16), (int)(h[2] | h[3] << 16), (int)(h[4] | h[5] << 16), (int)(h[6] | h[7] << 16)});
   }
 }
 
@@ -464,13 +466,13 @@ __global__ void __launch_bounds__(256) k_linear_dz(LinDz a) {
           u[e] = dy * z[e] * s;
           su[e] += u[e];
         }
-        if (a.dz) lin_split_store(a.dz, ((size_t)t * R + a.n + col) / 8, a.parts, u);
+        if (a.dz) lin_split_store(a, t, R, a.n + col, u);
       } else if (a.pre) {
         lin_act_grad(a.act, z, d);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) sg[e] += d[e];
-      if (a.dz) lin_split_store(a.dz, ((size_t)t * R + col) / 8, a.parts, d);
+      if (a.dz) lin_split_store(a, t, R, col, d);
     }
   }
   if (!a.part) return;

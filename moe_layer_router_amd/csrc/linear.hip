@@ -107,7 +107,7 @@ LinBwdLayout lin_bwd_layout(long T, int K, int N, int act) {
   const int R = lin_rows(N, act);
   LinBwdLayout L{};
   size_t o = 0;
-  L.dz = o; o = align256(o + (size_t)T * R * 6);
+  L.dz = o; o = align256(o + (size_t)T * ((R + 63) / 64 * 64) * 6);
   L.part = o; o = align256(o + (size_t)((T + lin_slab(T) - 1) / lin_slab(T)) * R * 4);
   L.sums = o;
   size_t sums = 0;
@@ -237,7 +237,7 @@ moe_status moe_linear_backward(int32_t T, int32_t K, int32_t N, int32_t act, con
   }
   LinGemm g{};
   g.p = whole ? static_cast<const uint16_t*>(dy) : dz;
-  g.ldp = (long)parts * R;
+  g.ldp = whole ? R : (long)parts * ((R + 63) / 64 * 64);
   g.pch = parts;
   g.part = reinterpret_cast<float*>(ws + L.sums);
   if (dx) {
