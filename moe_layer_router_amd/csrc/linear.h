@@ -418,6 +418,92 @@ __global__ void __launch_bounds__(256) k_linear_join(LinGemm g) {
   lin_finish<GATED>(g.e, row, c, v, u);
 }
 
+// ------------------------------------------------------------------ few rows
+// z for up to 16 TT rows of x (a decoded token, a small batch): bound by reading W once.  A workgroup does 16 rows of W (SwiGLU: 8
+// of the gate and the same 8 of up), its eight waves every eighth 64 k each; W and x go from memory to
+// the matrix cores' operands, eight steps of a wave in flight.  Lane l holds row l % 16 and k 16 (l / 16) .. + 15 of a step, in both operands, so
+// that a row's 128 bytes are read together; the waves' sums meet in LDS.
+template <int TT, int GATED>
+__global__ void __launch_bounds__(512, 2) k_linear_rows(LinGemm g) {
+  constexpr int NT = GATED ? 8 : 16, U = TT == 1 ? 8 : 4, kPitch = 20;
+  __shared__ __attribute__((aligned(16))) float sums[8][16 * TT][kPitch];
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c16 = lane & 15, gq = lane >> 4, j0 = blockIdx.x * NT;
+  const int wr = GATED ? (c16 < 8 ? j0 + c16 : g.cols + j0 + c16 - 8) : min(j0 + c16, g.cols - 1);
+  const uint16_t* wp = g.q + (long)wr * g.ldq + 16 * gq;
+  const uint16_t* xp[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) xp[t] = g.p + min((long)(16 * t + c16), g.rows - 1) * g.ldp + 16 * gq;   // (rows past the end: the last, never stored)
+  v4f acc[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
+  const int steps = (int)(g.K / 64), mine = (steps - w + 7) / 8;      // whole steps w, w + 8, ...
+  v4i wf[U][2], xf[U][TT][2];
+  auto load = [&](int i, int n) {
+    const long k = 64l * (w + 8 * min(n, mine - 1));                  // (past the end: the last step again, never used)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      wf[i][h] = ld16(wp + k + 8 * h);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) xf[i][t][h] = ld16(xp[t] + k + 8 * h);
+    }
+  };
+  auto mul = [&](const v4i (&a)[2], const v4i (&b)[TT][2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) acc[t] = mfma_bf16(as_v8bf(a[h]), as_v8bf(b[t][h]), acc[t]);
+  };
+  if (mine > 0) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) load(i, i);
+    for (int n = 0; n < mine; n += U) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (n + i < mine) mul(wf[i], xf[i]);
+        if (n + U < mine) load(i, n + U + i);
+      }
+    }
+  }
+  if (g.K % 64 && w == steps % 8) {                // what is left of k: zeros past the end
+    const long k = 64l * steps;
+    const v4i zero = v4i{0, 0, 0, 0};
+    v4i a[2], b[TT][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool in = k + 16 * gq + 8 * h < g.K;
+      const long at = in ? k + 8 * h : -16 * gq;   // (else the row's first elements)
+      a[h] = ld16(wp + at);
+      if (!in) a[h] = zero;
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        b[t][h] = ld16(xp[t] + at);
+        if (!in) b[t][h] = zero;
+      }
+    }
+    mul(a, b);
+  }
+#pragma unroll
+  for (int t = 0; t < TT; ++t) *reinterpret_cast<v4f*>(&sums[w][16 * t + c16][4 * gq]) = acc[t];
+  __syncthreads();
+  // 8 columns of a row per thread
+  const int row = GATED ? tid : tid >> 1, c = GATED ? 0 : 8 * (tid & 1);
+  if (row >= 16 * TT || row >= g.rows || j0 + c >= g.cols) return;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, u[8] = {0, 0, 0, 0, 0, 0, 0, 0}, x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    ln_load_f32(&sums[i][row][c], 0, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += x[e];
+    if (GATED) {
+      ln_load_f32(&sums[i][row][8], 0, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] += x[e];
+    }
+  }
+  lin_finish<GATED>(g.e, row, j0 + c, v, u);
+}
+
 // ---------------------------------------------------------------- dz and db
 struct LinDz {
   const void* dy;                          // [T][n]

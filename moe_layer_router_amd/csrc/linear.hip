@@ -96,6 +96,17 @@ moe_status launch_product(const LinGemm& g, int cus, hipStream_t st) {
   return launch_tiles<std::conditional_t<PARTS == 1, LinSmall, LinSmallParts>, PT, QT, PARTS, GATED>(g, cus, st);
 }
 
+// Few rows of x: W is read once by kernels that need no tile of rows.
+constexpr int kLinFewRows = 32;
+template <int GATED>
+moe_status launch_rows(const LinGemm& g, hipStream_t st) {
+  const dim3 grid((g.cols + (GATED ? 7 : 15)) / (GATED ? 8 : 16));
+  if (g.rows <= 16) hipLaunchKernelGGL((k_linear_rows<1, GATED>), grid, dim3(512), 0, st, g);
+  else hipLaunchKernelGGL((k_linear_rows<2, GATED>), grid, dim3(512), 0, st, g);
+  HIP_TRY(hipGetLastError());
+  return MOE_OK;
+}
+
 // Slabs of rows for the sums over the tokens.
 constexpr int kLinSlabs = 256;
 int lin_slab(long T) { return (int)std::max(16l, ((T + kLinSlabs - 1) / kLinSlabs + 3) / 4 * 4); }
@@ -170,6 +181,7 @@ moe_status moe_linear(int32_t T, int32_t K, int32_t N, int32_t act, const void* 
   g.e.act = act; g.e.n = N;
   g.e.y_f32 = y_dtype == MOE_DTYPE_F32; g.e.res_f32 = residual_dtype == MOE_DTYPE_F32; g.e.pre_f32 = pre_dtype == MOE_DTYPE_F32;
   hipStream_t st = static_cast<hipStream_t>(stream);
+  if (T <= kLinFewRows) return act == MOE_ACT_SWIGLU ? launch_rows<1>(g, st) : launch_rows<0>(g, st);
   return act == MOE_ACT_SWIGLU ? launch_product<0, 0, 1, 1>(g, di.cus, st) : launch_product<0, 0, 1, 0>(g, di.cus, st);
 }
 
