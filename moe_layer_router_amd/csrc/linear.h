@@ -203,12 +203,11 @@ constexpr uint32_t kLinNowhere = 0x7FFFFFF0u;                  // past every buf
 // two subtiles of the first part, then of the next.
 // GATED: the tile's columns are kCols / 2 of the gate and the same of up, q [2 cols][ldq].
 template <class TL, int PT, int QT, int PARTS, int GATED>
-__global__ void __launch_bounds__(TL::kThreads, 2) k_linear(LinGemm g) {
+DEV void lin_tile(const LinGemm& g, long block, char* lds) {
   constexpr int NJ = TL::NJ, NW = TL::NW, S = TL::kCols, SP = TL::prows(PARTS), IP = TL::subs(PARTS);
   constexpr int NI = PARTS == 1 ? 4 : 2, PP = SP / 8 / NW, QP = S / 8 / NW, kStage = TL::stage(PARTS);
   constexpr int MT = TL::rows(PARTS), NT = GATED ? S / 2 : S;  // rows and columns of the output's tile
   static_assert(SP % (8 * NW) == 0 && S % (8 * NW) == 0, "whole 1 KB pieces per wave");
-  extern __shared__ __attribute__((aligned(16))) char lds[];
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c16 = lane & 15, gq = lane >> 4, wm = w / TL::WN, wn = w % TL::WN;
 
@@ -216,11 +215,11 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_linear(LinGemm g) {
   const long per = (g.full + 7) / 8;
   long t;
   int part = -1;
-  if ((long)blockIdx.x < 8 * per) {
-    t = (long)(blockIdx.x % 8) * per + (long)(blockIdx.x / 8);
+  if (block < 8 * per) {
+    t = block % 8 * per + block / 8;
     if (t >= g.full) return;
   } else {
-    part = (int)((long)blockIdx.x - 8 * per);
+    part = (int)(block - 8 * per);
     t = g.full + part / g.split;
   }
   const long i0 = t / g.tj * MT;
@@ -393,6 +392,12 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_linear(LinGemm g) {
   }
 }
 
+template <class TL, int PT, int QT, int PARTS, int GATED>
+__global__ void __launch_bounds__(TL::kThreads, 2) k_linear(LinGemm g) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  lin_tile<TL, PT, QT, PARTS, GATED>(g, blockIdx.x, lds);
+}
+
 // The tiles worked on in parts: 8 columns of a row per thread, the parts added in order.
 template <class TL, int PARTS, int GATED>
 __global__ void __launch_bounds__(256) k_linear_join(LinGemm g) {
@@ -539,6 +544,7 @@ __global__ void __launch_bounds__(256) k_linear_dz(LinDz a) {
   float sg[8] = {0, 0, 0, 0, 0, 0, 0, 0}, su[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   const long t1 = min((long)(blockIdx.y + 1) * a.slab, a.T);
   if (live) {
+#pragma unroll 2
     for (long t = (long)blockIdx.y * a.slab + w; t < t1; t += 4) {
       float d[8], z[8], u[8];
       lin_load8(a.dy, a.dy_f32, (size_t)t * a.n + col, d);
@@ -575,16 +581,40 @@ __global__ void __launch_bounds__(256) k_linear_dz(LinDz a) {
   ln_store_f32(a.part, (size_t)blockIdx.y * R + (w ? a.n : 0) + col, v);
 }
 
-// db: the slabs' sums, 64 columns per workgroup, each of its waves every fourth slab.
-__global__ void __launch_bounds__(256) k_linear_dbias(const float* part, int slabs, int R, float* db) {
-  __shared__ float red[4][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
+// db: the slabs' sums, 64 columns per workgroup of NW waves, each of them every NW-th slab.
+struct LinDbias {
+  const float* part;
+  float* db;
+  int slabs, R;
+};
+template <int NW>
+DEV void lin_dbias(const LinDbias& a, int block, float* red) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = block * 64 + lane;
   float s = 0.f;
-  if (c < R)
-    for (int i = w; i < slabs; i += 4) s += part[(size_t)i * R + c];
-  red[w][lane] = s;
+  if (c < a.R) {
+#pragma unroll 8
+    for (int i = w; i < a.slabs; i += NW) s += a.part[(size_t)i * a.R + c];
+  }
+  red[threadIdx.x] = s;
   __syncthreads();
-  if (w == 0 && c < R) db[c] = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+  if (w || c >= a.R) return;
+#pragma unroll
+  for (int i = 1; i < NW; ++i) s += red[64 * i + lane];
+  a.db[c] = s;
+}
+__global__ void __launch_bounds__(256) k_linear_dbias(LinDbias a) {
+  __shared__ float red[256];
+  lin_dbias<4>(a, blockIdx.x, red);
+}
+
+// dx, dW and db together, where one of them does not fill the GPU: nx workgroups for dx, nw for dW, the others for db.
+template <class TL, int PX, int PW>
+__global__ void __launch_bounds__(TL::kThreads, 2) k_linear_grads(LinGemm x, LinGemm w, LinDbias b, int nx, int nw) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int block = blockIdx.x;
+  if (block < nx) lin_tile<TL, 0, 1, PX, 0>(x, block, lds);
+  else if (block < nx + nw) lin_tile<TL, 1, 1, PW, 0>(w, block - nx, lds);
+  else lin_dbias<TL::NW>(b, block - nx - nw, reinterpret_cast<float*>(lds));
 }
 
 }  // namespace moe

@@ -12,8 +12,9 @@ namespace {
 
 using LinBig = LinTile<4, 2, 8, 2>;        // 256 columns, eight waves, one workgroup per CU
 using LinMid = LinTile<2, 2, 4, 2>;        // 128 columns, two workgroups per CU
-using LinSmall = LinTile<1, 2, 2, 3>;      // 64 columns
-using LinSmallParts = LinTile<2, 1, 4, 2>; // the same, and as many rows of P in parts
+using LinMidDeep = LinTile<2, 2, 4, 4>;    // the same with four steps in LDS, one workgroup per CU
+using LinSmall = LinTile<1, 2, 2, 4>;      // 64 columns
+using LinSmallParts = LinTile<2, 2, 2, 4>; // the same, and as many rows of P in parts
 constexpr int kLinMaxDim = 1 << 17;        // (offsets in a tile's 256 rows of two parts fit 32 bits)
 
 template <auto K>
@@ -55,11 +56,12 @@ size_t lin_parts(long rows, int cols, long K, int parts, bool gated) {
                               : lin_part_bytes<LinSmallParts>(rows, cols, K, parts, gated)});
 }
 
-template <class TL, int PT, int QT, int PARTS, int GATED>
-moe_status launch_tiles(LinGemm g, int cus, hipStream_t st) {
-  constexpr int MT = TL::rows(PARTS), NT = GATED ? TL::kCols / 2 : TL::kCols, kLds = TL::lds(PARTS);
+// How a product's tiles are worked on; the workgroups.
+template <class TL, int PARTS, int GATED>
+moe_status plan_tiles(LinGemm& g, int cus, unsigned* grid) {
+  constexpr int MT = TL::rows(PARTS), NT = GATED ? TL::kCols / 2 : TL::kCols;
   g.tj = (g.cols + NT - 1) / NT;
-  const long total = (g.rows + MT - 1) / MT * g.tj, slots = (long)cus * (160 * 1024 / kLds);
+  const long total = (g.rows + MT - 1) / MT * g.tj, slots = (long)cus * (160 * 1024 / TL::lds(PARTS));
   if (total > 0x7FFFFFFFl - 16) return fail(MOE_ERR_UNSUPPORTED, "the output has too many tiles");
   g.full = total;
   g.split = 1;
@@ -72,28 +74,76 @@ moe_status launch_tiles(LinGemm g, int cus, hipStream_t st) {
     g.split = (int)split;
     g.rest = (int)rest;
   }
-  constexpr auto kernel = k_linear<TL, PT, QT, PARTS, GATED>;
-  TRY(set_lds_limit_once<kernel>(kLds));
-  const unsigned grid = (unsigned)((g.full + 7) / 8 * 8 + (long)g.rest * g.split);
-  hipLaunchKernelGGL(kernel, dim3(grid), dim3(TL::kThreads), kLds, st, g);
-  HIP_TRY(hipGetLastError());
-  if (g.rest) {
-    hipLaunchKernelGGL((k_linear_join<TL, PARTS, GATED>), dim3((unsigned)((long)g.rest * MT * NT / 8 / 256)), dim3(256), 0, st, g);
-    HIP_TRY(hipGetLastError());
-  }
+  *grid = (unsigned)((g.full + 7) / 8 * 8 + (long)g.rest * g.split);
   return MOE_OK;
 }
+template <class TL, int PARTS, int GATED>
+moe_status launch_join(const LinGemm& g, hipStream_t st) {
+  constexpr int MT = TL::rows(PARTS), NT = GATED ? TL::kCols / 2 : TL::kCols;
+  if (!g.rest) return MOE_OK;
+  hipLaunchKernelGGL((k_linear_join<TL, PARTS, GATED>), dim3((unsigned)((long)g.rest * MT * NT / 8 / 256)), dim3(256), 0, st, g);
+  HIP_TRY(hipGetLastError());
+  return MOE_OK;
+}
+template <class TL, int PT, int QT, int PARTS, int GATED>
+moe_status launch_tiles(LinGemm g, int cus, hipStream_t st) {
+  constexpr auto kernel = k_linear<TL, PT, QT, PARTS, GATED>;
+  unsigned grid;
+  TRY((plan_tiles<TL, PARTS, GATED>(g, cus, &grid)));
+  TRY(set_lds_limit_once<kernel>(TL::lds(PARTS)));
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(TL::kThreads), TL::lds(PARTS), st, g);
+  HIP_TRY(hipGetLastError());
+  return launch_join<TL, PARTS, GATED>(g, st);
+}
 
-template <int PT, int QT, int PARTS, int GATED>
-moe_status launch_product(const LinGemm& g, int cus, hipStream_t st) {
+enum { LIN_BIG, LIN_MID, LIN_DEEP, LIN_SMALL };
+template <int PARTS>
+using LinLeast = std::conditional_t<PARTS == 1, LinSmall, LinSmallParts>;
+template <int PARTS, int GATED>
+int lin_kind(const LinGemm& g, int cus) {
   const auto tiles = [&](long mt, long nt) {
     if (GATED) nt /= 2;
     return ((g.rows + mt - 1) / mt) * ((g.cols + nt - 1) / nt);
   };
   const long big = tiles(LinBig::rows(PARTS), LinBig::kCols), mid = tiles(LinMid::rows(PARTS), LinMid::kCols);
-  if (big >= cus && 16 * big <= 5 * mid) return launch_tiles<LinBig, PT, QT, PARTS, GATED>(g, cus, st);
-  if (mid >= cus) return launch_tiles<LinMid, PT, QT, PARTS, GATED>(g, cus, st);
-  return launch_tiles<std::conditional_t<PARTS == 1, LinSmall, LinSmallParts>, PT, QT, PARTS, GATED>(g, cus, st);
+  if (big >= cus && 16 * big <= 5 * mid) return LIN_BIG;
+  return mid > cus ? LIN_MID : 2 * mid > cus ? LIN_DEEP : LIN_SMALL;
+}
+template <int PT, int QT, int PARTS, int GATED>
+moe_status launch_product(const LinGemm& g, int cus, hipStream_t st) {
+  switch (lin_kind<PARTS, GATED>(g, cus)) {
+    case LIN_BIG: return launch_tiles<LinBig, PT, QT, PARTS, GATED>(g, cus, st);
+    case LIN_MID: return launch_tiles<LinMid, PT, QT, PARTS, GATED>(g, cus, st);
+    case LIN_DEEP: return launch_tiles<LinMidDeep, PT, QT, PARTS, GATED>(g, cus, st);
+    default: return launch_tiles<LinLeast<PARTS>, PT, QT, PARTS, GATED>(g, cus, st);
+  }
+}
+
+// dx, dw and (b.db) dbias: together where both products have small tiles, else one after another.
+template <int PX, int PW>
+moe_status launch_grads(LinGemm x, LinGemm w, const LinDbias& b, int cus, hipStream_t st) {
+  using TL = LinLeast<PW>;
+  const unsigned nb = b.db ? (unsigned)(b.R + 63) / 64 : 0;
+  if (lin_kind<PX, 0>(x, cus) == LIN_SMALL && lin_kind<PW, 0>(w, cus) == LIN_SMALL) {
+    constexpr auto kernel = k_linear_grads<TL, PX, PW>;
+    constexpr int kLds = TL::lds(PX) > TL::lds(PW) ? TL::lds(PX) : TL::lds(PW);
+    unsigned nx, nw;
+    TRY((plan_tiles<TL, PX, 0>(x, cus, &nx)));
+    TRY((plan_tiles<TL, PW, 0>(w, cus, &nw)));
+    // (each has sums of its own)
+    w.part = x.part + (size_t)x.rest * x.split * TL::sums(PX);
+    TRY(set_lds_limit_once<kernel>(kLds));
+    hipLaunchKernelGGL(kernel, dim3(nx + nw + nb), dim3(TL::kThreads), kLds, st, x, w, b, (int)nx, (int)nw);
+    HIP_TRY(hipGetLastError());
+    TRY((launch_join<TL, PX, 0>(x, st)));
+    return launch_join<TL, PW, 0>(w, st);
+  }
+  if (nb) {
+    hipLaunchKernelGGL(k_linear_dbias, dim3(nb), dim3(256), 0, st, b);
+    HIP_TRY(hipGetLastError());
+  }
+  TRY((launch_product<0, 1, PX, 0>(x, cus, st)));
+  return launch_product<1, 1, PW, 0>(w, cus, st);
 }
 
 // Few rows of x: W is read once by kernels that need no tile of rows.
@@ -109,7 +159,7 @@ moe_status launch_rows(const LinGemm& g, hipStream_t st) {
 
 // Slabs of rows for the sums over the tokens.
 constexpr int kLinSlabs = 256;
-int lin_slab(long T) { return (int)std::max(16l, ((T + kLinSlabs - 1) / kLinSlabs + 3) / 4 * 4); }
+int lin_slab(long T) { return (int)std::max(4l, ((T + kLinSlabs - 1) / kLinSlabs + 3) / 4 * 4); }
 
 struct LinBwdLayout {
   size_t dz, part, sums, total;
@@ -124,7 +174,10 @@ LinBwdLayout lin_bwd_layout(long T, int K, int N, int act) {
   size_t sums = 0;
   for (int parts = 1; parts <= 3; ++parts)
     sums = std::max({sums, lin_parts(T, K, R, parts, false), lin_parts(R, K, T, parts, false)});
-  L.total = align256(o + sums);
+  // dx's and dw's side by side with small tiles
+  const size_t both = lin_part_bytes<LinSmallParts>(T, K, R, 3, false) + lin_part_bytes<LinSmallParts>(R, K, T, 3, false);
+  const size_t both1 = lin_part_bytes<LinSmall>(T, K, R, 1, false) + lin_part_bytes<LinSmall>(R, K, T, 1, false);
+  L.total = align256(o + std::max({sums, both, both1}));
   return L;
 }
 
@@ -230,6 +283,7 @@ moe_status moe_linear_backward(int32_t T, int32_t K, int32_t N, int32_t act, con
   const bool want_dz = !whole && (dx || dw);
   // parts of dz in memory: three for fp32 results, two for BF16 ones
   const int parts = whole ? 1 : dw || (dx && dx_dtype == MOE_DTYPE_F32) ? 3 : 2;
+  LinDbias b{};
   if (want_dz || dbias) {
     LinDz a{};
     a.dy = dy; a.pre = act == MOE_ACT_NONE ? nullptr : pre;
@@ -242,31 +296,37 @@ moe_status moe_linear_backward(int32_t T, int32_t K, int32_t N, int32_t act, con
     if (act == MOE_ACT_SWIGLU) hipLaunchKernelGGL(k_linear_dz<1>, grid, dim3(256), 0, st, a);
     else hipLaunchKernelGGL(k_linear_dz<0>, grid, dim3(256), 0, st, a);
     HIP_TRY(hipGetLastError());
-    if (dbias) {
-      hipLaunchKernelGGL(k_linear_dbias, dim3((R + 63) / 64), dim3(256), 0, st, sums, slabs, R, dbias);
-      HIP_TRY(hipGetLastError());
-    }
+    b = LinDbias{sums, dbias, slabs, R};
   }
   LinGemm g{};
   g.p = whole ? static_cast<const uint16_t*>(dy) : dz;
   g.ldp = whole ? R : (long)parts * ((R + 63) / 64 * 64);
   g.pch = parts;
+  g.ldq = K;
+  g.cols = K;
+  g.e.n = K;
   g.part = reinterpret_cast<float*>(ws + L.sums);
+  LinGemm gx = g, gw = g;
+  gx.q = static_cast<const uint16_t*>(w);
+  gx.rows = T; gx.K = R;
+  gx.e.y = dx; gx.e.y_f32 = dx_dtype == MOE_DTYPE_F32;
+  gw.q = static_cast<const uint16_t*>(x);
+  gw.rows = R; gw.K = T;
+  gw.e.y = dw; gw.e.y_f32 = 1;
+  const bool two = !whole && dx_dtype == MOE_DTYPE_BF16;       // parts of dz in dx's product
+  if (dx && dw) {
+    if (whole) return launch_grads<1, 1>(gx, gw, b, di.cus, st);
+    return two ? launch_grads<2, 3>(gx, gw, b, di.cus, st) : launch_grads<3, 3>(gx, gw, b, di.cus, st);
+  }
+  if (dbias) {
+    hipLaunchKernelGGL(k_linear_dbias, dim3((R + 63) / 64), dim3(256), 0, st, b);
+    HIP_TRY(hipGetLastError());
+  }
   if (dx) {
-    g.q = static_cast<const uint16_t*>(w);
-    g.ldq = K;
-    g.rows = T; g.cols = K; g.K = R;
-    g.e.y = dx; g.e.n = K; g.e.y_f32 = dx_dtype == MOE_DTYPE_F32;
-    TRY((whole ? launch_product<0, 1, 1, 0>(g, di.cus, st)
-               : dx_dtype == MOE_DTYPE_F32 ? launch_product<0, 1, 3, 0>(g, di.cus, st) : launch_product<0, 1, 2, 0>(g, di.cus, st)));
+    if (whole) return launch_product<0, 1, 1, 0>(gx, di.cus, st);
+    return two ? launch_product<0, 1, 2, 0>(gx, di.cus, st) : launch_product<0, 1, 3, 0>(gx, di.cus, st);
   }
-  if (dw) {
-    g.q = static_cast<const uint16_t*>(x);
-    g.ldq = K;
-    g.rows = R; g.cols = K; g.K = T;
-    g.e.y = dw; g.e.n = K; g.e.y_f32 = 1;
-    TRY((whole ? launch_product<1, 1, 1, 0>(g, di.cus, st) : launch_product<1, 1, 3, 0>(g, di.cus, st)));
-  }
+  if (dw) return whole ? launch_product<1, 1, 1, 0>(gw, di.cus, st) : launch_product<1, 1, 3, 0>(gw, di.cus, st);
   return MOE_OK;
 }
 
