@@ -228,7 +228,7 @@ def _on(device, stream):
             stream = torch.cuda.ExternalStream(stream, device)
         _need(stream.device == device, f"stream must be one of {device} (got one of {stream.device})")
         return torch.cuda.stream(stream)
-    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _HERE if device.index == lib._device() else torch.cuda.device(device)
 
 
 def _scratch(workspace, device, nbytes):
@@ -242,6 +242,8 @@ def _scratch(workspace, device, nbytes):
 
 def _dense(t):
     """t, or a copy of it that is contiguous and starts on a 16-byte boundary."""
+    if t.is_contiguous() and not t.data_ptr() & 15:
+        return t
     t = t.contiguous()
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
@@ -609,7 +611,7 @@ class AdamW:
     tensor on the GPU (int64 [1]), so that a captured step() counts and corrects its
     bias at every replay; lr may then be a float32 tensor [1] there too.
     The tensors are kept, not their addresses; `states`, `masters` and `count`
-    are what a checkpoint needs."""
+    are what a checkpoint needs.  betas, eps, weight_decay and seed stay as they are given here."""
 
     def __init__(self, params, masters=None, states=None, state: str = None, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay=0.0, seed: int = 0, count: int = 0, capturable: bool = False):
@@ -650,9 +652,14 @@ class AdamW:
         return [t for p, w, s in zip(self.params, self.masters, self.states) for t in (p, w, *[s[k] for k in names])]
 
     def _fill(self):
-        """The table of the call but for the gradients."""
+        """The arguments of the call but for the gradients and what step() takes."""
         self._table = (lib.MoeAdamwTensor * len(self.params))()
+        self._rows = list(self._table)             # (views of it)
         f8 = self.state == "fp8"
+        o = self._options = lib.MoeAdamwOptions()
+        o.beta1, o.beta2 = self.betas
+        o.eps, o.seed = self.eps, self.seed
+        o.state_dtype = lib.MOE_DTYPE_FP8_E4M3 if f8 else lib.MOE_DTYPE_F32
         for i, (p, w, s) in enumerate(zip(self.params, self.masters, self.states)):
             n = p.numel()
             _is(p, f"params[{i}]", p.shape, _FLOATS, self.device, True)
@@ -680,34 +687,32 @@ class AdamW:
         _need(len(grads) == len(self.params), "grads must have one entry per tensor")
         with _on(dev, stream):
             # (tensors whose memory was exchanged since the last step, as by .data or .to, are looked at again)
-            at = [None if t is None else t.data_ptr() for t in self._kept()]
+            at = [t if t is None else t.data_ptr() for t in self._kept()]
             if at != self._at:
                 self._fill()
                 self._at = at
-            table, dense = self._table, []
-            for i, (g, p) in enumerate(zip(grads, self.params)):
-                _is(g, f"grads[{i}]", p.shape, _FLOATS, dev)
+            dense = []                             # (copies live until the launch)
+            for row, g, p in zip(self._rows, grads, self.params):
+                if not (g.shape == p.shape and g.dtype in _FLOATS and g.device == dev):
+                    _is(g, "a gradient", p.shape, _FLOATS, dev)
                 g = _dense(g)
                 dense.append(g)
-                table[i].grad = g.data_ptr()
-                table[i].grad_dtype = lib.MOE_DTYPE_F32 if g.dtype == torch.float32 else lib.MOE_DTYPE_BF16
-            o = lib.MoeAdamwOptions()
-            o.beta1, o.beta2 = self.betas
-            o.eps, o.seed = self.eps, self.seed
-            o.state_dtype = lib.MOE_DTYPE_FP8_E4M3 if self.state == "fp8" else lib.MOE_DTYPE_F32
+                row.grad = g.data_ptr()
+                row.grad_dtype = lib.MOE_DTYPE_F32 if g.dtype is torch.float32 else lib.MOE_DTYPE_BF16
+            o = self._options
             if isinstance(lr, torch.Tensor):
                 _is(lr, "lr", (1,), _F32, dev)
                 o.lr_dev = lr.data_ptr()
             else:
-                o.lr = lr
+                o.lr, o.lr_dev = lr, None
             if grad_scale is not None:
                 _is(grad_scale, "grad_scale", (1,), _F32, dev)
-                o.grad_scale = grad_scale.data_ptr()
+            o.grad_scale = None if grad_scale is None else grad_scale.data_ptr()
             if self.capturable:
                 self.count.add_(1)
                 o.step_dev = self.count.data_ptr()
             else:
                 o.step = self.count + 1
-            lib.moe_adamw(table, o)
+            lib.moe_adamw(self._table, o)
             if not self.capturable:
                 self.count += 1

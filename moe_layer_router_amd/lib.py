@@ -212,9 +212,12 @@ def _nbytes(t):
     return t.numel() * t.element_size()
 
 
+_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _stream(stream):
     if stream is None:      # (the handle alone: a torch.cuda.Stream object per call would cost as much as a launch)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -393,16 +396,23 @@ def make_selection(T, E, top_k, scoring="sigmoid", n_group=1, topk_group=1, grou
                         1 if renormalize else 0, scale)
 
 
+# (A call of a small kernel waits for this code: addresses and the stream are taken without further functions.)
 def moe_select_experts(sel, logits, bias, topk_ids, topk_weights, stream=None):
     """logits [T, E] float32, bias [E] float32 or None; topk_ids [T, k] int32, topk_weights [T, k] float32."""
-    _check(_lib.moe_select_experts(ctypes.byref(sel), _ptr(logits), _ptr(bias), _ptr(topk_ids), _ptr(topk_weights),
-                                   _stream(stream)), "moe_select_experts")
+    st = _lib.moe_select_experts(ctypes.byref(sel), logits.data_ptr(), None if bias is None else bias.data_ptr(),
+                                 topk_ids.data_ptr(), topk_weights.data_ptr(),
+                                 _raw_stream(_device()) if stream is None else _stream(stream))
+    if st:
+        raise MoeError(st, "moe_select_experts")
 
 
 def moe_select_experts_backward(sel, logits, topk_ids, dweights, dlogits, stream=None):
     """logits, dlogits [T, E] float32; topk_ids [T, k] int32, dweights [T, k] float32."""
-    _check(_lib.moe_select_experts_backward(ctypes.byref(sel), _ptr(logits), _ptr(topk_ids), _ptr(dweights),
-                                            _ptr(dlogits), _stream(stream)), "moe_select_experts_backward")
+    st = _lib.moe_select_experts_backward(ctypes.byref(sel), logits.data_ptr(), topk_ids.data_ptr(),
+                                          dweights.data_ptr(), dlogits.data_ptr(),
+                                          _raw_stream(_device()) if stream is None else _stream(stream))
+    if st:
+        raise MoeError(st, "moe_select_experts_backward")
 
 
 def moe_backward_selected(desc, sel, x, router_w, w_gate_up, w_down, logits, topk_ids, topk_weights, dy, dlogits, dx,
@@ -418,14 +428,21 @@ def moe_linear_workspace_size(T: int, K: int, N: int, act) -> int:
     return _lib.moe_linear_workspace_size(T, K, N, ACTS.get(act, act))
 
 
+def _float_arg(t):
+    """Address and dtype of an optional bfloat16 or float32 tensor."""
+    return (None, MOE_DTYPE_BF16) if t is None else (t.data_ptr(), MOE_DTYPE_BF16 if t.dtype is torch.bfloat16 else MOE_DTYPE_F32)
+
+
 def moe_linear(x, w, bias, residual, y, pre, act, workspace, stream=None):
     """x [T, K], w [R, K] bfloat16; bias [R] float32 or None; residual (or None), y [T, N], pre (or None) [T, R]
     bfloat16 or float32."""
     T, K = x.shape
-    kind = lambda t: MOE_DTYPE_BF16 if t is None else _float_dtype(t)
-    _check(_lib.moe_linear(T, K, y.shape[1], ACTS.get(act, act), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual),
-                           kind(residual), _ptr(y), kind(y), _ptr(pre), kind(pre), _ptr(workspace),
-                           _nbytes(workspace), _stream(stream)), "moe_linear")
+    st = _lib.moe_linear(T, K, y.shape[1], ACTS.get(act, act), x.data_ptr(), w.data_ptr(),
+                         None if bias is None else bias.data_ptr(), *_float_arg(residual), *_float_arg(y),
+                         *_float_arg(pre), workspace.data_ptr(), _nbytes(workspace),
+                         _raw_stream(_device()) if stream is None else _stream(stream))
+    if st:
+        raise MoeError(st, "moe_linear")
 
 
 def moe_linear_backward_workspace_size(T: int, K: int, N: int, act) -> int:
@@ -436,15 +453,20 @@ def moe_linear_backward(x, w, pre, dy, dx, dw, dbias, act, workspace, stream=Non
     """x [T, K], w [R, K] bfloat16; pre (or None) [T, R], dy [T, N], dx (or None) [T, K] bfloat16 or float32; dw [R, K],
     dbias [R] (or None) float32."""
     T, K = x.shape
-    kind = lambda t: MOE_DTYPE_BF16 if t is None else _float_dtype(t)
-    _check(_lib.moe_linear_backward(T, K, dy.shape[1], ACTS.get(act, act), _ptr(x), _ptr(w), _ptr(pre), kind(pre),
-                                    _ptr(dy), kind(dy), _ptr(dx), kind(dx), _ptr(dw), _ptr(dbias), _ptr(workspace),
-                                    _nbytes(workspace), _stream(stream)), "moe_linear_backward")
+    st = _lib.moe_linear_backward(T, K, dy.shape[1], ACTS.get(act, act), x.data_ptr(), w.data_ptr(), *_float_arg(pre),
+                                  *_float_arg(dy), *_float_arg(dx), None if dw is None else dw.data_ptr(),
+                                  None if dbias is None else dbias.data_ptr(), workspace.data_ptr(),
+                                  _nbytes(workspace), _raw_stream(_device()) if stream is None else _stream(stream))
+    if st:
+        raise MoeError(st, "moe_linear_backward")
 
 
 def moe_adamw(tensors, options, stream=None):
     """tensors: a ctypes array of MoeAdamwTensor; options: a MoeAdamwOptions."""
-    _check(_lib.moe_adamw(len(tensors), tensors, ctypes.byref(options), _stream(stream)), "moe_adamw")
+    st = _lib.moe_adamw(len(tensors), tensors, ctypes.byref(options),
+                        _raw_stream(_device()) if stream is None else _stream(stream))
+    if st:
+        raise MoeError(st, "moe_adamw")
 
 
 def moe_route(desc, x, x_scales, router_w, router_bias, logits, topk_ids, topk_weights, workspace,
