@@ -63,19 +63,26 @@ DEV uint32_t adam_mix(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// E4M3 code of x, |x| <= 448, rounded up in magnitude with probability (dropped part) by the 16 bits r.
-DEV uint32_t adam_e4m3(float x, uint32_t r) {
-  const float a = fminf(fabsf(x), 448.0f);
+// E4M3 code of the magnitude a (at most 448 but for rounding), rounded up with probability (dropped part) by the 16 bits r.
+DEV uint32_t adam_e4m3(float a, uint32_t r) {
+  a = fminf(a, 448.0f);
   // from 2^-6 on 20 bits of the fraction are dropped; below, codes are multiples of 2^-9
   const uint32_t normal = ((__float_as_uint(a) + (r << 4)) >> 20) - (120u << 3);
-  const uint32_t small = (uint32_t)__builtin_fmaf(a, 512.0f, (float)r * 0x1p-16f);
-  return (a < 0x1p-6f ? small : normal) | ((__float_as_uint(x) >> 24) & 0x80u);
+  const uint32_t small = ((uint32_t)(a * 0x1p25f) + r) >> 16;
+  return a < 0x1p-6f ? small : normal;
 }
-// fp32 to BF16 in the same way; infinities and NaN as they are.
+// fp32 to BF16 in the same way; infinities and (quiet) NaN as they are.
 DEV uint32_t adam_bf16(float x, uint32_t r) {
   const uint32_t u = __float_as_uint(x);
-  if ((u & 0x7F800000u) == 0x7F800000u) return f32_to_bf16_rne(x);
-  return (u + r) >> 16;
+  return (u + (__builtin_isfpclass(x, 0x207) ? 0 : r)) >> 16;      // (NaN, infinities: their classes)
+}
+// The square root of x >= 2^-96 (or zero), correctly rounded: the instruction's result, or one of its
+// neighbours where the residue says so.
+DEV float adam_sqrt(float x) {
+  const float s = __builtin_amdgcn_sqrtf(x);
+  const float down = __uint_as_float(__float_as_uint(s) - 1), up = __uint_as_float(__float_as_uint(s) + 1);
+  float y = __builtin_fmaf(-down, s, x) <= 0.f ? down : s;
+  return __builtin_fmaf(-up, s, x) > 0.f ? up : y;
 }
 
 DEV uint32_t row_max16_u32(uint32_t v) {
@@ -146,8 +153,9 @@ DEV void adam_store_fp8(void* p, float* scales, int64_t i, int64_t n, const floa
   uint32_t w[2] = {0, 0};
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    uint32_t c = adam_e4m3(v[e] * inv, r[e]);
-    if (ROOT && v[e] > 0.f) c = max(c, 1u);
+    uint32_t c = adam_e4m3(ROOT ? v[e] * inv : fabsf(v[e] * inv), r[e]);
+    if (ROOT) c = max(c, min(__float_as_uint(v[e]), 1u));
+    else c |= __float_as_uint(v[e]) >> 24 & 0x80u;
     w[e >> 2] |= c << (8 * (e & 3));
   }
   uint8_t* q = static_cast<uint8_t*>(p) + i;
@@ -203,14 +211,24 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw(const AdamArgs a) {
       adam_load<0>(t.v, i, n, v);
     }
     float root[8];
-    uint32_t rm[8], rv[8], rw[8];
+    uint32_t rm[8], rv[8], rw[8], least = ~0u;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float x = g[e] * gs;
       if (S8) v[e] *= v[e];
       m[e] = adam_mean(a.b1, m[e], a.a1, x);
       v[e] = adam_mean(a.b2, v[e], a.a2, x * x);
-      root[e] = sqrtf(v[e]);
+      least = min(least, __float_as_uint(v[e]) - 1);     // (zero is not small)
+    }
+    if (__ballot(least < 0x0F800000u)) {             // 2^-96
+#pragma unroll
+      for (int e = 0; e < 8; ++e) root[e] = sqrtf(v[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) root[e] = adam_sqrt(v[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
       const float u = m[e] * __builtin_amdgcn_rcpf(__builtin_fmaf(root[e], rs, a.eps));
       w[e] = __builtin_fmaf(-step, u, __builtin_fmaf(shrink, w[e], w[e]));
       if (S8 || W == ADAM_BF16) {

@@ -340,6 +340,31 @@ def test_adamw_wrapper(gpu_lib):
     L.AdamW([torch.zeros(0, device="cuda"), w]).step([torch.zeros(0, device="cuda"), g], 0.0)
 
 
+def test_adamw_moments_and_roots_are_rounded_once_per_operation(gpu_lib):
+    """The states bit for bit as fp32 operations one at a time give them (the root correctly rounded), over all magnitudes down to
+    the smallest: a last bit may decide a stochastic rounding."""
+    from moe_layer_router_amd import layer as L
+    rng = np.random.default_rng(1)
+    n = 128 * 4000
+    f = np.float32
+    size = (10.0 ** rng.uniform(-22, 15, n // 128)).astype(f).repeat(128)
+    g = (size * rng.normal(size=n)).astype(f)
+    m0, r0 = (size * rng.normal(size=n)).astype(f), np.abs(size * rng.normal(size=n)).astype(f)
+    c = dict(dtype=torch.float32, device="cuda")
+    st = dict(m=torch.tensor(m0, **c), v=torch.tensor(r0 * r0, **c))
+    L.AdamW([torch.zeros(n, **c)], states=[st]).step([torch.tensor(g, **c)], 1e-3)
+    m = f(0.9) * m0 + f(1 - 0.9) * g
+    v = f(0.999) * (r0 * r0) + f(1 - 0.999) * (g * g)
+    assert np.array_equal(st["m"].cpu().numpy(), m) and np.array_equal(st["v"].cpu().numpy(), v)
+    one = lambda: torch.ones(n // 128, **c)
+    st = dict(m=torch.zeros(n, dtype=torch.uint8, device="cuda"), v=torch.zeros(n, dtype=torch.uint8, device="cuda"), m_scales=one(), v_scales=one())
+    L.AdamW([torch.zeros(n, **c)], states=[st]).step([torch.tensor(g, **c)], 1e-3)
+    root = np.sqrt(f(1 - 0.999) * (g * g))
+    for k, x in (("m_scales", np.abs(f(1 - 0.9) * g)), ("v_scales", root)):
+        top = x.reshape(-1, 128).max(1)
+        assert np.array_equal(st[k].cpu().numpy(), np.where(top < 2.0 ** -100, f(1), top * f(1 / 448))), k
+
+
 def test_adamw_scales_in_one_buffer(gpu_lib):
     """Scales of several tensors one after another: only the first lies on 16 bytes."""
     from moe_layer_router_amd import layer as L
