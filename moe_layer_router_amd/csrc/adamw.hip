@@ -69,24 +69,19 @@ moe_status check_tensors(int32_t count, const moe_adamw_tensor* ts, int32_t stat
   return MOE_OK;
 }
 
-// Elements of a workgroup: enough of them to amortise finding the tensor, few while there are not
-// several workgroups per CU.
-constexpr int kAdamSmall = 2048, kAdamLarge = 8192;
-
 template <int W, int GBF, int S8>
-moe_status launch_adamw(const AdamArgs& a, int64_t chunks, bool large, hipStream_t st) {
-  if (large) hipLaunchKernelGGL((k_adamw<W, GBF, S8, kAdamLarge>), dim3((unsigned)chunks), dim3(kAdamThreads), 0, st, a);
-  else hipLaunchKernelGGL((k_adamw<W, GBF, S8, kAdamSmall>), dim3((unsigned)chunks), dim3(kAdamThreads), 0, st, a);
+moe_status launch_adamw(const AdamArgs& a, int64_t chunks, hipStream_t st) {
+  hipLaunchKernelGGL((k_adamw<W, GBF, S8>), dim3((unsigned)chunks), dim3(kAdamThreads), 0, st, a);
   HIP_TRY(hipGetLastError());
   return MOE_OK;
 }
 template <int W, int GBF>
-moe_status launch_adamw(const AdamArgs& a, int64_t chunks, bool large, bool f8, hipStream_t st) {
-  return f8 ? launch_adamw<W, GBF, 1>(a, chunks, large, st) : launch_adamw<W, GBF, 0>(a, chunks, large, st);
+moe_status launch_adamw(const AdamArgs& a, int64_t chunks, bool f8, hipStream_t st) {
+  return f8 ? launch_adamw<W, GBF, 1>(a, chunks, st) : launch_adamw<W, GBF, 0>(a, chunks, st);
 }
 template <int W>
-moe_status launch_adamw(const AdamArgs& a, int64_t chunks, bool large, bool f8, bool gbf, hipStream_t st) {
-  return gbf ? launch_adamw<W, 1>(a, chunks, large, f8, st) : launch_adamw<W, 0>(a, chunks, large, f8, st);
+moe_status launch_adamw(const AdamArgs& a, int64_t chunks, bool f8, bool gbf, hipStream_t st) {
+  return gbf ? launch_adamw<W, 1>(a, chunks, f8, st) : launch_adamw<W, 0>(a, chunks, f8, st);
 }
 
 }  // namespace
@@ -119,22 +114,18 @@ moe_status moe_adamw(int32_t n_tensors, const moe_adamw_tensor* tensors, const m
   AdamArgs a{};
   a.b1 = (float)o->beta1; a.a1 = (float)(1 - o->beta1);
   a.b2 = (float)o->beta2; a.a2 = (float)(1 - o->beta2);
-  a.beta1 = o->beta1; a.beta2 = o->beta2;
+  a.log_b1 = std::log(o->beta1); a.log_b2 = std::log(o->beta2);
   a.eps = (float)o->eps;
   a.lr = (float)o->lr;
   a.grad_scale = o->grad_scale; a.lr_dev = o->lr_dev; a.t_dev = o->step_dev;
   a.seed = o->seed;
   if (!o->step_dev) {
     const double t = (double)o->step;
-    const double c1 = -std::expm1(t * std::log(o->beta1)), c2 = -std::expm1(t * std::log(o->beta2));
+    const double c1 = -std::expm1(t * a.log_b1), c2 = -std::expm1(t * a.log_b2);
     a.step = (float)((o->lr_dev ? 1.0 : o->lr) / c1);
     a.rs = (float)(1 / std::sqrt(c2));
     a.t_lo = (uint32_t)o->step;
   }
-  int64_t total = 0;
-  for (int32_t i = 0; i < n_tensors; ++i) total += tensors[i].n;
-  const bool large = total >= (int64_t)di.cus * 8 * kAdamLarge;
-  const int64_t chunk = large ? kAdamLarge : kAdamSmall;
   // tensors of one kind of weights and gradients go together, as many as one launch takes
   for (int kind = 0; kind < 6; ++kind) {
     const int w = kind >> 1;
@@ -143,9 +134,9 @@ moe_status moe_adamw(int32_t n_tensors, const moe_adamw_tensor* tensors, const m
     const auto flush = [&]() -> moe_status {
       if (!a.count) return MOE_OK;
       a.first[a.count] = (uint32_t)chunks;
-      if (w == ADAM_F32) TRY(launch_adamw<ADAM_F32>(a, chunks, large, f8, gbf, st));
-      else if (w == ADAM_BF16) TRY(launch_adamw<ADAM_BF16>(a, chunks, large, f8, gbf, st));
-      else TRY(launch_adamw<ADAM_MASTER>(a, chunks, large, f8, gbf, st));
+      if (w == ADAM_F32) TRY(launch_adamw<ADAM_F32>(a, chunks, f8, gbf, st));
+      else if (w == ADAM_BF16) TRY(launch_adamw<ADAM_BF16>(a, chunks, f8, gbf, st));
+      else TRY(launch_adamw<ADAM_MASTER>(a, chunks, f8, gbf, st));
       a.count = 0;
       chunks = 0;
       return MOE_OK;
@@ -154,7 +145,7 @@ moe_status moe_adamw(int32_t n_tensors, const moe_adamw_tensor* tensors, const m
       const moe_adamw_tensor& t = tensors[i];
       const int tw = t.param_dtype == MOE_DTYPE_F32 ? ADAM_F32 : t.master ? ADAM_MASTER : ADAM_BF16;
       if (!t.n || tw != w || (t.grad_dtype == MOE_DTYPE_BF16) != gbf) continue;
-      const int64_t mine = (t.n + chunk - 1) / chunk;
+      const int64_t mine = (t.n + kAdamChunk - 1) / kAdamChunk;
       if (a.count == kAdamTensors || chunks + mine > (int64_t)1 << 30) TRY(flush());
       a.t[a.count] = AdamTensor{t.param, t.grad, t.m, t.v, t.m_scales, t.v_scales, t.master, t.n, t.weight_decay, i};
       a.first[a.count++] = (uint32_t)chunks;
