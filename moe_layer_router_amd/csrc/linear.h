@@ -169,7 +169,7 @@ DEV void lin_finish(const LinEpi& e, long row, int col, float (&v)[8], float (&u
 // Along k an LDS row is 64 k of one row, its 16-byte chunk c at c ^ lin_swz(row), so that the 16 rows of an operand read
 // fall in distinct banks.  Across k it is one k of the tile's columns, its 32-byte chunk c at c ^ lin_swz_t(k), so that the 8 k
 // of 32 lanes do.
-DEV int lin_swz(int r) { return (r ^ (r >> 3)) & 7; }
+DEV int lin_swz(int r) { return (r & 2) | ((r >> 1) & 4); }
 template <int COLS>
 DEV int lin_swz_t(int r) {
   static_assert(COLS % 64 == 0, "whole groups of 4 chunks");
