@@ -426,11 +426,11 @@ __global__ void __launch_bounds__(256) k_linear_join(LinGemm g) {
 // ------------------------------------------------------------------ few rows
 // z for up to 16 TT rows of x (a decoded token, a small batch): bound by reading W once.  A workgroup does 16 rows of W (SwiGLU: 8
 // of the gate and the same 8 of up), its eight waves every eighth 64 k each; W and x go from memory to
-// the matrix cores' operands, eight steps of a wave in flight.  Lane l holds row l % 16 and k 16 (l / 16) .. + 15 of a step, in both operands, so
+// the matrix cores' operands, four steps of a wave in flight (with eight, K = 2048 takes 7.6 us for 5.4: a wave has four).  Lane l holds row l % 16 and k 16 (l / 16) .. + 15 of a step, in both operands, so
 // that a row's 128 bytes are read together; the waves' sums meet in LDS.
 template <int TT, int GATED>
 __global__ void __launch_bounds__(512, 2) k_linear_rows(LinGemm g) {
-  constexpr int NT = GATED ? 8 : 16, U = TT == 1 ? 8 : 4, kPitch = 20;
+  constexpr int NT = GATED ? 8 : 16, U = 4, kPitch = 20;
   __shared__ __attribute__((aligned(16))) float sums[8][16 * TT][kPitch];
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c16 = lane & 15, gq = lane >> 4, j0 = blockIdx.x * NT;
@@ -528,7 +528,10 @@ DEV void lin_split_store(const LinDz& a, long t, int R, int col, float (&v)[8]) 
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       h[e] = f32_to_bf16_rne(v[e]);
-      v[e] -= bf16_to_f32(h[e]);
+      // (what rounds up to infinity is cut instead; infinity and NaN leave nothing for the other parts)
+      const bool over = (h[e] & 0x7F80) == 0x7F80, inf = over && !(fabsf(v[e]) <= 3.4028234e38f);
+      if (over && !inf) h[e] = __builtin_bit_cast(uint32_t, v[e]) >> 16;
+      v[e] = inf ? 0.f : v[e] - bf16_to_f32(h[e]);
     }
     st16(at + 64 * p, v4i{(int)(h[0] | h[1] << 16), (int)(h[2] | h[3] << 16), (int)(h[4] | h[5] << 16), (int)(h[6] | h[7] << 16)});
   }

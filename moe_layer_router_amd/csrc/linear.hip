@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <climits>
 #include <type_traits>
 
 using namespace moe;
@@ -99,19 +100,42 @@ moe_status launch_tiles(LinGemm g, int cus, hipStream_t st) {
 enum { LIN_BIG, LIN_MID, LIN_DEEP, LIN_SMALL };
 template <int PARTS>
 using LinLeast = std::conditional_t<PARTS == 1, LinSmall, LinSmallParts>;
-template <int PARTS, int GATED>
-int lin_kind(const LinGemm& g, int cus) {
-  const auto tiles = [&](long mt, long nt) {
-    if (GATED) nt /= 2;
-    return ((g.rows + mt - 1) / mt) * ((g.cols + nt - 1) / nt);
-  };
-  const long big = tiles(LinBig::rows(PARTS), LinBig::kCols), mid = tiles(LinMid::rows(PARTS), LinMid::kCols);
-  if (big >= cus && 16 * big <= 5 * mid) return LIN_BIG;
-  return mid > cus ? LIN_MID : 2 * mid > cus ? LIN_DEEP : LIN_SMALL;
+// The tiles are chosen by the time that a product takes with each, in ns: rounds of the GPU's slots, each with its 64-k steps and
+// what its first loads and last stores leave uncovered, and for tiles in parts the second launch and the sums' way through the
+// caches.  A step takes, with every slot at work,
+//   big 1.65 us, mid 1.05, deep 0.58, small 0.48 with both operands along k, 1.15 times that with one across it,
+//   1.35 times with P in three parts,
+// and a round 8, 4, 7 and 2.5 us besides.  Measured, T x K x N:
+//   4096 x 2048 x 7168  big 117 us, mid 153, deep 180, small 258        700 x 2048 x 7168  big 43.5, mid 34.9, deep 43.9, small 55.8
+//   4096 x 1024 x 1024  big 35.7, mid 26.2, deep 18.3, small 21.6       700 x 2048 x 2048  big 36.0, mid 23.5, deep 23.6, small 18.8
+template <class TL, int QT, int PARTS, int GATED>
+long lin_cost(const LinGemm& g, int cus, long step, long round) {
+  LinGemm p = g;
+  unsigned grid;
+  if (plan_tiles<TL, PARTS, GATED>(p, cus, &grid) != MOE_OK) return LONG_MAX / 4;
+  const long slots = (long)cus * (160 * 1024 / TL::lds(PARTS)), steps = (g.K + 63) / 64, full = (p.full + slots - 1) / slots;
+  step = step * (QT ? PARTS == 3 ? 27 : 23 : 20) / 20;
+  long ns = full * (steps * step + round);
+  if (p.rest)                                        // (8 bytes of each sum at 8 TB/s)
+    ns += (steps + p.split - 1) / p.split * step + round + 3000 + (long)p.rest * p.split * TL::sums(PARTS) / 1000;
+  return ns;
+}
+struct LinChoice {
+  int kind;
+  long ns, small;                          // the kind's and the smallest tiles' time
+};
+template <int QT, int PARTS, int GATED>
+LinChoice lin_choose(const LinGemm& g, int cus) {
+  const long ns[4] = {lin_cost<LinBig, QT, PARTS, GATED>(g, cus, 1650, 8000), lin_cost<LinMid, QT, PARTS, GATED>(g, cus, 1050, 4000),
+                      lin_cost<LinMidDeep, QT, PARTS, GATED>(g, cus, 580, 7000), lin_cost<LinLeast<PARTS>, QT, PARTS, GATED>(g, cus, 480, 2500)};
+  int best = LIN_SMALL;
+  for (int k = LIN_DEEP; k >= LIN_BIG; --k)
+    if (ns[k] < ns[best]) best = k;
+  return {best, ns[best], ns[LIN_SMALL]};
 }
 template <int PT, int QT, int PARTS, int GATED>
 moe_status launch_product(const LinGemm& g, int cus, hipStream_t st) {
-  switch (lin_kind<PARTS, GATED>(g, cus)) {
+  switch (lin_choose<QT, PARTS, GATED>(g, cus).kind) {
     case LIN_BIG: return launch_tiles<LinBig, PT, QT, PARTS, GATED>(g, cus, st);
     case LIN_MID: return launch_tiles<LinMid, PT, QT, PARTS, GATED>(g, cus, st);
     case LIN_DEEP: return launch_tiles<LinMidDeep, PT, QT, PARTS, GATED>(g, cus, st);
@@ -119,12 +143,15 @@ moe_status launch_product(const LinGemm& g, int cus, hipStream_t st) {
   }
 }
 
-// dx, dw and (b.db) dbias: together where both products have small tiles, else one after another.
+// dx, dw and (b.db) dbias: together with small tiles where that takes no longer than one after another with each its own: two
+// launches fewer.
+constexpr long kLinJointNs = 6000;
 template <int PX, int PW>
 moe_status launch_grads(LinGemm x, LinGemm w, const LinDbias& b, int cus, hipStream_t st) {
   using TL = LinLeast<PW>;
   const unsigned nb = b.db ? (unsigned)(b.R + 63) / 64 : 0;
-  if (lin_kind<PX, 0>(x, cus) == LIN_SMALL && lin_kind<PW, 0>(w, cus) == LIN_SMALL) {
+  const LinChoice cx = lin_choose<1, PX, 0>(x, cus), cw = lin_choose<1, PW, 0>(w, cus);
+  if (cx.small + cw.small <= cx.ns + cw.ns + kLinJointNs) {
     constexpr auto kernel = k_linear_grads<TL, PX, PW>;
     constexpr int kLds = TL::lds(PX) > TL::lds(PW) ? TL::lds(PX) : TL::lds(PW);
     unsigned nx, nw;
@@ -146,8 +173,13 @@ moe_status launch_grads(LinGemm x, LinGemm w, const LinDbias& b, int cus, hipStr
   return launch_product<1, 1, PW, 0>(w, cus, st);
 }
 
-// Few rows of x: W is read once by kernels that need no tile of rows.
-constexpr int kLinFewRows = 32;
+// Few rows of x: W is read once by kernels that need no tile of rows.  They read x once per 16 rows of W, so that the tiles win with many
+// rows and a long k.  Both in us, of a captured run of calls (N = 2048):
+//   K = 2048:  T = 1 5.4 (tiles 9.5), T = 16 6.8 (10.2), T = 32 8.5 (10.4)
+//   K = 7168:  T = 1 11.8 (16.7), T = 4 13.2 (16.9), T = 16 17.5 (17.1), T = 32 24.2 (17.8)
+//   K = 16384: T = 1 21.0 (21.6), T = 16 31.3 (21.3)
+//   K = 4096, N = 7168: T = 16 17.5 (17.9), T = 17 19.2 (17.9), T = 32 24.0 (17.8)
+bool lin_few(long T, long K) { return T <= 16 ? (T + 16) * K <= 1 << 18 : T <= 32 && K <= 2048; }
 template <int GATED>
 moe_status launch_rows(const LinGemm& g, hipStream_t st) {
   const dim3 grid((g.cols + (GATED ? 7 : 15)) / (GATED ? 8 : 16));
@@ -187,7 +219,7 @@ extern "C" {
 
 size_t moe_linear_workspace_size(int32_t T, int32_t K, int32_t N, int32_t act) {
   if (check_linear(T, K, N, act) != MOE_OK) return 0;
-  return std::max((size_t)256, lin_parts(T, N, K, 1, act == MOE_ACT_SWIGLU));
+  return lin_few(T, K) ? 256 : std::max((size_t)256, lin_parts(T, N, K, 1, act == MOE_ACT_SWIGLU));
 }
 
 moe_status moe_linear(int32_t T, int32_t K, int32_t N, int32_t act, const void* x, const void* w, const float* bias,
@@ -234,7 +266,7 @@ moe_status moe_linear(int32_t T, int32_t K, int32_t N, int32_t act, const void* 
   g.e.act = act; g.e.n = N;
   g.e.y_f32 = y_dtype == MOE_DTYPE_F32; g.e.res_f32 = residual_dtype == MOE_DTYPE_F32; g.e.pre_f32 = pre_dtype == MOE_DTYPE_F32;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (T <= kLinFewRows) return act == MOE_ACT_SWIGLU ? launch_rows<1>(g, st) : launch_rows<0>(g, st);
+  if (lin_few(T, K)) return act == MOE_ACT_SWIGLU ? launch_rows<1>(g, st) : launch_rows<0>(g, st);
   return act == MOE_ACT_SWIGLU ? launch_product<0, 0, 1, 1>(g, di.cus, st) : launch_product<0, 0, 1, 0>(g, di.cus, st);
 }
 

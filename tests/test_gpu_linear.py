@@ -367,3 +367,64 @@ def test_offsets_past_32_bits(gpu_lib):
     assert float((d["dx"][-3:].double() - ref).abs().max()) <= 1e-4 * float(ref.abs().max()) and float(d["dx"][:-3].abs().max()) == 0
     ref = _mm(dy[-3:].t(), x[-3:])
     assert float((d["dw"].double() - ref).abs().max()) <= 2.0 ** -14 * float(ref.abs().max())
+
+
+@pytest.mark.parametrize("T,K,N", [s for s in SHAPES if s[0] >= 33] + [(2048, 2048, 7168), (300, 7168, 2048)])
+@pytest.mark.parametrize("dx,want_dw", [("bf16", False), ("bf16", True), ("f32", True)])
+def test_linear_backward_in_parts_with_every_tile(gpu_lib, T, K, N, dx, want_dw):
+    """dz in two parts, in two of three, in three."""
+    from moe_layer_router_amd import layer as L
+    x, w, d, p = _bwd_inputs(T, K, N, "silu", "f32", "bf16")
+    out = L.linear_backward(x, w, d, "silu", p, dx_dtype=dx, want_dw=want_dw, want_dbias=True)
+    _check_bwd(x, w, d, "silu", p, dx, out)
+
+
+@pytest.mark.parametrize("T", [3, 70, 700])
+def test_infinities_and_the_largest_numbers(gpu_lib, T):
+    """An infinity in x, W or dy gives infinities (of its products' signs) where it enters, in whichever part, and nothing beside; dy
+    above the largest BF16 number is no infinity."""
+    from moe_layer_router_amd import layer as L
+    K, N = 200, 72
+    x, w, _, _ = _inputs(T, K, N, "none")
+    x, w = torch.where(x == 0, 1.0, x).to(torch.bfloat16), torch.where(w == 0, 1.0, w).to(torch.bfloat16)
+    inf = float("inf")
+    rest = torch.arange(T, device="cuda") != 2
+    xi = x.clone()
+    xi[2, 5] = inf
+    y = L.linear(xi, w)["y"]
+    assert torch.equal(y[2].float(), inf * torch.sign(w[:, 5].float())) and bool(torch.isfinite(y[rest]).all())
+    wi = w.clone()
+    wi[7, 5] = -inf
+    y = L.linear(x, wi)["y"]
+    assert torch.equal(y[:, 7].float(), -inf * torch.sign(x[:, 5].float())) and bool(torch.isfinite(y[:, 8:]).all())
+    dy = torch.randn(T, N, device="cuda")
+    dy[2, 4] = -inf
+    d = L.linear_backward(x, w, dy, want_dbias=True)
+    assert torch.equal(d["dx"][2], -inf * torch.sign(w[4].float())) and bool(torch.isfinite(d["dx"][rest]).all())
+    assert torch.equal(d["dw"][4], -inf * torch.sign(x[2].float())) and bool(torch.isfinite(d["dw"][5:]).all())
+    assert float(d["dbias"][4]) == -inf and bool(torch.isfinite(d["dbias"][5:]).all())
+    dy = torch.zeros(T, N, device="cuda")
+    dy[2, 4] = 3.4e38
+    ws, xs = (w.float() * 2.0 ** -12).to(torch.bfloat16), (x.float() * 2.0 ** -12).to(torch.bfloat16)
+    d = L.linear_backward(xs, ws, dy)
+    # (one product each: three exact terms, added in fp32)
+    for got, of in ((d["dx"][2], ws[4]), (d["dw"][4], xs[2])):
+        ref = of.double() * float(dy[2, 4])
+        assert bool(((got.double() - ref).abs() <= 4 * U * ref.abs()).all())
+
+
+def test_two_calls_at_once(gpu_lib):
+    """Two streams, each with a workspace of its own, tiles in parts in both."""
+    from moe_layer_router_amd import layer as L
+    sets = [_bwd_inputs(300, 2048, 512, "silu", "f32", "bf16"), _bwd_inputs(130, 4096, 264, "silu", "f32", "bf16")]
+    ref = [(L.linear(x, w), L.linear_backward(x, w, d, "silu", p, want_dbias=True)) for x, w, d, p in sets]
+    torch.cuda.synchronize()
+    streams, spaces, got = [torch.cuda.Stream(), torch.cuda.Stream()], [L.Workspace("cuda"), L.Workspace("cuda")], []
+    for _ in range(4):
+        for s, ws, (x, w, d, p) in zip(streams, spaces, sets):
+            got.append((L.linear(x, w, stream=s, workspace=ws),
+                        L.linear_backward(x, w, d, "silu", p, want_dbias=True, stream=s, workspace=ws)))
+    for s in streams:
+        s.synchronize()
+    for i, (f, g) in enumerate(got):
+        assert torch.equal(f["y"], ref[i % 2][0]["y"]) and all(torch.equal(g[n], ref[i % 2][1][n]) for n in g)
