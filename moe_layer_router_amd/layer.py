@@ -647,9 +647,10 @@ class AdamW:
         return s
 
     def _kept(self):
-        """The tensors that a step writes, None for those that are not there."""
+        """Where the tensors lie that a step writes (None: not there), and the weights' shapes and types."""
         names = ("m", "v", "m_scales", "v_scales") if self.state == "fp8" else ("m", "v")
-        return [t for p, w, s in zip(self.params, self.masters, self.states) for t in (p, w, *[s[k] for k in names])]
+        return [x for p, w, s in zip(self.params, self.masters, self.states)
+                for x in (p.shape, p.dtype, p.data_ptr(), None if w is None else w.data_ptr(), *[s[k].data_ptr() for k in names])]
 
     def _fill(self):
         """The arguments of the call but for the gradients and what step() takes."""
@@ -687,7 +688,7 @@ class AdamW:
         _need(len(grads) == len(self.params), "grads must have one entry per tensor")
         with _on(dev, stream):
             # (tensors whose memory was exchanged since the last step, as by .data or .to, are looked at again)
-            at = [t if t is None else t.data_ptr() for t in self._kept()]
+            at = self._kept()
             if at != self._at:
                 self._fill()
                 self._at = at
