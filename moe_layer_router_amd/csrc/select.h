@@ -8,7 +8,6 @@
 // a token elsewhere: the order is that of fp64.  fp32 decides where its error cannot matter, in all but
 // about one in a hundred tokens; the others are done again in fp64.
 //
-// One wave per token.
 #pragma once
 #include "device_common.h"
 #include "select_host.h"
@@ -182,13 +181,13 @@ DEV void sel_lanes_top2(float& m1, float& m2, int L) {
   if (L > 32) sel_top2(m1, m2, __shfl_xor(m1, 32), __shfl_xor(m2, 32));
 }
 
-// The m candidates of a token ranked again by their fp64 scores (without bias or groups: by the logits).
-template <int NV>
-__device__ __noinline__ int sel_near(SelRule a, const float* row, SelCand* q, int m) {
+// The m candidates `ce` of a token ranked again by their fp64 scores (without bias or groups: by the logits), through `se`.
+template <int UNROLL>
+__device__ __noinline__ int sel_near(SelRule a, const float* row, const int* ce, int* se, int m) {
   const int lane = threadIdx.x & 63;
-  const int mine = lane < m ? q->e[lane] : 0;
+  const int mine = lane < m ? ce[lane] : 0;
   double c = row[mine];
-  if (a.bias) c = sel_choice64(a, sel_row64<NV / 4>(a, row), mine);
+  if (a.bias) c = sel_choice64(a, sel_row64<UNROLL>(a, row), mine);
   const uint64_t key = lane < m ? f64_order_key(c) : 0;
   int rank = 0;
   for (int j = 0; j < m; ++j) {
@@ -197,9 +196,9 @@ __device__ __noinline__ int sel_near(SelRule a, const float* row, SelCand* q, in
     const uint64_t o = (uint64_t)hi << 32 | lo;
     rank += o > key || (o == key && __builtin_amdgcn_readlane(mine, j) < mine);
   }
-  if (lane < m && rank < a.k) q->se[rank] = mine;
+  if (lane < m && rank < a.k) se[rank] = mine;
   __builtin_amdgcn_wave_barrier();
-  const int id = q->se[min(lane, 15)];
+  const int id = se[min(lane, 15)];
   __builtin_amdgcn_wave_barrier();
   return id;
 }
@@ -226,13 +225,7 @@ DEV int sel_fast(const SelArgs& a, int lane, float (&c)[NV], float bmax, float* 
     for (int i = 0; i < NV; ++i) fine += __popcll(__ballot(c[i] < __builtin_inff()));
     if (fine != a.E) return SEL_ALL;
     float m1 = -__builtin_inff(), m2 = m1;         // the two largest
-    if (NV == 4 && a.direct) {                     // a group's experts are those of its lanes
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        m2 = fmaxf(m2, fminf(m1, c[i]));
-        m1 = fmaxf(m1, c[i]);
-      }
-    } else {
+    {
       if (a.E % 4 == 0) {
 #pragma unroll
         for (int i = 0; i < NV; i += 4)
@@ -264,10 +257,7 @@ DEV int sel_fast(const SelArgs& a, int lane, float (&c)[NV], float bmax, float* 
     const float lo = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(score), __builtin_ctzll(last)));
     const float hi = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(score), __builtin_ctzll(next)));
     if (!(lo - hi > a.tol * (fabsf(lo) + fabsf(hi) + 4.0f * bmax))) return SEL_ALL;
-    if (NV == 4 && a.direct) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = in ? c[i] : nan;
-    } else {
+    {
       const float per = 1.0f / (float)n;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -352,7 +342,7 @@ DEV float sel_scores16(bool sigmoid, bool live, float lj) {
 
 // GROUPED: some groups are left out.
 template <int NV, int SIGMOID, int GROUPED>
-__global__ void __launch_bounds__(64 * kSelWaves, NV == 4 ? 8 : 4) k_select(SelArgs a) {
+__global__ void __launch_bounds__(64 * kSelWaves, 4) k_select(SelArgs a) {
   __shared__ __attribute__((aligned(16))) double buf[kSelWaves][64 * NV];
   __shared__ __attribute__((aligned(16))) SelCand cand[kSelWaves];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -399,7 +389,7 @@ __global__ void __launch_bounds__(64 * kSelWaves, NV == 4 ? 8 : 4) k_select(SelA
     int e, m;
     const bool live = lane < a.k;
     const int state = sel_fast<NV, GROUPED>(a, lane, c, bmax, reinterpret_cast<float*>(buf[w]), cand[w], &m, &e);
-    if (state != SEL_CLEAR) e = state == SEL_NEAR ? sel_near<NV>(rule, row, &cand[w], m) : sel_exact(rule, row, buf[w]);
+    if (state != SEL_CLEAR) e = state == SEL_NEAR ? sel_near<NV / 4>(rule, row, cand[w].e, cand[w].se, m) : sel_exact(rule, row, buf[w]);
     const float lj = row[live ? e : 0];
     float s;
     if (a.renorm) {
@@ -415,6 +405,317 @@ __global__ void __launch_bounds__(64 * kSelWaves, NV == 4 ? 8 : 4) k_select(SelA
       a.ids[t * a.k + lane] = e;
       a.w[t * a.k + lane] = a.scale * s;
     }
+  }
+}
+
+// ------------------------------------------------------------------ up to 256 experts
+// Two tokens per wave, 32 lanes each: what a token costs beside its experts (the bisection, the ranks, the weights' exponentials) is
+// done for both by the same instructions.  V experts in a row per lane, twice: 32 V (i / V) + V l + i % V.
+// (8192 tokens of 256 experts in 8 groups: PAIRUS us; one token per wave PAIR1 us.)
+struct SelHalf {
+  float c[36];               // candidates
+  int e[32];
+  float sc[20];              // by rank
+  int se[20];
+  float g[64], gr[68];       // groups' scores, and by rank
+};
+template <int V>
+DEV int sel_expert2(int l, int i) { return 32 * V * (i / V) + V * l + i % V; }
+// Of the half's 32 lanes: from the two 16s, and over all of them.
+DEV float sel_max16s(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+DEV float sel_half_max(float v) { return row_max16(sel_max16s(v)); }
+DEV float sel_half_sum(float v) {
+  v = row_sum16(v);
+  const uint32_t u = __float_as_uint(v);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// A ballot's bits of this lane's half.
+DEV uint32_t sel_half_bits(bool upper, uint64_t who) { return upper ? (uint32_t)(who >> 32) : (uint32_t)who; }
+// A lane mask of both halves' conditions, which are the scalar unit's.
+DEV uint64_t sel_halves(bool lower, bool upper) { return (lower ? 0xFFFFFFFFull : 0) | (upper ? 0xFFFFFFFFull << 32 : 0); }
+DEV bool sel_lane_bit(uint64_t mask) { return __builtin_amdgcn_inverse_ballot_w64(mask); }
+// Inclusive sum over the half's lanes up to this one.
+DEV int sel_half_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);     // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+  return v + __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, true);   // the last lane of rows 0 and 2, in rows 1 and 3
+}
+// Rows of E floats at r's start, each half its own.  (What a lane without experts reads is another row's, or zeros past the last.)
+template <int V>
+DEV void sel_load2(rsrc_t r, int E, int l, int at, float (&c)[2 * V]) {
+  if (E % V == 0) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if constexpr (V == 4) {
+        const v4i v = buf_ld16(r, at + 16 * l, 512 * q);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[4 * q + j] = __int_as_float(v[j]);
+      } else {
+        const auto v = __builtin_amdgcn_raw_buffer_load_b64(r, at + 8 * l, 256 * q, 0);
+        c[2 * q] = __uint_as_float(v[0]);
+        c[2 * q + 1] = __uint_as_float(v[1]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2 * V; ++i) c[i] = buf_ldf(r, at + 4 * V * l + 4 * (i % V), 128 * V * (i / V));
+  }
+}
+// The groups that a token keeps: NaN for the experts of the others.  The lanes of tokens that fp32 can tell it for.
+template <int V>
+DEV uint64_t sel_groups2(const SelArgs& a, int l, bool upper, float (&c)[2 * V], float bmax, float* buf, SelHalf& q) {
+  constexpr int NV = 2 * V;
+  const float nan = __builtin_nanf("");
+  const int n = a.per, lg = a.lanes_log2, L = 1 << lg;
+  bool fine = true;                                // (minima and maxima pass over a NaN)
+#pragma unroll
+  for (int i = 0; i < NV; ++i) fine = fine && (c[i] < __builtin_inff() || sel_expert2<V>(l, i) >= a.E);
+  const uint64_t bad = __ballot(!fine);
+  q.g[l] = nan;
+  q.g[32 + l] = nan;
+  q.gr[l] = nan;
+  q.gr[32 + l] = nan;
+  if (l < 4) q.gr[64 + l] = nan;
+  __builtin_amdgcn_wave_barrier();
+  if (a.direct) {                                  // a group is V experts of each of L lanes
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float m1 = c[V * h], m2 = -__builtin_inff();
+#pragma unroll
+      for (int i = 1; i < V; ++i) {
+        m2 = fmaxf(m2, fminf(m1, c[V * h + i]));
+        m1 = fmaxf(m1, c[V * h + i]);
+      }
+      sel_lanes_top2(m1, m2, L);
+      const int g = (32 * h + l) >> lg;
+      if ((l & (L - 1)) == 0 && g < a.groups) q.g[g] = a.top == 2 ? m1 + m2 : m1;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (sel_expert2<V>(l, i) < a.E) buf[sel_expert2<V>(l, i)] = c[i];
+    __builtin_amdgcn_wave_barrier();
+    for (int g = l >> lg; __ballot(g < a.groups); g += 32 >> lg) {         // (all lanes: those of a group share what they found)
+      float m1 = -__builtin_inff(), m2 = m1;
+      if (g < a.groups) {
+        for (int e = l & (L - 1); e < n; e += L) {
+          const float v = buf[g * n + e];
+          m2 = fmaxf(m2, fminf(m1, v));
+          m1 = fmaxf(m1, v);
+        }
+      }
+      sel_lanes_top2(m1, m2, L);
+      if ((l & (L - 1)) == 0 && g < a.groups) q.g[g] = a.top == 2 ? m1 + m2 : m1;
+    }
+  }
+  __builtin_amdgcn_wave_barrier();
+  uint32_t kept[2] = {0, 0};
+  for (int h = 0; 32 * h < a.groups; ++h) {        // lane l: group 32 h + l
+    const float mine = q.g[32 * h + l];
+    int rank = 0;
+    for (int j = 0; j < a.groups; j += 4) {
+      const v4f o = *reinterpret_cast<const v4f*>(q.g + j);
+      rank += (o[0] > mine) + (o[1] > mine) + (o[2] > mine) + (o[3] > mine);
+    }
+    const bool in = 32 * h + l < a.groups;
+    if (in) q.gr[rank] = mine;                     // (equal scores share a rank, and the one behind it stays NaN)
+    kept[h] = sel_half_bits(upper, __ballot(in && rank < a.keep));
+  }
+  __builtin_amdgcn_wave_barrier();
+  const float lo = q.gr[a.keep - 1], hi = q.gr[a.keep];
+  __builtin_amdgcn_wave_barrier();
+  if (a.direct) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int g = (32 * h + l) >> lg;
+      const bool in = (g < 32 ? kept[0] >> g : kept[1] >> (g & 31)) & 1;
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[V * h + i] = in ? c[V * h + i] : nan;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      // (e / n: the quotient is at least 1 / 512 away from the next whole number)
+      const int g = (int)(((float)sel_expert2<V>(l, i) + 0.5f) * a.per_inv);
+      if (!((g < 32 ? kept[0] >> g : kept[1] >> (g & 31)) & 1)) c[i] = nan;
+    }
+  }
+  return __ballot(lo - hi > a.tol * (fabsf(lo) + fabsf(hi) + 4.0f * bmax)) & sel_halves(!(uint32_t)bad, !(uint32_t)(bad >> 32));
+}
+// The k experts of both tokens (lane j of a half: expert j); per token SEL_*, and how many candidates.  there: of the upper half.
+template <int V, int GROUPED>
+DEV int sel_fast2(const SelArgs& a, int l, bool upper, bool there, float (&c)[2 * V], float bmax, float* buf, SelHalf& q,
+                  int (&count)[2], int (&state)[2]) {
+  constexpr int NV = 2 * V;
+  const float nan = __builtin_nanf(""), none = -__builtin_inff();
+  uint64_t fine = ~0ull;
+  if (GROUPED) fine = sel_groups2<V>(a, l, upper, c, bmax, buf, q);
+  if (a.E != 32 * NV) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (sel_expert2<V>(l, i) >= a.E) c[i] = nan;
+  }
+  float t = c[0];
+#pragma unroll
+  for (int i = 1; i < NV; ++i) t = fmaxf(t, c[i]);
+  // Bisection of the lanes' largest, between what one lane of each of 16 pairs at least reaches and the largest of all.
+  if (!(t == t)) t = none;
+  float lo = sel_max16s(t), hi = row_max16(lo);
+  lo = -row_max16(-lo);
+  uint64_t empty = __ballot(lo == none);
+  if (empty) {                                     // (a pair without experts: the least of the lanes that have some)
+    const uint64_t some = __ballot(t > none);
+    const float least = -sel_half_max(t > none ? -t : none);
+    empty &= ~sel_halves(__popc((uint32_t)some) >= a.k, __popc((uint32_t)(some >> 32)) >= a.k);
+    lo = lo == none && !sel_lane_bit(empty) ? least : lo;
+  }
+  bool go0 = !(uint32_t)empty, go1 = there && !(uint32_t)(empty >> 32);
+  for (int i = 0; i < 16 && (go0 || go1); ++i) {
+    const float mid = 0.5f * lo + 0.5f * hi;
+    const uint64_t in = __ballot(t >= mid);
+    const int in0 = __popc((uint32_t)in), in1 = __popc((uint32_t)(in >> 32));
+    const bool enough = sel_lane_bit(sel_halves(in0 >= a.k, in1 >= a.k));
+    lo = enough ? mid : lo;
+    hi = enough ? hi : mid;
+    go0 = go0 && !(in0 >= a.k && in0 <= a.k + 4);
+    go1 = go1 && !(in1 >= a.k && in1 <= a.k + 4);
+  }
+  const float from = lo == none ? none : lo - 4.0f * a.tol * (fabsf(lo) + bmax);
+  int mine_n = 0;                                  // a lane's candidates
+#pragma unroll
+  for (int i = 0; i < NV; ++i) mine_n += c[i] >= from;
+  const int upto = sel_half_scan(mine_n);
+  int m0 = __builtin_amdgcn_readlane(upto, 31), m1 = __builtin_amdgcn_readlane(upto, 63);
+  fine &= sel_halves(m0 >= a.k && m0 <= 32, m1 >= a.k && m1 <= 32);
+  m0 = min(m0, 32);
+  m1 = min(m1, 32);
+  const int m = upper ? m1 : m0;
+  int at = upto - mine_n;
+  if (upto <= 32) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (c[i] >= from) {
+        q.c[at] = c[i];
+        q.e[at++] = sel_expert2<V>(l, i);
+      }
+    }
+  }
+  __builtin_amdgcn_wave_barrier();
+  const float mine = l < m ? q.c[l] : nan;
+  const int me = q.e[l];
+  if (l >= m) q.c[l] = nan;
+  if (l < 20) q.sc[l] = nan;
+  __builtin_amdgcn_wave_barrier();
+  int rank = 0;
+  for (int j = 0; j < max(m0, m1); j += 4) {
+    const v4f o = *reinterpret_cast<const v4f*>(q.c + j);
+    rank += (o[0] > mine) + (o[1] > mine) + (o[2] > mine) + (o[3] > mine);
+  }
+  if (l < m && rank <= a.k) {
+    q.sc[rank] = mine;
+    q.se[rank] = me;
+  }
+  __builtin_amdgcn_wave_barrier();
+  const int r = min(l, 16);
+  const float x = q.sc[r], y = q.sc[r + 1];        // (equal ones share a place: the next stays NaN)
+  const int id = q.se[r];
+  __builtin_amdgcn_wave_barrier();
+  const bool exact = !a.bias && !GROUPED;          // (logits themselves)
+  const bool clear = x - y > (exact ? 0.f : a.tol * (fabsf(x) + fabsf(y) + 2.0f * bmax)) || (r == a.k - 1 && m == a.k);
+  const uint64_t near = __ballot(l < a.k && !clear);
+  count[0] = m0;
+  count[1] = m1;
+  state[0] = !(uint32_t)fine ? SEL_ALL : (uint32_t)near ? SEL_NEAR : SEL_CLEAR;
+  state[1] = !there ? SEL_CLEAR : !(uint32_t)(fine >> 32) ? SEL_ALL : (uint32_t)(near >> 32) ? SEL_NEAR : SEL_CLEAR;
+  return id;
+}
+
+template <int V, int SIGMOID, int GROUPED>
+__global__ void __launch_bounds__(64 * kSelWaves, 4) k_select_pair(SelArgs a) {
+  constexpr int NV = 2 * V;
+  __shared__ __attribute__((aligned(16))) double buf[kSelWaves][32 * NV];
+  __shared__ __attribute__((aligned(16))) SelHalf half[kSelWaves][2];
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, l = lane & 31;
+  const bool upper = lane >= 32;
+  const long t0 = 2 * ((long)blockIdx.x * kSelWaves + w);
+  if (t0 >= a.T) return;
+  const SelRule rule{a.bias, a.E, a.k, SIGMOID, a.groups, a.keep, a.top};
+  const bool scored = a.bias || GROUPED;      // (else the logits' order is the scores')
+  const bool dense = !SIGMOID && (!a.renorm || scored);      // softmax over all experts
+  float b[NV], bmax = 0.f;                         // of the finite ones
+  if (a.bias) {
+    sel_load2<V>(make_rsrc(a.bias, (uint32_t)a.E * 4), a.E, l, 0, b);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) bmax = fmaxf(bmax, fabsf(b[i]) < __builtin_inff() ? fabsf(b[i]) : 0.f);
+    bmax = sel_half_max(bmax);
+  }
+  const bool two = uni(t0 + 1 < a.T);
+  const float* row = a.logits + t0 * a.E;
+  float c[NV], mx = 0.f, inv = 0.f;              // logits, then scores, then c
+  sel_load2<V>(make_rsrc(row, (two ? 8 : 4) * (uint32_t)a.E), a.E, l, upper ? 4 * a.E : 0, c);
+  if (dense) {
+    if (a.E != 32 * NV) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (sel_expert2<V>(l, i) >= a.E) c[i] = -__builtin_inff();
+    }
+    mx = c[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) mx = fmaxf(mx, c[i]);
+    mx = sel_half_max(mx);
+    float sum = 0.f;
+    float e[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) sum += e[i] = sel_exp(c[i] - mx);
+    inv = __builtin_amdgcn_rcpf(sel_half_sum(sum));
+    if (scored) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) c[i] = e[i] * inv;
+    }
+  } else if (scored) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) c[i] = __builtin_amdgcn_rcpf(1.0f + sel_exp(-c[i]));
+  }
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) c[i] += b[i];
+  }
+  SelHalf& q = half[w][upper];
+  int m[2], state[2];
+  int e = sel_fast2<V, GROUPED>(a, l, upper, two, c, bmax, reinterpret_cast<float*>(buf[w]) + (upper ? 32 * NV : 0), q, m, state);
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {                  // the tokens that fp32 does not settle, the whole wave at each
+    const int st = h ? state[1] : state[0];
+    if (st == SEL_CLEAR) continue;
+    const float* r = row + (long)h * a.E;
+    const int id = st == SEL_NEAR ? sel_near<NV / 4>(rule, r, half[w][h].e, half[w][h].se, h ? m[1] : m[0])
+                                  : sel_exact(rule, r, buf[w]);
+    const int mine = __shfl(id, l & 15);
+    if (upper == (h == 1)) e = mine;
+  }
+  const bool live = l < a.k && (two || !upper);
+  const float lj = row[live ? (upper ? a.E : 0) + e : 0];
+  float s;
+  if (a.renorm) {
+    s = sel_scores16(SIGMOID, live, lj);
+    const float z = row_sum16(s);
+    s = z == 0.f ? 0.f : s * __builtin_amdgcn_rcpf(z);
+  } else if (SIGMOID) {
+    s = __builtin_amdgcn_rcpf(1.0f + sel_exp(-lj));
+  } else {
+    s = mx == -__builtin_inff() ? 0.f : sel_exp(lj - mx) * inv;
+  }
+  if (live) {
+    const size_t at = (size_t)(t0 + upper) * a.k + l;
+    a.ids[at] = e;
+    a.w[at] = a.scale * s;
   }
 }
 

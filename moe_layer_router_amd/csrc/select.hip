@@ -41,12 +41,14 @@ SelArgs sel_args(const moe_selection* s) {
   a.sigmoid = s->scoring == MOE_SCORING_SIGMOID;
   a.groups = s->n_group; a.keep = s->topk_group; a.top = s->group_top;
   a.renorm = s->renormalize != 0;
-  while (s->n_group << (a.lanes_log2 + 1) <= 64) ++a.lanes_log2;
-  const int per = s->E / s->n_group, lanes = per / 4;
-  if (s->E <= 256 && per % 4 == 0 && (lanes & (lanes - 1)) == 0) {
+  a.per = s->E / s->n_group;
+  a.per_inv = 1.0f / (float)a.per;
+  const int lanes = s->E <= 256 ? 32 : 64, v = s->E <= 128 ? 2 : 4, in = a.per / v;
+  while (s->n_group << (a.lanes_log2 + 1) <= lanes) ++a.lanes_log2;
+  if (s->E <= 256 && a.per % v == 0 && in <= 32 && (in & (in - 1)) == 0) {
     a.direct = 1;
     a.lanes_log2 = 0;
-    while (1 << a.lanes_log2 < lanes) ++a.lanes_log2;
+    while (1 << a.lanes_log2 < in) ++a.lanes_log2;
   }
   a.tol = a.sigmoid ? 0x1p-21f : 0x1p-19f;
   a.scale = s->scale;
@@ -54,6 +56,28 @@ SelArgs sel_args(const moe_selection* s) {
 }
 
 unsigned sel_grid(long T, int cus) { return (unsigned)std::min((T + kSelWaves - 1) / kSelWaves, (long)cus * 8); }
+
+// Experts of a token in 32 lanes, V at a time.
+constexpr long kSelLaunch = 1l << 26;              // tokens of a launch (a grid has less than 2^32 threads)
+template <int V>
+moe_status launch_pair(SelArgs a, hipStream_t st) {
+  for (long left = a.T; left > 0; left -= kSelLaunch) {
+    a.T = std::min(left, kSelLaunch);
+    const dim3 grid((unsigned)((a.T + 2 * kSelWaves - 1) / (2 * kSelWaves))), wg(64 * kSelWaves);
+    if (a.keep < a.groups) {
+      if (a.sigmoid) hipLaunchKernelGGL((k_select_pair<V, 1, 1>), grid, wg, 0, st, a);
+      else hipLaunchKernelGGL((k_select_pair<V, 0, 1>), grid, wg, 0, st, a);
+    } else {
+      if (a.sigmoid) hipLaunchKernelGGL((k_select_pair<V, 1, 0>), grid, wg, 0, st, a);
+      else hipLaunchKernelGGL((k_select_pair<V, 0, 0>), grid, wg, 0, st, a);
+    }
+    HIP_TRY(hipGetLastError());
+    a.logits += a.T * a.E;
+    a.ids += a.T * a.k;
+    a.w += a.T * a.k;
+  }
+  return MOE_OK;
+}
 
 template <int NV>
 moe_status launch_select(const SelArgs& a, int cus, hipStream_t st) {
@@ -119,7 +143,8 @@ moe_status moe_select_experts(const moe_selection* s, const float* logits, const
   SelArgs a = sel_args(s);
   a.logits = logits; a.bias = bias; a.ids = topk_ids; a.w = topk_weights;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (a.E <= 256) return launch_select<4>(a, di.cus, st);
+  if (a.E <= 128) return launch_pair<2>(a, st);
+  if (a.E <= 256) return launch_pair<4>(a, st);
   if (a.E <= 512) return launch_select<8>(a, di.cus, st);
   return launch_select<16>(a, di.cus, st);
 }

@@ -15,7 +15,9 @@ struct SelArgs {
   long T;
   int E, k, sigmoid, groups, keep, top, renorm;
   int lanes_log2;            // lanes that share a group, as a power of two
-  int direct;                // E <= 256, and a group is 4 experts of each of those lanes
+  int direct;                // E <= 256, and a group is the same 2 (E <= 128) or 4 experts of each of those lanes
+  int per;                   // experts of a group
+  float per_inv;
   float tol;                 // what fp32 scores are compared up to, relative
   float scale;
   // backward
