@@ -149,6 +149,9 @@ __device__ __noinline__ int sel_exact(SelRule a, const float* row, double* buf) 
 // exp(v) by the instruction for 2^v: within 2 units, and the argument's rounding; what is below 2^-126 is zero.
 DEV float sel_exp(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504f); }
 
+// exp(v - m), m common to a row: its product's rounding is one factor of the whole row.
+DEV float sel_exp_from(float v, float m) { return __builtin_amdgcn_exp2f(__builtin_fmaf(v, 1.44269504f, -(m * 1.44269504f))); }
+
 // The same in fp32, where its rounding cannot change the result; false where it might.
 //   - sigmoid: c has an error of 4 units u = 2^-24 of s (the exponential's argument |l| u, weighted with s (1 - s) |l| <= 0.23, its
 //     function 2 u, weighted with 1/4, the sum and the reciprocal) and one of c.  softmax: the argument's grows with the distance to
@@ -207,12 +210,6 @@ enum { SEL_CLEAR = 0, SEL_NEAR = 1, SEL_ALL = 2 };   // done; candidates too nea
 template <int NV, int GROUPED>
 DEV int sel_fast(const SelArgs& a, int lane, float (&c)[NV], float bmax, float* buf, SelCand& q, int* count, int* id) {
   const float nan = __builtin_nanf("");            // (an expert that is out: no comparison holds)
-  if (a.bias) {
-    float b[NV];
-    sel_load<NV>(a.bias, a.E, lane, b);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) c[i] += b[i];
-  }
   if (a.E != 64 * NV) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -363,6 +360,8 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select(SelArgs a) {
     const float* row = a.logits + t * a.E;
     float c[NV], mx = 0.f, inv = 0.f;              // logits, then scores, then c
     sel_load<NV>(row, a.E, lane, c);
+    float b[NV];
+    if (a.bias) sel_load<NV>(a.bias, a.E, lane, b);
     if (dense) {
       if (a.E != 64 * NV) {
 #pragma unroll
@@ -376,15 +375,22 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select(SelArgs a) {
       float sum = 0.f;
       float e[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) sum += e[i] = sel_exp(c[i] - mx);
+      for (int i = 0; i < NV; ++i) sum += e[i] = sel_exp_from(c[i], mx);
       inv = __builtin_amdgcn_rcpf(wave_sum(sum));
-      if (scored) {
+      if (a.bias) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) c[i] = __builtin_fmaf(e[i], inv, b[i]);
+      } else if (scored) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) c[i] = e[i] * inv;
       }
     } else if (scored) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) c[i] = __builtin_amdgcn_rcpf(1.0f + sel_exp(-c[i]));
+      if (a.bias) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) c[i] += b[i];
+      }
     }
     int e, m;
     const bool live = lane < a.k;
@@ -399,7 +405,7 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select(SelArgs a) {
     } else if (SIGMOID) {
       s = __builtin_amdgcn_rcpf(1.0f + sel_exp(-lj));
     } else {
-      s = mx == -__builtin_inff() ? 0.f : sel_exp(lj - mx) * inv;
+      s = mx == -__builtin_inff() ? 0.f : sel_exp_from(lj, mx) * inv;
     }
     if (live) {
       a.ids[t * a.k + lane] = e;
@@ -673,19 +679,22 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select_pair(SelArgs a) {
     float sum = 0.f;
     float e[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) sum += e[i] = sel_exp(c[i] - mx);
+    for (int i = 0; i < NV; ++i) sum += e[i] = sel_exp_from(c[i], mx);
     inv = __builtin_amdgcn_rcpf(sel_half_sum(sum));
-    if (scored) {
+    if (a.bias) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) c[i] = __builtin_fmaf(e[i], inv, b[i]);
+    } else if (scored) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) c[i] = e[i] * inv;
     }
   } else if (scored) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) c[i] = __builtin_amdgcn_rcpf(1.0f + sel_exp(-c[i]));
-  }
-  if (a.bias) {
+    if (a.bias) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) c[i] += b[i];
+      for (int i = 0; i < NV; ++i) c[i] += b[i];
+    }
   }
   SelHalf& q = half[w][upper];
   int m[2], state[2];
@@ -710,7 +719,7 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select_pair(SelArgs a) {
   } else if (SIGMOID) {
     s = __builtin_amdgcn_rcpf(1.0f + sel_exp(-lj));
   } else {
-    s = mx == -__builtin_inff() ? 0.f : sel_exp(lj - mx) * inv;
+    s = mx == -__builtin_inff() ? 0.f : sel_exp_from(lj, mx) * inv;
   }
   if (live) {
     const size_t at = (size_t)(t0 + upper) * a.k + l;

@@ -81,7 +81,8 @@ moe_status launch_pair(SelArgs a, hipStream_t st) {
 
 template <int NV>
 moe_status launch_select(const SelArgs& a, int cus, hipStream_t st) {
-  const dim3 grid(sel_grid(a.T, cus)), wg(64 * kSelWaves);
+  // (as many workgroups as fit: each wave has the bias's largest once)
+  const dim3 grid(std::min(sel_grid(a.T, cus), (unsigned)cus * (NV == 16 ? 4 : 6))), wg(64 * kSelWaves);
   if (a.keep < a.groups) {
     if (a.sigmoid) hipLaunchKernelGGL((k_select<NV, 1, 1>), grid, wg, 0, st, a);
     else hipLaunchKernelGGL((k_select<NV, 0, 1>), grid, wg, 0, st, a);
