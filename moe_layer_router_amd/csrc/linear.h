@@ -400,9 +400,9 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_linear(LinGemm g) {
 
 // The tiles worked on in parts: 8 columns of a row per thread, the parts added in order.
 template <class TL, int PARTS, int GATED>
-__global__ void __launch_bounds__(256) k_linear_join(LinGemm g) {
+DEV void lin_join(const LinGemm& g, int block) {
   constexpr int S = TL::kCols, MT = TL::rows(PARTS), NT = GATED ? S / 2 : S;
-  const int n = blockIdx.x * 256 + threadIdx.x;    // (MT NT / 8 of a tile: whole workgroups)
+  const int n = block * 256 + threadIdx.x;         // (MT NT / 8 of a tile: whole workgroups)
   const int r = n / (MT * (NT / 8)), l = n % (MT * (NT / 8)), tr = l / (NT / 8), col = 8 * (l % (NT / 8));
   const long t = g.full + r, row = t / g.tj * MT + tr;
   const int c = (int)(t % g.tj) * NT + col;
@@ -421,6 +421,15 @@ __global__ void __launch_bounds__(256) k_linear_join(LinGemm g) {
     }
   }
   lin_finish<GATED>(g.e, row, c, v, u);
+}
+template <class TL, int PARTS, int GATED>
+__global__ void __launch_bounds__(256) k_linear_join(LinGemm g) { lin_join<TL, PARTS, GATED>(g, blockIdx.x); }
+// Of dx and dW: nx workgroups for dx.
+template <class TL, int PX, int PW>
+__global__ void __launch_bounds__(256) k_linear_joins(LinGemm x, LinGemm w, int nx) {
+  const int block = blockIdx.x;
+  if (block < nx) lin_join<TL, PX, 0>(x, block);
+  else lin_join<TL, PW, 0>(w, block - nx);
 }
 
 // ------------------------------------------------------------------ few rows

@@ -57,8 +57,20 @@ size_t lin_parts(long rows, int cols, long K, int parts, bool gated) {
                               : lin_part_bytes<LinSmallParts>(rows, cols, K, parts, gated)});
 }
 
+// What work on the tiles takes, in ns (measured with every slot of the GPU at work): a 64-k step with both operands along k, 1.15
+// times that with one across it, 1.35 times with P in three parts; what a round's first loads and last stores leave uncovered.
+template <class TL>
+constexpr long kLinStep = std::is_same_v<TL, LinBig> ? 1650 : std::is_same_v<TL, LinMid> ? 1050 : std::is_same_v<TL, LinMidDeep> ? 580 : 480;
+template <class TL>
+constexpr long kLinRound = std::is_same_v<TL, LinBig> ? 8000 : std::is_same_v<TL, LinMid> ? 4000 : std::is_same_v<TL, LinMidDeep> ? 7000 : 2500;
+template <class TL, int QT, int PARTS>
+constexpr long lin_step() { return kLinStep<TL> * (QT ? PARTS == 3 ? 27 : 23 : 20) / 20; }
+// Tiles in parts take a second launch, and their sums' way through the caches (8 bytes each at 8 TB/s).
+template <class TL, int PARTS>
+constexpr long lin_join_ns(long parts) { return 3000 + parts * (long)TL::sums(PARTS) / 1000; }
+
 // How a product's tiles are worked on; the workgroups.
-template <class TL, int PARTS, int GATED>
+template <class TL, int QT, int PARTS, int GATED>
 moe_status plan_tiles(LinGemm& g, int cus, unsigned* grid) {
   constexpr int MT = TL::rows(PARTS), NT = GATED ? TL::kCols / 2 : TL::kCols;
   g.tj = (g.cols + NT - 1) / NT;
@@ -67,10 +79,15 @@ moe_status plan_tiles(LinGemm& g, int cus, unsigned* grid) {
   g.full = total;
   g.split = 1;
   g.rest = 0;
-  // what does not fill a whole round of the GPU is split along k, as far as the slots and 256-k parts go
-  const long rest = total % slots;
-  const long split = rest ? std::min({slots / rest, g.K / 256, (long)kLinParts / rest}) : 1;
-  if (split >= 2) {
+  // what does not fill a whole round of the GPU is split along k, as far as the slots and 256-k parts go and the second launch
+  // leaves a gain
+  const long rest = total % slots, steps = (g.K + 63) / 64;
+  const long most = rest ? std::min({slots / rest, g.K / 256, (long)kLinParts / rest}) : 1;
+  long least = steps * lin_step<TL, QT, PARTS>();
+  for (long split = most; split >= 2; split /= 2) {
+    const long ns = (steps + split - 1) / split * lin_step<TL, QT, PARTS>() + lin_join_ns<TL, PARTS>(rest * split);
+    if (ns >= least) continue;
+    least = ns;
     g.full = total - rest;
     g.split = (int)split;
     g.rest = (int)rest;
@@ -79,10 +96,13 @@ moe_status plan_tiles(LinGemm& g, int cus, unsigned* grid) {
   return MOE_OK;
 }
 template <class TL, int PARTS, int GATED>
+constexpr long lin_join_groups(const LinGemm& g) {
+  return (long)g.rest * TL::rows(PARTS) * (GATED ? TL::kCols / 2 : TL::kCols) / 8 / 256;
+}
+template <class TL, int PARTS, int GATED>
 moe_status launch_join(const LinGemm& g, hipStream_t st) {
-  constexpr int MT = TL::rows(PARTS), NT = GATED ? TL::kCols / 2 : TL::kCols;
   if (!g.rest) return MOE_OK;
-  hipLaunchKernelGGL((k_linear_join<TL, PARTS, GATED>), dim3((unsigned)((long)g.rest * MT * NT / 8 / 256)), dim3(256), 0, st, g);
+  hipLaunchKernelGGL((k_linear_join<TL, PARTS, GATED>), dim3((unsigned)lin_join_groups<TL, PARTS, GATED>(g)), dim3(256), 0, st, g);
   HIP_TRY(hipGetLastError());
   return MOE_OK;
 }
@@ -90,7 +110,7 @@ template <class TL, int PT, int QT, int PARTS, int GATED>
 moe_status launch_tiles(LinGemm g, int cus, hipStream_t st) {
   constexpr auto kernel = k_linear<TL, PT, QT, PARTS, GATED>;
   unsigned grid;
-  TRY((plan_tiles<TL, PARTS, GATED>(g, cus, &grid)));
+  TRY((plan_tiles<TL, QT, PARTS, GATED>(g, cus, &grid)));
   TRY(set_lds_limit_once<kernel>(TL::lds(PARTS)));
   hipLaunchKernelGGL(kernel, dim3(grid), dim3(TL::kThreads), TL::lds(PARTS), st, g);
   HIP_TRY(hipGetLastError());
@@ -100,24 +120,18 @@ moe_status launch_tiles(LinGemm g, int cus, hipStream_t st) {
 enum { LIN_BIG, LIN_MID, LIN_DEEP, LIN_SMALL };
 template <int PARTS>
 using LinLeast = std::conditional_t<PARTS == 1, LinSmall, LinSmallParts>;
-// The tiles are chosen by the time that a product takes with each, in ns: rounds of the GPU's slots, each with its 64-k steps and
-// what its first loads and last stores leave uncovered, and for tiles in parts the second launch and the sums' way through the
-// caches.  A step takes, with every slot at work,
-//   big 1.65 us, mid 1.05, deep 0.58, small 0.48 with both operands along k, 1.15 times that with one across it,
-//   1.35 times with P in three parts,
-// and a round 8, 4, 7 and 2.5 us besides.  Measured, T x K x N:
+// The tiles are chosen by the time that a product takes with each.  Measured, T x K x N:
 //   4096 x 2048 x 7168  big 117 us, mid 153, deep 180, small 258        700 x 2048 x 7168  big 43.5, mid 34.9, deep 43.9, small 55.8
 //   4096 x 1024 x 1024  big 35.7, mid 26.2, deep 18.3, small 21.6       700 x 2048 x 2048  big 36.0, mid 23.5, deep 23.6, small 18.8
 template <class TL, int QT, int PARTS, int GATED>
-long lin_cost(const LinGemm& g, int cus, long step, long round) {
+long lin_cost(const LinGemm& g, int cus) {
   LinGemm p = g;
   unsigned grid;
-  if (plan_tiles<TL, PARTS, GATED>(p, cus, &grid) != MOE_OK) return LONG_MAX / 4;
+  if (plan_tiles<TL, QT, PARTS, GATED>(p, cus, &grid) != MOE_OK) return LONG_MAX / 4;
   const long slots = (long)cus * (160 * 1024 / TL::lds(PARTS)), steps = (g.K + 63) / 64, full = (p.full + slots - 1) / slots;
-  step = step * (QT ? PARTS == 3 ? 27 : 23 : 20) / 20;
-  long ns = full * (steps * step + round);
-  if (p.rest)                                        // (8 bytes of each sum at 8 TB/s)
-    ns += (steps + p.split - 1) / p.split * step + round + 3000 + (long)p.rest * p.split * TL::sums(PARTS) / 1000;
+  long ns = full * (steps * lin_step<TL, QT, PARTS>() + kLinRound<TL>);
+  if (p.rest)
+    ns += (steps + p.split - 1) / p.split * lin_step<TL, QT, PARTS>() + kLinRound<TL> + lin_join_ns<TL, PARTS>((long)p.rest * p.split);
   return ns;
 }
 struct LinChoice {
@@ -126,8 +140,8 @@ struct LinChoice {
 };
 template <int QT, int PARTS, int GATED>
 LinChoice lin_choose(const LinGemm& g, int cus) {
-  const long ns[4] = {lin_cost<LinBig, QT, PARTS, GATED>(g, cus, 1650, 8000), lin_cost<LinMid, QT, PARTS, GATED>(g, cus, 1050, 4000),
-                      lin_cost<LinMidDeep, QT, PARTS, GATED>(g, cus, 580, 7000), lin_cost<LinLeast<PARTS>, QT, PARTS, GATED>(g, cus, 480, 2500)};
+  const long ns[4] = {lin_cost<LinBig, QT, PARTS, GATED>(g, cus), lin_cost<LinMid, QT, PARTS, GATED>(g, cus),
+                      lin_cost<LinMidDeep, QT, PARTS, GATED>(g, cus), lin_cost<LinLeast<PARTS>, QT, PARTS, GATED>(g, cus)};
   int best = LIN_SMALL;
   for (int k = LIN_DEEP; k >= LIN_BIG; --k)
     if (ns[k] < ns[best]) best = k;
@@ -155,15 +169,18 @@ moe_status launch_grads(LinGemm x, LinGemm w, const LinDbias& b, int cus, hipStr
     constexpr auto kernel = k_linear_grads<TL, PX, PW>;
     constexpr int kLds = TL::lds(PX) > TL::lds(PW) ? TL::lds(PX) : TL::lds(PW);
     unsigned nx, nw;
-    TRY((plan_tiles<TL, PX, 0>(x, cus, &nx)));
-    TRY((plan_tiles<TL, PW, 0>(w, cus, &nw)));
+    TRY((plan_tiles<TL, 1, PX, 0>(x, cus, &nx)));
+    TRY((plan_tiles<TL, 1, PW, 0>(w, cus, &nw)));
     // (each has sums of its own)
     w.part = x.part + (size_t)x.rest * x.split * TL::sums(PX);
     TRY(set_lds_limit_once<kernel>(kLds));
     hipLaunchKernelGGL(kernel, dim3(nx + nw + nb), dim3(TL::kThreads), kLds, st, x, w, b, (int)nx, (int)nw);
     HIP_TRY(hipGetLastError());
-    TRY((launch_join<TL, PX, 0>(x, st)));
-    return launch_join<TL, PW, 0>(w, st);
+    const long jx = lin_join_groups<TL, PX, 0>(x), jw = lin_join_groups<TL, PW, 0>(w);
+    if (jx + jw == 0) return MOE_OK;
+    hipLaunchKernelGGL((k_linear_joins<TL, PX, PW>), dim3((unsigned)(jx + jw)), dim3(256), 0, st, x, w, (int)jx);
+    HIP_TRY(hipGetLastError());
+    return MOE_OK;
   }
   if (nb) {
     hipLaunchKernelGGL(k_linear_dbias, dim3(nb), dim3(256), 0, st, b);
