@@ -21,6 +21,10 @@ enum { LIN_NONE = 0, LIN_RELU = 1, LIN_GELU = 2, LIN_GELU_TANH = 3, LIN_SILU = 4
 
 // WM x WN waves with NJ subtiles of 16 columns each, 64 k at a time, ST steps in LDS.  A wave has 4 subtiles of 16 rows in LDS; with P in
 // parts 2 subtiles of rows, times the parts.
+// Bound by the matrix cores and what feeds them in large products: 8192 x 7168 x 2 x 2048 with SwiGLU and z
+// kept takes 390 us (1230 TFLOP/s; a plain product of these sizes by the library 307 us, 1410), its gradients of three parts 1060 (dx) and 1020 us
+// (dW), 1390 TFLOP/s of the parts' products.  Four waves of 128 x 128 each, half the reads of LDS, took 544 us in place of 388: with one
+// wave per SIMD the sums move between the two halves of the registers.
 template <int WM_, int WN_, int NJ_, int ST_>
 struct LinTile {
   static constexpr int WM = WM_, WN = WN_, NJ = NJ_, ST = ST_, NW = WM * WN, kThreads = 64 * NW;
@@ -165,7 +169,8 @@ DEV void lin_finish(const LinEpi& e, long row, int col, float (&v)[8], float (&u
   lin_store8(e.y, e.y_f32, at, v);
 }
 
-// An operand's tile goes straight to LDS (16-byte buffer loads, out of range reads as zero).
+// An operand's tile goes straight to LDS (16-byte buffer loads, out of range reads as zero).  The swizzles leave no conflicts between
+// the lanes that LDS serves together (lanes 0-3, 12-15 and 20-27, and so on): 411 -> 388 us in the product above.
 // Along k an LDS row is 64 k of one row, its 16-byte chunk c at c ^ lin_swz(row), so that the 16 rows of an operand read
 // fall in distinct banks.  Across k it is one k of the tile's columns, its 32-byte chunk c at c ^ lin_swz_t(k), so that the 8 k
 // of 32 lanes do.
@@ -398,7 +403,7 @@ __global__ void __launch_bounds__(TL::kThreads, 2) k_linear(LinGemm g) {
   lin_tile<TL, PT, QT, PARTS, GATED>(g, blockIdx.x, lds);
 }
 
-// The tiles worked on in parts: 8 columns of a row per thread, the parts added in order.
+// The tiles worked on in parts: 8 columns of a row per thread, the parts added in order (128 tiles of 128 x 256 in two parts: 10 us).
 template <class TL, int PARTS, int GATED>
 DEV void lin_join(const LinGemm& g, int block) {
   constexpr int S = TL::kCols, MT = TL::rows(PARTS), NT = GATED ? S / 2 : S;
@@ -546,7 +551,8 @@ DEV void lin_split_store(const LinDz& a, long t, int R, int col, float (&v)[8]) 
   }
 }
 
-// Workgroup (x, y): 512 columns of y (8 per lane), slab y's rows (wave w every fourth).
+// Workgroup (x, y): 512 columns of y (8 per lane), slab y's rows (wave w every fourth).  Bound by memory: 8192 x 2048 SwiGLU, 302 MB
+// with three parts, in 59 us (5.1 TB/s).
 template <int GATED>
 __global__ void __launch_bounds__(256) k_linear_dz(LinDz a) {
   __shared__ float red[4][GATED ? 2 : 1][64][8];
@@ -619,7 +625,8 @@ __global__ void __launch_bounds__(256) k_linear_dbias(LinDbias a) {
   lin_dbias<4>(a, blockIdx.x, red);
 }
 
-// dx, dW and db together, where one of them does not fill the GPU: nx workgroups for dx, nw for dW, the others for db.
+// dx, dW and db together, where one of them does not fill the GPU: nx workgroups for dx, nw for dW, the others for db.  Bound by the
+// latency of a few steps: 333 x 1000 x 488 in 10.4 us, where the three apart took 26.
 template <class TL, int PX, int PW>
 __global__ void __launch_bounds__(TL::kThreads, 2) k_linear_grads(LinGemm x, LinGemm w, LinDbias b, int nx, int nw) {
   extern __shared__ __attribute__((aligned(16))) char lds[];

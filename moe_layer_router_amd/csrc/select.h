@@ -20,14 +20,29 @@ DEV uint64_t f64_order_key(double v) {
   const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0);
   return u >> 63 ? ~u : u | 0x8000000000000000ull;
 }
-DEV double sel_shfl_xor(double v, int d) { return __shfl_xor(v, d); }
+template <int CTRL>
+DEV uint64_t dpp_mov64(uint64_t x) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)x, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(x >> 32), CTRL, 0xF, 0xF, false);
+  return (uint64_t)hi << 32 | lo;
+}
+DEV uint64_t sel_larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
 DEV uint64_t sel_max64(uint64_t v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint64_t o = (uint64_t)__shfl_xor((unsigned long long)v, d);
-    v = o > v ? o : v;
-  }
-  return v;
+  v = sel_larger(v, dpp_mov64<0xB1>(v));
+  v = sel_larger(v, dpp_mov64<0x4E>(v));
+  v = sel_larger(v, dpp_mov64<0x141>(v));
+  v = sel_larger(v, dpp_mov64<0x140>(v));
+  const auto l16 = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
+  const auto h16 = __builtin_amdgcn_permlane16_swap((uint32_t)(v >> 32), (uint32_t)(v >> 32), false, false);
+  v = sel_larger((uint64_t)h16[0] << 32 | l16[0], (uint64_t)h16[1] << 32 | l16[1]);
+  const auto l32 = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
+  const auto h32 = __builtin_amdgcn_permlane32_swap((uint32_t)(v >> 32), (uint32_t)(v >> 32), false, false);
+  return sel_larger((uint64_t)h32[0] << 32 | l32[0], (uint64_t)h32[1] << 32 | l32[1]);
+}
+DEV uint64_t sel_readlane64(uint64_t v, int lane) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
+  return (uint64_t)hi << 32 | lo;
 }
 DEV float sel_max(float v) {
 #pragma unroll
@@ -91,40 +106,50 @@ DEV double sel_choice64(const SelRule& a, const SelRow& r, int e) {
   return a.bias ? s + (double)a.bias[e] : s;
 }
 
-// A token's k experts in fp64 for whatever there is in its row, expert j of them in lane j.  Few tokens get here: small
-// code rather than fast.  `buf`: E doubles of LDS of this wave's own.
+// A token's k experts in fp64 for whatever there is in its row, expert j of them in lane j.  Few tokens get here, but a launch lasts
+// until the last of them.  `buf`: E doubles of LDS of this wave's own.
 __device__ __noinline__ int sel_exact(SelRule a, const float* row, double* buf) {
   const int lane = threadIdx.x & 63, n = a.E / a.groups;
   uint64_t kept = ~0ull;
   if (a.bias || a.groups > 1) {                    // (else the logits' order is the scores')
-    const SelRow r = sel_row64<1>(a, row);
-#pragma unroll 1
+    const SelRow r = sel_row64<2>(a, row);
+#pragma unroll 2
     for (int e = lane; e < a.E; e += 64) buf[e] = sel_choice64(a, r, e);
   }
   __builtin_amdgcn_wave_barrier();
   if (a.groups > 1) {
+    int lg = 0;                                    // lanes of a group
+    while (a.groups << (lg + 1) <= 64) ++lg;
+    const int g = lane >> lg, L = 1 << lg;
     double m1 = -__builtin_inf(), m2 = m1;
-    if (lane < a.groups) {
-#pragma unroll 4
-      for (int e = 0; e < n; ++e) {
-        const double v = buf[lane * n + e];        // (NaN: never larger)
+    if (g < a.groups) {
+      for (int e = lane & (L - 1); e < n; e += L) {
+        const double v = buf[g * n + e];           // (NaN: never larger)
         if (v > m1) { m2 = m1; m1 = v; }
         else if (v > m2) m2 = v;
       }
     }
-    const uint64_t score = lane < a.groups ? f64_order_key(a.top == 2 ? m1 + m2 : m1) : 0;
-    int rank = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const uint64_t o = (uint64_t)__shfl((unsigned long long)score, g);
-      rank += o > score || (o == score && g < lane);
+    for (int d = 1; d < L; d <<= 1) {
+      const double o1 = __shfl_xor(m1, d), o2 = __shfl_xor(m2, d);
+      m2 = o1 > m1 ? (m1 > o2 ? m1 : o2) : (o1 > m2 ? o1 : m2);
+      m1 = o1 > m1 ? o1 : m1;
     }
-    kept = __ballot(lane < a.groups && rank < a.keep);
+    const uint64_t score = g < a.groups ? f64_order_key(a.top == 2 ? m1 + m2 : m1) : 0;
+    int rank = 0;
+    for (int h = 0; h < a.groups; ++h) {
+      const uint64_t o = sel_readlane64(score, h << lg);
+      rank += o > score || (o == score && h < g);
+    }
+    kept = __ballot(g < a.groups && rank < a.keep && (lane & (L - 1)) == 0);
+    __builtin_amdgcn_wave_barrier();
+    uint64_t* key = reinterpret_cast<uint64_t*>(buf);
+    for (int e = lane; e < a.E; e += 64)
+      key[e] = !(kept >> (e / n << lg) & 1) ? 0 : f64_order_key(a.bias ? buf[e] : (double)row[e]);
+  } else {
+    uint64_t* key = reinterpret_cast<uint64_t*>(buf);
+    for (int e = lane; e < a.E; e += 64) key[e] = f64_order_key(a.bias ? buf[e] : (double)row[e]);
   }
-  __builtin_amdgcn_wave_barrier();
   uint64_t* key = reinterpret_cast<uint64_t*>(buf);
-#pragma unroll 1
-  for (int e = lane; e < a.E; e += 64)
-    key[e] = a.groups > 1 && !(kept >> (e / n) & 1) ? 0 : f64_order_key(a.bias ? buf[e] : (double)row[e]);
   int mine = 0;
 #pragma unroll 1
   for (int j = 0; j < a.k; ++j) {
@@ -135,12 +160,15 @@ __device__ __noinline__ int sel_exact(SelRule a, const float* row, double* buf) 
       const uint64_t v = key[e];
       if (v > best) { best = v; at = e; }
     }
-    const uint64_t top = sel_max64(best);
-    if (best != top) at = 1 << 30;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) at = min(at, __shfl_xor(at, d));
-    if (lane == j) mine = at;
-    if ((at & 63) == lane) key[at] = 0;
+    const uint64_t top = sel_max64(best), who = __ballot(best == top && at < 1 << 30);
+    int id = __builtin_amdgcn_readlane(at, __builtin_ctzll(who));
+    if (who & (who - 1)) {                         // (several lanes have it)
+      int lowest = best == top ? at : 1 << 30;
+      for (int d = 1; d < 64; d <<= 1) lowest = min(lowest, __shfl_xor(lowest, d));
+      id = lowest;
+    }
+    if (lane == j) mine = id;
+    if ((id & 63) == lane) key[id] = 0;
   }
   __builtin_amdgcn_wave_barrier();
   return mine;
@@ -194,9 +222,7 @@ __device__ __noinline__ int sel_near(SelRule a, const float* row, const int* ce,
   const uint64_t key = lane < m ? f64_order_key(c) : 0;
   int rank = 0;
   for (int j = 0; j < m; ++j) {
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)key, j);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(key >> 32), j);
-    const uint64_t o = (uint64_t)hi << 32 | lo;
+    const uint64_t o = sel_readlane64(key, j);
     rank += o > key || (o == key && __builtin_amdgcn_readlane(mine, j) < mine);
   }
   if (lane < m && rank < a.k) se[rank] = mine;
@@ -337,7 +363,8 @@ DEV float sel_scores16(bool sigmoid, bool live, float lj) {
   return !live ? 0.f : sigmoid ? e * __builtin_amdgcn_rcpf(1.0f + sel_exp(-fabsf(lj))) : e;
 }
 
-// GROUPED: some groups are left out.
+// One token per wave; GROUPED: some groups are left out.  Bound by the vector unit (68% busy): 16384 tokens of 1024 experts with softmax
+// scores and a bias, 409 instructions each, take 24 us, 2.8 TB/s.
 template <int NV, int SIGMOID, int GROUPED>
 __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select(SelArgs a) {
   __shared__ __attribute__((aligned(16))) double buf[kSelWaves][64 * NV];
@@ -417,7 +444,8 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select(SelArgs a) {
 // ------------------------------------------------------------------ up to 256 experts
 // Two tokens per wave, 32 lanes each: what a token costs beside its experts (the bisection, the ranks, the weights' exponentials) is
 // done for both by the same instructions.  V experts in a row per lane, twice: 32 V (i / V) + V l + i % V.
-// (8192 tokens of 256 experts in 8 groups: PAIRUS us; one token per wave PAIR1 us.)
+// Bound by the vector unit's instructions: 262 per token of 256 experts in 8 groups.  8192 such tokens take 7.8 us (one token per
+// wave: 492 instructions, 10.4 us), one token 4.0 us.
 struct SelHalf {
   float c[36];               // candidates
   int e[32];
@@ -737,13 +765,10 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select_pair(SelArgs a) {
 // An expert that stands twice among a token's ids has the sum of both entries.
 //
 // A wave does four tokens at a time: their selected experts in the four rows of 16 lanes, their rows of E one after another.
+// Bound by the rows' way through memory with many experts (16384 tokens of 1024, dense: 27 us, 5 TB/s), by latency with
+// few (8192 tokens of 256, sparse: 5.4 us).
 template <int CTRL>
-DEV double dpp_movd(double v) {
-  const uint64_t x = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)x, CTRL, 0xF, 0xF, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(x >> 32), CTRL, 0xF, 0xF, false);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
+DEV double dpp_movd(double v) { return __builtin_bit_cast(double, dpp_mov64<CTRL>(__builtin_bit_cast(uint64_t, v))); }
 DEV double sel_row_sum16(double v) {
   v += dpp_movd<0xB1>(v);
   v += dpp_movd<0x4E>(v);
