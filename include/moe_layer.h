@@ -659,7 +659,7 @@ moe_status moe_linear_backward(int32_t T, int32_t K, int32_t N, int32_t act, con
  * grad_scale, lr_dev, step_dev: optional scalars in device memory (NULL: 1, lr,
  * step), read when the kernels run, for captured graphs; step_dev must be >= 1.  If grad_scale is
  * not finite nothing is written: a step whose gradients overflowed is left out.
- * 0 <= beta < 1, eps from 2^-100 to 2^100, n <= 2^40, |g| up to 2^63 (v' beyond is
+ * 0 <= beta < 1, eps from 2^-100 to 2^100, n <= 2^34, |g| up to 2^63 (v' beyond is
  * infinite); tensors 16-byte aligned, scales and scalars to their size; what is written
  * overlaps nothing else (a tensor stands in the list once).  No workspace; one launch for
  * each 48 tensors of one kind.  Enqueued on `stream`; errors as moe_forward, of arguments

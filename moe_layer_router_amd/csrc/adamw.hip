@@ -11,6 +11,8 @@ using namespace moe;
 
 namespace {
 
+constexpr int64_t kAdamChunks = (1 << 24) - 1;     // of a launch (a grid has less than 2^32 threads)
+
 struct Span {
   uintptr_t at, end;
   bool written;
@@ -28,7 +30,7 @@ moe_status check_tensors(int32_t count, const moe_adamw_tensor* ts, int32_t stat
   for (int32_t i = 0; i < count; ++i) {
     const moe_adamw_tensor& t = ts[i];
     if (t.n < 0) return fail(MOE_ERR_INVALID_ARGUMENT, "tensor %d: n must not be negative (got %lld)", i, (long long)t.n);
-    if (t.n > (int64_t)1 << 40) return fail(MOE_ERR_UNSUPPORTED, "tensor %d: n > 2^40 is not supported", i);
+    if (t.n > (int64_t)1 << 34) return fail(MOE_ERR_UNSUPPORTED, "tensor %d: n > 2^34 is not supported", i);
     if (t.param_dtype != MOE_DTYPE_F32 && t.param_dtype != MOE_DTYPE_BF16)
       return fail(MOE_ERR_UNSUPPORTED, "tensor %d: param_dtype must be MOE_DTYPE_F32 or MOE_DTYPE_BF16 (got %d)", i, t.param_dtype);
     if (t.grad_dtype != MOE_DTYPE_F32 && t.grad_dtype != MOE_DTYPE_BF16)
@@ -146,7 +148,7 @@ moe_status moe_adamw(int32_t n_tensors, const moe_adamw_tensor* tensors, const m
       const int tw = t.param_dtype == MOE_DTYPE_F32 ? ADAM_F32 : t.master ? ADAM_MASTER : ADAM_BF16;
       if (!t.n || tw != w || (t.grad_dtype == MOE_DTYPE_BF16) != gbf) continue;
       const int64_t mine = (t.n + kAdamChunk - 1) / kAdamChunk;
-      if (a.count == kAdamTensors || chunks + mine > (int64_t)1 << 30) TRY(flush());
+      if (a.count == kAdamTensors || chunks + mine > kAdamChunks) TRY(flush());
       a.t[a.count] = AdamTensor{t.param, t.grad, t.m, t.v, t.m_scales, t.v_scales, t.master, t.n, t.weight_decay, i};
       a.first[a.count++] = (uint32_t)chunks;
       chunks += mine;

@@ -75,7 +75,8 @@ moe_status plan_tiles(LinGemm& g, int cus, unsigned* grid) {
   constexpr int MT = TL::rows(PARTS), NT = GATED ? TL::kCols / 2 : TL::kCols;
   g.tj = (g.cols + NT - 1) / NT;
   const long total = (g.rows + MT - 1) / MT * g.tj, slots = (long)cus * (160 * 1024 / TL::lds(PARTS));
-  if (total > 0x7FFFFFFFl - 16) return fail(MOE_ERR_UNSUPPORTED, "the output has too many tiles");
+  if ((total + 16 + kLinParts) * TL::kThreads > UINT32_MAX)       // (threads of a grid)
+    return fail(MOE_ERR_UNSUPPORTED, "the output has too many tiles");
   g.full = total;
   g.split = 1;
   g.rest = 0;

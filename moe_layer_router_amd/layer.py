@@ -4,7 +4,11 @@ around the layer (layer_norm, balance_loss, backward, orthogonalize).  No
 arithmetic happens here."""
 
 import contextlib
+import ctypes
+from itertools import chain
+from operator import itemgetter
 
+import numpy as np
 import torch
 
 from . import lib
@@ -267,6 +271,8 @@ def _matrix(t, name, dtypes):
 
 
 _FLOATS = (torch.bfloat16, torch.float32)
+_FLOAT_SET = set(_FLOATS)
+_data_ptr, _contiguous = torch.Tensor.data_ptr, torch.Tensor.is_contiguous
 _F32 = (torch.float32,)
 _OUT_DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32, "fp8": torch.uint8}
 
@@ -442,7 +448,6 @@ def trace_phases(out: dict) -> dict:
     persistent kernel, from the per-workgroup stamps (100 MHz clock):
     microseconds from the first workgroup's entry to each phase boundary
     (first / median / last workgroup), and the items per workgroup."""
-    import numpy as np
     desc, ws = out["desc"], out["workspace"]
     reg = lib.moe_get_workspace_regions(desc)
     n = lib.MOE_TRACE_GROUPS * lib.MOE_TRACE_FIELDS
@@ -637,6 +642,7 @@ class AdamW:
         self.capturable = capturable
         self.count = torch.tensor([count], dtype=torch.int64, device=dev) if capturable else int(count)
         self._table, self._at = None, None
+        self._of_state = itemgetter("m", "v", "m_scales", "v_scales") if state == "fp8" else itemgetter("m", "v")
 
     def _zeros(self, p):
         dt = torch.uint8 if self.state == "fp8" else torch.float32
@@ -647,15 +653,14 @@ class AdamW:
         return s
 
     def _kept(self):
-        """Where the tensors lie that a step writes (None: not there), and the weights' shapes and types."""
-        names = ("m", "v", "m_scales", "v_scales") if self.state == "fp8" else ("m", "v")
-        return [x for p, w, s in zip(self.params, self.masters, self.states)
-                for x in (p.shape, p.dtype, p.data_ptr(), None if w is None else w.data_ptr(), *[s[k].data_ptr() for k in names])]
+        """Where the tensors lie that a step writes, which weights have masters, and the weights' shapes and types."""
+        masters = [w for w in self.masters if w is not None]
+        return (list(map(_data_ptr, chain(self.params, masters, chain.from_iterable(map(self._of_state, self.states))))),
+                [w is None for w in self.masters], [p.shape for p in self.params], [p.dtype for p in self.params])
 
     def _fill(self):
         """The arguments of the call but for the gradients and what step() takes."""
         self._table = (lib.MoeAdamwTensor * len(self.params))()
-        self._rows = list(self._table)             # (views of it)
         f8 = self.state == "fp8"
         o = self._options = lib.MoeAdamwOptions()
         o.beta1, o.beta2 = self.betas
@@ -678,6 +683,11 @@ class AdamW:
                 t.m_scales, t.v_scales = s["m_scales"].data_ptr(), s["v_scales"].data_ptr()
             t.param_dtype = lib.MOE_DTYPE_BF16 if p.dtype == torch.bfloat16 else lib.MOE_DTYPE_F32
             t.weight_decay = self.weight_decay[i]
+        row = lib.MoeAdamwTensor
+        self._columns = np.frombuffer(self._table, np.dtype(dict(          # (a view of it)
+            names=("grad", "grad_dtype"), formats=("u8", "i4"), offsets=(row.grad.offset, row.grad_dtype.offset),
+            itemsize=ctypes.sizeof(row))))
+        self._types = None
 
     def step(self, grads, lr, grad_scale: torch.Tensor = None, stream=None):
         """One step with the gradients `grads` (bfloat16 or float32 tensors of the
@@ -692,14 +702,19 @@ class AdamW:
             if at != self._at:
                 self._fill()
                 self._at = at
-            dense = []                             # (copies live until the launch)
-            for row, g, p in zip(self._rows, grads, self.params):
-                if not (g.shape == p.shape and g.dtype in _FLOATS and g.device == dev):
+            # (lists rather than a loop: a step of many small tensors costs the host more than the GPU)
+            shapes, types = [getattr(g, "shape", None) for g in grads], [getattr(g, "dtype", None) for g in grads]
+            if not (shapes == at[2] and set(types) <= _FLOAT_SET and {g.device for g in grads} == {dev}):
+                for g, p in zip(grads, self.params):
                     _is(g, "a gradient", p.shape, _FLOATS, dev)
-                g = _dense(g)
-                dense.append(g)
-                row.grad = g.data_ptr()
-                row.grad_dtype = lib.MOE_DTYPE_F32 if g.dtype is torch.float32 else lib.MOE_DTYPE_BF16
+            where = list(map(_data_ptr, grads))
+            if not all(map(_contiguous, grads)) or any(g & 15 for g in where):
+                grads = [_dense(g) for g in grads]                         # (copies live until the launch)
+                where = list(map(_data_ptr, grads))
+            self._columns["grad"] = where
+            if types != self._types:
+                self._columns["grad_dtype"] = [lib.MOE_DTYPE_F32 if t is torch.float32 else lib.MOE_DTYPE_BF16 for t in types]
+                self._types = types
             o = self._options
             if isinstance(lr, torch.Tensor):
                 _is(lr, "lr", (1,), _F32, dev)
