@@ -65,9 +65,9 @@ template <class TL>
 constexpr long kLinRound = std::is_same_v<TL, LinBig> ? 8000 : std::is_same_v<TL, LinMid> ? 4000 : std::is_same_v<TL, LinMidDeep> ? 7000 : 2500;
 template <class TL, int QT, int PARTS>
 constexpr long lin_step() { return kLinStep<TL> * (QT ? PARTS == 3 ? 27 : 23 : 20) / 20; }
-// Tiles in parts take a second launch, and their sums' way through the caches (8 bytes each at 8 TB/s).
+// Tiles in parts take a second launch (3 us on the GPU, 4 of the host's) and their sums' way through the caches (8 bytes each at 10 TB/s).
 template <class TL, int PARTS>
-constexpr long lin_join_ns(long parts) { return 3000 + parts * (long)TL::sums(PARTS) / 1000; }
+constexpr long lin_join_ns(long parts) { return 5000 + parts * (long)TL::sums(PARTS) / 1250; }
 
 // How a product's tiles are worked on; the workgroups.
 template <class TL, int QT, int PARTS, int GATED>
