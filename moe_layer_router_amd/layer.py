@@ -1,7 +1,8 @@
 """Convenience wrapper: allocate outputs and workspace with PyTorch and call
 moe_forward / moe_route / moe_permute, and the operators of a training step
-around the layer (layer_norm, balance_loss, backward, orthogonalize).  No
-arithmetic happens here."""
+around the layer (layer_norm, balance_loss, backward, orthogonalize) and of a
+block with it (select_experts, linear, their gradients, AdamW).  No arithmetic
+happens here."""
 
 import contextlib
 import ctypes
