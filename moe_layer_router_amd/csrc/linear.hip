@@ -16,7 +16,7 @@ using LinMid = LinTile<2, 2, 4, 2>;        // 128 columns, two workgroups per CU
 using LinMidDeep = LinTile<2, 2, 4, 4>;    // the same with four steps in LDS, one workgroup per CU
 using LinSmall = LinTile<1, 2, 2, 4>;      // 64 columns
 using LinSmallParts = LinTile<2, 2, 2, 4>; // the same, and as many rows of P in parts
-constexpr int kLinMaxDim = 1 << 17;        // (offsets in a tile's 256 rows of two parts fit 32 bits)
+constexpr int kLinMaxDim = 1 << 17;        // (offsets in a tile's 256 rows of three parts fit 32 bits)
 
 template <auto K>
 moe_status set_lds_limit_once(int bytes) {

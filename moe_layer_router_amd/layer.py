@@ -189,6 +189,7 @@ def backward(inputs: dict, topk_ids: torch.Tensor, topk_weights: torch.Tensor, d
     _need((selection is None) == (logits is None), "selection and logits belong together")
     if selection is not None:
         _is(logits, "logits", (T, E), _F32, dev)
+        _need(selection.get("scoring", "sigmoid") in lib.SCORINGS, f"unknown scoring {selection.get('scoring')!r}")
         sel = lib.make_selection(T, E, k, **{n: v for n, v in selection.items() if n != "bias"})
     with _on(dev, stream):
         f32 = dict(dtype=torch.float32, device=dev)
@@ -700,7 +701,7 @@ class AdamW:
         with _on(dev, stream):
             # (tensors whose memory was exchanged since the last step, as by .data or .to, are looked at again)
             at = self._kept()
-            if at != self._at:
+            if at != self._at or not all(map(_contiguous, self.params)):
                 self._fill()
                 self._at = at
             # (lists rather than a loop: a step of many small tensors costs the host more than the GPU)
@@ -730,6 +731,11 @@ class AdamW:
                 o.step_dev = self.count.data_ptr()
             else:
                 o.step = self.count + 1
-            lib.moe_adamw(self._table, o)
+            try:
+                lib.moe_adamw(self._table, o)
+            except lib.MoeError:
+                if self.capturable:
+                    self.count.sub_(1)
+                raise
             if not self.capturable:
                 self.count += 1

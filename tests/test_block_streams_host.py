@@ -98,3 +98,30 @@ def test_optimiser_on_the_stream_of_the_call(monkeypatch):
     opt.states[0] = {n: v[:2] for n, v in opt.states[0].items()}
     opt.step([g[:2]], 1e-3, stream=stream)
     assert calls[2][0][0] == 10 and calls[2][0][1] == p.data_ptr()
+    looked = []
+    monkeypatch.setattr(L, "_is", lambda *a: looked.append(a[1]))
+    p.data = torch.zeros(5, 5)
+    opt.states[0] = {n: torch.zeros(5, 5) for n in ("m", "v")}
+    opt.step([torch.ones(5, 5)], 1e-3, stream=stream)
+    del looked[:]
+    opt.step([torch.ones(5, 5)], 1e-3, stream=stream)
+    assert not looked
+    p.data = p.data.t()                                                    # the same address and shape, no longer dense
+    opt.step([torch.ones(5, 5)], 1e-3, stream=stream)
+    assert "params[0]" in looked
+
+
+def test_a_refused_step_does_not_count(monkeypatch):
+    class P(torch.Tensor):
+        is_cuda = True
+
+    def entry(*a):
+        raise lib.MoeError(1, "moe_adamw")
+
+    monkeypatch.setattr(L, "_on", lambda *a: contextlib.nullcontext())
+    monkeypatch.setattr(lib, "moe_adamw", entry)
+    for capturable in (False, True):
+        opt = L.AdamW([torch.zeros(8).as_subclass(P)], capturable=capturable, count=3)
+        with pytest.raises(lib.MoeError):
+            opt.step([torch.zeros(8)], 1e-3)
+        assert int(opt.count) == 3

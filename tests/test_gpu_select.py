@@ -312,3 +312,48 @@ def test_layer_routed_by_a_selection(gpu_lib, kw, aux):
         r, v = ref[name], _np(got[name])
         rms = np.sqrt((r ** 2).mean(axis=axes, keepdims=True))
         assert np.all(np.isfinite(v)) and np.max(np.abs(v - r) / np.maximum(np.maximum(np.abs(r), rms), 1e-30)) <= 1e-3, name
+
+
+def test_two_tokens_per_wave_past_32_bits(gpu_lib):
+    """More than 2^32 logits of 256 experts, an odd number of tokens."""
+    from moe_layer_router_amd import layer as L
+    T, E = (1 << 24) + 7, 256
+    l = torch.zeros(T, E, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rows = [0, (1 << 22) + 1, (1 << 23) - 1, 1 << 23, 1 << 24, T - 2, T - 1]
+    for t in rows:
+        l[t] = torch.randn(E, generator=g, device="cuda")
+    out = L.select_experts(l, 8, n_group=8, topk_group=4)
+    ids, w = B.select_experts(_np(l[rows]), 8, n_group=8, topk_group=4)
+    assert np.array_equal(_np(out["topk_ids"][rows]), ids)
+    assert np.all(np.abs(_np(out["topk_weights"][rows]) - w) <= 80 * U * w)
+    rest = torch.ones(T, dtype=torch.bool, device="cuda")
+    rest[rows] = False
+    assert bool((out["topk_ids"][rest] == torch.arange(8, device="cuda")).all())
+
+
+def test_more_tokens_than_one_launch_takes(gpu_lib):
+    from moe_layer_router_amd import layer as L
+    T, E = (1 << 26) + 3, 3
+    l = torch.randn(T, E, generator=torch.Generator(device="cuda").manual_seed(5), device="cuda")
+    out = L.select_experts(l, 2, scoring="softmax", renormalize=False)
+    top = torch.topk(l, 2, dim=1)
+    same = (torch.gather(l, 1, out["topk_ids"].long()) == top.values).all(1)
+    assert bool(same.all())
+    p = torch.softmax(l[-5:].double(), 1)
+    assert float((out["topk_weights"][-5:].double() - torch.gather(p, 1, out["topk_ids"][-5:].long())).abs().max()) <= 80 * U
+
+
+def test_many_tokens_that_fp32_does_not_settle(gpu_lib):
+    """Every token of a large batch near a tie, in one of its halves, in both, or in its groups; and more candidates than lanes."""
+    rng = np.random.default_rng(12)
+    for E, groups, keep in ((256, 8, 4), (128, 4, 2), (64, 16, 5), (200, 1, 1), (1000, 10, 4)):
+        T = 331
+        l = rng.normal(size=(T, E)).astype(np.float32)
+        l[::3] = np.round(l[::3] * 2) / 2                  # a few values: ties everywhere
+        l[1::3] = 1.0 + rng.integers(0, 64, size=l[1::3].shape).astype(np.float32) * np.float32(2.0 ** -23)
+        bias = (1e-9 * rng.normal(size=E)).astype(np.float32)
+        for scoring in ("sigmoid", "softmax"):
+            for b in (None, bias):
+                _check(l, 7, b, scoring=scoring, n_group=groups, topk_group=keep, group_top=2, renormalize=True)
+                _check(l, 16, b, scoring=scoring, n_group=groups, topk_group=keep, group_top=1, renormalize=False)
