@@ -23,8 +23,8 @@ enum { LIN_NONE = 0, LIN_RELU = 1, LIN_GELU = 2, LIN_GELU_TANH = 3, LIN_SILU = 4
 // parts 2 subtiles of rows, times the parts.
 // Bound by the matrix cores and what feeds them in large products: 8192 x 7168 x 2 x 2048 with SwiGLU and z
 // kept takes 390 us (1230 TFLOP/s; a plain product of these sizes by the library 307 us, 1410), its gradients of three parts 1060 (dx) and 1020 us
-// (dW), 1390 TFLOP/s of the parts' products.  Four waves of 128 x 128 each, half the reads of LDS, took 544 us in place of 388: with one
-// wave per SIMD the sums move between the two halves of the registers.
+// (dW), 1390 TFLOP/s of the parts' products.  Four waves of 128 x 128 each, half the reads of LDS, took 405 us in place of 395: one wave
+// per SIMD has nothing to multiply at the barriers.
 template <int WM_, int WN_, int NJ_, int ST_>
 struct LinTile {
   static constexpr int WM = WM_, WN = WN_, NJ = NJ_, ST = ST_, NW = WM * WN, kThreads = 64 * NW;
