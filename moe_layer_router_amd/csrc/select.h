@@ -181,10 +181,10 @@ DEV float sel_exp(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504f); }
 DEV float sel_exp_from(float v, float m) { return __builtin_amdgcn_exp2f(__builtin_fmaf(v, 1.44269504f, -(m * 1.44269504f))); }
 
 // The same in fp32, where its rounding cannot change the result; false where it might.
-//   - sigmoid: c has an error of 4 units u = 2^-24 of s (the exponential's argument |l| u, weighted with s (1 - s) |l| <= 0.23, its
-//     function 2 u, weighted with 1/4, the sum and the reciprocal) and one of c.  softmax: the argument's grows with the distance to
-//     the largest logit, 2.5 u each, and the sum's is common to all: under 32 u for the experts in question.  Two c (or group
-//     scores) are told apart only if they differ by more than tol = 8 u or 32 u of their magnitudes.
+//   - with u = 2^-24: the exponential's argument d (|l|, or softmax's distance to the largest logit) is off by 1.2 d u, which is s's
+//     relative error, its function by 2 u, the sum, the reciprocal and the bias by 4 u, softmax's sum, common to all, by 16 u.  With S = |c| +
+//     the bias's largest >= s, and d <= ln(1 / s), all of it is below S (8 + log2(1 / S)) u, softmax's below S (32 + log2(1 / S)) u.  Two c
+//     (or group scores) are told apart only if they differ by more than that of both.
 //   - A value that k to k + 4 of the 64 lanes' largest c reach is found by bisection.  The k best are among the experts that reach it,
 //     some 1.3 k of up to 1024 (those of lanes with two of them).  They go to LDS, one to a lane, and are ranked by counting.
 // Candidates too near to each other are ranked again by fp64 scores of their own.  A NaN, group scores too near to each other or
@@ -202,14 +202,13 @@ DEV void sel_top2(float& m1, float& m2, float o1, float o2) {
   m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
   m1 = fmaxf(m1, o1);
 }
-// The two largest over L lanes in a row, from those of each.
+// The two largest over L lanes in a row (up to 32: two groups at least), from those of each.
 DEV void sel_lanes_top2(float& m1, float& m2, int L) {
   if (L > 1) sel_top2(m1, m2, dpp_mov<0xB1>(m1), dpp_mov<0xB1>(m2));
   if (L > 2) sel_top2(m1, m2, dpp_mov<0x4E>(m1), dpp_mov<0x4E>(m2));
   if (L > 4) sel_top2(m1, m2, dpp_mov<0x141>(m1), dpp_mov<0x141>(m2));
   if (L > 8) sel_top2(m1, m2, dpp_mov<0x140>(m1), dpp_mov<0x140>(m2));
   if (L > 16) sel_top2(m1, m2, __shfl_xor(m1, 16), __shfl_xor(m2, 16));
-  if (L > 32) sel_top2(m1, m2, __shfl_xor(m1, 32), __shfl_xor(m2, 32));
 }
 
 // The m candidates `ce` of a token ranked again by their fp64 scores (without bias or groups: by the logits), through `se`.
@@ -232,6 +231,9 @@ __device__ __noinline__ int sel_near(SelRule a, const float* row, const int* ce,
   return id;
 }
 
+// What scores of size S are off by, relative to it (infinite for zero: underflowed scores are told apart by none).
+DEV float sel_tol(const SelArgs& a, float size) { return a.tol + 0x1p-24f * fmaxf(0.f, -__builtin_amdgcn_logf(size)); }
+
 enum { SEL_CLEAR = 0, SEL_NEAR = 1, SEL_ALL = 2 };   // done; candidates too near; all in fp64
 template <int NV, int GROUPED>
 DEV int sel_fast(const SelArgs& a, int lane, float (&c)[NV], float bmax, float* buf, SelCand& q, int* count, int* id) {
@@ -242,32 +244,30 @@ DEV int sel_fast(const SelArgs& a, int lane, float (&c)[NV], float bmax, float* 
       if (sel_expert(lane, i) >= a.E) c[i] = nan;
   }
   if (GROUPED) {
-    const int n = a.E / a.groups, lg = a.lanes_log2, L = 1 << lg, g = lane >> lg;
+    const int n = a.per, lg = a.lanes_log2, L = 1 << lg, g = lane >> lg;
     int fine = 0;                                  // (minima and maxima pass over a NaN)
 #pragma unroll
     for (int i = 0; i < NV; ++i) fine += __popcll(__ballot(c[i] < __builtin_inff()));
     if (fine != a.E) return SEL_ALL;
     float m1 = -__builtin_inff(), m2 = m1;         // the two largest
-    {
-      if (a.E % 4 == 0) {
+    if (a.E % 4 == 0) {
 #pragma unroll
-        for (int i = 0; i < NV; i += 4)
-          if (sel_expert(lane, i) < a.E) *reinterpret_cast<v4f*>(buf + sel_expert(lane, i)) = v4f{c[i], c[i + 1], c[i + 2], c[i + 3]};
-      } else {
+      for (int i = 0; i < NV; i += 4)
+        if (sel_expert(lane, i) < a.E) *reinterpret_cast<v4f*>(buf + sel_expert(lane, i)) = v4f{c[i], c[i + 1], c[i + 2], c[i + 3]};
+    } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (sel_expert(lane, i) < a.E) buf[sel_expert(lane, i)] = c[i];
-      }
-      __builtin_amdgcn_wave_barrier();
-      if (g < a.groups) {
-        for (int e = lane & (L - 1); e < n; e += L) {
-          const float v = buf[g * n + e];
-          m2 = fmaxf(m2, fminf(m1, v));
-          m1 = fmaxf(m1, v);
-        }
-      }
-      __builtin_amdgcn_wave_barrier();
+      for (int i = 0; i < NV; ++i)
+        if (sel_expert(lane, i) < a.E) buf[sel_expert(lane, i)] = c[i];
     }
+    __builtin_amdgcn_wave_barrier();
+    if (g < a.groups) {
+      for (int e = lane & (L - 1); e < n; e += L) {
+        const float v = buf[g * n + e];
+        m2 = fmaxf(m2, fminf(m1, v));
+        m1 = fmaxf(m1, v);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
     sel_lanes_top2(m1, m2, L);
     const float score = g < a.groups ? (a.top == 2 ? m1 + m2 : m1) : nan;
     int rank = 0;
@@ -279,15 +279,12 @@ DEV int sel_fast(const SelArgs& a, int lane, float (&c)[NV], float bmax, float* 
     if (!last || !next) return SEL_ALL;
     const float lo = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(score), __builtin_ctzll(last)));
     const float hi = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(score), __builtin_ctzll(next)));
-    if (!(lo - hi > a.tol * (fabsf(lo) + fabsf(hi) + 4.0f * bmax))) return SEL_ALL;
-    {
-      const float per = 1.0f / (float)n;
+    if (!(lo - hi > sel_tol(a, fabsf(hi) + 2.0f * bmax) * (fabsf(lo) + fabsf(hi) + 4.0f * bmax))) return SEL_ALL;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        // (e / n: the quotient is at least 1 / 2048 away from the next whole number)
-        const int of = (int)(((float)sel_expert(lane, i) + 0.5f) * per);
-        if (!(kept >> (of << lg & 63) & 1)) c[i] = nan;
-      }
+    for (int i = 0; i < NV; ++i) {
+      // (e / n: the quotient is at least 1 / 2048 away from the next whole number)
+      const int of = (int)(((float)sel_expert(lane, i) + 0.5f) * a.per_inv);
+      if (!(kept >> (of << lg & 63) & 1)) c[i] = nan;
     }
   }
   float t = c[0];
@@ -307,7 +304,7 @@ DEV int sel_fast(const SelArgs& a, int lane, float (&c)[NV], float bmax, float* 
       if (in >= a.k) lo = mid; else hi = mid;
       if (in >= a.k && in <= a.k + 4) break;
     }
-    from = lo - 4.0f * a.tol * (fabsf(lo) + bmax);
+    from = lo - 4.0f * sel_tol(a, fabsf(lo) + bmax) * (fabsf(lo) + bmax);
   }
   int m = 0;
   int* be = reinterpret_cast<int*>(buf) + 64 * NV;             // candidates: c, and their experts
@@ -347,7 +344,7 @@ DEV int sel_fast(const SelArgs& a, int lane, float (&c)[NV], float bmax, float* 
   *id = q.se[r];
   __builtin_amdgcn_wave_barrier();
   const bool exact = !a.bias && !GROUPED;          // (logits themselves)
-  const bool clear = x - y > (exact ? 0.f : a.tol * (fabsf(x) + fabsf(y) + 2.0f * bmax)) || (r == a.k - 1 && m == a.k);
+  const bool clear = x - y > (exact ? 0.f : sel_tol(a, fabsf(y) + bmax) * (fabsf(x) + fabsf(y) + 2.0f * bmax)) || (r == a.k - 1 && m == a.k);
   return __ballot(lane < a.k && !clear) ? SEL_NEAR : SEL_CLEAR;
 }
 
@@ -581,7 +578,7 @@ DEV uint64_t sel_groups2(const SelArgs& a, int l, bool upper, float (&c)[2 * V],
       if (!((g < 32 ? kept[0] >> g : kept[1] >> (g & 31)) & 1)) c[i] = nan;
     }
   }
-  return __ballot(lo - hi > a.tol * (fabsf(lo) + fabsf(hi) + 4.0f * bmax)) & sel_halves(!(uint32_t)bad, !(uint32_t)(bad >> 32));
+  return __ballot(lo - hi > sel_tol(a, fabsf(hi) + 2.0f * bmax) * (fabsf(lo) + fabsf(hi) + 4.0f * bmax)) & sel_halves(!(uint32_t)bad, !(uint32_t)(bad >> 32));
 }
 // The k experts of both tokens (lane j of a half: expert j); per token SEL_*, and how many candidates.  there: of the upper half.
 template <int V, int GROUPED>
@@ -621,7 +618,7 @@ DEV int sel_fast2(const SelArgs& a, int l, bool upper, bool there, float (&c)[2 
     go0 = go0 && !(in0 >= a.k && in0 <= a.k + 4);
     go1 = go1 && !(in1 >= a.k && in1 <= a.k + 4);
   }
-  const float from = lo == none ? none : lo - 4.0f * a.tol * (fabsf(lo) + bmax);
+  const float from = lo == none ? none : lo - 4.0f * sel_tol(a, fabsf(lo) + bmax) * (fabsf(lo) + bmax);
   int mine_n = 0;                                  // a lane's candidates
 #pragma unroll
   for (int i = 0; i < NV; ++i) mine_n += c[i] >= from;
@@ -662,7 +659,7 @@ DEV int sel_fast2(const SelArgs& a, int l, bool upper, bool there, float (&c)[2 
   const int id = q.se[r];
   __builtin_amdgcn_wave_barrier();
   const bool exact = !a.bias && !GROUPED;          // (logits themselves)
-  const bool clear = x - y > (exact ? 0.f : a.tol * (fabsf(x) + fabsf(y) + 2.0f * bmax)) || (r == a.k - 1 && m == a.k);
+  const bool clear = x - y > (exact ? 0.f : sel_tol(a, fabsf(y) + bmax) * (fabsf(x) + fabsf(y) + 2.0f * bmax)) || (r == a.k - 1 && m == a.k);
   const uint64_t near = __ballot(l < a.k && !clear);
   count[0] = m0;
   count[1] = m1;

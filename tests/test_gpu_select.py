@@ -357,3 +357,25 @@ def test_many_tokens_that_fp32_does_not_settle(gpu_lib):
             for b in (None, bias):
                 _check(l, 7, b, scoring=scoring, n_group=groups, topk_group=keep, group_top=2, renormalize=True)
                 _check(l, 16, b, scoring=scoring, n_group=groups, topk_group=keep, group_top=1, renormalize=False)
+
+
+@pytest.mark.parametrize("E,groups,keep", [(256, 8, 4), (96, 3, 2), (512, 4, 2), (1024, 8, 3)])
+@pytest.mark.parametrize("at", [-6.0, -20.0, -60.0, -85.0])
+def test_small_scores_a_unit_of_the_logits_apart(gpu_lib, E, groups, keep, at):
+    """Logits that differ by a few of their last bits, where an fp32 exponential's argument is off by as much: without a bias the
+    order is the logits', whatever their scores round to; with one smaller than the scores it is that of 64-bit scores."""
+    rng = np.random.default_rng(E + int(at))
+    T = 400
+    unit = float(np.spacing(np.float32(abs(at))))
+    step = rng.permuted(np.tile(np.arange(E), (T, 1)), axis=1)
+    l = (at + step * unit).astype(np.float32)
+    assert len(np.unique(l[0])) == E
+    _check(l, 8, None, n_group=groups, topk_group=keep, group_top=2)
+    _check(l, 8, None, n_group=groups, topk_group=keep, group_top=1, renormalize=False)
+    s = 1 / (1 + np.exp(-float(at)))
+    bias = (1e-7 * s * rng.normal(size=E)).astype(np.float32)
+    _check(l, 8, bias, n_group=groups, topk_group=keep, group_top=2)
+    # softmax: the same differences far below one large logit
+    l[:, 0] = l[:, 0] + 2 * abs(at)
+    _check(l, 8, None, scoring="softmax", n_group=groups, topk_group=keep, group_top=2)
+    _check(l, 8, np.float32(0.5) * bias, scoring="softmax", renormalize=False)
