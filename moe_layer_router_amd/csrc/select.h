@@ -39,6 +39,7 @@ DEV uint64_t sel_max64(uint64_t v) {
   const auto h32 = __builtin_amdgcn_permlane32_swap((uint32_t)(v >> 32), (uint32_t)(v >> 32), false, false);
   return sel_larger((uint64_t)h32[0] << 32 | l32[0], (uint64_t)h32[1] << 32 | l32[1]);
 }
+DEV float sel_readlane(float v, int lane) { return __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(v), lane)); }
 DEV uint64_t sel_readlane64(uint64_t v, int lane) {
   const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
   const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
@@ -212,17 +213,36 @@ DEV void sel_lanes_top2(float& m1, float& m2, int L) {
 }
 
 // The m candidates `ce` of a token ranked again by their fp64 scores (without bias or groups: by the logits), through `se`.
+// mx and sum: softmax's in fp32.  The sum's error (32 u, and what the largest logit's product was rounded by) moves all scores by one
+// factor, so that it matters for two c only as far as their s differ: E exponentials in fp64 are formed only where that may decide.
 template <int UNROLL>
-__device__ __noinline__ int sel_near(SelRule a, const float* row, const int* ce, int* se, int m) {
+__device__ __noinline__ int sel_near(SelRule a, const float* row, const int* ce, int* se, int m, float mx, float sum) {
   const int lane = threadIdx.x & 63;
   const int mine = lane < m ? ce[lane] : 0;
   double c = row[mine];
-  if (a.bias) c = sel_choice64(a, sel_row64<UNROLL>(a, row), mine);
-  const uint64_t key = lane < m ? f64_order_key(c) : 0;
-  int rank = 0;
-  for (int j = 0; j < m; ++j) {
-    const uint64_t o = sel_readlane64(key, j);
-    rank += o > key || (o == key && __builtin_amdgcn_readlane(mine, j) < mine);
+  if (a.bias) c = sel_choice64(a, SelRow{row, mx, a.sigmoid ? 1.0 : (double)sum}, mine);
+  const auto place = [&]() {
+    const uint64_t key = lane < m ? f64_order_key(c) : 0;
+    int rank = 0;
+    for (int j = 0; j < m; ++j) {
+      const uint64_t o = sel_readlane64(key, j);
+      rank += o > key || (o == key && __builtin_amdgcn_readlane(mine, j) < mine);
+    }
+    return rank;
+  };
+  int rank = place();
+  if (a.bias && !a.sigmoid) {
+    const double s = c - (double)a.bias[mine], eps = 0x1p-24 * (40.0 + fabs((double)mx));
+    bool doubt = false;
+    for (int j = 0; j < m; ++j) {                  // the one behind
+      const double cj = __builtin_bit_cast(double, sel_readlane64(__builtin_bit_cast(uint64_t, c), j));
+      const double sj = __builtin_bit_cast(double, sel_readlane64(__builtin_bit_cast(uint64_t, s), j));
+      if (__builtin_amdgcn_readlane(rank, j) == rank + 1) doubt = !(c - cj > eps * fabs(s - sj) + 0x1p-48 * (fabs(c) + fabs(cj)));
+    }
+    if (__ballot(lane < m && rank < a.k && doubt)) {
+      c = sel_choice64(a, sel_row64<UNROLL>(a, row), mine);
+      rank = place();
+    }
   }
   if (lane < m && rank < a.k) se[rank] = mine;
   __builtin_amdgcn_wave_barrier();
@@ -360,8 +380,8 @@ DEV float sel_scores16(bool sigmoid, bool live, float lj) {
   return !live ? 0.f : sigmoid ? e * __builtin_amdgcn_rcpf(1.0f + sel_exp(-fabsf(lj))) : e;
 }
 
-// One token per wave; GROUPED: some groups are left out.  Bound by the vector unit (68% busy): 16384 tokens of 1024 experts with softmax
-// scores and a bias, 409 instructions each, take 24 us, 2.8 TB/s.
+// One token per wave; GROUPED: some groups are left out.  Bound by the vector unit: 16384 tokens of 1024 experts with softmax
+// scores and a bias, some 420 instructions each, take 22.5 us, 3.1 TB/s (27 us where every near-tie forms E exponentials in fp64).
 template <int NV, int SIGMOID, int GROUPED>
 __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select(SelArgs a) {
   __shared__ __attribute__((aligned(16))) double buf[kSelWaves][64 * NV];
@@ -382,7 +402,7 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select(SelArgs a) {
     // (opaque: what depends on the lane alone is formed again for each token, cheaper than the registers to keep it)
     const int lane = (int)opaque(threadIdx.x & 63);
     const float* row = a.logits + t * a.E;
-    float c[NV], mx = 0.f, inv = 0.f;              // logits, then scores, then c
+    float c[NV], mx = 0.f, inv = 0.f, total = 1.f;   // logits, then scores, then c
     sel_load<NV>(row, a.E, lane, c);
     float b[NV];
     if (a.bias) sel_load<NV>(a.bias, a.E, lane, b);
@@ -400,7 +420,8 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select(SelArgs a) {
       float e[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) sum += e[i] = sel_exp_from(c[i], mx);
-      inv = __builtin_amdgcn_rcpf(wave_sum(sum));
+      total = wave_sum(sum);
+      inv = __builtin_amdgcn_rcpf(total);
       if (a.bias) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) c[i] = __builtin_fmaf(e[i], inv, b[i]);
@@ -419,7 +440,7 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select(SelArgs a) {
     int e, m;
     const bool live = lane < a.k;
     const int state = sel_fast<NV, GROUPED>(a, lane, c, bmax, reinterpret_cast<float*>(buf[w]), cand[w], &m, &e);
-    if (state != SEL_CLEAR) e = state == SEL_NEAR ? sel_near<NV / 4>(rule, row, cand[w].e, cand[w].se, m) : sel_exact(rule, row, buf[w]);
+    if (state != SEL_CLEAR) e = state == SEL_NEAR ? sel_near<NV / 4>(rule, row, cand[w].e, cand[w].se, m, mx, total) : sel_exact(rule, row, buf[w]);
     const float lj = row[live ? e : 0];
     float s;
     if (a.renorm) {
@@ -441,7 +462,7 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select(SelArgs a) {
 // ------------------------------------------------------------------ up to 256 experts
 // Two tokens per wave, 32 lanes each: what a token costs beside its experts (the bisection, the ranks, the weights' exponentials) is
 // done for both by the same instructions.  V experts in a row per lane, twice: 32 V (i / V) + V l + i % V.
-// Bound by the vector unit's instructions: 262 per token of 256 experts in 8 groups.  8192 such tokens take 7.8 us (one token per
+// Bound by the vector unit's instructions: 271 per token of 256 experts in 8 groups.  8192 such tokens take 7.8 us (one token per
 // wave: 492 instructions, 10.4 us), one token 4.0 us.
 struct SelHalf {
   float c[36];               // candidates
@@ -689,7 +710,7 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select_pair(SelArgs a) {
   }
   const bool two = uni(t0 + 1 < a.T);
   const float* row = a.logits + t0 * a.E;
-  float c[NV], mx = 0.f, inv = 0.f;              // logits, then scores, then c
+  float c[NV], mx = 0.f, inv = 0.f, total = 1.f;   // logits, then scores, then c
   sel_load2<V>(make_rsrc(row, (two ? 8 : 4) * (uint32_t)a.E), a.E, l, upper ? 4 * a.E : 0, c);
   if (dense) {
     if (a.E != 32 * NV) {
@@ -705,7 +726,8 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select_pair(SelArgs a) {
     float e[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) sum += e[i] = sel_exp_from(c[i], mx);
-    inv = __builtin_amdgcn_rcpf(sel_half_sum(sum));
+    total = sel_half_sum(sum);
+    inv = __builtin_amdgcn_rcpf(total);
     if (a.bias) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) c[i] = __builtin_fmaf(e[i], inv, b[i]);
@@ -729,7 +751,8 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select_pair(SelArgs a) {
     const int st = h ? state[1] : state[0];
     if (st == SEL_CLEAR) continue;
     const float* r = row + (long)h * a.E;
-    const int id = st == SEL_NEAR ? sel_near<NV / 4>(rule, r, half[w][h].e, half[w][h].se, h ? m[1] : m[0])
+    const int id = st == SEL_NEAR ? sel_near<NV / 4>(rule, r, half[w][h].e, half[w][h].se, h ? m[1] : m[0],
+                                                      sel_readlane(mx, 32 * h), sel_readlane(total, 32 * h))
                                   : sel_exact(rule, r, buf[w]);
     const int mine = __shfl(id, l & 15);
     if (upper == (h == 1)) e = mine;

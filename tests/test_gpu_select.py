@@ -379,3 +379,18 @@ def test_small_scores_a_unit_of_the_logits_apart(gpu_lib, E, groups, keep, at):
     l[:, 0] = l[:, 0] + 2 * abs(at)
     _check(l, 8, None, scoring="softmax", n_group=groups, topk_group=keep, group_top=2)
     _check(l, 8, np.float32(0.5) * bias, scoring="softmax", renormalize=False)
+
+
+@pytest.mark.parametrize("E", [100, 256, 1000])
+@pytest.mark.parametrize("at", [0.0, 300.0])
+def test_biases_that_even_out_softmax_scores(gpu_lib, E, at):
+    """A bias that makes all c of some rows equal but for its own rounding: their order is that of the fp64 sum."""
+    rng = np.random.default_rng(E)
+    rows = (rng.normal(size=(3, E)) + at).astype(np.float32)
+    for i in range(3):
+        s = np.exp(rows[i].astype(np.float64) - rows[i].max())
+        s /= s.sum()
+        bias = (s.max() + 0.01 - s).astype(np.float32)
+        l = np.concatenate([rows, rows + rng.integers(-1, 2, size=rows.shape).astype(np.float32) * np.float32(2.0 ** -15), rows])
+        _check(l, 8, bias, scoring="softmax", renormalize=False)
+        _check(l, 16, bias, scoring="softmax")
