@@ -178,8 +178,26 @@ __device__ __noinline__ int sel_exact(SelRule a, const float* row, double* buf) 
 // exp(v) by the instruction for 2^v: within 2 units, and the argument's rounding; what is below 2^-126 is zero.
 DEV float sel_exp(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504f); }
 
-// exp(v - m), m common to a row: its product's rounding is one factor of the whole row.
+// exp(v - m), m common to a row: its product's rounding is one factor of the whole row, which the sum divides out again, up to 2^(1/16)
+// with |m| = kSelNear. From 1.5 10^9 on it could leave fp32's range: beyond kSelNear the difference is formed first (it is exact where it
+// matters, within a factor of two of m), and an expert at -infinity has no part in the sum, also where m is.
+constexpr float kSelNear = 0x1p20f;
 DEV float sel_exp_from(float v, float m) { return __builtin_amdgcn_exp2f(__builtin_fmaf(v, 1.44269504f, -(m * 1.44269504f))); }
+DEV float sel_exp_far(float v, float m) { return v == -__builtin_inff() ? 0.f : sel_exp(v - m); }
+// Of a row with the largest logit m (in each half its own, or the wave's), and this lane's sum of them.
+template <int NV>
+DEV float sel_row_exps(const float (&v)[NV], float m, float (&e)[NV]) {
+  const bool far = !(fabsf(m) <= kSelNear);
+  float sum = 0.f;
+  if (__ballot(far)) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) sum += e[i] = far ? sel_exp_far(v[i], m) : sel_exp_from(v[i], m);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) sum += e[i] = sel_exp_from(v[i], m);
+  }
+  return sum;
+}
 
 // The same in fp32, where its rounding cannot change the result; false where it might.
 //   - with u = 2^-24: the exponential's argument d (|l|, or softmax's distance to the largest logit) is off by 1.2 d u, which is s's
@@ -416,11 +434,8 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select(SelArgs a) {
 #pragma unroll
       for (int i = 1; i < NV; ++i) mx = fmaxf(mx, c[i]);
       mx = sel_wave_max(mx);
-      float sum = 0.f;
       float e[NV];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) sum += e[i] = sel_exp_from(c[i], mx);
-      total = wave_sum(sum);
+      total = wave_sum(sel_row_exps<NV>(c, mx, e));
       inv = __builtin_amdgcn_rcpf(total);
       if (a.bias) {
 #pragma unroll
@@ -450,7 +465,7 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select(SelArgs a) {
     } else if (SIGMOID) {
       s = __builtin_amdgcn_rcpf(1.0f + sel_exp(-lj));
     } else {
-      s = mx == -__builtin_inff() ? 0.f : sel_exp_from(lj, mx) * inv;
+      s = mx == -__builtin_inff() ? 0.f : (fabsf(mx) <= kSelNear ? sel_exp_from(lj, mx) : sel_exp_far(lj, mx)) * inv;
     }
     if (live) {
       a.ids[t * a.k + lane] = e;
@@ -722,11 +737,8 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select_pair(SelArgs a) {
 #pragma unroll
     for (int i = 1; i < NV; ++i) mx = fmaxf(mx, c[i]);
     mx = sel_half_max(mx);
-    float sum = 0.f;
     float e[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) sum += e[i] = sel_exp_from(c[i], mx);
-    total = sel_half_sum(sum);
+    total = sel_half_sum(sel_row_exps<NV>(c, mx, e));
     inv = __builtin_amdgcn_rcpf(total);
     if (a.bias) {
 #pragma unroll
@@ -767,7 +779,7 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select_pair(SelArgs a) {
   } else if (SIGMOID) {
     s = __builtin_amdgcn_rcpf(1.0f + sel_exp(-lj));
   } else {
-    s = mx == -__builtin_inff() ? 0.f : sel_exp_from(lj, mx) * inv;
+    s = mx == -__builtin_inff() ? 0.f : (fabsf(mx) <= kSelNear ? sel_exp_from(lj, mx) : sel_exp_far(lj, mx)) * inv;
   }
   if (live) {
     const size_t at = (size_t)(t0 + upper) * a.k + l;
