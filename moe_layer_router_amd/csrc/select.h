@@ -233,6 +233,7 @@ DEV void sel_lanes_top2(float& m1, float& m2, int L) {
 // The m candidates `ce` of a token ranked again by their fp64 scores (without bias or groups: by the logits), through `se`.
 // mx and sum: softmax's in fp32.  The sum's error (32 u, and what the largest logit's product was rounded by) moves all scores by one
 // factor, so that it matters for two c only as far as their s differ: E exponentials in fp64 are formed only where that may decide.
+// The factor is (1 + 32 u) e^(|mx| u) at most, which 1 + (40 + 1.1 |mx|) u covers up to |mx| = kSelNear; beyond, the sum has no such factor.
 template <int UNROLL>
 __device__ __noinline__ int sel_near(SelRule a, const float* row, const int* ce, int* se, int m, float mx, float sum) {
   const int lane = threadIdx.x & 63;
@@ -250,7 +251,7 @@ __device__ __noinline__ int sel_near(SelRule a, const float* row, const int* ce,
   };
   int rank = place();
   if (a.bias && !a.sigmoid) {
-    const double s = c - (double)a.bias[mine], eps = 0x1p-24 * (40.0 + fabs((double)mx));
+    const double s = c - (double)a.bias[mine], eps = 0x1p-24 * (40.0 + 1.1 * fabs((double)mx));
     bool doubt = false;
     for (int j = 0; j < m; ++j) {                  // the one behind
       const double cj = __builtin_bit_cast(double, sel_readlane64(__builtin_bit_cast(uint64_t, c), j));
