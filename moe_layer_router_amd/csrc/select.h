@@ -253,10 +253,10 @@ __device__ __noinline__ int sel_near(SelRule a, const float* row, const int* ce,
   if (a.bias && !a.sigmoid) {
     const double s = c - (double)a.bias[mine], eps = 0x1p-24 * (40.0 + 1.1 * fabs((double)mx));
     bool doubt = false;
-    for (int j = 0; j < m; ++j) {                  // the one behind
+    for (int j = 0; j < m; ++j) {                  // all that are behind: one further back may differ by more in s
       const double cj = __builtin_bit_cast(double, sel_readlane64(__builtin_bit_cast(uint64_t, c), j));
       const double sj = __builtin_bit_cast(double, sel_readlane64(__builtin_bit_cast(uint64_t, s), j));
-      if (__builtin_amdgcn_readlane(rank, j) == rank + 1) doubt = !(c - cj > eps * fabs(s - sj) + 0x1p-48 * (fabs(c) + fabs(cj)));
+      doubt |= __builtin_amdgcn_readlane(rank, j) > rank && !(c - cj > eps * fabs(s - sj) + 0x1p-48 * (fabs(c) + fabs(cj)));
     }
     if (__ballot(lane < m && rank < a.k && doubt)) {
       c = sel_choice64(a, sel_row64<UNROLL>(a, row), mine);

@@ -51,3 +51,21 @@ def test_two_candidates_of_different_scores(gpu_lib, E, at, d):
         bias[at[1]] = _below(s[at[0]] - s[at[1]])              # the first is ahead, by less than fp32 can tell
         _check(l, bias, 1)
         _check(l, bias, 2)
+
+
+@pytest.mark.parametrize("E,at", [(8, (0, 3, 6)), (200, (17, 150, 40)), (256, (255, 4, 130)), (300, (299, 256, 7)), (1024, (5, 900, 333))])
+@pytest.mark.parametrize("d", [1.0, 3.0])
+def test_a_candidate_behind_two_of_equal_scores(gpu_lib, E, at, d):
+    """The sum decides between the last place and the second one behind it; the one between them has the last place's score and
+    a bias a unit lower."""
+    a, b, c = at
+    for m in _logits_of_a_large_factor(709.8, 712, 12):
+        l = np.full((2, E), m - 300, F)
+        l[:, a] = l[:, b] = m - F(d)
+        l[:, c] = m
+        s = B.scores(l[0].astype(np.float64), "softmax")
+        bias = np.zeros(E, F)
+        bias[a] = _below(s[c] - s[a])                          # c is ahead of a, and a of b
+        bias[b] = np.nextafter(bias[a], F(0))
+        _check(l, bias, 1)
+        _check(l, bias, 2)
