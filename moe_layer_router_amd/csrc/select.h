@@ -206,6 +206,7 @@ DEV float sel_row_exps(const float (&v)[NV], float m, float (&e)[NV]) {
 //     (or group scores) are told apart only if they differ by more than that of both.
 //   - A value that k to k + 4 of the 64 lanes' largest c reach is found by bisection.  The k best are among the experts that reach it,
 //     some 1.3 k of up to 1024 (those of lanes with two of them).  They go to LDS, one to a lane, and are ranked by counting.
+//   - A NaN reaches no value.  It counts as -infinity, so that it may be among the k best only where that is the value.
 // Candidates too near to each other are ranked again by fp64 scores of their own.  A NaN, group scores too near to each other or
 // too many candidates (few lanes with experts left) leave it all to sel_exact.
 struct SelCand {
@@ -360,6 +361,7 @@ DEV int sel_fast(const SelArgs& a, int lane, float (&c)[NV], float bmax, float* 
   }
   *count = m;
   if (m > 64 || m < a.k) return SEL_ALL;
+  if (!GROUPED && lo == -__builtin_inff() && m != a.E) return SEL_ALL;
   __builtin_amdgcn_wave_barrier();
   const float mine = lane < m ? buf[lane] : nan;
   const int me = be[lane];
@@ -662,6 +664,10 @@ DEV int sel_fast2(const SelArgs& a, int l, bool upper, bool there, float (&c)[2 
   const int upto = sel_half_scan(mine_n);
   int m0 = __builtin_amdgcn_readlane(upto, 31), m1 = __builtin_amdgcn_readlane(upto, 63);
   fine &= sel_halves(m0 >= a.k && m0 <= 32, m1 >= a.k && m1 <= 32);
+  if (!GROUPED) {                                  // (a NaN where experts at -infinity are needed)
+    const uint64_t last = __ballot(lo == none);
+    fine &= ~sel_halves((uint32_t)last && m0 != a.E, (uint32_t)(last >> 32) && m1 != a.E);
+  }
   m0 = min(m0, 32);
   m1 = min(m1, 32);
   const int m = upper ? m1 : m0;

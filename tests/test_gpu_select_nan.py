@@ -1,0 +1,49 @@
+"""NaN among logits of -infinity on the GPU: a NaN counts as -infinity, and equal ones go to the lower index; with softmax scores a
+NaN is in every score of its token."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import block as B
+
+pytestmark = pytest.mark.gpu
+
+
+def _ids(l, k, bias=None, **kw):
+    from moe_layer_router_amd import layer as L
+    with np.errstate(invalid="ignore"):
+        ids, w = B.select_experts(l, k, bias=bias, **kw)
+    out = L.select_experts(torch.from_numpy(l).cuda(), k, bias=None if bias is None else torch.from_numpy(bias).cuda(), **kw)
+    got = out["topk_ids"].cpu().numpy()
+    assert np.array_equal(got, ids), (kw, np.flatnonzero((got != ids).any(1)), got[(got != ids).any(1)][:2], ids[(got != ids).any(1)][:2])
+    return out["topk_weights"].cpu().numpy(), w
+
+
+@pytest.mark.parametrize("E", [8, 30, 70, 129, 200, 256, 300, 1000])
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+def test_fewer_finite_logits_than_places(gpu_lib, E, scoring):
+    """NaN and -infinity in turn behind the finite ones, in the first or the second token of a pair."""
+    rng = np.random.default_rng(E)
+    l = rng.normal(size=(9, E)).astype(np.float32)
+    for t in (1, 2, 5, 8):
+        l[t] = -np.inf
+        l[t, rng.permutation(E)[:E // 3]] = np.nan
+        l[t, rng.permutation(E)[:t % 4]] = rng.normal(size=t % 4)
+    l[7] = np.nan
+    l[7, E - 2] = 1.0
+    for k in (2, 4, 6):
+        for groups, keep in ((1, 1), (2, 2)):
+            if E % groups == 0:
+                _ids(l, k, scoring=scoring, n_group=groups, topk_group=keep)
+
+
+@pytest.mark.parametrize("E", [8, 70, 256, 300, 1000])
+def test_a_nan_with_biases_of_minus_infinity(gpu_lib, E):
+    rng = np.random.default_rng(E)
+    l = rng.normal(size=(7, E)).astype(np.float32)
+    bias = np.full(E, -np.inf, np.float32)
+    bias[[1, 4]] = 0.1
+    l[2, 2], l[3, [0, 4]] = np.nan, np.nan
+    _ids(l, 4, bias)
+    _ids(l, 4, bias, renormalize=False)
