@@ -81,7 +81,7 @@ struct SelRule {
   const float* bias;
   int E, k, sigmoid, groups, keep, top;
 };
-// fp64 scores of a row.  softmax: its largest logit and the sum of the exponentials (a row of -infinity: no score at all).
+// fp64 scores of a row.  softmax: its largest logit and the sum of the exponentials (a row of -infinity: zero, no score at all; with a NaN: NaN, in every score).
 struct SelRow {
   const float* l;
   float mx;
@@ -103,7 +103,7 @@ DEV SelRow sel_row64(const SelRule& a, const float* row) {
 }
 DEV double sel_choice64(const SelRule& a, const SelRow& r, int e) {
   const float l = r.l[e];
-  double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : r.sum == 0.0 || l == -__builtin_inff() ? 0.0 : exp((double)l - (double)r.mx) / r.sum;
+  double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : r.sum == 0.0 ? 0.0 : exp((double)l - (double)r.mx) / r.sum;
   return a.bias ? s + (double)a.bias[e] : s;
 }
 
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select(SelArgs a) {
     } else if (SIGMOID) {
       s = __builtin_amdgcn_rcpf(1.0f + sel_exp(-lj));
     } else {
-      s = mx == -__builtin_inff() ? 0.f : (fabsf(mx) <= kSelNear ? sel_exp_from(lj, mx) : sel_exp_far(lj, mx)) * inv;
+      s = total == 0.f ? 0.f : (fabsf(mx) <= kSelNear ? sel_exp_from(lj, mx) : sel_exp_far(lj, mx)) * inv;
     }
     if (live) {
       a.ids[t * a.k + lane] = e;
@@ -786,7 +786,7 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select_pair(SelArgs a) {
   } else if (SIGMOID) {
     s = __builtin_amdgcn_rcpf(1.0f + sel_exp(-lj));
   } else {
-    s = mx == -__builtin_inff() ? 0.f : (fabsf(mx) <= kSelNear ? sel_exp_from(lj, mx) : sel_exp_far(lj, mx)) * inv;
+    s = total == 0.f ? 0.f : (fabsf(mx) <= kSelNear ? sel_exp_from(lj, mx) : sel_exp_far(lj, mx)) * inv;
   }
   if (live) {
     const size_t at = (size_t)(t0 + upper) * a.k + l;

@@ -47,3 +47,20 @@ def test_a_nan_with_biases_of_minus_infinity(gpu_lib, E):
     l[2, 2], l[3, [0, 4]] = np.nan, np.nan
     _ids(l, 4, bias)
     _ids(l, 4, bias, renormalize=False)
+
+
+@pytest.mark.parametrize("E,groups", [(8, 2), (96, 6), (256, 8), (300, 6), (1000, 10)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_a_nan_is_in_every_softmax_score(gpu_lib, E, groups, biased):
+    """... of experts at -infinity too, whose score is zero without one."""
+    rng = np.random.default_rng(E)
+    l = rng.normal(size=(6, E)).astype(np.float32)
+    l[1, 3], l[1, 5:] = np.nan, -np.inf
+    l[2], l[2, E - 1] = -np.inf, np.nan
+    l[3, ::2], l[3, 1] = -np.inf, np.nan
+    l[4] = -np.inf
+    bias = (0.1 * rng.normal(size=E)).astype(np.float32) if biased else None
+    for kw in (dict(), dict(n_group=groups, topk_group=groups // 2)):
+        g, w = _ids(l, 4, bias, scoring="softmax", renormalize=False, **kw)
+        assert np.array_equal(np.isnan(g), np.isnan(w))
+        assert np.allclose(g, w, rtol=1e-5, atol=0, equal_nan=True)
