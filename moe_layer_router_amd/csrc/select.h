@@ -897,7 +897,7 @@ __global__ void __launch_bounds__(64 * kSelWaves) k_select_bwd(SelArgs a) {
         for (int i = 1; i < NV; ++i) m = fmaxf(m, e[i]);
         m = sel_wave_max(m);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) s += e[i] = m == -__builtin_inff() ? 0.f : sel_exp(e[i] - m);
+        for (int i = 0; i < NV; ++i) s += e[i] = sel_exp_far(e[i], m);
         s = wave_sum(s);
         if (lane >> 4 == r) { mx = m; sum = s; }
       }

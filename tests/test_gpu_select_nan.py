@@ -64,3 +64,26 @@ def test_a_nan_is_in_every_softmax_score(gpu_lib, E, groups, biased):
         g, w = _ids(l, 4, bias, scoring="softmax", renormalize=False, **kw)
         assert np.array_equal(np.isnan(g), np.isnan(w))
         assert np.allclose(g, w, rtol=1e-5, atol=0, equal_nan=True)
+
+
+@pytest.mark.parametrize("E", [8, 70, 256, 300, 1000])
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_a_nan_is_in_the_gradient(gpu_lib, E, scoring, renorm):
+    """NaN where the definition has one (only softmax scores that are not renormalised have experts that are not selected in it)."""
+    from moe_layer_router_amd import layer as L
+    rng = np.random.default_rng(E)
+    l = rng.normal(size=(6, E)).astype(np.float32)
+    ids = np.argsort(-l, axis=1, kind="stable")[:, :3]
+    l[1, ids[1, 0]] = np.nan
+    l[2], l[2, ids[2, 1]] = -np.inf, np.nan
+    l[3, ids[3, 2]], l[3, ids[3, 0]] = np.nan, -np.inf
+    l[4] = np.nan
+    dw = rng.normal(size=ids.shape).astype(np.float32)
+    with np.errstate(invalid="ignore"):
+        ref = B.select_experts_backward(l, ids, dw, scoring=scoring, renormalize=renorm)
+    got = L.select_experts_backward(torch.from_numpy(l).cuda(), torch.from_numpy(ids.astype(np.int32)).cuda(),
+                                    torch.from_numpy(dw).cuda(), scoring=scoring, renormalize=renorm).cpu().numpy()
+    if scoring == "sigmoid" or renorm:
+        ref, got = np.take_along_axis(ref, ids, 1), np.take_along_axis(got, ids, 1)
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
