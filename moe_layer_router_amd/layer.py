@@ -702,6 +702,7 @@ class AdamW:
             # (tensors whose memory was exchanged since the last step, as by .data or .to, are looked at again)
             at = self._kept()
             if at != self._at or not all(map(_contiguous, self.params)):
+                self._at = None                    # (a table that a refused tensor leaves half filled is never used)
                 self._fill()
                 self._at = at
             # (lists rather than a loop: a step of many small tensors costs the host more than the GPU)
