@@ -36,6 +36,7 @@ moe_status check_tensors(int32_t count, const moe_adamw_tensor* ts, int32_t stat
     if (t.grad_dtype != MOE_DTYPE_F32 && t.grad_dtype != MOE_DTYPE_BF16)
       return fail(MOE_ERR_UNSUPPORTED, "tensor %d: grad_dtype must be MOE_DTYPE_F32 or MOE_DTYPE_BF16 (got %d)", i, t.grad_dtype);
     if (!std::isfinite(t.weight_decay)) return fail(MOE_ERR_INVALID_ARGUMENT, "tensor %d: weight_decay must be finite", i);
+    if (t.reserved != 0) return fail(MOE_ERR_INVALID_ARGUMENT, "tensor %d: reserved must be 0 (got %d)", i, t.reserved);
     if (t.master && t.param_dtype == MOE_DTYPE_F32)
       return fail(MOE_ERR_INVALID_ARGUMENT, "tensor %d: fp32 weights have no master weights", i);
     if (!f8 && (t.m_scales || t.v_scales))

@@ -1,7 +1,8 @@
-"""The optimiser's wrapper on the host (no GPU): what it hands to moe_adamw after a step that was refused, by stand-ins
-for the library's entry point and for the GPU's tensors."""
+"""The optimiser on the host (no GPU): what its wrapper hands to moe_adamw after a step that was refused, by stand-ins
+for the library's entry point and for the GPU's tensors; moe_adamw's refusal of what it does not know."""
 
 import contextlib
+import ctypes
 
 import pytest
 import torch
@@ -69,3 +70,13 @@ def test_a_first_step_that_is_refused(monkeypatch):
     params[1].data = params[1].data.t()
     opt.step([torch.ones(8, 8)] * 2, 1e-3)
     assert len(calls) == 1 and [r[0] for r in calls[0]] == [64, 64] and all(r[1] and r[2] for r in calls[0])
+
+
+@pytest.mark.parametrize("reserved", [1, -1, 1 << 30])
+@pytest.mark.parametrize("n", [0, 100])
+def test_reserved_has_to_be_zero(reserved, n):
+    a = 0x100000                                                           # made-up addresses: the checks never dereference
+    ts = (lib.MoeAdamwTensor * 1)(lib.MoeAdamwTensor(a, 2 * a, 3 * a, 4 * a, None, None, None, n, lib.MOE_DTYPE_F32, lib.MOE_DTYPE_F32, 0.0, reserved))
+    o = lib.MoeAdamwOptions(1e-3, 0.9, 0.999, 1e-8, 1, None, None, None, lib.MOE_DTYPE_F32, 0)
+    assert lib._lib.moe_adamw(1, ts, ctypes.byref(o), None) == lib.MOE_ERR_INVALID_ARGUMENT
+    assert "reserved" in lib.moe_last_error()
