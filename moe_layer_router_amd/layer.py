@@ -6,10 +6,10 @@ happens here."""
 
 import contextlib
 import ctypes
+from array import array
 from itertools import chain
 from operator import itemgetter
 
-import numpy as np
 import torch
 
 from . import lib
@@ -450,6 +450,8 @@ def trace_phases(out: dict) -> dict:
     persistent kernel, from the per-workgroup stamps (100 MHz clock):
     microseconds from the first workgroup's entry to each phase boundary
     (first / median / last workgroup), and the items per workgroup."""
+    import numpy as np
+
     desc, ws = out["desc"], out["workspace"]
     reg = lib.moe_get_workspace_regions(desc)
     n = lib.MOE_TRACE_GROUPS * lib.MOE_TRACE_FIELDS
@@ -662,7 +664,9 @@ class AdamW:
 
     def _fill(self):
         """The arguments of the call but for the gradients and what step() takes."""
-        self._table = (lib.MoeAdamwTensor * len(self.params))()
+        row, size = lib.MoeAdamwTensor, ctypes.sizeof(lib.MoeAdamwTensor)
+        memory = bytearray(len(self.params) * size)
+        self._table = (row * len(self.params)).from_buffer(memory)
         f8 = self.state == "fp8"
         o = self._options = lib.MoeAdamwOptions()
         o.beta1, o.beta2 = self.betas
@@ -685,10 +689,9 @@ class AdamW:
                 t.m_scales, t.v_scales = s["m_scales"].data_ptr(), s["v_scales"].data_ptr()
             t.param_dtype = lib.MOE_DTYPE_BF16 if p.dtype == torch.bfloat16 else lib.MOE_DTYPE_F32
             t.weight_decay = self.weight_decay[i]
-        row = lib.MoeAdamwTensor
-        self._columns = np.frombuffer(self._table, np.dtype(dict(          # (a view of it)
-            names=("grad", "grad_dtype"), formats=("u8", "i4"), offsets=(row.grad.offset, row.grad_dtype.offset),
-            itemsize=ctypes.sizeof(row))))
+        # (columns of the table)
+        self._grad = memoryview(memory).cast("Q")[row.grad.offset // 8::size // 8]
+        self._grad_dtype = memoryview(memory).cast("i")[row.grad_dtype.offset // 4::size // 4]
         self._types = None
 
     def step(self, grads, lr, grad_scale: torch.Tensor = None, stream=None):
@@ -714,9 +717,9 @@ class AdamW:
             if not all(map(_contiguous, grads)) or any(g & 15 for g in where):
                 grads = [_dense(g) for g in grads]                         # (copies live until the launch)
                 where = list(map(_data_ptr, grads))
-            self._columns["grad"] = where
+            self._grad[:] = array("Q", where)
             if types != self._types:
-                self._columns["grad_dtype"] = [lib.MOE_DTYPE_F32 if t is torch.float32 else lib.MOE_DTYPE_BF16 for t in types]
+                self._grad_dtype[:] = array("i", [lib.MOE_DTYPE_F32 if t is torch.float32 else lib.MOE_DTYPE_BF16 for t in types])
                 self._types = types
             o = self._options
             if isinstance(lr, torch.Tensor):
