@@ -107,7 +107,8 @@ DEV void lin_act_grad(int act, const float (&z)[8], float (&d)[8]) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float s = lin_sigmoid(1.5957691216f * (z[e] + 0.044715f * z[e] * z[e] * z[e]));
-        d[e] *= s + z[e] * s * (1.0f - s) * 1.5957691216f * (1.0f + 0.134145f * z[e] * z[e]);
+        const float n = __builtin_amdgcn_fmed3f(z[e], -1024.0f, 1024.0f);      // (s (1 - s) is zero beyond, and z^2 may be infinite)
+        d[e] *= s + n * s * (1.0f - s) * 1.5957691216f * (1.0f + 0.134145f * n * n);
       }
       break;
     case LIN_SILU:
