@@ -573,8 +573,8 @@ __global__ void __launch_bounds__(256) k_linear_dz(LinDz a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float s = lin_sigmoid(z[e]), dy = d[e];
-          d[e] = dy * u[e] * s * (1.0f + z[e] * (1.0f - s));
-          u[e] = dy * z[e] * s;
+          d[e] = dy * (u[e] * (s * (1.0f + z[e] * (1.0f - s))));      // (what is at most 1.1 first: no infinity where s is zero)
+          u[e] = dy * (z[e] * s);
           su[e] += u[e];
         }
         if (a.dz) lin_split_store(a, t, R, a.n + col, u);

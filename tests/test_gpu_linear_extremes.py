@@ -31,3 +31,24 @@ def test_derivatives_of_large_finite_z(gpu_lib, act):
     bound = 60 * U * np.abs(dy) * (1 + np.minimum(np.abs(z), 20))
     assert np.all(np.abs(_np(out["dbias"]) - ref) <= bound), (_np(out["dbias"]), ref)
     assert np.all(np.abs(_np(out["dw"])[:, 0] - ref) <= bound) and np.all(np.isfinite(_np(out["dx"])))
+
+
+def test_swiglu_of_large_finite_factors(gpu_lib):
+    """dy z_up and dy z_gate beyond fp32's largest number where SiLU or its derivative is zero."""
+    from moe_layer_router_amd import layer as L
+    gate = np.array([-3e38, -1e30, -200, -110, -3e38, 2, 2, 0], np.float32)
+    up = np.array([3e38, 3e38, 3e38, -3e38, 1, 1e30, -1e30, 1], np.float32)
+    dy = np.array([8, 1e10, 4, 100, 50, 1e-3, 1e-3, 3], np.float32)
+    N, K = 8, 8
+    x, w = torch.ones(1, K, dtype=torch.bfloat16, device="cuda"), torch.ones(2 * N, K, dtype=torch.bfloat16, device="cuda")
+    pre = torch.from_numpy(np.concatenate([gate, up])[None]).cuda()
+    out = L.linear_backward(x, w, torch.from_numpy(dy[None]).cuda(), "swiglu", pre, want_dbias=True)
+    with np.errstate(over="ignore", under="ignore"):
+        ref = B.activate_grad(_np(pre), dy[None].astype(np.float64), "swiglu")[0]
+    size = np.concatenate([np.abs(dy * up.astype(np.float64)), np.abs(dy).astype(np.float64)])
+    g2 = np.tile(np.minimum(np.abs(gate), 20), 2)
+    got = _np(out["dbias"])
+    # (sigmoid(-110) is below fp32's normal numbers: 2^-126 of dy z_up)
+    bound = np.where(np.tile(gate, 2) < -88, 2.0 ** -126 * 128 * size, 60 * U * size * (1 + g2))
+    assert np.all(np.abs(got - ref) <= bound), (got, ref)
+    assert np.all(np.abs(_np(out["dw"])[:, 0] - ref) <= bound)
