@@ -627,7 +627,9 @@ moe_status moe_linear(int32_t T, int32_t K, int32_t N, int32_t act, const void* 
  * and the residual's gradient is dy.  dx [T][K] of dx_dtype, dw [R][K] fp32, dbias [R]
  * fp32: each optional (NULL = not computed; x is needed for dw, w for dx), overwritten.
  * dz enters the matrix cores as three BF16 parts (the fp32 value; for a BF16 dx two,
- * within 2^-17 of it), or as it is where it is a BF16 dy; sums are fp32 in a fixed order.  Limits as moe_linear; no
+ * within 2^-17 of it), or as it is where it is a BF16 dy; sums are fp32 in a fixed order.  What is not finite in dz
+ * comes out as from one product.  An infinity in x or w meets every part of dz, zeros and such of the other sign among
+ * them: where dz is in parts, the elements of dw or dx that it enters are an infinity or NaN.  Limits as moe_linear; no
  * overlap of outputs, workspace and inputs.  workspace:
  * moe_linear_backward_workspace_size bytes (0 for sizes that are refused): 6 T R
  * (R rounded up to 64),

@@ -8,7 +8,7 @@
 // dx, neither does in dW.  An operand along k is read from LDS 8 k at a time, one across it by the transposing load.
 // dz is an fp32 value: it enters as BF16 parts (bf16(dz), bf16 of what is left, and so on), each with a
 // product of its own into the same sum.  Three hold all 24 bits, for fp32 results; two (within 2^-17) do for a BF16 dx, whose
-// own rounding is 2^-8.  (Two parts for fp32 results take two thirds of the time and leave an error of 2.5e-6 in
+// own rounding is 2^-8.  (An infinity of the other operand times the later parts, zeros or of the other sign, is NaN.)  (Two parts for fp32 results take two thirds of the time and leave an error of 2.5e-6 in
 // the Frobenius norm where the fp32 sums alone leave 4e-7 to 1.6e-6.)  Where dz is the BF16 dy itself (no activation) there is one.
 #pragma once
 #include "elements.h"

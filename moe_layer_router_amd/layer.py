@@ -573,8 +573,9 @@ def linear_backward(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, act: str
     """Gradients of linear (moe_linear_backward) for dy [T, N] bfloat16 or
     float32 and the pre that linear returned (needed with an activation).
     Returns dict(dx [T, K] of dx_dtype, dw float32 of w's shape, dbias float32),
-    None where not wanted; the residual's gradient is dy.  `out`, a previous
-    result, is reused."""
+    None where not wanted; the residual's gradient is dy.  An infinity in x or w
+    may come out as NaN, but for a bfloat16 dy without an activation.  `out`, a
+    previous result, is reused."""
     _matrix(x, "x", _BF16)
     T, K = x.shape
     dev = x.device

@@ -52,3 +52,27 @@ def test_swiglu_of_large_finite_factors(gpu_lib):
     bound = np.where(np.tile(gate, 2) < -88, 2.0 ** -126 * 128 * size, 60 * U * size * (1 + g2))
     assert np.all(np.abs(got - ref) <= bound), (got, ref)
     assert np.all(np.abs(_np(out["dw"])[:, 0] - ref) <= bound)
+
+
+@pytest.mark.parametrize("T", [3, 70, 700])
+def test_infinities_of_the_other_operand(gpu_lib, T):
+    """An infinity in W (x) with a dz in parts: the elements of dx (dW) that it enters are not finite, an infinity or a NaN;
+    the others are those of the call without it.  With a BF16 dy of no activation, one part, it is an infinity of the product's sign."""
+    from moe_layer_router_amd import layer as L
+    K, N = 200, 72
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, K, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn(N, K, generator=g, device="cuda").to(torch.bfloat16)
+    dy = torch.randn(T, N, generator=g, device="cuda")
+    dy[dy == 0] = 1
+    xi, wi = x.clone(), w.clone()
+    xi[2, 5], wi[7, 9] = -float("inf"), float("inf")
+    for d in (dy, dy.to(torch.bfloat16)):
+        ref, out = L.linear_backward(x, w, d), L.linear_backward(xi, wi, d)
+        for name, col in (("dx", 9), ("dw", 5)):
+            other = torch.arange(K, device="cuda") != col
+            assert torch.equal(out[name][:, other], ref[name][:, other]), name
+            assert not bool(torch.isfinite(out[name][:, col]).any()), name
+        if d.dtype == torch.bfloat16:
+            assert torch.equal(out["dx"][:, 9], float("inf") * torch.sign(d[:, 7].float()))
+            assert torch.equal(out["dw"][:, 5], -float("inf") * torch.sign(d[2].float()))
