@@ -657,10 +657,10 @@ moe_status moe_linear_backward(int32_t T, int32_t K, int32_t N, int32_t act, con
  * and rounds to the code above or below stochastically, a nonzero root of v never
  * to zero.  Zero codes with scales of 1 are the states before the first step.
  * Stochastic rounding adds 16 random bits, a hash of (seed, t, the tensor's place in
- * the call, the element's index), to what is dropped: the same call gives the same bits.
+ * the call, the element's index; of t and the index the low 32 bits), to what is dropped: the same call gives the same bits.
  * grad_scale, lr_dev, step_dev: optional scalars in device memory (NULL: 1, lr,
  * step), read when the kernels run, for captured graphs; step_dev must be >= 1.  If grad_scale is
- * not finite nothing is written: a step whose gradients overflowed is left out.
+ * not finite nothing is written: a step whose gradients overflowed is left out (whether t goes on is the caller's).
  * 0 <= beta < 1, eps from 2^-100 to 2^100, n <= 2^34, |g| up to 2^63 (v' beyond is
  * infinite); tensors 16-byte aligned, scales and scalars to their size; what is written
  * overlaps nothing else (a tensor stands in the list once).  No workspace; one launch for

@@ -699,7 +699,10 @@ class AdamW:
         """One step with the gradients `grads` (bfloat16 or float32 tensors of the
         params' shapes, in their order).  grad_scale: a float32 tensor [1] on the
         GPU that they are multiplied by (a clipping or unscaling factor); if it is
-        not finite nothing is updated (the count goes on)."""
+        not finite nothing is updated.  The count goes on, and with it the bias
+        corrections; a caller for whom it counts updates takes it back after the
+        step, with count -= 1, or (capturable, in a graph too, with no wait for the
+        GPU) count.add_(torch.isfinite(grad_scale).long() - 1)."""
         dev = self.device
         _need(len(grads) == len(self.params), "grads must have one entry per tensor")
         with _on(dev, stream):
