@@ -103,7 +103,7 @@ DEV SelRow sel_row64(const SelRule& a, const float* row) {
 }
 DEV double sel_choice64(const SelRule& a, const SelRow& r, int e) {
   const float l = r.l[e];
-  double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : r.sum == 0.0 ? 0.0 : exp((double)l - (double)r.mx) / r.sum;
+  double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : r.sum == 0.0 || (l == -__builtin_inff() && r.sum == r.sum) ? 0.0 : exp((double)l - (double)r.mx) / r.sum;
   return a.bias ? s + (double)a.bias[e] : s;
 }
 
