@@ -501,7 +501,8 @@ moe_status moe_balance_loss(int32_t T, int32_t E, int32_t top_k, int32_t n_seq, 
  * Scores, group scores and what is compared are those of 64-bit arithmetic, so
  * that near-ties are not decided by fp32 rounding; weights are fp32 (with
  * renormalize also where all scores underflow).  A NaN is ordered as -infinity;
- * it makes the weights NaN that it enters.  With renormalize, selected scores
+ * it makes the weights NaN that it enters (a softmax over all E: every score of its
+ * token, but renormalised weights only where it is selected).  With renormalize, selected scores
  * that are all zero (logits of -infinity) give zero weights; with softmax a row
  * of -infinity has zero scores.  A bias of -infinity takes an expert out as
  * long as others are left.  Output goes to moe_forward with

@@ -78,8 +78,10 @@ DEV uint32_t adam_bf16(float x, uint32_t r) {
   const uint32_t u = __float_as_uint(x);
   return (u + (__builtin_isfpclass(x, 0x207) ? 0 : r)) >> 16;      // (NaN, infinities: their classes)
 }
-// The square root of x >= 2^-96 (or zero), correctly rounded: the instruction's result, or one of its
-// neighbours where the residue says so.
+// The square root of x >= 2^-96 (or zero), correctly rounded: the instruction's result s, at most a unit off, or one of its neighbours, by
+// Tuckerman's test.  The root lies below s - ulp / 2, half way to the neighbour below, where x < (s - ulp / 2)^2 = s (s - ulp) + ulp^2 / 4;
+// x and s (s - ulp) are multiples of ulp^2, so that this is x <= s (s - ulp), and above half way up likewise x > s (s + ulp).
+// A fused residue has the exact difference's sign.
 DEV float adam_sqrt(float x) {
   const float s = __builtin_amdgcn_sqrtf(x);
   const float down = __uint_as_float(__float_as_uint(s) - 1), up = __uint_as_float(__float_as_uint(s) + 1);

@@ -192,11 +192,15 @@ moe_status launch_grads(LinGemm x, LinGemm w, const LinDbias& b, int cus, hipStr
 }
 
 // Few rows of x: W is read once by kernels that need no tile of rows.  They read x once per 16 rows of W, so that the tiles win with many
-// rows and a long k.  Both in us, of a captured run of calls (N = 2048):
-//   K = 2048:  T = 1 5.4 (tiles 9.5), T = 16 6.8 (10.2), T = 32 8.5 (10.4)
-//   K = 7168:  T = 1 11.8 (16.7), T = 4 13.2 (16.9), T = 16 17.5 (17.1), T = 32 24.2 (17.8)
-//   K = 16384: T = 1 21.0 (21.6), T = 16 31.3 (21.3)
-//   K = 4096, N = 7168: T = 16 17.5 (17.9), T = 17 19.2 (17.9), T = 32 24.0 (17.8)
+// rows and a long k.  Both in us, of a captured run of calls:
+//   N = 2048:  K = 2048   T = 1 5.5 (tiles 9.5), T = 16 6.8 (9.6), T = 32 8.4 (10.3)
+//              K = 7168   T = 1 11.8 (16.4), T = 4 13.5 (16.6), T = 16 17.4 (16.8), T = 32 23.9 (17.0)
+//              K = 16384  T = 1 20.5 (21.5), T = 16 30.7 (21.9)
+//   N = 7168:  K = 2048   T = 1 8.6 (16.3), T = 16 10.5 (14.3), T = 32 14.0 (17.0)
+//              K = 4096   T = 16 17.6 (18.1), T = 17 19.1 (17.5), T = 32 24.0 (18.0)
+//              K = 7168   T = 1 23.7 (25.7), T = 4 26.0 (24.8), T = 16 33.7 (25.5)
+// (The rule does not know N: it takes the slower side at K = 7168 with N = 7168 and T = 4 to 16, and at K = 4096 with N = 2048 and T = 17 to 32,
+// where these kernels take 11.2 to 13.8 for 15.5.)
 bool lin_few(long T, long K) { return T <= 16 ? (T + 16) * K <= 1 << 18 : T <= 32 && K <= 2048; }
 template <int GATED>
 moe_status launch_rows(const LinGemm& g, hipStream_t st) {

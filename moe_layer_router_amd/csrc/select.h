@@ -207,8 +207,8 @@ DEV float sel_row_exps(const float (&v)[NV], float m, float (&e)[NV]) {
 //   - A value that k to k + 4 of the 64 lanes' largest c reach is found by bisection.  The k best are among the experts that reach it,
 //     some 1.3 k of up to 1024 (those of lanes with two of them).  They go to LDS, one to a lane, and are ranked by counting.
 //   - A NaN reaches no value.  It counts as -infinity, so that it may be among the k best only where that is the value.
-// Candidates too near to each other are ranked again by fp64 scores of their own.  A NaN, group scores too near to each other or
-// too many candidates (few lanes with experts left) leave it all to sel_exact.
+// Candidates too near to each other are ranked again by fp64 scores of their own.  A NaN that may matter, group scores too near to each
+// other or too many candidates (few lanes with experts left) leave it all to sel_exact.
 struct SelCand {
   float c[68];
   int e[64];
@@ -402,7 +402,7 @@ DEV float sel_scores16(bool sigmoid, bool live, float lj) {
 }
 
 // One token per wave; GROUPED: some groups are left out.  Bound by the vector unit: 16384 tokens of 1024 experts with softmax
-// scores and a bias, some 420 instructions each, take 22.5 us, 3.1 TB/s (27 us where every near-tie forms E exponentials in fp64).
+// scores and a bias, some 420 instructions each, take 23.0 us, 3.0 TB/s (27 us where every near-tie forms E exponentials in fp64).
 template <int NV, int SIGMOID, int GROUPED>
 __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select(SelArgs a) {
   __shared__ __attribute__((aligned(16))) double buf[kSelWaves][64 * NV];
@@ -800,7 +800,7 @@ __global__ void __launch_bounds__(64 * kSelWaves, 4) k_select_pair(SelArgs a) {
 //   sigmoid: dl_j = d_j s_j (1 - s_j), zero elsewhere
 //   softmax: dl_e = s_e ([e selected] d_e - sum_i s_i d_i); with renorm the sum is zero: dl_j = q_j (...)
 // The differences cancel (1 - s of a sure expert, dw against its mean): they are formed in
-// fp64, which only the k selected experts need.
+// fp64, which only the k selected experts need.  Softmax's sum over all experts is fp32's: s, and 1 - s with it, are off by some 16 2^-24.
 // An expert that stands twice among a token's ids has the sum of both entries.
 //
 // A wave does four tokens at a time: their selected experts in the four rows of 16 lanes, their rows of E one after another.
